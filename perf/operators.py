@@ -1,0 +1,610 @@
+"""The timed cases of the operators around a QLoRA layer with experts: dropout
+from a counter-based generator, the layer whose adapter input is dropped out,
+the layer grouped by expert, and the two exchanges that surround it (token
+rows into expert order, expert rows back into token order).
+
+Each case is a dict of plain values.  `prepare` makes its inputs from a seed,
+`run` makes one pass: with `own` false in elementary torch operations (32-bit
+arithmetic, rounded once at the end), with `own` true through this
+repository's package.  `exact` gives the same outputs from the definitions in
+64 bits, and `work` the bytes and operations a pass cannot do without.
+
+Definitions
+  mask      element i of a tensor (its row-major index) belongs to piece i / 8;
+            the piece's 128 random bits are Philox4x32-7 of the counter (piece
+            low, piece high, offset low, offset high) under the key (seed low,
+            seed high), where seed and offset are the two 64-bit words of the
+            state; element i takes 16-bit half i % 8 (low half of word 0
+            first) and is kept when that is at least t = min(round(p 65536),
+            65535).  Kept elements are scaled by c = 65536 / (65536 - t).
+  dropout   y = mask c x
+  layer     T = c (mask X) A,  Y = X W^T + s T B
+            G = dY B^T,  dX = dY W + s c mask (G A^T),  dA = s c (mask X)^T G,
+            dB = s T^T dY
+  grouped   the layer for each expert e on its rows [offsets[e], offsets[e+1])
+            with its own weight, A and B (without dropout: mask = c = 1)
+  route     slots (token, choice) sorted by expert, stably: offsets, order
+            (row -> slot, -1 behind the last row), inverse (slot -> row, -1 for
+            an id outside 0..E-1), and row i = X[order[i] / topk]
+  merge     out[t] = sum_j w[t, j] Y[inverse[t, j]], and its gradients
+            dY[inverse[t, j]] = w[t, j] dOut[t], dw[t, j] = dOut[t] . Y[inverse[t, j]]
+W is 4-bit codes in blocks of 64 with one constant c_b each (an 8-bit integer
+times one fp32 per 256 blocks, or fp32): bf16(level[code] c_b).
+"""
+import math
+import statistics
+
+import numpy as np
+import torch
+
+own = False
+
+DEV = "cuda"
+
+
+# ---------------------------------------------------------------------------
+# Cases
+# ---------------------------------------------------------------------------
+
+def listed():
+    return [
+        # one decode step's hidden state (16 tokens of width 1024): latency
+        dict(name="dropout_16x1024", kind="dropout", n=16 * 1024, p=0.1),
+        # the FFN activations of a 33B-shaped layer at 4096 tokens
+        dict(name="dropout_4096x17920", kind="dropout", n=4096 * 17920, p=0.05),
+        # the smallest training step: the 1024 x 1024 linear, 16 tokens
+        dict(name="linear_fwd_1k", kind="linear", back=False, M=16, N=1024, K=1024, r=16, p=0.1,
+             book="nf4", dq=True),
+        # gradients of a 7B layer's up projection, 2048 tokens
+        dict(name="linear_bwd_7b_up", kind="linear", back=True, M=2048, N=11008, K=4096, r=64,
+             p=0.05, book="nf4", dq=True),
+        # two tokens, two experts each: one decode step of eight 4096-wide experts
+        dict(name="grouped_fwd_decode", kind="grouped", back=False, sizes="1,0,0,2,0,1,0,0",
+             N=4096, K=4096, r=16, p=0.0, book="nf4", dq=True),
+        # 48 tokens, two experts each: a serving batch on the up projection
+        dict(name="grouped_fwd_batch", kind="grouped", back=False, sizes="11,17,0,9,21,5,30,3",
+             N=11008, K=4096, r=64, p=0.0, book="nf4", dq=True),
+        # 4096 tokens, two experts each, ragged: training forward of the up
+        # projection with adapter dropout
+        dict(name="grouped_fwd_train", kind="grouped", back=False,
+             sizes="1203,871,1518,402,1100,1337,64,1697", N=11008, K=4096, r=64, p=0.05,
+             book="nf4", dq=True),
+        # the same rows through the down projection, backward
+        dict(name="grouped_bwd_train", kind="grouped", back=True,
+             sizes="1203,871,1518,402,1100,1337,64,1697", N=4096, K=11008, r=64, p=0.0,
+             book="nf4", dq=True),
+        # a decode step's tokens sorted by expert: latency
+        dict(name="route_8", kind="route", tokens=8, topk=2, E=8, K=4096, drop=0.0),
+        # a training batch of a fine-grained expert layer
+        dict(name="route_8192", kind="route", tokens=8192, topk=4, E=64, K=4096, drop=0.0),
+        # expert outputs of the decode step back into token order
+        dict(name="merge_8", kind="merge", tokens=8, topk=2, E=8, K=4096, drop=0.0, back=False),
+        # and of the training batch, with the gradients
+        dict(name="merge_8192", kind="merge", tokens=8192, topk=4, E=64, K=4096, drop=0.0,
+             back=True),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def _draw_weight(rng):
+    """N (a multiple of 8), K (of 64), r (of 8), the codebook and constants."""
+    N = 8 * _log_int(rng, 8, 1376)
+    K = 64 * _log_int(rng, 1, 172)
+    r = 8 * _log_int(rng, 1, 16)
+    return N, K, r, rng.choice(["nf4", "nf4", "nf4", "int4", "fp4"]), rng.random() < 0.75
+
+
+def draw(rng):
+    kind = rng.choice(["dropout", "linear", "grouped", "grouped", "route", "merge"])
+    if kind == "dropout":
+        return dict(kind=kind, n=_log_int(rng, 1, 4096 * 8192), p=round(rng.uniform(0.0, 0.6), 3))
+    if kind == "linear":
+        N, K, r, book, dq = _draw_weight(rng)
+        return dict(kind=kind, back=rng.random() < 0.5, M=_log_int(rng, 1, 2048), N=N, K=K, r=r,
+                    p=round(rng.uniform(0.0, 0.6), 3), book=book, dq=dq)
+    if kind == "grouped":
+        N, K, r, book, dq = _draw_weight(rng)
+        E = _log_int(rng, 1, 48)
+        while E * N * K > 8 * 11008 * 4096:
+            E = (E + 1) // 2
+        if dq:   # an expert's weight is whole groups of 256 blocks
+            step = 16384 // math.gcd(16384, 8 * K)
+            N = 8 * step * max(1, round(N / (8 * step)))
+        M = _log_int(rng, 1, 4096)
+        M = min(M, max(1, 8192 * 4096 * 11008 // (2 * N * K)))
+        # shares of the experts: from even to a few that take most
+        share = [rng.random() ** rng.choice([0.2, 1, 4]) for _ in range(E)]
+        sizes = [0] * E
+        for _ in range(M):
+            sizes[rng.choices(range(E), share)[0]] += 1
+        p = rng.choice([0.0, 0.0, round(rng.uniform(0.0, 0.6), 3)])
+        return dict(kind=kind, back=rng.random() < 0.5, sizes=",".join(map(str, sizes)), N=N, K=K,
+                    r=r, p=p, book=book, dq=dq)
+    E = _log_int(rng, 1, 256)
+    case = dict(kind=kind, tokens=_log_int(rng, 1, 8192), topk=rng.randint(1, min(6, E)), E=E,
+                K=8 * _log_int(rng, 1, 512), drop=rng.choice([0.0, 0.0, 0.1]))
+    if kind == "merge":
+        case["back"] = rng.random() < 0.5
+    return case
+
+
+def _sizes(case):
+    return [int(v) for v in case["sizes"].split(",")]
+
+
+def work(case):
+    kind = case["kind"]
+    if kind == "dropout":
+        return {"bytes": 4 * case["n"], "flops": case["n"]}
+    if kind in ("route", "merge"):
+        n, K = case["tokens"] * case["topk"], case["K"]
+        rows = n * K * 2
+        if kind == "route":   # ids; offsets, order, inverse; each token row once, each slot's row
+            return {"bytes": 12 * n + 4 * case["E"] + case["tokens"] * K * 2 + rows, "flops": 0}
+        b = 8 * n + rows + case["tokens"] * K * 2    # inverse, weights, Y -> out
+        f = 2 * n * K
+        if case["back"]:                             # dOut -> dY, dw (Y is in hand: read once)
+            b += case["tokens"] * K * 2 + rows + 4 * n
+            f += 3 * n * K
+        return {"bytes": b, "flops": f}
+    N, K, r = case["N"], case["K"], case["r"]
+    sizes = [case["M"]] if kind == "linear" else _sizes(case)
+    M, active = sum(sizes), sum(1 for m in sizes if m)
+    wbytes = N * K / 2 + (N * K / 64 * (1 + 4 / 256) if case["dq"] else N * K / 64 * 4)
+    adapters = 2 * r * (N + K)
+    b = active * (wbytes + adapters) + 2 * M * (N + K) + 4 * M * r
+    f = 2 * M * N * K + 2 * M * r * (N + K)
+    if case["back"]:
+        # + X for dA; dA and dB of every expert
+        b += 2 * M * K + len(sizes) * adapters
+        f += 2 * M * r * (N + K)
+    return {"bytes": int(b), "flops": f}
+
+
+# ---------------------------------------------------------------------------
+# Inputs
+# ---------------------------------------------------------------------------
+
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def _bf16(g, shape, std=1.0):
+    return (torch.randn(shape, generator=g, device=DEV) * std).to(torch.bfloat16)
+
+
+def _state(g):
+    return torch.randint(-2 ** 63, 2 ** 63 - 1, (2,), generator=g, device=DEV, dtype=torch.int64)
+
+
+def _weight(g, rows, K, dq):
+    """Codes and constants of a weight of standard deviation about 0.02: the
+    codes are near uniform (each level of NF4 covers equal probability mass)
+    and a block's largest magnitude is near 2.4 standard deviations."""
+    nb = rows * K // 64
+    codes = torch.randint(0, 256, (rows * K // 2,), generator=g, device=DEV, dtype=torch.uint8)
+    if not dq:
+        q = None
+        scale = 0.048 * (0.7 + 0.6 * torch.rand(nb, generator=g, device=DEV))
+    else:
+        q = torch.randint(100, 256, (nb,), generator=g, device=DEV, dtype=torch.uint8)
+        ng = (nb + 255) // 256
+        scale = 0.065 / 255 * (0.9 + 0.2 * torch.rand(ng, generator=g, device=DEV))
+    return codes, q, scale
+
+
+def _own_weight(w, rows, K, case):
+    import bit_quantized_fine_amd as q
+    return q.Q4Weight(w[0], w[1], w[2], rows, K, case["book"], case["dq"])
+
+
+def _ids(g, case):
+    """topk different experts for every token; a share of the slots dropped."""
+    key = torch.rand((case["tokens"], case["E"]), generator=g, device=DEV)
+    key += 0.5 * torch.rand((1, case["E"]), generator=g, device=DEV)   # popular experts
+    ids = key.topk(case["topk"], dim=1).indices.to(torch.int32)
+    lost = torch.rand(ids.shape, generator=g, device=DEV) < case["drop"]
+    return torch.where(lost, torch.full_like(ids, -1), ids)
+
+
+def _make(case, seed):
+    """The inputs of a case, the same for every form."""
+    g = _gen(seed)
+    kind = case["kind"]
+    if kind == "dropout":
+        return dict(x=_bf16(g, (case["n"],)), state=_state(g))
+    if kind in ("route", "merge"):
+        n = case["tokens"] * case["topk"]
+        st = dict(ids=_ids(g, case))
+        if kind == "route":
+            st["X"] = _bf16(g, (case["tokens"], case["K"]))
+            return st
+        st["Y"] = _bf16(g, (n, case["K"]))
+        st["w"] = torch.rand((case["tokens"], case["topk"]), generator=g, device=DEV)
+        if case["back"]:
+            st["dOut"] = _bf16(g, (case["tokens"], case["K"]))
+        return st
+    N, K, r = case["N"], case["K"], case["r"]
+    sizes = [case["M"]] if kind == "linear" else _sizes(case)
+    E, M = len(sizes), sum(sizes)
+    st = dict(X=_bf16(g, (M, K)), w=_weight(g, E * N, K, case["dq"]),
+              A=_bf16(g, (E, K, r), 1.0 / r), B=_bf16(g, (E, r, N), 0.01), state=_state(g))
+    if case["back"]:
+        st["dY"] = _bf16(g, (M, N))
+    return st
+
+
+def prepare(case, seed):
+    st = _make(case, seed)
+    kind = case["kind"]
+    st["case"] = case
+    if kind in ("route", "merge"):
+        # the plan's row of every slot, from a stable sort of the ids
+        E = case["E"]
+        flat = st["ids"].reshape(-1).long()
+        flat = torch.where((flat < 0) | (flat >= E), torch.full_like(flat, E), flat)
+        order = torch.sort(flat, stable=True).indices
+        inv = torch.empty_like(order)
+        inv[order] = torch.arange(order.numel(), device=DEV)
+        inv = torch.where(flat < E, inv, torch.full_like(inv, -1))
+        if kind == "route":
+            st["rows"] = torch.zeros((flat.numel(), case["K"]), dtype=torch.bfloat16, device=DEV)
+        else:
+            st["inverse"] = inv.to(torch.int32).reshape(st["ids"].shape)
+            if case["back"]:
+                st["dY"] = torch.zeros_like(st["Y"])
+        return st
+    if kind == "dropout":
+        return st
+    sizes = [case["M"]] if kind == "linear" else _sizes(case)
+    st["sizes"] = sizes
+    st["offsets"] = torch.tensor(np.concatenate([[0], np.cumsum(sizes)]), dtype=torch.int32,
+                                 device=DEV)
+    if own:
+        st["ow"] = _own_weight(st["w"], len(sizes) * case["N"], case["K"], case)
+        if kind == "linear":
+            st["A"], st["B"] = st["A"][0], st["B"][0]
+            if case["back"]:   # what the forward pass kept
+                import bit_quantized_fine_amd as q
+                st["T"] = q.qlora_linear_dropout_fwd(st["X"], st["ow"], st["A"], st["B"],
+                                                     _S, case["p"], st["state"])[1]
+        elif case["back"]:
+            import bit_quantized_fine_amd as q
+            st["T"] = q.qlora_grouped_fwd(st["X"], st["offsets"], st["ow"], len(sizes), st["A"],
+                                          st["B"], _S, case["p"], st["state"])[1]
+    elif case["back"]:
+        st["T"] = _plain_t(st)
+    return st
+
+
+_S = 0.25   # the adapters' scale, alpha / r of 16 / 64
+
+
+# ---------------------------------------------------------------------------
+# The plain forms
+# ---------------------------------------------------------------------------
+
+def _threshold(p):
+    return min(65535, int(math.floor(float(np.float32(p)) * 65536 + 0.5)))
+
+
+def _keep_scale(p):
+    return float(np.float32(65536.0 / (65536 - _threshold(p))))
+
+
+def _mask(state, n, p):
+    """keep [n] (bool): Philox4x32-7 in wrapping 64-bit integers."""
+    lo32 = 0xFFFFFFFF
+    piece = torch.arange((n + 7) // 8, device=DEV, dtype=torch.int64)
+    c = [piece & lo32, (piece >> 32) & lo32,
+         (state[1] & lo32).expand_as(piece), ((state[1] >> 32) & lo32).expand_as(piece)]
+    k0, k1 = state[0] & lo32, (state[0] >> 32) & lo32
+    for _ in range(7):
+        a, b = c[0] * 0xD2511F53, c[2] * 0xCD9E8D57
+        c = [((b >> 32) & lo32) ^ c[1] ^ k0, b & lo32, ((a >> 32) & lo32) ^ c[3] ^ k1, a & lo32]
+        k0, k1 = (k0 + 0x9E3779B9) & lo32, (k1 + 0xBB67AE85) & lo32
+    halves = torch.stack([h for w in c for h in (w & 0xFFFF, w >> 16)], dim=1)
+    return halves.reshape(-1)[:n] >= _threshold(p)
+
+
+def _levels(book):
+    if book == "nf4":
+        pos = torch.special.ndtri(0.5 + (torch.arange(1, 9, dtype=torch.float64) - 0.5) / 16)
+        neg = torch.special.ndtri(0.5 + (torch.arange(1, 8, dtype=torch.float64) - 0.5) / 14)
+        lv = torch.cat([-neg.flip(0) / neg[-1], torch.zeros(1, dtype=torch.float64),
+                        pos / pos[-1]])
+    elif book == "int4":
+        lv = (2 * torch.arange(16, dtype=torch.float64) - 15) / 15
+    else:
+        mag = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64) / 6
+        lv = torch.cat([-mag.flip(0)[:7], torch.zeros(1, dtype=torch.float64), -mag[:1], mag[1:]])
+    return lv.to(torch.float32).to(DEV)
+
+
+def _dequant(st, e):
+    """Weight of expert e, fp32 [N, K] holding bf16 values."""
+    case = st["case"]
+    N, K = case["N"], case["K"]
+    codes, q, scale = st["w"]
+    nb = N * K // 64
+    c = codes[e * N * K // 2:(e + 1) * N * K // 2]
+    lv = _levels(case["book"])
+    w = torch.stack([lv[(c & 15).long()], lv[(c >> 4).long()]], dim=1).reshape(nb, 64)
+    blocks = torch.arange(e * nb, (e + 1) * nb, device=DEV)
+    ch = q[blocks].float() * scale[blocks // 256] if q is not None else scale[blocks]
+    return (w * ch[:, None]).to(torch.bfloat16).float().reshape(N, K)
+
+
+def _spans(st):
+    lo = 0
+    for e, m in enumerate(st["sizes"]):
+        yield e, slice(lo, lo + m)
+        lo += m
+
+
+def _dropped(st):
+    """X in fp32 with the mask applied (not scaled), and the mask or None."""
+    X, p = st["X"].float(), st["case"]["p"]
+    if st["case"]["kind"] == "grouped" and p == 0:
+        return X, None, 1.0
+    keep = _mask(st["state"], X.numel(), p).reshape(X.shape)
+    return torch.where(keep, X, torch.zeros_like(X)), keep, _keep_scale(p)
+
+
+def _plain_t(st):
+    Xd, _, c = _dropped(st)
+    T = torch.empty((Xd.shape[0], st["case"]["r"]), device=DEV)
+    for e, rows in _spans(st):
+        T[rows] = c * (Xd[rows] @ st["A"][e].float())
+    return T
+
+
+def _plain_fwd(st):
+    X, T = st["X"].float(), _plain_t(st)
+    Y = torch.empty((X.shape[0], st["case"]["N"]), dtype=torch.bfloat16, device=DEV)
+    for e, rows in _spans(st):
+        if rows.stop > rows.start:
+            Y[rows] = (X[rows] @ _dequant(st, e).t()
+                       + _S * (T[rows] @ st["B"][e].float())).to(torch.bfloat16)
+    return Y, T
+
+
+def _plain_bwd(st):
+    case = st["case"]
+    Xd, keep, c = _dropped(st)
+    dY, T = st["dY"].float(), st["T"]
+    dX = torch.empty_like(st["X"])
+    dA, dB = torch.empty_like(st["A"]), torch.empty_like(st["B"])
+    for e, rows in _spans(st):
+        G = dY[rows] @ st["B"][e].float().t()
+        dA[e] = (_S * c * (Xd[rows].t() @ G)).to(torch.bfloat16)
+        dB[e] = (_S * (T[rows].t() @ dY[rows])).to(torch.bfloat16)
+        if rows.stop > rows.start:
+            L = _S * c * (G @ st["A"][e].float().t())
+            if keep is not None:
+                L = torch.where(keep[rows], L, torch.zeros_like(L))
+            dX[rows] = (dY[rows] @ _dequant(st, e) + L).to(torch.bfloat16)
+    if case["kind"] == "linear":
+        dA, dB = dA[0], dB[0]
+    return dX, dA, dB
+
+
+def _plain_route(st):
+    case = st["case"]
+    E, topk = case["E"], case["topk"]
+    ids = st["ids"].reshape(-1).long()
+    ids = torch.where((ids < 0) | (ids >= E), torch.full_like(ids, E), ids)
+    key, order = torch.sort(ids, stable=True)
+    offsets = torch.searchsorted(key, torch.arange(E + 1, device=DEV))
+    inverse = torch.empty_like(order)
+    inverse[order] = torch.arange(order.numel(), device=DEV)
+    inverse = torch.where(ids < E, inverse, torch.full_like(inverse, -1))
+    live = key < E
+    rows = torch.where(live[:, None], st["X"][order // topk], torch.zeros_like(st["rows"]))
+    order = torch.where(live, order, torch.full_like(order, -1))
+    return (offsets.to(torch.int32), order.to(torch.int32),
+            inverse.to(torch.int32).reshape(st["ids"].shape), rows)
+
+
+def _plain_merge(st):
+    inv = st["inverse"].long()
+    live = inv >= 0
+    Y = st["Y"].float()[inv.clamp(min=0)]                   # [tokens, topk, K]
+    w = torch.where(live, st["w"], torch.zeros_like(st["w"]))
+    out = (w[:, :, None] * Y).sum(dim=1).to(torch.bfloat16)
+    if not st["case"]["back"]:
+        return out
+    dOut = st["dOut"].float()
+    dw = torch.where(live, (dOut[:, None, :] * Y).sum(dim=2), torch.zeros_like(w))
+    dY = torch.zeros_like(st["Y"])
+    rows = (w[:, :, None] * dOut[:, None, :]).to(torch.bfloat16)
+    dY[inv[live]] = rows[live]
+    return out, dY, dw
+
+
+def _plain_dropout(st):
+    x, p = st["x"], st["case"]["p"]
+    keep = _mask(st["state"], x.numel(), p)
+    return torch.where(keep, x.float() * _keep_scale(p), torch.zeros((), device=DEV)).to(x.dtype)
+
+
+# ---------------------------------------------------------------------------
+# One pass
+# ---------------------------------------------------------------------------
+
+def run(st):
+    case = st["case"]
+    kind = case["kind"]
+    if not own:
+        if kind == "dropout":
+            return _plain_dropout(st)
+        if kind == "route":
+            return _plain_route(st)
+        if kind == "merge":
+            return _plain_merge(st)
+        return _plain_bwd(st) if case["back"] else _plain_fwd(st)
+    import bit_quantized_fine_amd as q
+    if kind == "dropout":
+        return q.qlora_dropout(st["x"], case["p"], st["state"])
+    if kind == "route":
+        offsets, order, inverse = q.qlora_expert_plan(st["ids"], case["E"])
+        rows = q.qlora_expert_gather(st["X"], order, offsets, case["topk"], out=st["rows"])
+        return offsets, order, inverse, rows
+    if kind == "merge":
+        out = q.qlora_expert_combine(st["Y"], st["inverse"], st["w"])
+        if not case["back"]:
+            return out
+        dY, dw = q.qlora_expert_combine_bwd(st["dOut"], st["Y"], st["inverse"], st["w"],
+                                            dY=st["dY"])
+        return out, dY, dw
+    if kind == "linear":
+        if case["back"]:
+            return q.qlora_linear_dropout_bwd(st["dY"], st["X"], st["ow"], st["A"], st["B"], _S,
+                                              case["p"], st["state"], T=st["T"])
+        return q.qlora_linear_dropout_fwd(st["X"], st["ow"], st["A"], st["B"], _S, case["p"],
+                                          st["state"])
+    E = len(st["sizes"])
+    if case["back"]:
+        return q.qlora_grouped_bwd(st["dY"], st["X"], st["offsets"], st["ow"], E, st["A"], st["B"],
+                                   _S, case["p"], st["state"], T=st["T"])
+    return q.qlora_grouped_fwd(st["X"], st["offsets"], st["ow"], E, st["A"], st["B"], _S,
+                               case["p"], st["state"])
+
+
+# ---------------------------------------------------------------------------
+# The definitions in 64 bits, apart from the plain forms above
+# ---------------------------------------------------------------------------
+
+def _keep64(state, n, p):
+    """The mask from numpy's unsigned integers, on the host."""
+    seed, off = (int(v) % 2 ** 64 for v in state.cpu())
+    m = (n + 7) // 8
+    idx = np.arange(m, dtype=np.uint64)
+    lo = np.uint64(0xFFFFFFFF)
+    sh = np.uint64(32)
+    x0, x1 = idx & lo, idx >> sh
+    x2 = np.full(m, off & 0xFFFFFFFF, np.uint64)
+    x3 = np.full(m, off >> 32, np.uint64)
+    for i in range(7):
+        ka = np.uint64(((seed & 0xFFFFFFFF) + i * 0x9E3779B9) & 0xFFFFFFFF)
+        kb = np.uint64(((seed >> 32) + i * 0xBB67AE85) & 0xFFFFFFFF)
+        u, v = x0 * np.uint64(0xD2511F53), x2 * np.uint64(0xCD9E8D57)
+        x0, x1, x2, x3 = (v >> sh) ^ x1 ^ ka, v & lo, (u >> sh) ^ x3 ^ kb, u & lo
+    words = np.stack([x0, x1, x2, x3], axis=1).astype("<u4")
+    halves = words.view("<u2").reshape(-1)[:n]
+    t = min(65535, int(np.floor(np.float64(np.float32(p)) * 65536.0 + 0.5)))
+    return torch.from_numpy(halves >= t).to(DEV), 65536.0 / (65536 - t)
+
+
+def _levels64(book):
+    """The fp32 levels of a codebook (part of the format), from the standard
+    library's normal quantiles and from the E2M1 bit patterns."""
+    if book == "nf4":
+        z = statistics.NormalDist().inv_cdf
+        pos = [z(0.5 + (j - 0.5) / 16) for j in range(1, 9)]
+        neg = [z(0.5 + (j - 0.5) / 14) for j in range(1, 8)]
+        lv = [-v / neg[-1] for v in reversed(neg)] + [0.0] + [v / pos[-1] for v in pos]
+    elif book == "int4":
+        lv = [(2 * k - 15) / 15 for k in range(16)]
+    else:
+        mag = [(b & 1) * 0.5 if b < 2 else math.ldexp(1 + (b & 1) / 2, (b >> 1) - 1)
+               for b in range(8)]
+        lv = [-v / 6 for v in reversed(mag[1:])] + [0.0, -0.0] + [v / 6 for v in mag[1:]]
+    return torch.from_numpy(np.array(lv).astype(np.float32)).to(DEV)
+
+
+def _w64(codes, q, scale, lv, N, K, e):
+    """deq(W_e) in 64 bits: the rounding to bf16 of the exact products of the
+    fp32 level and the fp32 constant is part of the format, and so is the
+    constant's own rounding to fp32."""
+    nb = N * K // 64
+    byte = codes.reshape(-1, nb, 32)[e].int()
+    idx = torch.empty((nb, 64), dtype=torch.int64, device=DEV)
+    idx[:, 0::2], idx[:, 1::2] = byte % 16, byte // 16
+    if q is not None:
+        b = torch.arange(e * nb, e * nb + nb, device=DEV)
+        c = (q.reshape(-1, nb)[e].double() * scale.double()[b // 256]).float()
+    else:
+        c = scale.reshape(-1, nb)[e]
+    prod = (lv.double()[idx] * c.double()[:, None]).float()
+    return prod.bfloat16().double().reshape(N, K)
+
+
+def exact(case, seed):
+    st = _make(case, seed)
+    kind = case["kind"]
+    if kind == "dropout":
+        keep, c = _keep64(st["state"], case["n"], case["p"])
+        return torch.where(keep, st["x"].double() * c, torch.zeros((), device=DEV,
+                                                                  dtype=torch.float64))
+    if kind in ("route", "merge"):
+        E, topk, K = case["E"], case["topk"], case["K"]
+        ids = st["ids"].cpu().numpy().reshape(-1)
+        order = np.full(ids.size, -1, np.int32)
+        inverse = np.full(ids.size, -1, np.int32)
+        offsets = np.zeros(E + 1, np.int32)
+        at = 0
+        for e in range(E):
+            hit = np.flatnonzero(ids == e)
+            order[at:at + hit.size] = hit
+            inverse[hit] = np.arange(at, at + hit.size)
+            at += hit.size
+            offsets[e + 1] = at
+        if kind == "route":
+            rows = torch.zeros((ids.size, K), dtype=torch.float64, device=DEV)
+            rows[:at] = st["X"].double()[torch.from_numpy(order[:at] // topk).long().to(DEV)]
+            return (torch.from_numpy(offsets).to(DEV), torch.from_numpy(order).to(DEV),
+                    torch.from_numpy(inverse.reshape(-1, topk)).to(DEV), rows)
+        out = torch.zeros((case["tokens"], K), dtype=torch.float64, device=DEV)
+        dY = torch.zeros((ids.size, K), dtype=torch.float64, device=DEV)
+        dw = torch.zeros((case["tokens"], topk), dtype=torch.float64, device=DEV)
+        for j in range(topk):
+            row = inverse.reshape(-1, topk)[:, j]
+            tok = torch.from_numpy(np.flatnonzero(row >= 0)).to(DEV)
+            row = torch.from_numpy(row[row >= 0]).long().to(DEV)
+            w, y = st["w"][tok, j].double()[:, None], st["Y"][row].double()
+            out[tok] += w * y
+            if case["back"]:
+                d = st["dOut"][tok].double()
+                dY[row] = w * d
+                dw[tok, j] = (d * y).sum(1)
+        return (out, dY, dw) if case["back"] else out
+    N, K, r, p = case["N"], case["K"], case["r"], case["p"]
+    sizes = [case["M"]] if kind == "linear" else _sizes(case)
+    M = sum(sizes)
+    X = st["X"].double()
+    keep, c = None, 1.0
+    if kind == "linear" or p > 0:
+        keep, c = _keep64(st["state"], M * K, p)
+        keep = keep.reshape(M, K).double() * c
+    Xd = X if keep is None else X * keep
+    lv = _levels64(case["book"])
+    T = torch.empty((M, r), dtype=torch.float64, device=DEV)
+    first = torch.empty((M, K if case["back"] else N), dtype=torch.float64, device=DEV)
+    dA = torch.zeros((len(sizes), K, r), dtype=torch.float64, device=DEV)
+    dB = torch.zeros((len(sizes), r, N), dtype=torch.float64, device=DEV)
+    ends = np.cumsum(sizes)
+    for e, m in enumerate(sizes):
+        if m == 0:
+            continue
+        a, b = int(ends[e]) - m, int(ends[e])
+        A, B = st["A"][e].double(), st["B"][e].double()
+        W = _w64(*st["w"], lv, N, K, e)
+        T[a:b] = torch.mm(Xd[a:b], A)
+        if not case["back"]:
+            first[a:b] = torch.mm(X[a:b], W.T) + torch.mm(T[a:b], _S * B)
+            continue
+        dY = st["dY"][a:b].double()
+        G = torch.mm(dY, B.T) * _S
+        low = torch.mm(G, A.T)
+        first[a:b] = torch.mm(dY, W) + (low if keep is None else low * keep[a:b])
+        dA[e] = torch.mm(Xd[a:b].T, G)
+        dB[e] = torch.mm(T[a:b].T, dY) * _S
+    if not case["back"]:
+        return first, T
+    return (first, dA[0], dB[0]) if kind == "linear" else (first, dA, dB)
