@@ -453,7 +453,7 @@ def run(st):
         return q.qlora_dropout(st["x"], case["p"], st["state"])
     if kind == "route":
         offsets, order, inverse = q.qlora_expert_plan(st["ids"], case["E"])
-        rows = q.qlora_expert_gather(st["X"], order, offsets, case["topk"], out=st["rows"])
+        rows = q.qlora_expert_gather(st["X"], inverse, out=st["rows"])
         return offsets, order, inverse, rows
     if kind == "merge":
         out = q.qlora_expert_combine(st["Y"], st["inverse"], st["w"])
