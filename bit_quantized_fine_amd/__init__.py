@@ -36,6 +36,10 @@ class _Q4Weight(ctypes.Structure):
                 ("double_quant", ctypes.c_int32)]
 
 
+class _Dropout(ctypes.Structure):
+    _fields_ = [("state", ctypes.c_void_p), ("p", ctypes.c_float)]
+
+
 class _AdamWConfig(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float)]
@@ -125,6 +129,49 @@ _SIGS = {
                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
                                            ctypes.c_void_p]),
+    "qlora_dropout_apply": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64,
+                                           ctypes.POINTER(_Dropout), ctypes.c_void_p,
+                                           ctypes.c_void_p]),
+    "qlora_linear_dropout_fwd_workspace_bytes": (ctypes.c_size_t, [
+        ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
+    "qlora_linear_dropout_bwd_workspace_bytes": (ctypes.c_size_t, [
+        ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
+    "qlora_linear_dropout_fwd": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(_Q4Weight), ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.POINTER(_Dropout), ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qlora_linear_dropout_bwd": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(_Q4Weight),
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.POINTER(_Dropout),
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_size_t, ctypes.c_void_p]),
+    "qlora_grouped_fwd_workspace_bytes": (ctypes.c_size_t, [
+        ctypes.c_int64, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
+    "qlora_grouped_bwd_workspace_bytes": (ctypes.c_size_t, [
+        ctypes.c_int64, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
+    "qlora_grouped_fwd": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int,
+        ctypes.POINTER(_Q4Weight), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_float,
+        ctypes.POINTER(_Dropout), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_size_t, ctypes.c_void_p]),
+    "qlora_grouped_bwd": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int,
+        ctypes.POINTER(_Q4Weight), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_float,
+        ctypes.POINTER(_Dropout), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qlora_expert_plan_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int]),
+    "qlora_expert_plan": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qlora_expert_gather": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_void_p]),
+    "qlora_expert_combine": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "qlora_expert_combine_bwd": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int64,
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "qlora_adamw_step": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                         ctypes.c_void_p, ctypes.c_int64,
                                         ctypes.POINTER(_AdamWConfig), ctypes.c_int64,
@@ -543,6 +590,320 @@ def qlora_q4_linear_bwd(dY, X, w: Q4Weight, A=None, B=None, s: float = 1.0, T=No
     _x_rows(X, w.K)
     return _bwd("qlora_q4_linear_bwd", dY, X, w, _check_q4_weight(w), w._c(), A, B, s, T,
                 need_dx, dX, dA, dB, workspace)
+
+
+def _as_q4(w) -> Q4Weight:
+    """An NF4Weight as the Q4Weight it is."""
+    if isinstance(w, NF4Weight):
+        return Q4Weight(w.codes, w.absmax_q, w.absmax_scale, w.N, w.K, "nf4", True)
+    return w
+
+
+def _call(fn, dev, *args):
+    """Call a C entry point on dev's current stream, with dev current."""
+    import torch
+    stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    if dev.index == torch.cuda.current_device():
+        _check(fn, getattr(lib(), fn)(*args, stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, getattr(lib(), fn)(*args, stream))
+
+
+def _drop(p, state):
+    """The C descriptor of dropout with probability p, and state's (name,
+    tensor) pairs.  state is an int64 [2] tensor {seed, offset} on the GPU (the
+    64-bit words as they are); it may be None when p is 0."""
+    import torch
+    if state is not None:
+        _need(state, "state", (2,), torch.int64)
+    elif p != 0:
+        raise ValueError("state is required for p > 0")
+    return _Dropout(state.data_ptr() if state is not None else None, float(p)), [("state", state)]
+
+
+def _scratch(workspace, need, dev):
+    """The caller's workspace if it is large enough, else one of need bytes."""
+    import torch
+    if workspace is not None:
+        _need(workspace, "workspace", (workspace.numel(),), torch.uint8)
+    if workspace is None or workspace.numel() < need:
+        return _ws(need, dev)
+    return workspace
+
+
+def qlora_dropout(x, p: float, state, out=None):
+    """x with its elements dropped with probability p and the rest scaled by
+    1 / (1 - p) (to 16 bits of p): bf16, any shape, contiguous; the mask is a
+    function of state (int64 [2] on the GPU: seed, offset) and the element's
+    position.  The backward is the same call on the gradient; out may be x."""
+    import torch
+    _need(x, "x", tuple(x.shape), torch.bfloat16)
+    if out is not None:
+        _need(out, "out", tuple(x.shape), torch.bfloat16)
+    d, named = _drop(p, state)
+    _on_gpu([("x", x), ("out", out)] + named)
+    if out is None:
+        out = torch.empty_like(x)
+    _call("qlora_dropout_apply", x.device, _ptr(x), x.numel(), ctypes.byref(d), _ptr(out))
+    return out
+
+
+def qlora_linear_dropout_fwd(X, w, A=None, B=None, s: float = 1.0, p: float = 0.0, state=None,
+                             Y=None, T=None, workspace=None):
+    """The layer with dropout on its adapter's input: Y = X . deq(W)^T + s . T . B
+    with T = drop(X) . A.  w is an NF4Weight or a Q4Weight.  Returns (Y bf16
+    [M,N], T fp32 [M,r])."""
+    import torch
+    M = _x_rows(X, w.K)
+    w = _as_q4(w)
+    wt = _check_q4_weight(w)
+    r = _check_adapters(A, B, w)
+    d, named = _drop(p, state)
+    if Y is not None:
+        _need(Y, "Y", (M, w.N), torch.bfloat16)
+    if T is not None and r > 0:
+        _need(T, "T", (M, r), torch.float32)
+    _on_gpu([("X", X)] + wt + named + [("A", A), ("B", B), ("Y", Y), ("T", T if r > 0 else None),
+                                       ("workspace", workspace)])
+    dev = X.device
+    if Y is None:
+        Y = torch.empty((M, w.N), dtype=torch.bfloat16, device=dev)
+    if T is None and r > 0:
+        T = torch.empty((M, r), dtype=torch.float32, device=dev)
+    need = lib().qlora_linear_dropout_fwd_workspace_bytes(M, w.N, w.K, r)
+    workspace = _scratch(workspace, need, dev)
+    cw = w._c()
+    _call("qlora_linear_dropout_fwd", dev, _ptr(X), M, ctypes.byref(cw), _ptr(A), _ptr(B), r,
+          float(s), ctypes.byref(d), _ptr(Y), _ptr(T), _ptr(workspace), need)
+    return Y, T
+
+
+def qlora_linear_dropout_bwd(dY, X, w, A=None, B=None, s: float = 1.0, p: float = 0.0, state=None,
+                             T=None, need_dx: bool = True, dX=None, dA=None, dB=None,
+                             workspace=None):
+    """Backward of qlora_linear_dropout_fwd with the same p and state:
+    (dX bf16 [M,K] or None, dA bf16 [K,r], dB bf16 [r,N]); T None recomputes
+    it."""
+    import torch
+    M = _x_rows(X, w.K)
+    w = _as_q4(w)
+    wt = _check_q4_weight(w)
+    _need(dY, "dY", (M, w.N), torch.bfloat16)
+    r = _check_adapters(A, B, w)
+    d, named = _drop(p, state)
+    if T is not None and r > 0:
+        _need(T, "T", (M, r), torch.float32)
+    if need_dx and dX is not None:
+        _need(dX, "dX", (M, w.K), torch.bfloat16)
+    if r > 0 and dA is not None:
+        _need(dA, "dA", (w.K, r), torch.bfloat16)
+    if r > 0 and dB is not None:
+        _need(dB, "dB", (r, w.N), torch.bfloat16)
+    _on_gpu([("X", X), ("dY", dY)] + wt + named +
+            [("A", A), ("B", B), ("T", T if r > 0 else None), ("dX", dX if need_dx else None),
+             ("dA", dA if r > 0 else None), ("dB", dB if r > 0 else None),
+             ("workspace", workspace)])
+    dev = X.device
+    if need_dx and dX is None:
+        dX = torch.empty((M, w.K), dtype=torch.bfloat16, device=dev)
+    if r > 0 and dA is None:
+        dA = torch.empty((w.K, r), dtype=torch.bfloat16, device=dev)
+    if r > 0 and dB is None:
+        dB = torch.empty((r, w.N), dtype=torch.bfloat16, device=dev)
+    need = lib().qlora_linear_dropout_bwd_workspace_bytes(M, w.N, w.K, r)
+    workspace = _scratch(workspace, need, dev)
+    cw = w._c()
+    _call("qlora_linear_dropout_bwd", dev, _ptr(dY), _ptr(X), M, ctypes.byref(cw), _ptr(A),
+          _ptr(B), r, float(s), ctypes.byref(d), _ptr(T if r > 0 else None),
+          _ptr(dX if need_dx else None), _ptr(dA if r > 0 else None),
+          _ptr(dB if r > 0 else None), _ptr(workspace), need)
+    return (dX if need_dx else None), dA, dB
+
+
+def _grouped(X, offsets, w, E, A, B):
+    """Checks shared by the grouped calls: (M, N, r, w, named tensors)."""
+    import torch
+    M = _x_rows(X, w.K)
+    w = _as_q4(w)
+    named = [("X", X)] + _check_q4_weight(w)
+    if E < 1 or w.N % E:
+        raise ValueError(f"w.N = {w.N} is not a multiple of E = {E}")
+    N = w.N // E
+    _need(offsets, "offsets", (E + 1,), torch.int32)
+    if A is None or B is None:
+        if A is not None or B is not None:
+            raise ValueError("A and B go together (both None selects r = 0)")
+        r = 0
+    else:
+        if A.dim() != 3:
+            raise ValueError("A must be [E, K, r]")
+        r = A.shape[2]
+        _need(A, "A", (E, w.K, r), torch.bfloat16)
+        _need(B, "B", (E, r, N), torch.bfloat16)
+    return M, N, r, w, named + [("offsets", offsets), ("A", A), ("B", B)]
+
+
+def qlora_grouped_fwd(X, offsets, w, E: int, A=None, B=None, s: float = 1.0, p: float = 0.0,
+                      state=None, Y=None, T=None, workspace=None):
+    """The layer grouped by expert: rows offsets[e] .. offsets[e+1]-1 of X [M, K]
+    through expert e's rows of w [E*N, K] (NF4Weight or Q4Weight) and its
+    adapters A [E, K, r], B [E, r, N]; p and state as in
+    qlora_linear_dropout_fwd.  offsets is int32 [E+1] on the GPU.  Returns (Y
+    bf16 [M,N], T fp32 [M,r]); rows outside all groups are left as they were."""
+    import torch
+    M, N, r, w, named = _grouped(X, offsets, w, E, A, B)
+    d, dn = _drop(p, state)
+    if Y is not None:
+        _need(Y, "Y", (M, N), torch.bfloat16)
+    if T is not None and r > 0:
+        _need(T, "T", (M, r), torch.float32)
+    _on_gpu(named + dn + [("Y", Y), ("T", T if r > 0 else None), ("workspace", workspace)])
+    dev = X.device
+    if Y is None:
+        Y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    if T is None and r > 0:
+        T = torch.empty((M, r), dtype=torch.float32, device=dev)
+    need = lib().qlora_grouped_fwd_workspace_bytes(M, E, N, w.K, r)
+    workspace = _scratch(workspace, need, dev)
+    cw = w._c()
+    _call("qlora_grouped_fwd", dev, _ptr(X), M, _ptr(offsets), E, ctypes.byref(cw), _ptr(A),
+          _ptr(B), r, float(s), ctypes.byref(d), _ptr(Y), _ptr(T), _ptr(workspace), need)
+    return Y, T
+
+
+def qlora_grouped_bwd(dY, X, offsets, w, E: int, A=None, B=None, s: float = 1.0, p: float = 0.0,
+                      state=None, T=None, need_dx: bool = True, dX=None, dA=None, dB=None,
+                      workspace=None):
+    """Backward of qlora_grouped_fwd: (dX bf16 [M,K] or None, dA bf16 [E,K,r],
+    dB bf16 [E,r,N]); T None recomputes it.  dA and dB are zero for an expert
+    without rows."""
+    import torch
+    M, N, r, w, named = _grouped(X, offsets, w, E, A, B)
+    _need(dY, "dY", (M, N), torch.bfloat16)
+    d, dn = _drop(p, state)
+    if T is not None and r > 0:
+        _need(T, "T", (M, r), torch.float32)
+    if need_dx and dX is not None:
+        _need(dX, "dX", (M, w.K), torch.bfloat16)
+    if r > 0 and dA is not None:
+        _need(dA, "dA", (E, w.K, r), torch.bfloat16)
+    if r > 0 and dB is not None:
+        _need(dB, "dB", (E, r, N), torch.bfloat16)
+    _on_gpu(named + dn + [("dY", dY), ("T", T if r > 0 else None),
+                          ("dX", dX if need_dx else None), ("dA", dA if r > 0 else None),
+                          ("dB", dB if r > 0 else None), ("workspace", workspace)])
+    dev = X.device
+    if need_dx and dX is None:
+        dX = torch.empty((M, w.K), dtype=torch.bfloat16, device=dev)
+    if r > 0 and dA is None:
+        dA = torch.empty((E, w.K, r), dtype=torch.bfloat16, device=dev)
+    if r > 0 and dB is None:
+        dB = torch.empty((E, r, N), dtype=torch.bfloat16, device=dev)
+    need = lib().qlora_grouped_bwd_workspace_bytes(M, E, N, w.K, r)
+    workspace = _scratch(workspace, need, dev)
+    cw = w._c()
+    _call("qlora_grouped_bwd", dev, _ptr(dY), _ptr(X), M, _ptr(offsets), E, ctypes.byref(cw),
+          _ptr(A), _ptr(B), r, float(s), ctypes.byref(d), _ptr(T if r > 0 else None),
+          _ptr(dX if need_dx else None), _ptr(dA if r > 0 else None),
+          _ptr(dB if r > 0 else None), _ptr(workspace), need)
+    return (dX if need_dx else None), dA, dB
+
+
+def qlora_expert_plan(ids, E: int, workspace=None):
+    """Slots sorted by expert, stably, on the GPU.  ids int32 [tokens, topk] (or
+    any shape of n slots); an id outside 0 .. E-1 gets no row.  Returns int32
+    tensors (offsets [E+1], order [n]: row -> slot or -1, inverse, of ids'
+    shape: slot -> row or -1)."""
+    import torch
+    _need(ids, "ids", tuple(ids.shape), torch.int32)
+    _on_gpu([("ids", ids), ("workspace", workspace)])
+    dev, n = ids.device, ids.numel()
+    offsets = torch.empty(max(E, 0) + 1, dtype=torch.int32, device=dev)
+    order = torch.empty(n, dtype=torch.int32, device=dev)
+    inverse = torch.empty_like(ids)
+    need = lib().qlora_expert_plan_workspace_bytes(n, E)
+    workspace = _scratch(workspace, need, dev)
+    _call("qlora_expert_plan", dev, _ptr(ids), n, E, _ptr(offsets), _ptr(order), _ptr(inverse),
+          _ptr(workspace), need)
+    return offsets, order, inverse
+
+
+def _slots(inverse):
+    import torch
+    if inverse.dim() != 2:
+        raise ValueError("inverse must be [tokens, topk]")
+    _need(inverse, "inverse", tuple(inverse.shape), torch.int32)
+    return inverse.shape
+
+
+def qlora_expert_gather(X, inverse, out=None):
+    """Token rows in expert order: row inverse[t, j] of the result [tokens*topk, K]
+    is X[t].  Rows no slot has are left as they were (undefined in a result
+    allocated here)."""
+    import torch
+    tokens, topk = _slots(inverse)
+    if X.dim() != 2:
+        raise ValueError("X must be [tokens, K]")
+    K = X.shape[1]
+    _need(X, "X", (tokens, K), torch.bfloat16)
+    if out is not None:
+        _need(out, "out", (tokens * topk, K), torch.bfloat16)
+    _on_gpu([("X", X), ("inverse", inverse), ("out", out)])
+    if out is None:
+        out = torch.empty((tokens * topk, K), dtype=torch.bfloat16, device=X.device)
+    _call("qlora_expert_gather", X.device, _ptr(X), tokens, topk, K, _ptr(inverse), _ptr(out))
+    return out
+
+
+def qlora_expert_combine(Y, inverse, weights=None, out=None):
+    """Expert rows in token order: out[t] = sum_j weights[t, j] Y[inverse[t, j]]
+    (weights fp32 [tokens, topk], or None for 1, which is the backward of
+    qlora_expert_gather).  A slot without a row adds nothing."""
+    import torch
+    tokens, topk = _slots(inverse)
+    if Y.dim() != 2:
+        raise ValueError("Y must be [tokens*topk, K]")
+    K = Y.shape[1]
+    _need(Y, "Y", (tokens * topk, K), torch.bfloat16)
+    if weights is not None:
+        _need(weights, "weights", (tokens, topk), torch.float32)
+    if out is not None:
+        _need(out, "out", (tokens, K), torch.bfloat16)
+    _on_gpu([("Y", Y), ("inverse", inverse), ("weights", weights), ("out", out)])
+    if out is None:
+        out = torch.empty((tokens, K), dtype=torch.bfloat16, device=Y.device)
+    _call("qlora_expert_combine", Y.device, _ptr(Y), tokens, topk, K, _ptr(inverse),
+          _ptr(weights), _ptr(out))
+    return out
+
+
+def qlora_expert_combine_bwd(dOut, Y, inverse, weights, dY=None, dweights=None):
+    """Backward of qlora_expert_combine: (dY bf16 [tokens*topk, K] with rows
+    inverse[t, j] = weights[t, j] dOut[t], the others left as they were;
+    dweights fp32 [tokens, topk] = dOut[t] . Y[inverse[t, j]], 0 without a
+    row)."""
+    import torch
+    tokens, topk = _slots(inverse)
+    if Y.dim() != 2:
+        raise ValueError("Y must be [tokens*topk, K]")
+    K = Y.shape[1]
+    _need(Y, "Y", (tokens * topk, K), torch.bfloat16)
+    _need(dOut, "dOut", (tokens, K), torch.bfloat16)
+    _need(weights, "weights", (tokens, topk), torch.float32)
+    if dY is not None:
+        _need(dY, "dY", (tokens * topk, K), torch.bfloat16)
+    if dweights is not None:
+        _need(dweights, "dweights", (tokens, topk), torch.float32)
+    _on_gpu([("dOut", dOut), ("Y", Y), ("inverse", inverse), ("weights", weights), ("dY", dY),
+             ("dweights", dweights)])
+    if dY is None:
+        dY = torch.empty_like(Y)
+    if dweights is None:
+        dweights = torch.empty_like(weights)
+    _call("qlora_expert_combine_bwd", Y.device, _ptr(dOut), _ptr(Y), tokens, topk, K,
+          _ptr(inverse), _ptr(weights), _ptr(dY), _ptr(dweights))
+    return dY, dweights
 
 
 def _addr(x):

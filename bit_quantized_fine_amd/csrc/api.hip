@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "device_common.hpp"
+#include "group_tiles.hpp"
 #include "kernels.hpp"
 #include "qlora_nf4.h"
 
@@ -134,8 +135,8 @@ int hip_status(hipError_t e) { return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP
 
 // Forward workspace: the split-reduction partials of T, then (reusing the
 // same bytes once T is final) those of the GEMM when it splits its reduction.
-size_t fwd_ws_bytes(int64_t M, int64_t N, int64_t K, int r) {
-  size_t f = lora_down_ws_floats(M, K, r);
+size_t fwd_ws_bytes(int64_t M, int64_t N, int64_t K, int r, bool drop = false) {
+  size_t f = lora_down_ws_floats(M, K, r, drop);
   if (!decode_fits(M, K)) {
     const GemmSplit sp = fwd_gemm_split(M, N, K);
     if (sp.splits > 1) f = std::max<size_t>(f, (size_t)sp.splits * M * N);
@@ -145,9 +146,10 @@ size_t fwd_ws_bytes(int64_t M, int64_t N, int64_t K, int r) {
 
 // Backward workspace: G [M][r] and the recomputed T [M][r] (r > 0), then the
 // partials of the rank products, whose bytes the dX GEMM's partials reuse.
-size_t bwd_ws_bytes(int64_t M, int64_t N, int64_t K, int r) {
+size_t bwd_ws_bytes(int64_t M, int64_t N, int64_t K, int r, bool drop = false) {
   const size_t mr = r > 0 ? round_up((size_t)M * r * sizeof(float), 256) : 0;
   size_t f = r > 0 ? rank_ws_floats(M, N, K, r) : 0;
+  if (drop) f = std::max(f, lora_down_ws_floats(M, K, r, true));
   const GemmSplit sp = dx_gemm_split(M, N, K);
   if (sp.splits > 1) f = std::max<size_t>(f, (size_t)sp.splits * M * K);
   return 2 * mr + round_up(f * sizeof(float), 256);
@@ -228,10 +230,10 @@ int scratch_for_current_device(float** out) {
 // fwd_ws_bytes(M, N, K, r) bytes.
 int fwd_impl(const uint16_t* X, int64_t M, const Nf4View& v, const Nf4Tables& tb,
              const uint16_t* A, const uint16_t* B, int r, float s, uint16_t* Y, float* T,
-             float* ws, hipStream_t hs) {
+             float* ws, hipStream_t hs, const Drop& d = {}) {
   hipError_t e = hipSuccess;
   const bool decode = decode_fits(M, v.K);
-  if (decode && decode_folds_t(M, r)) {
+  if (decode && decode_folds_t(M, r) && !d.on()) {
     // T's partial sums are added up inside the decode kernel (no reduction
     // launch); its workgroup 0 writes T.
     int nz = 0;
@@ -239,7 +241,7 @@ int fwd_impl(const uint16_t* X, int64_t M, const Nf4View& v, const Nf4Tables& tb
     if (e == hipSuccess) e = launch_fwd_decode(X, M, v, ws, nz, T, B, r, s, Y, tb, hs);
     return hip_status(e);
   }
-  if (r > 0) e = launch_lora_down(X, M, v.K, A, r, T, ws, hs);
+  if (r > 0) e = launch_lora_down(X, M, v.K, A, r, T, ws, hs, d);
   if (e != hipSuccess) return QLORA_ERR_HIP;
   if (decode)
     e = launch_fwd_decode(X, M, v, T, 0, nullptr, B, r, s, Y, tb, hs);
@@ -252,7 +254,7 @@ int fwd_impl(const uint16_t* X, int64_t M, const Nf4View& v, const Nf4Tables& tb
 int bwd_impl(const uint16_t* dY, const uint16_t* X, int64_t M, const Nf4View& v,
              const Nf4Tables& tb, const uint16_t* A, const uint16_t* B, int r, float s, const float* T_saved,
              uint16_t* dX, uint16_t* dA, uint16_t* dB, void* workspace, size_t workspace_bytes,
-             hipStream_t hs) {
+             hipStream_t hs, const Drop& d = {}) {
   int st = check_rank(r);
   if (st) return st;
   if (!dY || !X) return QLORA_ERR_NULL;
@@ -262,7 +264,7 @@ int bwd_impl(const uint16_t* dY, const uint16_t* X, int64_t M, const Nf4View& v,
       (r > 0 && (!aligned16(A) || !aligned16(B) || !aligned16(dA) || !aligned16(dB) ||
                  (T_saved && !aligned16(T_saved)))))
     return QLORA_ERR_ALIGN;
-  const size_t need = bwd_ws_bytes(M, v.N, v.K, r);
+  const size_t need = bwd_ws_bytes(M, v.N, v.K, r, d.on());
   if (need > 0 && (!workspace || workspace_bytes < need)) return QLORA_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return QLORA_ERR_ALIGN;
 
@@ -276,14 +278,14 @@ int bwd_impl(const uint16_t* dY, const uint16_t* X, int64_t M, const Nf4View& v,
     float* Tr = reinterpret_cast<float*>(base + mr);
     const float* T = T_saved;
     if (!T) {
-      e = launch_lora_down(X, M, v.K, A, r, Tr, part, hs);
+      e = launch_lora_down(X, M, v.K, A, r, Tr, part, hs, d);
       T = Tr;
     }
     if (e == hipSuccess) e = launch_grad_in_and_b(dY, M, v.N, B, T, r, s, G, dB, part, hs);
-    if (e == hipSuccess) e = launch_grad_a(X, M, v.K, G, r, s, dA, part, hs);
+    if (e == hipSuccess) e = launch_grad_a(X, M, v.K, G, r, s, dA, part, hs, d);
     if (e != hipSuccess) return QLORA_ERR_HIP;
   }
-  if (dX) e = launch_dx_gemm(dY, M, v, G, A, r, s, dX, part, tb, hs);
+  if (dX) e = launch_dx_gemm(dY, M, v, G, A, r, s, dX, part, tb, hs, r > 0 ? d : Drop{});
   return hip_status(e);
 }
 
@@ -346,6 +348,57 @@ size_t block_bwd_ws_bytes(int64_t M, int S, int64_t nseg, int64_t K, int r) {
   const size_t mr = round_up((size_t)M * S * r * sizeof(float), 256);
   size_t f = std::max(rank_ws_floats(M, nseg, K, r), rank_ws_floats(M, S * nseg, K, S * r));
   const GemmSplit sp = dx_gemm_split(M, S * nseg, K);
+  if (sp.splits > 1) f = std::max<size_t>(f, (size_t)sp.splits * M * K);
+  return 2 * mr + round_up(f * sizeof(float), 256);
+}
+
+// ---------------------------------------------------------------------------
+// Dropout of the adapter's input, and layers grouped by expert.
+// ---------------------------------------------------------------------------
+
+// p -> the threshold on the generator's 16-bit values; a null descriptor or
+// p = 0 (to 16 bits) drops nothing.
+int check_dropout(const qlora_dropout* d, Drop* out) {
+  *out = Drop{};
+  if (!d) return QLORA_OK;
+  if (!(d->p >= 0.f && d->p < 1.f)) return QLORA_ERR_DROPOUT;   // NaN too
+  const double t = std::floor(static_cast<double>(d->p) * 65536.0 + 0.5);
+  out->thr = static_cast<uint32_t>(std::min(t, 65535.0));
+  if (!out->on()) return QLORA_OK;
+  if (!d->state) return QLORA_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(d->state) & 7u) return QLORA_ERR_ALIGN;
+  out->state = d->state;
+  return QLORA_OK;
+}
+
+constexpr int kMaxExperts = 1024;
+
+// Limits of the expert layout: each expert's rows start at a group of 256
+// block constants (so they are a weight of their own), and the grids fit.
+int check_experts(const qlora_q4_weight* w, int64_t M, int E) {
+  if (E < 1 || E > kMaxExperts || w->N % E != 0) return QLORA_ERR_EXPERT;
+  const int64_t N = w->N / E;
+  if (N % 8 != 0) return QLORA_ERR_SHAPE;
+  if (w->double_quant && (N * w->K / kBlock) % kGroup != 0) return QLORA_ERR_EXPERT;
+  if (M < 0 || M > INT32_MAX) return QLORA_ERR_SHAPE;
+  const int64_t wide = (std::max(N, w->K) + 127) / 128;
+  if (group_tile_bound(M, E, 64) > (int64_t(1) << 30) / wide) return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+
+size_t grouped_fwd_ws_bytes(int64_t M, int E, int64_t N, int64_t K, int r) {
+  if (M == 0) return 0;
+  size_t f = grouped_down_ws_floats(M, E, K, r);
+  const GemmSplit sp = grouped_fwd_split(M, E, N, K);
+  if (sp.splits > 1) f = std::max<size_t>(f, (size_t)sp.splits * M * N);
+  return round_up(f * sizeof(float), 256);
+}
+
+size_t grouped_bwd_ws_bytes(int64_t M, int E, int64_t N, int64_t K, int r) {
+  if (M == 0) return 0;
+  const size_t mr = r > 0 ? round_up((size_t)M * r * sizeof(float), 256) : 0;
+  size_t f = grouped_rank_ws_floats(M, E, N, K, r);
+  const GemmSplit sp = grouped_dx_split(M, E, N, K);
   if (sp.splits > 1) f = std::max<size_t>(f, (size_t)sp.splits * M * K);
   return 2 * mr + round_up(f * sizeof(float), 256);
 }
@@ -444,6 +497,10 @@ const char* qlora_status_string(int status) {
              "(QLORA_NOALLOC_SCRATCH_BYTES)";
     case QLORA_ERR_FORMAT:
       return "unknown codebook or constant format (codebook 0..2, double_quant 0 or 1)";
+    case QLORA_ERR_EXPERT:
+      return "invalid expert layout (need 1<=E<=1024 dividing the weight's rows, whole groups of "
+             "256 block constants per expert with double quantization, 1<=topk<=64)";
+    case QLORA_ERR_DROPOUT: return "dropout probability outside [0, 1)";
     default: return "unknown status";
   }
 }
@@ -752,6 +809,145 @@ int qlora_block_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const qlor
   // dX = sum_j dY_j . deq(W_j) + s . G_j . A_j^T: one GEMM over all S nseg rows
   if (e == hipSuccess && dX)
     e = launch_dx_gemm(dY, M, view(w), G, A, rt, s, dX, part, tables(), hs);
+  return hip_status(e);
+}
+
+int qlora_dropout_apply(const uint16_t* x, int64_t n, const qlora_dropout* d, uint16_t* y,
+                        qlora_stream_t stream) {
+  Drop dr;
+  int st = d ? check_dropout(d, &dr) : QLORA_ERR_NULL;
+  if (st) return st;
+  if (n < 0) return QLORA_ERR_SHAPE;
+  if (n == 0) return QLORA_OK;
+  if (!x || !y) return QLORA_ERR_NULL;
+  if (!aligned16(x) || !aligned16(y)) return QLORA_ERR_ALIGN;
+  return hip_status(launch_dropout(x, n, dr, y, static_cast<hipStream_t>(stream)));
+}
+
+size_t qlora_linear_dropout_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int r) {
+  if (M < 1 || N < 1 || K < 1 || r < 0) return 0;
+  return std::max(fwd_ws_bytes(M, N, K, r), fwd_ws_bytes(M, N, K, r, true));
+}
+
+size_t qlora_linear_dropout_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int r) {
+  if (M < 1 || N < 1 || K < 1 || r < 0) return 0;
+  return bwd_ws_bytes(M, N, K, r, true);
+}
+
+int qlora_linear_dropout_fwd(const uint16_t* X, int64_t M, const qlora_q4_weight* w,
+                             const uint16_t* A, const uint16_t* B, int r, float s,
+                             const qlora_dropout* d, uint16_t* Y, float* T, void* workspace,
+                             size_t workspace_bytes, qlora_stream_t stream) {
+  int st = check_q4_weight(w);
+  if (st) return st;
+  if ((st = check_fwd_rest(X, M, w->N, A, B, r, Y, T))) return st;
+  Drop dr;
+  if ((st = check_dropout(d, &dr))) return st;
+  const size_t need = qlora_linear_dropout_fwd_workspace_bytes(M, w->N, w->K, r);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return QLORA_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return QLORA_ERR_ALIGN;
+  return fwd_impl(X, M, q4_view(w), tables(w->codebook), A, B, r, s, Y, T,
+                  static_cast<float*>(workspace), static_cast<hipStream_t>(stream), dr);
+}
+
+int qlora_linear_dropout_bwd(const uint16_t* dY, const uint16_t* X, int64_t M,
+                             const qlora_q4_weight* w, const uint16_t* A, const uint16_t* B,
+                             int r, float s, const qlora_dropout* d, const float* T_saved,
+                             uint16_t* dX, uint16_t* dA, uint16_t* dB, void* workspace,
+                             size_t workspace_bytes, qlora_stream_t stream) {
+  int st = check_q4_weight(w);
+  if (st) return st;
+  Drop dr;
+  if ((st = check_dropout(d, &dr))) return st;
+  return bwd_impl(dY, X, M, q4_view(w), tables(w->codebook), A, B, r, s, T_saved, dX, dA, dB,
+                  workspace, workspace_bytes, static_cast<hipStream_t>(stream), dr);
+}
+
+size_t qlora_grouped_fwd_workspace_bytes(int64_t M, int E, int64_t N, int64_t K, int r) {
+  if (M < 0 || E < 1 || E > kMaxExperts || N < 1 || K < 1 || r < 0) return 0;
+  return grouped_fwd_ws_bytes(M, E, N, K, r);
+}
+
+size_t qlora_grouped_bwd_workspace_bytes(int64_t M, int E, int64_t N, int64_t K, int r) {
+  if (M < 0 || E < 1 || E > kMaxExperts || N < 1 || K < 1 || r < 0) return 0;
+  return grouped_bwd_ws_bytes(M, E, N, K, r);
+}
+
+int qlora_grouped_fwd(const uint16_t* X, int64_t M, const int32_t* offsets, int E,
+                      const qlora_q4_weight* w, const uint16_t* A, const uint16_t* B, int r,
+                      float s, const qlora_dropout* d, uint16_t* Y, float* T, void* workspace,
+                      size_t workspace_bytes, qlora_stream_t stream) {
+  int st = check_q4_weight(w);
+  if (st) return st;
+  if ((st = check_rank(r))) return st;
+  if ((st = check_experts(w, M, E))) return st;
+  Drop dr;
+  if ((st = check_dropout(d, &dr))) return st;
+  if (!offsets || (r > 0 && (!A || !B))) return QLORA_ERR_NULL;
+  if (M == 0) return QLORA_OK;
+  if (!X || !Y || (r > 0 && !T)) return QLORA_ERR_NULL;
+  if (!aligned16(X) || !aligned16(Y) || (reinterpret_cast<uintptr_t>(offsets) & 3u) ||
+      (r > 0 && (!aligned16(A) || !aligned16(B) || !aligned16(T))))
+    return QLORA_ERR_ALIGN;
+  const int64_t N = w->N / E;
+  const size_t need = grouped_fwd_ws_bytes(M, E, N, w->K, r);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return QLORA_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return QLORA_ERR_ALIGN;
+
+  const hipStream_t hs = static_cast<hipStream_t>(stream);
+  float* ws = static_cast<float*>(workspace);
+  hipError_t e = hipSuccess;
+  if (r > 0) e = launch_grouped_down(X, M, offsets, E, w->K, A, r, T, ws, hs, dr);
+  if (e == hipSuccess)
+    e = launch_grouped_fwd_gemm(X, M, offsets, E, q4_view(w), T, B, r, s, Y, ws,
+                                tables(w->codebook), hs);
+  return hip_status(e);
+}
+
+int qlora_grouped_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const int32_t* offsets,
+                      int E, const qlora_q4_weight* w, const uint16_t* A, const uint16_t* B,
+                      int r, float s, const qlora_dropout* d, const float* T_saved, uint16_t* dX,
+                      uint16_t* dA, uint16_t* dB, void* workspace, size_t workspace_bytes,
+                      qlora_stream_t stream) {
+  int st = check_q4_weight(w);
+  if (st) return st;
+  if ((st = check_rank(r))) return st;
+  if ((st = check_experts(w, M, E))) return st;
+  Drop dr;
+  if ((st = check_dropout(d, &dr))) return st;
+  if (!offsets || (r > 0 && (!A || !B || !dA || !dB))) return QLORA_ERR_NULL;
+  if (M > 0 && (!dY || !X)) return QLORA_ERR_NULL;
+  if (!aligned16(dY) || !aligned16(X) || !aligned16(dX) ||
+      (reinterpret_cast<uintptr_t>(offsets) & 3u) ||
+      (r > 0 && (!aligned16(A) || !aligned16(B) || !aligned16(dA) || !aligned16(dB) ||
+                 !aligned16(T_saved))))
+    return QLORA_ERR_ALIGN;
+  const int64_t N = w->N / E;
+  const size_t need = grouped_bwd_ws_bytes(M, E, N, w->K, r);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return QLORA_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return QLORA_ERR_ALIGN;
+
+  const hipStream_t hs = static_cast<hipStream_t>(stream);
+  char* base = static_cast<char*>(workspace);
+  const size_t mr = r > 0 ? round_up((size_t)M * r * sizeof(float), 256) : 0;
+  float* G = reinterpret_cast<float*>(base);
+  float* Tr = base ? reinterpret_cast<float*>(base + mr) : nullptr;
+  float* part = base ? reinterpret_cast<float*>(base + 2 * mr) : nullptr;
+  hipError_t e = hipSuccess;
+  if (r > 0) {
+    const float* T = T_saved;
+    if (!T && M > 0) {
+      e = launch_grouped_down(X, M, offsets, E, w->K, A, r, Tr, part, hs, dr);
+      T = Tr;
+    }
+    if (e == hipSuccess)
+      e = launch_grouped_grad_in_and_b(dY, M, offsets, E, N, B, T, r, s, G, dB, part, hs);
+    if (e == hipSuccess)
+      e = launch_grouped_grad_a(X, M, offsets, E, w->K, G, r, s, dA, part, hs, dr);
+  }
+  if (e == hipSuccess && dX && M > 0)
+    e = launch_grouped_dx_gemm(dY, M, offsets, E, q4_view(w), G, A, r, s, dX, part,
+                               tables(w->codebook), hs, r > 0 ? dr : Drop{});
   return hip_status(e);
 }
 

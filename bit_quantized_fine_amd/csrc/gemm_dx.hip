@@ -29,9 +29,24 @@
 // LoRA baseline): each thread loads its 16 weights of row t/8 (32 bytes) and
 // stores them where the dequantized values would go.  kFormNoDq reads one
 // fp32 constant per block (codes without double quantization).
+//
+// kExperts instantiates it over token rows grouped by expert (see the forward
+// GEMM): the reduction runs over the rows of the tile's expert.  With kQ = 64
+// a tile is 64 tokens and the four wave columns split the 128 output columns.
+//
+// kDrop is the backward of the layer whose adapter input was dropped out:
+// dX = dY . deq(W) + s . mask . (G . A^T), s holding the mask's scale.  The
+// adapter's term then needs sums of its own, masked before they are added:
+// each wave forms them after the exchange, for the subtiles it stores, over
+// all ranks.  The mask is regenerated there.  A piece of the generator covers
+// eight columns of a token, two lanes' outputs, so the lane pair computes one
+// piece each for two subtiles and hands over the half the other needs: 32
+// outputs a lane take 8 generator calls instead of 16.
 #include <type_traits>
 
 #include "device_common.hpp"
+#include "dropout.hpp"
+#include "group_tiles.hpp"
 #include "kernels.hpp"
 
 namespace qnf4 {
@@ -39,20 +54,26 @@ namespace qnf4 {
 namespace {
 
 constexpr int XP = 128;          // output columns k per workgroup
-constexpr int XQ = 256;          // tokens per workgroup
 constexpr int XN = 64;           // weight rows n per chunk
-constexpr int XWT = 4;           // token groups
+constexpr int XWC = 4;           // wave columns: kQ / 64 token groups x column groups
 constexpr int XKS = 2;           // waves splitting a chunk's two 32-n steps
-constexpr int XW = XWT * XKS;    // waves
+constexpr int XW = XWC * XKS;    // waves
 constexpr int XT = 64 * XW;      // threads
 constexpr int XAS = XP;          // LDS row stride of the weight tile (256 B, swizzled)
 constexpr int XYS = XN;          // LDS row stride of the dY tile (128 B, swizzled)
-constexpr int XTA = XP / 16;     // 16-column subtiles (8)
-constexpr int XTB = XQ / XWT / 16;   // 16-token subtiles per wave (4)
+constexpr int XTB = 4;           // 16-token subtiles per wave
 constexpr int kXA = XN * XAS;    // elements of one weight tile buffer
-constexpr int kXY = XQ * XYS;    // elements of one dY tile buffer
-constexpr int kDxLds = kRepTabBytes + 2 * kXA * 2 + 2 * kXY * 2;
-constexpr int XYPT = XQ * XN / 8 / XT;   // 16-byte dY pieces a thread stages per chunk (4)
+
+// A tile of kQ tokens (256 or 64).
+template <int kQ>
+struct DxTile {
+  static constexpr int WT = kQ / 64;              // token groups
+  static constexpr int WR = XWC / WT;             // column groups
+  static constexpr int TA = XP / 16 / WR;         // 16-column subtiles per wave (8 or 2)
+  static constexpr int YTILE = kQ * XYS;          // elements of one dY tile buffer
+  static constexpr int YPT = kQ * XN / 8 / XT;    // 16-byte dY pieces a thread stages per chunk
+  static constexpr int LDS = kRepTabBytes + 2 * kXA * 2 + 2 * YTILE * 2;
+};
 
 __device__ __forceinline__ int xcd_remap_dx(int b, int total) {
   const int n8 = total >> 3, rem = total & 7;
@@ -70,14 +91,17 @@ typedef __attribute__((address_space(3))) v4i16 LdsV4i16;
 
 }  // namespace
 
-template <int kForm>
+template <int kForm, int kQ, bool kExperts, bool kDrop>
 __global__ __launch_bounds__(XT) void k_dx_gemm(
     const uint16_t* __restrict__ dY, int64_t M, const uint16_t* __restrict__ Wd,
     const uint8_t* __restrict__ codes,
     const uint8_t* __restrict__ absmax_q, const float* __restrict__ absmax_scale,
     int64_t N, int64_t K, const float* __restrict__ G, const uint16_t* __restrict__ Al,
     int r, float s, uint16_t* __restrict__ dX, int ptiles, int qtiles, int cps,
-    float* __restrict__ part, Nf4Tables tb) {
+    float* __restrict__ part, Nf4Tables tb, const int* __restrict__ offsets, int E,
+    const uint64_t* __restrict__ state, uint32_t thr) {
+  using Tile = DxTile<kQ>;
+  constexpr int XQ = kQ, XTA = Tile::TA, kXY = Tile::YTILE, XYPT = Tile::YPT;
   // Dynamic LDS only (the level table sits at address 0): the replicated
   // table, two weight tiles, two dY tiles; the table's bytes hold the
   // accumulator exchange after the main loop.
@@ -89,24 +113,43 @@ __global__ __launch_bounds__(XT) void k_dx_gemm(
   const int tid = threadIdx.x;
   const int wave = wave_id(), lane = tid & 63;
   const int li = lane & 15, g = lane >> 4;
-  const int wt = wave % XWT, ks = wave / XWT;
+  const int wc = wave % XWC, ks = wave / XWC;
+  const int wt = wc % Tile::WT, wr = wc / Tile::WT;
   if constexpr (kForm != kFormDense) build_rep_pair_table<XT>(tab, load_levels(tb), tid);
 
   // With a split reduction (few tiles), workgroup b takes row chunks
   // [z cps, (z + 1) cps) of its tile and writes fp32 partial sums.
-  const int ntiles = ptiles * qtiles;
-  const int lin = xcd_remap_dx(blockIdx.x, static_cast<int>(gridDim.x));
+  int ntiles = ptiles * qtiles, work = static_cast<int>(gridDim.x);
+  if constexpr (kExperts) {   // only the tiles that the groups have
+    const int splits = work / ntiles;
+    ntiles = ptiles * min(qtiles, group_tile_count(offsets, E, M, XQ));
+    work = min(work, ntiles * splits);
+    if (static_cast<int>(blockIdx.x) >= work) return;
+  }
+  const int lin = xcd_remap_dx(blockIdx.x, work);
   const int z = lin / ntiles, tile = lin - z * ntiles;
   const int qt = tile / ptiles, pt = tile - qt * ptiles;
-  const int64_t k0 = (int64_t)pt * XP, q0 = (int64_t)qt * XQ;
+  const int64_t k0 = (int64_t)pt * XP;
+  int64_t q0 = (int64_t)qt * XQ, mend = M;   // the tile's tokens: q0 .. mend - 1 at most
+  int64_t n0 = 0;                            // first row of W of the tile's expert
+  if constexpr (kExperts) {
+    const GroupTile gt = group_tile(offsets, E, M, XQ, qt);
+    if (gt.e < 0) return;
+    q0 = gt.row0;
+    mend = gt.end;
+    n0 = (int64_t)gt.e * N;
+    Al += (int64_t)gt.e * K * r;
+  }
+  const int64_t NW = kExperts ? N * E : N;     // rows of W
   const int c0 = z * cps;
   // end of this split's row chunks
   const int nchunks = min(static_cast<int>((N + XN - 1) / XN), c0 + cps);
   const int KB = static_cast<int>(K / kBlock);
 
-  // Buffer descriptors: rows n >= N and tokens m >= M read as zero.
-  const uint32_t nb = static_cast<uint32_t>(N * K / kBlock);
-  const BufRes rc = make_bufres(codes, static_cast<uint32_t>(N * K / 2));
+  // Buffer descriptors: rows past W and tokens past the tile read as zero (a
+  // row n >= N of an expert is the next one's; its dY columns read as zero).
+  const uint32_t nb = static_cast<uint32_t>(NW * K / kBlock);
+  const BufRes rc = make_bufres(codes, static_cast<uint32_t>(NW * K / 2));
   const BufRes re = make_bufres(absmax_q, nb);
   // second-level scales, or one fp32 constant per block (kFormNoDq)
   const BufRes rd = make_bufres(
@@ -117,15 +160,15 @@ __global__ __launch_bounds__(XT) void k_dx_gemm(
   // than 2^31 bytes for N <= 2^22).  (A plain conditional, not min(): the
   // 64-bit min is opaque to the compiler's uniformity analysis and would put
   // the descriptor in vector registers.)
-  const int64_t tile_rows = M - q0 < XQ ? M - q0 : XQ;
+  const int64_t tile_rows = mend - q0 < XQ ? mend - q0 : XQ;
   const BufRes ry = make_bufres(dY + q0 * N, static_cast<uint32_t>(tile_rows * N * 2));
 
   // Dequantization role: row dr of the chunk, columns k0 + 16 dp .. +15.
   // Columns past K (a half tile when K % 128 == 64) get a zero constant.
   const int dr = tid >> 3, dp = tid & 7;
   const bool dkok = k0 + 16 * dp < K;
-  const uint32_t dcode = static_cast<uint32_t>(dr * (K / 2) + k0 / 2 + 8 * dp);   // + c 64 K/2
-  const uint32_t dblk = static_cast<uint32_t>(dr * KB + (k0 + 16 * dp) / kBlock);   // + c 64 KB
+  const uint32_t dcode = static_cast<uint32_t>((n0 + dr) * (K / 2) + k0 / 2 + 8 * dp);   // + c 64 K/2
+  const uint32_t dblk = static_cast<uint32_t>((n0 + dr) * KB + (k0 + 16 * dp) / kBlock);   // + c 64 KB
   // kFormDense: the same 16 weights as bf16, byte offset (+ c 64 K 2)
   const uint32_t dw = static_cast<uint32_t>((dr * K + k0 + 16 * dp) * 2);
   u32x2 cw[2];
@@ -236,7 +279,7 @@ __global__ __launch_bounds__(XT) void k_dx_gemm(
       v4i16 h[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint16_t* src = wt0 + rbase[e] + 16 * (a ^ sw[e]);
+        const uint16_t* src = wt0 + rbase[e] + 16 * ((wr * XTA + a) ^ sw[e]);
         h[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV4i16*)(src));
       }
       const u32x2 h0 = __builtin_bit_cast(u32x2, h[0]), h1 = __builtin_bit_cast(u32x2, h[1]);
@@ -283,115 +326,209 @@ __global__ __launch_bounds__(XT) void k_dx_gemm(
     iter(c + 1, std::integral_constant<int, 1>{});
   }
 
-  // LoRA term (the first split only): extra steps over the rank, 32 at a
-  // time, alternating between the two halves before their accumulators are
-  // added.
-  for (int j0 = 32 * ks; z == 0 && j0 < r; j0 += 64) {
-    const int j = j0 + 8 * g;
-    u32x4 gh[XTB], gl[XTB];
-#pragma unroll
-    for (int b = 0; b < XTB; ++b) {
-      const int64_t m = q0 + 64 * wt + 16 * b + li;
-      uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-      if (m < M && j < r) {
-        const f32x4 t0 = *reinterpret_cast<const f32x4*>(G + m * r + j);
-        const f32x4 t1 = *reinterpret_cast<const f32x4*>(G + m * r + j + 4);
-        const float v[8] = {t0.x * s, t0.y * s, t0.z * s, t0.w * s,
-                            t1.x * s, t1.y * s, t1.z * s, t1.w * s};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) split_bf16x2(v[2 * e], v[2 * e + 1], hi[e], lo[e]);
-      }
-      gh[b] = u32x4{hi[0], hi[1], hi[2], hi[3]};
-      gl[b] = u32x4{lo[0], lo[1], lo[2], lo[3]};
-    }
-#pragma unroll
-    for (int a = 0; a < XTA; ++a) {
-      const int64_t k = k0 + 16 * a + li;
-      const u32x4 af = (k < K && j < r) ? *reinterpret_cast<const u32x4*>(Al + k * r + j)
-                                        : u32x4{0, 0, 0, 0};
+  // LoRA term of column subtiles A0 .. A0 + TN - 1 (the first split only):
+  // extra steps over the rank, ranks j0, j0 + step, ... 32 at a time.
+  auto lora = [&](auto a0c, auto tnc, f32x4 (*dst)[XTB], int j0, int step) {
+    constexpr int A0 = decltype(a0c)::value, TN = decltype(tnc)::value;
+    for (; z == 0 && j0 < r; j0 += step) {
+      const int j = j0 + 8 * g;
+      u32x4 gh[XTB], gl[XTB];
 #pragma unroll
       for (int b = 0; b < XTB; ++b) {
-        acc[a][b] = mfma16(af, gh[b], acc[a][b]);
-        acc[a][b] = mfma16(af, gl[b], acc[a][b]);
+        const int64_t m = q0 + 64 * wt + 16 * b + li;
+        uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+        if (m < mend && j < r) {
+          const f32x4 t0 = *reinterpret_cast<const f32x4*>(G + m * r + j);
+          const f32x4 t1 = *reinterpret_cast<const f32x4*>(G + m * r + j + 4);
+          const float v[8] = {t0.x * s, t0.y * s, t0.z * s, t0.w * s,
+                              t1.x * s, t1.y * s, t1.z * s, t1.w * s};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split_bf16x2(v[2 * e], v[2 * e + 1], hi[e], lo[e]);
+        }
+        gh[b] = u32x4{hi[0], hi[1], hi[2], hi[3]};
+        gl[b] = u32x4{lo[0], lo[1], lo[2], lo[3]};
       }
-    }
-  }
-
-  // Add the second n half into the first through LDS, half of the column
-  // subtiles at a time.
-  f32x4* xch = reinterpret_cast<f32x4*>(dyn);   // [XWT][XTA/2][XTB][64]
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (ks == 1) {
+      for (int a = 0; a < TN; ++a) {
+        const int64_t k = k0 + 16 * (wr * XTA + A0 + a) + li;
+        const u32x4 af = (k < K && j < r) ? *reinterpret_cast<const u32x4*>(Al + k * r + j)
+                                          : u32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int a = 0; a < XTA / 2; ++a)
-#pragma unroll
-        for (int b = 0; b < XTB; ++b)
-          xch[((wt * (XTA / 2) + a) * XTB + b) * 64 + lane] = acc[h * (XTA / 2) + a][b];
-    }
-    __syncthreads();
-    if (ks == 0) {
-#pragma unroll
-      for (int a = 0; a < XTA / 2; ++a)
-#pragma unroll
-        for (int b = 0; b < XTB; ++b)
-          acc[h * (XTA / 2) + a][b] += xch[((wt * (XTA / 2) + a) * XTB + b) * 64 + lane];
-    }
-    __syncthreads();
-  }
-  if (ks != 0) return;
-
-  // dX[m, k..k+3] for the lane's 4 consecutive columns k of each subtile
-  // (bf16), or this split's fp32 partial sums part[z][m][k..k+3]
-#pragma unroll
-  for (int a = 0; a < XTA; ++a) {
-    const int64_t k = k0 + 16 * a + 4 * g;
-#pragma unroll
-    for (int b = 0; b < XTB; ++b) {
-      const int64_t m = q0 + 64 * wt + 16 * b + li;
-      if (m < M && k < K) {
-        const f32x4 v = acc[a][b];
-        if (part) {
-          *reinterpret_cast<f32x4*>(part + ((int64_t)z * M + m) * K + k) = v;
-        } else {
-          *reinterpret_cast<u32x2*>(dX + m * K + k) =
-              u32x2{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+        for (int b = 0; b < XTB; ++b) {
+          dst[a][b] = mfma16(af, gh[b], dst[a][b]);
+          dst[a][b] = mfma16(af, gl[b], dst[a][b]);
         }
       }
     }
-  }
+  };
+  // Without dropout the two halves take the rank steps in turn, before their
+  // accumulators are added.
+  if constexpr (!kDrop)
+    lora(std::integral_constant<int, 0>{}, std::integral_constant<int, XTA>{}, acc, 32 * ks, 64);
+
+  // Add the two n halves: wave ks keeps half of its column subtiles and
+  // receives them from its partner (the other ks, same wave column) through
+  // LDS, in one round; each half then stores its own column subtiles.
+  constexpr int TH = XTA / 2;
+  f32x4* xch = reinterpret_cast<f32x4*>(dyn);   // [2][XWC][TH][XTB][64]
+  auto hand = [&](auto kc) {
+    constexpr int GIVE = 1 - decltype(kc)::value;
+#pragma unroll
+    for (int a = 0; a < TH; ++a)
+#pragma unroll
+      for (int b = 0; b < XTB; ++b)
+        xch[(((GIVE * XWC + wc) * TH + a) * XTB + b) * 64 + lane] = acc[GIVE * TH + a][b];
+  };
+  // dX[m, k..k+3] for the lane's 4 consecutive columns k of each subtile
+  // (bf16), or this split's fp32 partial sums part[z][m][k..k+3]
+  auto finish = [&](auto kc) {
+    constexpr int K0 = decltype(kc)::value;
+#pragma unroll
+    for (int a = 0; a < TH; ++a)
+#pragma unroll
+      for (int b = 0; b < XTB; ++b)
+        acc[K0 * TH + a][b] += xch[(((K0 * XWC + wc) * TH + a) * XTB + b) * 64 + lane];
+    if constexpr (kDrop) {
+      if (z == 0 && r > 0) {
+        f32x4 low[TH][XTB];
+#pragma unroll
+        for (int a = 0; a < TH; ++a)
+#pragma unroll
+          for (int b = 0; b < XTB; ++b) low[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+        lora(std::integral_constant<int, K0 * TH>{}, std::integral_constant<int, TH>{}, low, 0,
+             32);
+        const DropKey key = load_drop_key(state, thr);
+#pragma unroll
+        for (int b = 0; b < XTB; ++b) {
+          const int64_t m = q0 + 64 * wt + 16 * b + li;
+          // first of the two pieces of a subtile's 16 columns
+          const uint64_t p0 =
+              static_cast<uint64_t>(m * K + k0 + 16 * (wr * XTA + K0 * TH)) / 8 + (g >> 1);
+          auto add = [&](int a, uint32_t w0, uint32_t w1) {
+            f32x4 v = low[a][b];
+            v.x = (w0 & 0xFFFFu) >= thr ? v.x : 0.f;
+            v.y = (w0 >> 16) >= thr ? v.y : 0.f;
+            v.z = (w1 & 0xFFFFu) >= thr ? v.z : 0.f;
+            v.w = (w1 >> 16) >= thr ? v.w : 0.f;
+            acc[K0 * TH + a][b] += v;
+          };
+          if constexpr (TH == 1) {
+            const u32x4 w = philox_piece(key, p0);
+            add(0, (g & 1) ? w.z : w.x, (g & 1) ? w.w : w.y);
+          } else {
+#pragma unroll
+            for (int a = 0; a < TH; a += 2) {
+              // lanes of even g (columns 0-3 of a piece) compute the piece of
+              // subtile a, lanes of odd g (columns 4-7) that of subtile a + 1
+              const bool odd = g & 1;
+              const u32x4 w = philox_piece(key, p0 + 2 * (a + (odd ? 1 : 0)));
+              const uint32_t g0 = __shfl_xor(odd ? w.x : w.z, 16);
+              const uint32_t g1 = __shfl_xor(odd ? w.y : w.w, 16);
+              add(a, odd ? g0 : w.x, odd ? g1 : w.y);
+              add(a + 1, odd ? w.z : g0, odd ? w.w : g1);
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < TH; ++a) {
+      const int64_t k = k0 + 16 * (wr * XTA + K0 * TH + a) + 4 * g;
+#pragma unroll
+      for (int b = 0; b < XTB; ++b) {
+        const int64_t m = q0 + 64 * wt + 16 * b + li;
+        if (m < mend && k < K) {
+          const f32x4 v = acc[K0 * TH + a][b];
+          if (part) {
+            *reinterpret_cast<f32x4*>(part + ((int64_t)z * M + m) * K + k) = v;
+          } else {
+            *reinterpret_cast<u32x2*>(dX + m * K + k) =
+                u32x2{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+          }
+        }
+      }
+    }
+  };
+  if (ks == 0) hand(std::integral_constant<int, 0>{}); else hand(std::integral_constant<int, 1>{});
+  __syncthreads();
+  if (ks == 0) finish(std::integral_constant<int, 0>{}); else finish(std::integral_constant<int, 1>{});
 }
 
+namespace {
+
+constexpr int kPlainQ = 256;   // tokens a tile without groups
+
+template <int kForm, int kQ, bool kExperts, bool kDrop>
+hipError_t launch_dx_tiles(const uint16_t* dY, int64_t M, const Nf4View& w, int64_t N,
+                           const float* G, const uint16_t* A, int r, float s, uint16_t* dX,
+                           float* part, const Nf4Tables& tb, hipStream_t stream, int qtiles,
+                           const GemmSplit& sp, const int* offsets, int E, const Drop& d) {
+  constexpr int kLds = DxTile<kQ>::LDS;
+  static const hipError_t attr =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(&k_dx_gemm<kForm, kQ, kExperts, kDrop>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if (attr != hipSuccess) return attr;
+  if (sp.splits > 1 && !part) return hipErrorInvalidValue;
+  const int ptiles = static_cast<int>((w.K + XP - 1) / XP);
+  hipLaunchKernelGGL((k_dx_gemm<kForm, kQ, kExperts, kDrop>), dim3(ptiles * qtiles * sp.splits),
+                     dim3(XT), kLds, stream, dY, M, w.dense, w.codes, w.absmax_q, w.absmax_scale,
+                     N, w.K, G, A, r, kDrop ? s * d.scale() : s, dX, ptiles, qtiles, sp.cps,
+                     sp.splits > 1 ? part : nullptr, tb, offsets, E, d.state, d.thr);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 GemmSplit dx_gemm_split(int64_t M, int64_t N, int64_t K) {
-  return gemm_split((K + XP - 1) / XP * ((M + XQ - 1) / XQ), (N + XN - 1) / XN);
+  return gemm_split((K + XP - 1) / XP * ((M + kPlainQ - 1) / kPlainQ), (N + XN - 1) / XN);
 }
 
 hipError_t launch_dx_gemm(const uint16_t* dY, int64_t M, const Nf4View& w,
                           const float* G, const uint16_t* A, int r, float s,
-                          uint16_t* dX, float* part, const Nf4Tables& tb, hipStream_t stream) {
-  static const hipError_t attr[3] = {
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&k_dx_gemm<kFormDq>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kDxLds),
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&k_dx_gemm<kFormNoDq>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kDxLds),
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&k_dx_gemm<kFormDense>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kDxLds)};
-  const int form = w.dense ? kFormDense : (w.dq ? kFormDq : kFormNoDq);
-  if (attr[form] != hipSuccess) return attr[form];
-  decltype(&k_dx_gemm<kFormDq>) kern =
-      form == kFormDense ? k_dx_gemm<kFormDense> : (form == kFormNoDq ? k_dx_gemm<kFormNoDq> : k_dx_gemm<kFormDq>);
-  const int ptiles = static_cast<int>((w.K + XP - 1) / XP);
-  const int qtiles = static_cast<int>((M + XQ - 1) / XQ);
+                          uint16_t* dX, float* part, const Nf4Tables& tb, hipStream_t stream,
+                          const Drop& d) {
+  const int qtiles = static_cast<int>((M + kPlainQ - 1) / kPlainQ);
   const GemmSplit sp = dx_gemm_split(M, w.N, w.K);
-  if (sp.splits > 1 && !part) return hipErrorInvalidValue;
+  if (w.dense && d.on()) return hipErrorInvalidValue;
+  auto launch = w.dense ? launch_dx_tiles<kFormDense, kPlainQ, false, false>
+                : d.on() ? (w.dq ? launch_dx_tiles<kFormDq, kPlainQ, false, true>
+                                 : launch_dx_tiles<kFormNoDq, kPlainQ, false, true>)
+                         : (w.dq ? launch_dx_tiles<kFormDq, kPlainQ, false, false>
+                                 : launch_dx_tiles<kFormNoDq, kPlainQ, false, false>);
   prof_begin(1, stream);
-  hipLaunchKernelGGL(kern,
-                     dim3(ptiles * qtiles * sp.splits), dim3(XT), kDxLds, stream, dY, M, w.dense,
-                     w.codes, w.absmax_q, w.absmax_scale, w.N, w.K, G, A, r, s, dX, ptiles,
-                     qtiles, sp.cps, sp.splits > 1 ? part : nullptr, tb);
-  hipError_t e = hipGetLastError();
+  hipError_t e = launch(dY, M, w, w.N, G, A, r, s, dX, part, tb, stream, qtiles, sp, nullptr, 0, d);
   if (e == hipSuccess && sp.splits > 1)
     e = launch_split_reduce_bf16(part, sp.splits, M * w.K, dX, stream);
+  prof_end(1, stream);
+  return e;
+}
+
+GemmSplit grouped_dx_split(int64_t M, int E, int64_t N, int64_t K) {
+  return gemm_split((K + XP - 1) / XP * group_tile_bound(M, E, grouped_tile(M, E)),
+                    (N + XN - 1) / XN);
+}
+
+hipError_t launch_grouped_dx_gemm(const uint16_t* dY, int64_t M, const int* offsets, int E,
+                                  const Nf4View& w, const float* G, const uint16_t* A, int r,
+                                  float s, uint16_t* dX, float* part, const Nf4Tables& tb,
+                                  hipStream_t stream, const Drop& d) {
+  const int64_t N = w.N / E;
+  const int q = grouped_tile(M, E);
+  const int qtiles = static_cast<int>(group_tile_bound(M, E, q));
+  const GemmSplit sp = grouped_dx_split(M, E, N, w.K);
+  auto pick = [&](auto qc) {
+    constexpr int Q = decltype(qc)::value;
+    return d.on() ? (w.dq ? launch_dx_tiles<kFormDq, Q, true, true>
+                          : launch_dx_tiles<kFormNoDq, Q, true, true>)
+                  : (w.dq ? launch_dx_tiles<kFormDq, Q, true, false>
+                          : launch_dx_tiles<kFormNoDq, Q, true, false>);
+  };
+  auto launch = q == 64 ? pick(std::integral_constant<int, 64>{})
+                        : pick(std::integral_constant<int, 256>{});
+  prof_begin(1, stream);
+  hipError_t e = launch(dY, M, w, N, G, A, r, s, dX, part, tb, stream, qtiles, sp, offsets, E, d);
+  if (e == hipSuccess && sp.splits > 1)
+    e = launch_group_reduce(part, sp.splits, M, w.K, 1.f, offsets, E, nullptr, dX, stream);
   prof_end(1, stream);
   return e;
 }

@@ -33,6 +33,15 @@ struct Nf4View {
   bool dq = true;
 };
 
+// Dropout of the adapter's input: the generator's state {seed, offset} in
+// device memory and the threshold on its 16-bit values; thr = 0 drops nothing.
+struct Drop {
+  const uint64_t* state = nullptr;
+  uint32_t thr = 0;
+  bool on() const { return thr > 0; }
+  float scale() const { return 65536.f / static_cast<float>(65536u - thr); }
+};
+
 // Profiling hook: the launchers call these around the launches of one
 // kernel family (no-ops unless profiling is enabled).
 void prof_begin(int family, hipStream_t stream);
@@ -47,7 +56,7 @@ struct GemmSplit {
 };
 GemmSplit gemm_split(int64_t tiles, int64_t nchunks);
 hipError_t launch_split_reduce_bf16(const float* part, int splits, int64_t count, uint16_t* out,
-                                    hipStream_t stream);
+                                    hipStream_t stream, float scale = 1.f);
 
 // Y[M,N] = bf16( X . deq(W)^T + s . T . B ), large-M MFMA path with the
 // dequantized weight tiles staged in LDS.  T [M, r] fp32 (may be null when
@@ -80,12 +89,13 @@ hipError_t launch_fwd_decode(const uint16_t* X, int64_t M, const Nf4View& w,
 GemmSplit dx_gemm_split(int64_t M, int64_t N, int64_t K);
 hipError_t launch_dx_gemm(const uint16_t* dY, int64_t M, const Nf4View& w,
                           const float* G, const uint16_t* A, int r, float s,
-                          uint16_t* dX, float* part, const Nf4Tables& tb, hipStream_t stream);
+                          uint16_t* dX, float* part, const Nf4Tables& tb, hipStream_t stream,
+                          const Drop& d = {});
 
 // Rank-r products with a split reduction; partials go to `ws`.
 size_t rank_ws_floats(int64_t M, int64_t N, int64_t K, int r);
 // The partials of T = X . A alone (the forward's rank product).
-size_t lora_down_ws_floats(int64_t M, int64_t K, int r);
+size_t lora_down_ws_floats(int64_t M, int64_t K, int r, bool drop = false);
 
 // Few-token LoRA down-projection: nz <= maxp fp32 partial sums [nz][M][r]
 // of T = X . A go to ws (nz returned); M <= 16, maxp <= kMaxDownPartials.
@@ -94,10 +104,10 @@ int lora_down_partial_count(int64_t K, int maxp);
 hipError_t launch_lora_down_partials(const uint16_t* X, int64_t M, int64_t K, const uint16_t* A,
                                      int r, int maxp, float* ws, int* nz, hipStream_t stream);
 
-// T[M,r] = X . A (fp32 out).
+// T[M,r] = X . A (fp32 out); with d on, scale . (mask X) . A.
 hipError_t launch_lora_down(const uint16_t* X, int64_t M, int64_t K,
                             const uint16_t* A, int r, float* T, float* ws,
-                            hipStream_t stream);
+                            hipStream_t stream, const Drop& d = {});
 // G[M,r] = dY . B^T (fp32 out) and dB[r,N] = bf16( s . T^T . dY ), both
 // products in one launch and both split reductions in one more.  Row strides
 // (0 = dense): ldy of dY, ldb of B and of dB, ldt of T and of G.
@@ -105,9 +115,52 @@ hipError_t launch_grad_in_and_b(const uint16_t* dY, int64_t M, int64_t N, const 
                                 const float* T, int r, float s, float* G, uint16_t* dB,
                                 float* ws, hipStream_t stream, int64_t ldy = 0, int64_t ldb = 0,
                                 int ldt = 0);
-// dA[K,r] = bf16( s . X^T . G ).
+// dA[K,r] = bf16( s . X^T . G ); with d on, bf16( s scale . (mask X)^T . G ).
 hipError_t launch_grad_a(const uint16_t* X, int64_t M, int64_t K, const float* G,
-                         int r, float s, uint16_t* dA, float* ws, hipStream_t stream);
+                         int r, float s, uint16_t* dA, float* ws, hipStream_t stream,
+                         const Drop& d = {});
+
+// ---------------------------------------------------------------------------
+// Layers grouped by expert: rows [offsets[e], offsets[e + 1]) of X belong to
+// expert e (offsets int32 [E + 1] in device memory).  The weight view holds the
+// E experts' weights of N = w.N / E rows one after the other, A is [E][K][r]
+// and B [E][r][N].  Rows outside all groups are neither read nor written.
+// ---------------------------------------------------------------------------
+
+// Tokens a GEMM tile holds (256 or 64) for M rows of E experts.
+int grouped_tile(int64_t M, int E);
+GemmSplit grouped_fwd_split(int64_t M, int E, int64_t N, int64_t K);
+GemmSplit grouped_dx_split(int64_t M, int E, int64_t N, int64_t K);
+hipError_t launch_grouped_fwd_gemm(const uint16_t* X, int64_t M, const int* offsets, int E,
+                                   const Nf4View& w, const float* T, const uint16_t* B, int r,
+                                   float s, uint16_t* Y, float* part, const Nf4Tables& tb,
+                                   hipStream_t stream);
+hipError_t launch_grouped_dx_gemm(const uint16_t* dY, int64_t M, const int* offsets, int E,
+                                  const Nf4View& w, const float* G, const uint16_t* A, int r,
+                                  float s, uint16_t* dX, float* part, const Nf4Tables& tb,
+                                  hipStream_t stream, const Drop& d);
+// out[m][i] = scale * sum_z part[z][m][i] for the rows of the groups; exactly
+// one of f32 and bf16 is the output.
+hipError_t launch_group_reduce(const float* part, int splits, int64_t M, int64_t cols, float scale,
+                               const int* offsets, int E, float* f32, uint16_t* bf16,
+                               hipStream_t stream);
+// Floats of workspace of the four rank products, and those of T alone.
+size_t grouped_rank_ws_floats(int64_t M, int E, int64_t N, int64_t K, int r);
+size_t grouped_down_ws_floats(int64_t M, int E, int64_t K, int r);
+hipError_t launch_grouped_down(const uint16_t* X, int64_t M, const int* offsets, int E, int64_t K,
+                               const uint16_t* A, int r, float* T, float* ws, hipStream_t stream,
+                               const Drop& d);
+hipError_t launch_grouped_grad_in_and_b(const uint16_t* dY, int64_t M, const int* offsets, int E,
+                                        int64_t N, const uint16_t* B, const float* T, int r,
+                                        float s, float* G, uint16_t* dB, float* ws,
+                                        hipStream_t stream);
+hipError_t launch_grouped_grad_a(const uint16_t* X, int64_t M, const int* offsets, int E,
+                                 int64_t K, const float* G, int r, float s, uint16_t* dA,
+                                 float* ws, hipStream_t stream, const Drop& d);
+
+// y[i] = mask scale x[i] (bf16, n elements; y may be x).
+hipError_t launch_dropout(const uint16_t* x, int64_t n, const Drop& d, uint16_t* y,
+                          hipStream_t stream);
 
 // One AdamW step over n parameters (bf16 p, g; fp32 m, v, device or
 // device-visible pinned host memory, 16-byte aligned), bias corrections for

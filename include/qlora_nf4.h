@@ -75,8 +75,13 @@ typedef enum {
   QLORA_ERR_WORKSPACE = 6,  /* workspace too small */
   QLORA_ERR_SCRATCH = 7,    /* qlora_linear_fwd_noalloc: the call needs more than
                                QLORA_NOALLOC_SCRATCH_BYTES of workspace */
-  QLORA_ERR_FORMAT = 8      /* qlora_q4_*: unknown codebook, or double_quant
+  QLORA_ERR_FORMAT = 8,     /* qlora_q4_*: unknown codebook, or double_quant
                                not 0 or 1 */
+  QLORA_ERR_EXPERT = 9,     /* qlora_grouped_*, qlora_expert_*: E outside
+                               [1, 1024] or not dividing the weight's rows, an
+                               expert that is not whole groups of 256 block
+                               constants, topk outside [1, 64] */
+  QLORA_ERR_DROPOUT = 10    /* dropout probability outside [0, 1) */
 } qlora_status;
 
 /* A hipStream_t, passed as an opaque pointer so this header needs no HIP. */
@@ -377,6 +382,142 @@ int qlora_q4_linear_bwd(const uint16_t* dY, const uint16_t* X, int64_t M,
                         float s, const float* T_saved, uint16_t* dX, uint16_t* dA,
                         uint16_t* dB, void* workspace, size_t workspace_bytes,
                         qlora_stream_t stream);
+
+/*
+ * Dropout on the adapter's input ("LoRA dropout", the regulariser of a QLoRA
+ * fine-tune), from a counter-based generator: the mask is a function of the
+ * state and the element's position, is regenerated wherever it is needed, and
+ * is never stored.
+ *
+ * Element i of a tensor (row-major index) belongs to piece i / 8.  The piece's
+ * 128 bits are Philox4x32 with 7 rounds (Salmon, Moraes, Dror, Shaw, SC11) of
+ * the counter words (low and high half of the piece, low and high half of
+ * offset) under the key (low and high half of seed).  Element i takes 16-bit
+ * half i % 8 (the low half of the first word first) and is kept when it is at
+ * least t = min(floor(65536 p + 1/2), 65535).  Kept elements are scaled by
+ * c = 65536 / (65536 - t); a dropped element gives 0 whatever it held.
+ *   state: {seed, offset} in device memory (8-byte aligned), read when the
+ *     kernels run: a captured graph draws another mask on each replay if
+ *     the caller changes the words in between.  Forward and backward of one
+ *     layer must see the same state.  Not read when t = 0 (may be NULL).
+ *   p in [0, 1) (QLORA_ERR_DROPOUT otherwise).
+ */
+typedef struct {
+  const uint64_t* state;
+  float p;
+} qlora_dropout;
+
+/*
+ * y = mask . c . x over n bf16 elements (any n >= 0; y may be x).  The
+ * backward is the same call on the gradient.
+ */
+int qlora_dropout_apply(const uint16_t* x, int64_t n, const qlora_dropout* d, uint16_t* y,
+                        qlora_stream_t stream);
+
+/*
+ * The layer with dropout on its adapter's input (the mask is that of X):
+ *   T  = c . (mask X) . A
+ *   Y  = X . deq(W)^T + s . T . B
+ *   G  = dY . B^T
+ *   dX = dY . deq(W) + s c . mask (G . A^T)
+ *   dA = s c . (mask X)^T . G
+ *   dB = s . T^T . dY
+ * The base product reads X itself.  T is the tensor the backward takes
+ * (NULL recomputes it).  d = NULL, or t = 0, is the plain layer.  Other
+ * arguments, limits and errors as qlora_q4_linear_fwd / qlora_q4_linear_bwd;
+ * workspaces of the sizes below.
+ */
+size_t qlora_linear_dropout_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int r);
+size_t qlora_linear_dropout_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int r);
+int qlora_linear_dropout_fwd(const uint16_t* X, int64_t M, const qlora_q4_weight* w,
+                             const uint16_t* A, const uint16_t* B, int r, float s,
+                             const qlora_dropout* d, uint16_t* Y, float* T, void* workspace,
+                             size_t workspace_bytes, qlora_stream_t stream);
+int qlora_linear_dropout_bwd(const uint16_t* dY, const uint16_t* X, int64_t M,
+                             const qlora_q4_weight* w, const uint16_t* A, const uint16_t* B,
+                             int r, float s, const qlora_dropout* d, const float* T_saved,
+                             uint16_t* dX, uint16_t* dA, uint16_t* dB, void* workspace,
+                             size_t workspace_bytes, qlora_stream_t stream);
+
+/*
+ * The layer grouped by expert: E layers of one shape, each on its own rows of
+ * X (a mixture of experts whose frozen weights are 4-bit, one adapter pair
+ * per expert).  Rows offsets[e] .. offsets[e+1]-1 belong to expert e:
+ *     Y[rows] = X[rows] . deq(W_e)^T + s . T[rows] . B_e,  T[rows] = X[rows] . A_e
+ *   X [M, K], Y, dY [M, N] bf16, T [M, r] fp32, dX [M, K] bf16.
+ *   offsets  int32 [E+1] in device memory (4-byte aligned), ascending, within
+ *      [0, M]; a group may be empty.  The library reads them on the GPU only.
+ *      Offsets outside [0, M] are clamped to it and a group that ends before
+ *      it starts is empty; which rows overlapping groups leave is undefined,
+ *      but nothing outside the buffers is touched.
+ *   Rows outside all groups (before offsets[0], from offsets[E] on) are not
+ *      read, and their rows of Y, T and dX are left as they were.
+ *   w  [E*N, K]: the experts' weights one after the other, quantized as one
+ *      weight.  E in [1, 1024] divides w->N; N % 8 == 0; with double
+ *      quantization N*K % 16384 == 0 (each expert starts at a group of 256
+ *      block constants).  QLORA_ERR_EXPERT / QLORA_ERR_SHAPE otherwise.
+ *   A  [E, K, r], B [E, r, N] bf16, dA and dB of the same shapes: zero for an
+ *      expert without rows.  r = 0 (A, B, T, dA, dB may be NULL): base only.
+ *   0 <= M < 2^31; M = 0 is allowed (X, Y, dY, dX, T may then be NULL).
+ *   d: dropout on the adapters' input as in qlora_linear_dropout_*, the
+ *      mask being that of X [M, K]; NULL for none.
+ * Backward, on each expert's rows: G = dY . B_e^T, dX = dY . deq(W_e) +
+ * s . G . A_e^T (skipped if dX == NULL), dA_e = s . X^T . G, dB_e = s . T^T . dY,
+ * with T_saved the forward's T or NULL to recompute it.
+ * Other limits and errors as qlora_q4_linear_fwd / qlora_q4_linear_bwd.
+ */
+size_t qlora_grouped_fwd_workspace_bytes(int64_t M, int E, int64_t N, int64_t K, int r);
+size_t qlora_grouped_bwd_workspace_bytes(int64_t M, int E, int64_t N, int64_t K, int r);
+int qlora_grouped_fwd(const uint16_t* X, int64_t M, const int32_t* offsets, int E,
+                      const qlora_q4_weight* w, const uint16_t* A, const uint16_t* B, int r,
+                      float s, const qlora_dropout* d, uint16_t* Y, float* T, void* workspace,
+                      size_t workspace_bytes, qlora_stream_t stream);
+int qlora_grouped_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const int32_t* offsets,
+                      int E, const qlora_q4_weight* w, const uint16_t* A, const uint16_t* B,
+                      int r, float s, const qlora_dropout* d, const float* T_saved, uint16_t* dX,
+                      uint16_t* dA, uint16_t* dB, void* workspace, size_t workspace_bytes,
+                      qlora_stream_t stream);
+
+/*
+ * The exchange around the grouped layer.  A router gives every token topk
+ * experts: ids [tokens, topk] int32, n = tokens * topk slots.
+ *
+ * qlora_expert_plan sorts the slots by expert on the GPU, stably:
+ *   offsets [E+1]: the groups' offsets; offsets[E] is the number of slots
+ *      that got a row.
+ *   order   [n]: the slot of row i, -1 from row offsets[E] on.
+ *   inverse [n]: the row of slot t*topk + j, -1 for a slot whose id is
+ *      outside [0, E) (a dropped or padded slot).
+ *   1 <= E <= 1024, 0 <= n <= 2^30; workspace of
+ *   qlora_expert_plan_workspace_bytes(n, E) bytes.
+ * qlora_expert_gather: Xs[inverse[t][j]] = X[t]: the token rows [tokens, K] in
+ *   expert order.  Rows of Xs that no slot has are left as they were.
+ * qlora_expert_combine: out[t] = sum_j w[t][j] . Y[inverse[t][j]] (summed in
+ *   fp32 in the order of j, rounded to bf16 once; a slot without a row adds
+ *   nothing).  weights [tokens, topk] fp32, or NULL for 1: then it is also the
+ *   backward of qlora_expert_gather.
+ * qlora_expert_combine_bwd: dY[inverse[t][j]] = w[t][j] . dOut[t] (rows no slot
+ *   has are left as they were) and dweights[t][j] = dOut[t] . Y[inverse[t][j]]
+ *   (0 for a slot without a row).
+ *   X, out, dOut [tokens, K], Xs, Y, dY [n, K] bf16, 16-byte aligned; the int32
+ *   and fp32 vectors 4-byte aligned.  K % 8 == 0, 8 <= K <= 2^22,
+ *   1 <= topk <= 64, 0 <= n <= 2^30.  inverse must name each row at most once
+ *   (as the plan does); entries outside [0, n) count as -1.
+ * Errors: QLORA_ERR_EXPERT (E or topk), QLORA_ERR_SHAPE, QLORA_ERR_NULL,
+ * QLORA_ERR_ALIGN, QLORA_ERR_WORKSPACE, QLORA_ERR_HIP.
+ */
+size_t qlora_expert_plan_workspace_bytes(int64_t n, int E);
+int qlora_expert_plan(const int32_t* ids, int64_t n, int E, int32_t* offsets, int32_t* order,
+                      int32_t* inverse, void* workspace, size_t workspace_bytes,
+                      qlora_stream_t stream);
+int qlora_expert_gather(const uint16_t* X, int64_t tokens, int topk, int64_t K,
+                        const int32_t* inverse, uint16_t* Xs, qlora_stream_t stream);
+int qlora_expert_combine(const uint16_t* Y, int64_t tokens, int topk, int64_t K,
+                         const int32_t* inverse, const float* weights, uint16_t* out,
+                         qlora_stream_t stream);
+int qlora_expert_combine_bwd(const uint16_t* dOut, const uint16_t* Y, int64_t tokens, int topk,
+                             int64_t K, const int32_t* inverse, const float* weights,
+                             uint16_t* dY, float* dweights, qlora_stream_t stream);
 
 /*
  * Optimizer step on the adapters, and its state paged between HBM and host
