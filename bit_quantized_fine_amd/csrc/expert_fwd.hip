@@ -1,0 +1,476 @@
+// Forward of the layer grouped by expert, Y = X . deq(W_e)^T + s . T . B_e on
+// each expert's rows, on bf16 MFMA with the weights dequantized straight into
+// MFMA operands.
+//
+// Workgroup = 8 waves, tile = 128 FR weight rows x 16 TB tokens of one expert.
+// Wave w owns 16 FR rows and all tokens of the tile, so every weight is
+// dequantized by exactly one wave and never passes through LDS: lane l = 16 g
+// + i loads the 16 code bytes at 16 g of row i's 64-byte segment of a 128-k
+// chunk, and dword t of them, dequantized, is the lane's share of the 16 x 32
+// operand of step t (k = 32 g + 8 t .. + 7).  X is what the waves share: it is
+// staged through LDS in the same k order, double-buffered, one barrier a chunk,
+// its 16-byte pieces XOR-swizzled by row.  Per 128-k chunk and 256 rows the
+// LDS serves 128 KB of level lookups whatever TB is and 8 x 4 TB KB of X
+// reads, against 64 TB MFMAs a SIMD.
+//
+// The operands of the next step are dequantized while the MFMAs of the current
+// one run.  X waits one or two chunks ahead in registers.  With TB = 16 a chunk's
+// X (64 KB twice) does not fit beside the level table, so it is staged as two
+// half chunks, steps 0-1 and steps 2-3.
+//
+// The offsets are read on the GPU: the grid holds the most tiles the groups
+// could make, a workgroup finds its expert and rows in them, and the last tile
+// of a group runs the narrowest body that holds its rows.
+#include <type_traits>
+
+#include "device_common.hpp"
+#include "group_tiles.hpp"
+#include "kernels.hpp"
+#include "rank_tiles.hpp"
+
+namespace qnf4 {
+
+namespace {
+
+constexpr int EW = 8;            // waves
+constexpr int ET = 64 * EW;      // threads
+constexpr uint32_t kOffNone = 0x80000000u;   // past the end of every buffer
+
+template <int FR, int TB>
+struct ExpertTile {
+  static constexpr int ROWS = 16 * FR * EW;       // weight rows
+  static constexpr int TQ = 16 * TB;              // tokens
+  static constexpr int SUB = TB > 8 ? 2 : 1;      // X stagings of a 128-k chunk
+  static constexpr int STEPS = 4 / SUB;           // 32-k steps of one staging
+  static constexpr int PPR = 4 * STEPS;           // 16-byte pieces of a token row
+  static constexpr int XBUF = TQ * PPR * 8;       // elements of one X buffer
+  static constexpr int PIECES = TQ * PPR;
+  static constexpr int PP = (PIECES + ET - 1) / ET;   // pieces a thread stages
+  static constexpr int XST = TB > 8 ? 1 : 2;      // register stages of X
+  static constexpr int MAIN = kRepTabBytes + 2 * XBUF * 2;
+  static constexpr int TAIL = ROWS * 128 + TQ * 256;   // B tile, T hi and lo tiles
+  static constexpr int LDS = MAIN > TAIL ? MAIN : TAIL;
+};
+
+// The narrower bodies a kernel of TB token subtiles holds (0: none): 12 -> 4,
+// 8; 4 -> 1, 2; 2 -> 1.  Its LDS is that of the largest.
+constexpr int narrow1(int tb) { return tb > 4 ? 4 : tb / 4; }
+constexpr int narrow2(int tb) { return tb > 4 ? 8 : tb / 2; }
+template <int FR, int TB>
+constexpr int expert_lds() {
+  int lds = ExpertTile<FR, TB>::LDS;
+  if constexpr (narrow1(TB) > 0)
+    lds = lds > ExpertTile<FR, narrow1(TB)>::LDS ? lds : ExpertTile<FR, narrow1(TB)>::LDS;
+  if constexpr (narrow2(TB) > 0)
+    lds = lds > ExpertTile<FR, narrow2(TB)>::LDS ? lds : ExpertTile<FR, narrow2(TB)>::LDS;
+  return lds;
+}
+
+struct ExpertArgs {
+  const uint16_t* X;
+  int64_t M;
+  const int* offsets;
+  int E;
+  const uint8_t* codes;
+  const uint8_t* absmax_q;
+  const float* absmax_scale;
+  int64_t N, K;
+  const float* T;
+  const uint16_t* B;
+  int r;
+  float s;
+  uint16_t* Y;
+  int ptiles, qtiles, cps;
+  float* part;
+};
+
+// Slot of 16-byte piece q of token row `row`.
+template <int PPR>
+__device__ __forceinline__ int xslot(int row, int q) {
+  return PPR == 16 ? q ^ (row & 15) : q ^ ((row >> 1) & 7);
+}
+
+template <int FR, int TB, bool NODQ>
+__device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, int e, int64_t q0,
+                                            int64_t mend, int pt, int z) {
+  using Tile = ExpertTile<FR, TB>;
+  constexpr int SUB = Tile::SUB, STEPS = Tile::STEPS, PPR = Tile::PPR, PP = Tile::PP;
+  constexpr int XST = Tile::XST;
+  constexpr int GB = TB < 4 ? TB : 4, NG = TB / GB;   // token subtiles a group, groups
+  constexpr int U = TB == 4 ? 2 : 1;                  // steps dequantized together
+  uint16_t* const Xs = reinterpret_cast<uint16_t*>(dyn + kRepTabBytes);
+  const int tid = threadIdx.x;
+  const int wave = wave_id(), lane = tid & 63;
+  const int li = lane & 15, g = lane >> 4;
+  const int64_t N = a.N, K = a.K;
+  const int K32 = static_cast<int>(K), KB = K32 / kBlock;
+  const int64_t p0 = (int64_t)pt * Tile::ROWS;
+  const int64_t NW = N * a.E;
+  const int c0 = z * a.cps;
+  const int nchunks = min((K32 + 127) / 128, c0 + a.cps);   // end of this split's chunks
+
+  // rows past W and tokens past the tile read as zero
+  const uint32_t nb = static_cast<uint32_t>(NW * K / kBlock);
+  const BufRes rc = make_bufres(a.codes, static_cast<uint32_t>(NW * K / 2));
+  const BufRes re = make_bufres(a.absmax_q, nb);
+  const BufRes rd = make_bufres(a.absmax_scale, (NODQ ? nb : (nb + kGroup - 1) / kGroup) * 4u);
+  const int64_t tile_rows = mend - q0 < Tile::TQ ? mend - q0 : Tile::TQ;
+  const BufRes rx = make_bufres(a.X + q0 * K, static_cast<uint32_t>(tile_rows * K * 2));
+
+  // codes and constants of the lane's FR rows, two chunks in flight
+  uint32_t cb[FR], eb[FR];
+#pragma unroll
+  for (int f = 0; f < FR; ++f) {
+    const int64_t n = (int64_t)e * N + p0 + 16 * (FR * wave + f) + li;
+    cb[f] = static_cast<uint32_t>(n * (K / 2)) + 16u * g;        // + 64 c
+    eb[f] = static_cast<uint32_t>(n * KB) + (g >> 1);            // + 2 c
+  }
+  u32x4 cw[2][FR];
+  uint32_t ce[2][FR];
+  float cd[2][FR];
+  auto load_codes = [&](int c, int st) {
+    const bool live = c < nchunks;
+    const bool blk = live && 2 * c + (g >> 1) < KB;   // the half chunk past K: constant 0
+#pragma unroll
+    for (int f = 0; f < FR; ++f) {
+      cw[st][f] = buf_load16(rc, live ? cb[f] + 64u * c : kOffNone);
+      const uint32_t b = eb[f] + 2u * c;
+      if constexpr (NODQ) {
+        ce[st][f] = 1u;
+        cd[st][f] = buf_load_f32(rd, blk ? b * 4u : kOffNone);
+      } else {
+        ce[st][f] = buf_load_u8(re, blk ? b : kOffNone);
+        cd[st][f] = buf_load_f32(rd, blk ? (b / kGroup) * 4u : kOffNone);
+      }
+    }
+  };
+
+  // X piece idx = tid + 512 j: token row idx / PPR, piece q = idx % PPR.  Piece q
+  // = g + 4 i is what lane group g takes at step i of the staging: k = 128 c +
+  // 8 (4 g + 2 h + i) .. + 7 (h: the half chunk).  In this order a 16-byte read,
+  // which the LDS serves in groups of 16 lanes of two g's, meets no bank twice;
+  // with q = 4 g + i it met every second one twice.
+  // (A thread's pieces are whole rows apart, so they share q and the swizzle.)
+  static_assert(ET % PPR == 0 && (ET / PPR) % 16 == 0, "piece rows apart");
+  const int xrow = tid / PPR, xq = tid % PPR;
+  const int xcp = SUB == 1 ? xq : 4 * (xq >> 1) + (xq & 1);
+  const uint32_t xsrc = static_cast<uint32_t>(xrow * K32 + 8 * xcp) * 2u;
+  const uint32_t xstep = static_cast<uint32_t>(ET / PPR * K32) * 2u;
+  uint16_t* const xdst = Xs + (xrow * PPR + xslot<PPR>(xrow, xq)) * 8;
+  const bool xlive = Tile::PIECES % ET == 0 || tid < Tile::PIECES;
+  u32x4 xw[XST][PP];
+  auto load_x = [&](int t, int st) {   // staging t of this split (t = SUB c + h)
+    const int k0 = SUB == 1 ? 128 * t : 128 * (t >> 1) + 16 * (t & 1);
+    const bool ok = xlive && t < SUB * nchunks && k0 + 8 * xcp < K32;
+    const uint32_t o = ok ? xsrc + 2u * k0 : kOffNone;   // (+ j xstep < 2^31: stays past the end)
+#pragma unroll
+    for (int j = 0; j < PP; ++j) xw[st][j] = buf_load16(rx, o + j * xstep);
+  };
+  auto store_x = [&](int st, int buf) {
+    if (xlive) {
+#pragma unroll
+      for (int j = 0; j < PP; ++j)
+        *reinterpret_cast<u32x4*>(xdst + buf * Tile::XBUF + j * ET * 8) = xw[st][j];
+    }
+  };
+
+  f32x4 acc[FR][TB];
+#pragma unroll
+  for (int f = 0; f < FR; ++f)
+#pragma unroll
+    for (int b = 0; b < TB; ++b) acc[f][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // The level pairs of the 8 codes of step t, and bf16_rne(fl32(level * c)).
+  struct Pairs {
+    f32x2 v[4];
+  };
+  const uint32_t ta = rep_lane_base(lane);
+  auto lookup = [&](int st, int f, int t) {
+    const uint32_t w = cw[st][f][t];
+    return Pairs{{rep_lookup<0>(ta, w), rep_lookup<1>(ta, w), rep_lookup<2>(ta, w),
+                  rep_lookup<3>(ta, w)}};
+  };
+  auto scaled = [&](int st, int f, const Pairs& p) {
+    const float ch = NODQ ? cd[st][f] : static_cast<float>(ce[st][f]) * cd[st][f];
+    return u32x4{pack_bf16x2(p.v[0].x * ch, p.v[0].y * ch),
+                 pack_bf16x2(p.v[1].x * ch, p.v[1].y * ch),
+                 pack_bf16x2(p.v[2].x * ch, p.v[2].y * ch),
+                 pack_bf16x2(p.v[3].x * ch, p.v[3].y * ch)};
+  };
+  // step i of the staging, token subtile b: token row 16 b + li, whose swizzle
+  // is that of row li
+  const uint16_t* const xsrow = Xs + li * PPR * 8;
+  const int xsw = PPR == 16 ? li : li >> 1;
+  auto read_x = [&](int buf, int i, int b) {
+    const int q = SUB == 1 ? 4 * g + i : 2 * g + i;
+    return *reinterpret_cast<const u32x4*>(xsrow + 8 * (q ^ xsw) + buf * Tile::XBUF +
+                                           16 * b * PPR * 8);
+  };
+
+  load_codes(c0, 0);
+  load_codes(c0 + 1, 1);
+  load_x(SUB * c0, 0);
+  if constexpr (XST == 2) load_x(SUB * c0 + 1, 1);
+  __syncthreads();   // the level table
+  store_x(0, 0);
+  if constexpr (XST == 2) load_x(SUB * c0 + 2, 0); else load_x(SUB * c0 + 1, 0);
+  u32x4 af[2][U][FR];   // operands of the current and the next U steps
+#pragma unroll
+  for (int i = 0; i < U; ++i)
+#pragma unroll
+    for (int f = 0; f < FR; ++f) af[0][i][f] = scaled(0, f, lookup(0, f, i));
+  __syncthreads();
+  // Chunk c, codes in stage ST.  A staging's products run in groups of GB token
+  // subtiles of one step.  While a group's MFMAs run, the X operands of the next
+  // group and (at the first group of U steps) the level pairs of the next U
+  // steps are on their way from LDS; the pairs become operands behind the last
+  // group's MFMAs.  The scheduling barriers keep that order: left alone, the
+  // compiler issues a pair's two lookups next to their use and waits for each.
+  auto chunk = [&](int c, auto stc) {
+    constexpr int ST = decltype(stc)::value;
+#pragma unroll
+    for (int h = 0; h < SUB; ++h) {
+      const int buf = SUB == 1 ? ST : h;
+      const int t = SUB * c + h;
+      const int xs = XST == 2 ? (ST ^ 1) : 0;
+      u32x4 xf[2][GB];
+#pragma unroll
+      for (int b = 0; b < GB; ++b) xf[0][b] = read_x(buf, 0, b);
+      Pairs pr[U][FR];
+#pragma unroll
+      for (int k = 0; k < STEPS * NG; ++k) {
+        const int i = k / NG;                      // step of the staging
+        const int unit = (STEPS * h + i) / U;      // run of U steps of the chunk
+        const bool first = k % (U * NG) == 0, last = k % (U * NG) == U * NG - 1;
+        const int nst = U * (unit + 1) < 4 ? ST : (ST ^ 1);   // codes of the next run
+        if (first) {
+#pragma unroll
+          for (int j = 0; j < U; ++j)
+#pragma unroll
+            for (int f = 0; f < FR; ++f) pr[j][f] = lookup(nst, f, (U * (unit + 1) + j) % 4);
+        }
+        if (k + 1 < STEPS * NG) {
+#pragma unroll
+          for (int b = 0; b < GB; ++b)
+            xf[(k + 1) & 1][b] = read_x(buf, (k + 1) / NG, GB * ((k + 1) % NG) + b);
+        }
+        if (k == 0) {   // X of the next staging, then the registers' next load
+          store_x(xs, buf ^ 1);
+          load_x(XST == 2 ? t + 3 : t + 2, xs);
+        }
+        if (first && unit == 4 / U - 1) load_codes(c + 2, ST);   // stage ST is used up
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int b = 0; b < GB; ++b)
+#pragma unroll
+          for (int f = 0; f < FR; ++f)
+            acc[f][GB * (k % NG) + b] =
+                mfma16(af[unit & 1][i % U][f], xf[k & 1][b], acc[f][GB * (k % NG) + b]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (last) {
+#pragma unroll
+          for (int j = 0; j < U; ++j)
+#pragma unroll
+            for (int f = 0; f < FR; ++f) af[(unit + 1) & 1][j][f] = scaled(nst, f, pr[j][f]);
+        }
+      }
+      __syncthreads();
+    }
+  };
+  // An odd chunk count adds one pass over a chunk past the end, all zeros.
+  for (int c = c0; c < nchunks; c += 2) {
+    chunk(c, std::integral_constant<int, 0>{});
+    chunk(c + 1, std::integral_constant<int, 1>{});
+  }
+
+  // LoRA update (the first split only): 64 ranks at a time, the B tile [64
+  // ranks][ROWS] as it lies in memory, read with transposing loads, and s . T as
+  // bf16 hi and lo tiles [TQ][64], swizzled like half-chunk X rows.
+  if (a.r > 0 && z == 0) {
+    uint16_t* const bt = reinterpret_cast<uint16_t*>(dyn);
+    uint16_t* const th = bt + Tile::ROWS * 64;
+    uint16_t* const tl = th + Tile::TQ * 64;
+    const uint16_t* const Be = a.B + (int64_t)e * a.r * N;
+    for (int j0 = 0; j0 < a.r; j0 += 64) {
+#pragma unroll
+      for (int i = 0; i < Tile::ROWS * 8 / ET; ++i) {
+        const int idx = tid + ET * i, red = idx / (Tile::ROWS / 8), pc = idx % (Tile::ROWS / 8);
+        const int64_t n = p0 + 8 * pc;
+        const u32x4 v = j0 + red < a.r && n < N ? ld16(Be + (int64_t)(j0 + red) * N + n)
+                                                : u32x4{0, 0, 0, 0};
+        st_lds16(bt + (pc / 16) * 64 * 128 + red * 128 + 8 * rm_slot<128>(red, pc % 16), v);
+      }
+      for (int idx = tid; idx < Tile::TQ * 8; idx += ET) {
+        const int row = idx / 8, q = idx % 8, j = j0 + 8 * q;
+        uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+        if (q0 + row < mend && j < a.r) {
+          const float* src = a.T + (q0 + row) * a.r + j;
+          const f32x4 t0 = *reinterpret_cast<const f32x4*>(src) * a.s;
+          const f32x4 t1 = *reinterpret_cast<const f32x4*>(src + 4) * a.s;
+          split_bf16x2(t0.x, t0.y, hi[0], lo[0]);
+          split_bf16x2(t0.z, t0.w, hi[1], lo[1]);
+          split_bf16x2(t1.x, t1.y, hi[2], lo[2]);
+          split_bf16x2(t1.z, t1.w, hi[3], lo[3]);
+        }
+        const int o = (row * 8 + xslot<8>(row, q)) * 8;
+        st_lds16(th + o, u32x4{hi[0], hi[1], hi[2], hi[3]});
+        st_lds16(tl + o, u32x4{lo[0], lo[1], lo[2], lo[3]});
+      }
+      __syncthreads();
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        u32x4 bf[FR];
+#pragma unroll
+        for (int f = 0; f < FR; ++f) {
+          const int col = 16 * (FR * wave + f);
+          bf[f] = rm_frag<128>(bt + (col / 128) * 64 * 128, col % 128, ks, lane);
+        }
+#pragma unroll
+        for (int b = 0; b < TB; ++b) {
+          const int row = 16 * b + li;
+          const int o = (row * 8 + xslot<8>(row, 4 * ks + g)) * 8;
+          const u32x4 hi = *reinterpret_cast<const u32x4*>(th + o);
+          const u32x4 lo = *reinterpret_cast<const u32x4*>(tl + o);
+#pragma unroll
+          for (int f = 0; f < FR; ++f) {
+            acc[f][b] = mfma16(bf[f], hi, acc[f][b]);
+            acc[f][b] = mfma16(bf[f], lo, acc[f][b]);
+          }
+        }
+      }
+      __syncthreads();
+    }
+  }
+
+  // Y[m, n..n+3] for the lane's 4 consecutive rows n of each subtile (bf16),
+  // or this split's fp32 partial sums part[z][m][n..n+3]
+#pragma unroll
+  for (int f = 0; f < FR; ++f) {
+    const int64_t n = p0 + 16 * (FR * wave + f) + 4 * g;
+#pragma unroll
+    for (int b = 0; b < TB; ++b) {
+      const int64_t m = q0 + 16 * b + li;
+      if (m < mend && n < N) {
+        const f32x4 v = acc[f][b];
+        if (a.part) {
+          *reinterpret_cast<f32x4*>(a.part + ((int64_t)z * a.M + m) * N + n) = v;
+        } else {
+          *reinterpret_cast<u32x2*>(a.Y + m * N + n) =
+              u32x2{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+        }
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ int xcd_remap_e(int b, int total) {
+  const int n8 = total >> 3, rem = total & 7;
+  const int x = b & 7, i = b >> 3;
+  return x * n8 + min(x, rem) + i;
+}
+
+}  // namespace
+
+template <int FR, int TB, bool NODQ>
+__global__ __launch_bounds__(ET) void k_expert_fwd(ExpertArgs a, Nf4Tables tb) {
+  // Dynamic LDS only: the level table sits at address 0.
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+  build_rep_pair_table<ET>(reinterpret_cast<char*>(dyn), load_levels(tb), threadIdx.x);
+  constexpr int TQ = 16 * TB;
+  // Only the tiles that the groups have are dealt out over the XCDs.
+  const int most = a.ptiles * a.qtiles;
+  const int splits = static_cast<int>(gridDim.x) / most;
+  const int ntiles = a.ptiles * min(a.qtiles, group_tile_count(a.offsets, a.E, a.M, TQ));
+  const int work = ntiles * splits;
+  if (static_cast<int>(blockIdx.x) >= work) return;
+  const int lin = xcd_remap_e(blockIdx.x, work);
+  const int z = lin / ntiles, tile = lin - z * ntiles;
+  const int qt = tile / a.ptiles, pt = tile - qt * a.ptiles;
+  const GroupTile gt = group_tile(a.offsets, a.E, a.M, TQ, qt);
+  if (gt.e < 0) return;
+  const int64_t rows = gt.end - gt.row0;
+  constexpr int T1 = narrow1(TB), T2 = narrow2(TB);
+  if constexpr (T1 > 0) {
+    if (rows <= 16 * T1) {
+      expert_tile<FR, T1, NODQ>(a, dyn, gt.e, gt.row0, gt.end, pt, z);
+      return;
+    }
+  }
+  if constexpr (T2 > 0) {
+    if (rows <= 16 * T2) {
+      expert_tile<FR, T2, NODQ>(a, dyn, gt.e, gt.row0, gt.end, pt, z);
+      return;
+    }
+  }
+  expert_tile<FR, TB, NODQ>(a, dyn, gt.e, gt.row0, gt.end, pt, z);
+}
+
+namespace {
+
+template <int FR, int TB, bool NODQ>
+hipError_t launch_variant(const ExpertArgs& a, const Nf4Tables& tb, int splits,
+                          hipStream_t stream) {
+  constexpr int kLds = expert_lds<FR, TB>();
+  static const hipError_t attr =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(&k_expert_fwd<FR, TB, NODQ>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if (attr != hipSuccess) return attr;
+  hipLaunchKernelGGL((k_expert_fwd<FR, TB, NODQ>), dim3(a.ptiles * a.qtiles * splits), dim3(ET),
+                     kLds, stream, a, tb);
+  return hipGetLastError();
+}
+
+struct ExpertPlan {
+  int fr, tb, ptiles, qtiles;
+  GemmSplit sp;
+};
+
+ExpertPlan plan_expert_fwd(int64_t M, int E, int64_t N, int64_t K) {
+  ExpertPlan p;
+  const int64_t mean = (M + E - 1) / E;
+  p.tb = mean > 48 ? 12 : (mean > 8 ? 4 : 2);
+  p.qtiles = static_cast<int>(group_tile_bound(M, E, 16 * p.tb));
+  p.fr = 2;
+  p.ptiles = static_cast<int>((N + 255) / 256);
+  if (static_cast<int64_t>(p.ptiles) * p.qtiles < 256) {
+    p.fr = 1;
+    p.ptiles = static_cast<int>((N + 127) / 128);
+  }
+  p.sp = gemm_split(static_cast<int64_t>(p.ptiles) * p.qtiles, (K + 127) / 128);
+  return p;
+}
+
+}  // namespace
+
+GemmSplit grouped_fwd_split(int64_t M, int E, int64_t N, int64_t K) {
+  return plan_expert_fwd(M, E, N, K).sp;
+}
+
+hipError_t launch_grouped_fwd_gemm(const uint16_t* X, int64_t M, const int* offsets, int E,
+                                   const Nf4View& w, const float* T, const uint16_t* B, int r,
+                                   float s, uint16_t* Y, float* part, const Nf4Tables& tb,
+                                   hipStream_t stream) {
+  const int64_t N = w.N / E;
+  const ExpertPlan p = plan_expert_fwd(M, E, N, w.K);
+  if (p.sp.splits > 1 && !part) return hipErrorInvalidValue;
+  const ExpertArgs a{X,    M, offsets,   E, w.codes,  w.absmax_q, w.absmax_scale, N,
+                     w.K,  T, B,         r, s,        Y,          p.ptiles,       p.qtiles,
+                     p.sp.cps, p.sp.splits > 1 ? part : nullptr};
+  auto pick = [&](auto nodq) {
+    constexpr bool ND = decltype(nodq)::value;
+    if (p.fr == 2)
+      return p.tb == 12 ? launch_variant<2, 12, ND> : (p.tb == 4 ? launch_variant<2, 4, ND>
+                                                                 : launch_variant<2, 2, ND>);
+    return p.tb == 12 ? launch_variant<1, 12, ND> : (p.tb == 4 ? launch_variant<1, 4, ND>
+                                                               : launch_variant<1, 2, ND>);
+  };
+  auto launch = w.dq ? pick(std::false_type{}) : pick(std::true_type{});
+  prof_begin(0, stream);
+  hipError_t e = launch(a, tb, p.sp.splits, stream);
+  if (e == hipSuccess && p.sp.splits > 1)
+    e = launch_group_reduce(part, p.sp.splits, M, N, 1.f, offsets, E, nullptr, Y, stream);
+  prof_end(0, stream);
+  return e;
+}
+
+}  // namespace qnf4

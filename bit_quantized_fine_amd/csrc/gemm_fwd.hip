@@ -32,16 +32,9 @@
 // kFormNoDq reads one fp32 constant per block in place of the 8-bit constant
 // and its group's scale (4-bit codes without double quantization); the level
 // table is an argument (NF4, INT4 or FP4).
-//
-// kExperts instantiates it over token rows grouped by expert: W holds the
-// experts' weights one after the other, each workgroup finds its expert and
-// its rows from the offsets in device memory, and adds that expert's adapter.
-// With kQ = 64 a tile is 64 tokens: the four wave columns then split the 128
-// weight rows instead of the tokens.
 #include <type_traits>
 
 #include "device_common.hpp"
-#include "group_tiles.hpp"
 #include "kernels.hpp"
 
 namespace qnf4 {
@@ -49,27 +42,21 @@ namespace qnf4 {
 namespace {
 
 constexpr int GP = 128;          // weight rows per workgroup
+constexpr int GQ = 256;          // tokens per workgroup
 constexpr int GK = 64;           // reduction elements per chunk (one block per row)
-constexpr int GWC = 4;           // wave columns: kQ / 64 token groups x row groups
+constexpr int GWT = 4;           // token groups
 constexpr int GKS = 2;           // waves splitting a chunk's two 32-k steps
-constexpr int GW = GWC * GKS;    // waves
+constexpr int GW = GWT * GKS;    // waves
 constexpr int GT = 64 * GW;      // threads
-constexpr int GTB = 4;           // 16-token subtiles per wave
+constexpr int GTA = GP / 16;     // 16-row subtiles (8)
+constexpr int GTB = GQ / GWT / 16;   // 16-token subtiles per wave (4)
 constexpr int BTS = 64 + 8;     // LDS row stride of the B^T tile
 constexpr int kAFrag = 64 * 8;   // bf16 elements of one 16 x 32 operand (1 KB)
-constexpr int kATile = GP / 16 * GKS * kAFrag;   // one dequantized 128 x 64 tile (16 KB)
+constexpr int kATile = GTA * GKS * kAFrag;   // one dequantized 128 x 64 tile (16 KB)
 constexpr int XTS = GK;          // LDS row stride of the X tile (128 B, XOR-swizzled)
-
-// A tile of kQ tokens (256 or 64).
-template <int kQ>
-struct FwdTile {
-  static constexpr int WT = kQ / 64;             // token groups
-  static constexpr int WR = GWC / WT;            // row groups
-  static constexpr int TA = GP / 16 / WR;        // 16-row subtiles per wave (8 or 2)
-  static constexpr int XTILE = kQ * XTS;         // elements of one X tile buffer
-  static constexpr int XPT = kQ * GK / 8 / GT;   // 16-byte X pieces a thread stages per chunk
-  static constexpr int LDS = kRepTabBytes + 2 * kATile * 2 + 2 * XTILE * 2;
-};
+constexpr int kXTile = GQ * XTS;   // elements of one X tile buffer
+constexpr int XPT = GQ * GK / 8 / GT;   // 16-byte X pieces a thread stages per chunk (4)
+constexpr int kFwdLds = kRepTabBytes + 2 * kATile * 2 + 2 * kXTile * 2;
 
 __device__ __forceinline__ int xcd_remap(int b, int total) {
   const int n8 = total >> 3, rem = total & 7;
@@ -79,17 +66,14 @@ __device__ __forceinline__ int xcd_remap(int b, int total) {
 
 }  // namespace
 
-template <int kForm, int kQ, bool kExperts>
+template <int kForm>
 __global__ __launch_bounds__(GT) void k_fwd_gemm(
     const uint16_t* __restrict__ X, int64_t M, const uint16_t* __restrict__ Wd,
     const uint8_t* __restrict__ codes,
     const uint8_t* __restrict__ absmax_q, const float* __restrict__ absmax_scale,
     int64_t N, int64_t K, const float* __restrict__ T, const uint16_t* __restrict__ Bl,
     int r, float s, uint16_t* __restrict__ Y, int ptiles, int qtiles, int cps,
-    float* __restrict__ part, Nf4Tables tb, int ldt, int seg_rows,
-    const int* __restrict__ offsets, int E) {
-  using Tile = FwdTile<kQ>;
-  constexpr int GQ = kQ, GTA = Tile::TA, kXTile = Tile::XTILE, XPT = Tile::XPT;
+    float* __restrict__ part, Nf4Tables tb, int ldt, int seg_rows) {
   // Dynamic LDS only (so the table sits at address 0): the replicated level
   // table, then two A tile buffers; after the main loop the same bytes hold
   // the accumulator exchange and the B^T tile of the LoRA update.
@@ -101,44 +85,23 @@ __global__ __launch_bounds__(GT) void k_fwd_gemm(
   const int tid = threadIdx.x;
   const int wave = wave_id(), lane = tid & 63;
   const int li = lane & 15, g = lane >> 4;
-  const int wc = wave % GWC, ks = wave / GWC;
-  const int wt = wc % Tile::WT, wr = wc / Tile::WT;
+  const int wt = wave % GWT, ks = wave / GWT;
   if constexpr (kForm != kFormDense) build_rep_pair_table<GT>(tab, load_levels(tb), tid);
 
   // With a split reduction (few tiles), workgroup b takes chunks
   // [z cps, (z + 1) cps) of its tile and writes fp32 partial sums.
-  // Grouped rows: only the tiles that the groups have are dealt out over the
-  // XCDs (the grid is sized for the most they could have).
-  int ntiles = ptiles * qtiles, work = static_cast<int>(gridDim.x);
-  if constexpr (kExperts) {
-    const int splits = work / ntiles;
-    ntiles = ptiles * min(qtiles, group_tile_count(offsets, E, M, GQ));
-    work = min(work, ntiles * splits);
-    if (static_cast<int>(blockIdx.x) >= work) return;
-  }
-  const int lin = xcd_remap(blockIdx.x, work);
+  const int ntiles = ptiles * qtiles;
+  const int lin = xcd_remap(blockIdx.x, static_cast<int>(gridDim.x));
   const int z = lin / ntiles, tile = lin - z * ntiles;
   const int qt = tile / ptiles, pt = tile - qt * ptiles;
-  const int64_t p0 = (int64_t)pt * GP;
-  int64_t q0 = (int64_t)qt * GQ, mend = M;   // the tile's tokens: q0 .. mend - 1 at most
-  int64_t n0 = 0;                            // first row of W of the tile's expert
-  if constexpr (kExperts) {
-    const GroupTile gt = group_tile(offsets, E, M, GQ, qt);
-    if (gt.e < 0) return;
-    q0 = gt.row0;
-    mend = gt.end;
-    n0 = (int64_t)gt.e * N;
-    Bl += (int64_t)gt.e * r * N;
-  }
-  const int64_t NW = kExperts ? N * E : N;     // rows of W
+  const int64_t p0 = (int64_t)pt * GP, q0 = (int64_t)qt * GQ;
   const int c0 = z * cps;
   const int nchunks = min(static_cast<int>(K / GK), c0 + cps);   // end of this split's chunks
   const int KB = static_cast<int>(K / kBlock);
 
-  // Buffer descriptors: rows past W and tokens past the tile read as zero
-  // (rows n >= N of an expert are the next one's, and are not stored).
-  const uint32_t nb = static_cast<uint32_t>(NW * K / kBlock);
-  const BufRes rc = make_bufres(codes, static_cast<uint32_t>(NW * K / 2));
+  // Buffer descriptors: rows n >= N and tokens m >= M read as zero.
+  const uint32_t nb = static_cast<uint32_t>(N * K / kBlock);
+  const BufRes rc = make_bufres(codes, static_cast<uint32_t>(N * K / 2));
   const BufRes re = make_bufres(absmax_q, nb);
   // second-level scales, or one fp32 constant per block (kFormNoDq)
   const BufRes rd = make_bufres(
@@ -149,14 +112,14 @@ __global__ __launch_bounds__(GT) void k_fwd_gemm(
   // than 2^31 bytes for K <= 2^22).  (A plain conditional, not min(): the
   // 64-bit min is opaque to the compiler's uniformity analysis and would put
   // the descriptor in vector registers.)
-  const int64_t tile_rows = mend - q0 < GQ ? mend - q0 : GQ;
+  const int64_t tile_rows = M - q0 < GQ ? M - q0 : GQ;
   const BufRes rx = make_bufres(X + q0 * K, static_cast<uint32_t>(tile_rows * K * 2));
 
   // Dequantization role: row 16 wave + li of the tile, codes 32 sd + 16 h ..
   // +15 of the chunk (sd = lane / 32, h = (lane / 16) % 2): pieces 2 h and
   // 2 h + 1 of the operand (row subtile wave, k half sd).
   const int sd = lane >> 5, h = (lane >> 4) & 1;
-  const int64_t dn = n0 + p0 + 16 * wave + li;
+  const int64_t dn = p0 + 16 * wave + li;
   const uint32_t dcode = static_cast<uint32_t>(dn * (K / 2)) + 16u * sd + 8u * h;   // + 32 c
   const uint32_t dblk = static_cast<uint32_t>(dn * KB);                           // + c
   // kFormDense: the same 16 weights as bf16, byte offset (+ 128 c)
@@ -240,7 +203,7 @@ __global__ __launch_bounds__(GT) void k_fwd_gemm(
 
   // A operand (row subtile a, k half ks): one contiguous 1 KB read; B
   // operand: token 64 wt + 16 b + li, piece g + 4 ks (swizzle (li / 2) % 8)
-  const uint16_t* const apiece = As + (2 * GTA * wr + ks) * kAFrag + lane * 8;
+  const uint16_t* const apiece = As + ks * kAFrag + lane * 8;
   const uint16_t* const xpiece = Xs + (64 * wt + li) * XTS + 8 * ((g + 4 * ks) ^ (li >> 1));
   // Operands of one 32-k step are read into registers first; the MFMAs then
   // touch no memory, so the compiler can interleave them with the staging
@@ -302,7 +265,7 @@ __global__ __launch_bounds__(GT) void k_fwd_gemm(
     // T columns of this tile's segment: rows [j seg_rows, (j + 1) seg_rows)
     // of W belong to adapter j, whose T occupies columns j r .. of T (row
     // stride ldt); a single segment is the plain layer.
-    const float* Tt = kExperts ? T : T + (p0 / seg_rows) * r;
+    const float* Tt = T + (p0 / seg_rows) * r;
     uint16_t* bt = As;
     for (int j0 = 0; j0 < r; j0 += 64) {
       // this wave's s.T operands, loaded before the B^T staging so that the
@@ -313,7 +276,7 @@ __global__ __launch_bounds__(GT) void k_fwd_gemm(
 #pragma unroll
       for (int b = 0; b < GTB; ++b) {
         const int64_t m = q0 + 64 * wt + 16 * b + li;
-        const bool ok = m < mend && jt < r;
+        const bool ok = m < M && jt < r;
         tok[b] = ok;
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
         traw[b][0] = ok ? *reinterpret_cast<const f32x4*>(Tt + m * ldt + jt) : zero;
@@ -355,8 +318,7 @@ __global__ __launch_bounds__(GT) void k_fwd_gemm(
 #pragma unroll
           for (int a = 0; a < GTA; ++a) {
             const u32x4 af =
-                *reinterpret_cast<const u32x4*>(bt + (16 * (wr * GTA + a) + li) * BTS + 32 * i +
-                                                8 * g);
+                *reinterpret_cast<const u32x4*>(bt + (16 * a + li) * BTS + 32 * i + 8 * g);
 #pragma unroll
             for (int b = 0; b < GTB; ++b) {
               acc[a][b] = mfma16(af, th[b], acc[a][b]);
@@ -369,10 +331,10 @@ __global__ __launch_bounds__(GT) void k_fwd_gemm(
     }
   }
 
-  // Add the two k halves: wave ks keeps half of its row subtiles and
-  // receives them from its partner (the other ks, same wave column) through
+  // Add the two k halves: wave ks keeps row subtiles 4 ks .. 4 ks + 3 and
+  // receives them from its partner (the other ks, same token group) through
   // LDS, in one round; each half then stores its own row subtiles.
-  f32x4* xch = reinterpret_cast<f32x4*>(dyn);   // [2][GWC][GTA/2][GTB][64]
+  f32x4* xch = reinterpret_cast<f32x4*>(dyn);   // [2][GWT][GTA/2][GTB][64]
   {
     // (compile-time accumulator indices on both sides of a scalar branch)
     auto hand = [&](auto kc) {
@@ -381,7 +343,7 @@ __global__ __launch_bounds__(GT) void k_fwd_gemm(
       for (int a = 0; a < GTA / 2; ++a)
 #pragma unroll
         for (int b = 0; b < GTB; ++b)
-          xch[(((GIVE * GWC + wc) * (GTA / 2) + a) * GTB + b) * 64 + lane] =
+          xch[(((GIVE * GWT + wt) * (GTA / 2) + a) * GTB + b) * 64 + lane] =
               acc[GIVE * (GTA / 2) + a][b];
     };
     auto take = [&](auto kc) {
@@ -391,7 +353,7 @@ __global__ __launch_bounds__(GT) void k_fwd_gemm(
 #pragma unroll
         for (int b = 0; b < GTB; ++b)
           acc[K0 * (GTA / 2) + a][b] +=
-              xch[(((K0 * GWC + wc) * (GTA / 2) + a) * GTB + b) * 64 + lane];
+              xch[(((K0 * GWT + wt) * (GTA / 2) + a) * GTB + b) * 64 + lane];
     };
     if (ks == 0) hand(std::integral_constant<int, 0>{}); else hand(std::integral_constant<int, 1>{});
     __syncthreads();
@@ -405,11 +367,11 @@ __global__ __launch_bounds__(GT) void k_fwd_gemm(
 #pragma unroll
     for (int a0 = 0; a0 < GTA / 2; ++a0) {
       const int a = K0 * (GTA / 2) + a0;
-      const int64_t n = p0 + 16 * (wr * GTA + a) + 4 * g;
+      const int64_t n = p0 + 16 * a + 4 * g;
 #pragma unroll
       for (int b = 0; b < GTB; ++b) {
         const int64_t m = q0 + 64 * wt + 16 * b + li;
-        if (m < mend && n < N) {
+        if (m < M && n < N) {
           const f32x4 v = acc[a][b];
           if (part) {
             *reinterpret_cast<f32x4*>(part + ((int64_t)z * M + m) * N + n) = v;
@@ -424,77 +386,38 @@ __global__ __launch_bounds__(GT) void k_fwd_gemm(
   if (ks == 0) store(std::integral_constant<int, 0>{}); else store(std::integral_constant<int, 1>{});
 }
 
-namespace {
-
-constexpr int kPlainQ = 256;   // tokens a tile without groups
-
-template <int kForm, int kQ, bool kExperts>
-hipError_t launch_fwd_tiles(const uint16_t* X, int64_t M, const Nf4View& w, int64_t N,
-                            const float* T, const uint16_t* B, int r, float s, uint16_t* Y,
-                            float* part, const Nf4Tables& tb, hipStream_t stream, int ptiles,
-                            int qtiles, const GemmSplit& sp, int ldt, int seg_rows,
-                            const int* offsets, int E) {
-  constexpr int kLds = FwdTile<kQ>::LDS;
-  static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&k_fwd_gemm<kForm, kQ, kExperts>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-  if (attr != hipSuccess) return attr;
-  if (sp.splits > 1 && !part) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((k_fwd_gemm<kForm, kQ, kExperts>), dim3(ptiles * qtiles * sp.splits), dim3(GT),
-                     kLds, stream, X, M, w.dense, w.codes, w.absmax_q, w.absmax_scale, N, w.K, T,
-                     B, r, s, Y, ptiles, qtiles, sp.cps, sp.splits > 1 ? part : nullptr, tb, ldt,
-                     seg_rows, offsets, E);
-  return hipGetLastError();
-}
-
-}  // namespace
-
 GemmSplit fwd_gemm_split(int64_t M, int64_t N, int64_t K) {
-  return gemm_split((N + GP - 1) / GP * ((M + kPlainQ - 1) / kPlainQ), K / GK);
+  return gemm_split((N + GP - 1) / GP * ((M + GQ - 1) / GQ), K / GK);
 }
 
 hipError_t launch_fwd_gemm(const uint16_t* X, int64_t M, const Nf4View& w,
                             const float* T, const uint16_t* B, int r, float s,
                             uint16_t* Y, float* part, const Nf4Tables& tb, hipStream_t stream,
                             int ldt, int64_t seg_rows) {
+  static const hipError_t attr[3] = {
+      hipFuncSetAttribute(reinterpret_cast<const void*>(&k_fwd_gemm<kFormDq>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, kFwdLds),
+      hipFuncSetAttribute(reinterpret_cast<const void*>(&k_fwd_gemm<kFormNoDq>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, kFwdLds),
+      hipFuncSetAttribute(reinterpret_cast<const void*>(&k_fwd_gemm<kFormDense>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, kFwdLds)};
+  const int form = w.dense ? kFormDense : (w.dq ? kFormDq : kFormNoDq);
+  if (attr[form] != hipSuccess) return attr[form];
+  decltype(&k_fwd_gemm<kFormDq>) kern =
+      form == kFormDense ? k_fwd_gemm<kFormDense> : (form == kFormNoDq ? k_fwd_gemm<kFormNoDq> : k_fwd_gemm<kFormDq>);
   const int ptiles = static_cast<int>((w.N + GP - 1) / GP);
-  const int qtiles = static_cast<int>((M + kPlainQ - 1) / kPlainQ);
+  const int qtiles = static_cast<int>((M + GQ - 1) / GQ);
   const GemmSplit sp = fwd_gemm_split(M, w.N, w.K);
-  auto launch = w.dense ? launch_fwd_tiles<kFormDense, kPlainQ, false>
-                        : (w.dq ? launch_fwd_tiles<kFormDq, kPlainQ, false>
-                                : launch_fwd_tiles<kFormNoDq, kPlainQ, false>);
+  if (sp.splits > 1 && !part) return hipErrorInvalidValue;
   prof_begin(0, stream);
-  hipError_t e = launch(
-      X, M, w, w.N, T, B, r, s, Y, part, tb, stream, ptiles, qtiles, sp, ldt > 0 ? ldt : r,
-      static_cast<int>(seg_rows > 0 ? seg_rows : w.N), nullptr, 0);
+  hipLaunchKernelGGL(kern,
+                     dim3(ptiles * qtiles * sp.splits), dim3(GT), kFwdLds, stream, X, M, w.dense,
+                     w.codes, w.absmax_q, w.absmax_scale, w.N, w.K, T, B, r, s, Y, ptiles,
+                     qtiles, sp.cps, sp.splits > 1 ? part : nullptr, tb, ldt > 0 ? ldt : r,
+                     static_cast<int>(seg_rows > 0 ? seg_rows : w.N));
+  hipError_t e = hipGetLastError();
   if (e == hipSuccess && sp.splits > 1)
     e = launch_split_reduce_bf16(part, sp.splits, M * w.N, Y, stream);
-  prof_end(0, stream);
-  return e;
-}
-
-GemmSplit grouped_fwd_split(int64_t M, int E, int64_t N, int64_t K) {
-  return gemm_split((N + GP - 1) / GP * group_tile_bound(M, E, grouped_tile(M, E)), K / GK);
-}
-
-hipError_t launch_grouped_fwd_gemm(const uint16_t* X, int64_t M, const int* offsets, int E,
-                                   const Nf4View& w, const float* T, const uint16_t* B, int r,
-                                   float s, uint16_t* Y, float* part, const Nf4Tables& tb,
-                                   hipStream_t stream) {
-  const int64_t N = w.N / E;
-  const int q = grouped_tile(M, E);
-  const int ptiles = static_cast<int>((N + GP - 1) / GP);
-  const int qtiles = static_cast<int>(group_tile_bound(M, E, q));
-  const GemmSplit sp = grouped_fwd_split(M, E, N, w.K);
-  auto launch = q == 64 ? (w.dq ? launch_fwd_tiles<kFormDq, 64, true>
-                                : launch_fwd_tiles<kFormNoDq, 64, true>)
-                        : (w.dq ? launch_fwd_tiles<kFormDq, 256, true>
-                                : launch_fwd_tiles<kFormNoDq, 256, true>);
-  prof_begin(0, stream);
-  hipError_t e = launch(X, M, w, N, T, B, r, s, Y, part, tb, stream, ptiles, qtiles, sp, r, 0,
-                        offsets, E);
-  if (e == hipSuccess && sp.splits > 1)
-    e = launch_group_reduce(part, sp.splits, M, N, 1.f, offsets, E, nullptr, Y, stream);
   prof_end(0, stream);
   return e;
 }

@@ -11,10 +11,13 @@
 
 namespace qnf4 {
 
+// Wave-uniform; rows fit 32 bits (M < 2^31).  The values come out of
+// readfirstlane, so that the compiler sees them as uniform and keeps the buffer
+// descriptors built from them in scalar registers.
 struct GroupTile {
-  int e;         // expert, or -1: past the last tile
-  int64_t row0;  // first row of the tile
-  int64_t end;   // end of the expert's rows
+  int e;      // expert, or -1: past the last tile
+  int row0;   // first row of the tile
+  int end;    // end of the expert's rows
 };
 
 __device__ __forceinline__ void group_range(const int* offsets, int64_t M, int e, int64_t& lo,
@@ -45,8 +48,7 @@ __device__ __forceinline__ int group_tile_count(const int* offsets, int E, int64
 __device__ __forceinline__ GroupTile group_tile(const int* offsets, int E, int64_t M, int tq,
                                                 int slot) {
   const int lane = threadIdx.x & 63;
-  GroupTile t{-1, 0, 0};
-  int base = 0;
+  int e = -1, row0 = 0, end = 0, base = 0;
   for (int e0 = 0; e0 < E; e0 += 64) {
     int64_t lo = 0, hi = 0;
     if (e0 + lane < E) group_range(offsets, M, e0 + lane, lo, hi);
@@ -61,16 +63,15 @@ __device__ __forceinline__ GroupTile group_tile(const int* offsets, int E, int64
     if (past != 0) {
       const int l = __builtin_ctzll(past);
       const int first = base + __builtin_amdgcn_readlane(incl - n, l);
-      const uint32_t r0 = __builtin_amdgcn_readlane(static_cast<int>(lo), l);
-      const uint32_t r1 = __builtin_amdgcn_readlane(static_cast<int>(hi), l);
-      t.e = e0 + l;
-      t.row0 = static_cast<int64_t>(r0) + static_cast<int64_t>(slot - first) * tq;
-      t.end = r1;
-      return t;
+      e = e0 + l;
+      row0 = __builtin_amdgcn_readlane(static_cast<int>(lo), l) + (slot - first) * tq;
+      end = __builtin_amdgcn_readlane(static_cast<int>(hi), l);
+      break;
     }
     base += __builtin_amdgcn_readlane(incl, 63);
   }
-  return t;
+  return GroupTile{__builtin_amdgcn_readfirstlane(e), __builtin_amdgcn_readfirstlane(row0),
+                   __builtin_amdgcn_readfirstlane(end)};
 }
 
 // Most tiles of tq rows that M rows of E experts can make.
