@@ -592,44 +592,96 @@ def qlora_q4_linear_bwd(dY, X, w: Q4Weight, A=None, B=None, s: float = 1.0, T=No
                 need_dx, dX, dA, dB, workspace)
 
 
-def _as_q4(w) -> Q4Weight:
-    """An NF4Weight as the Q4Weight it is."""
-    if isinstance(w, NF4Weight):
-        return Q4Weight(w.codes, w.absmax_q, w.absmax_scale, w.N, w.K, "nf4", True)
-    return w
+# ---------------------------------------------------------------------------
+# Dropout, layers grouped by expert and the exchange around them.  The same
+# checks as above; as their smallest calls run for a few microseconds on the
+# GPU, they are written to cost little on the host: one comparison a property,
+# names and messages only where something is wrong.
+# ---------------------------------------------------------------------------
+
+def _is(t, name, shape, dtype):
+    """_need for a torch.Size or tuple of ints."""
+    if t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _need(t, name, shape, dtype)
+
+
+def _maybe(t, name, shape, dtype):
+    if t is not None:
+        _is(t, name, shape, dtype)
+
+
+def _one_gpu(names, *tensors):
+    """The GPU of all tensors given (None where an argument is absent); names
+    holds theirs, separated by spaces."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            if t.device != dev or dev.type != "cuda":
+                _on_gpu(zip(names.split(), tensors))
+    return dev
 
 
 def _call(fn, dev, *args):
     """Call a C entry point on dev's current stream, with dev current."""
     import torch
-    stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
-    if dev.index == torch.cuda.current_device():
-        _check(fn, getattr(lib(), fn)(*args, stream))
+    f = getattr(_lib or lib(), fn)
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    if dev.index == torch._C._cuda_getDevice():
+        st = f(*args, stream)
     else:
         with torch.cuda.device(dev):
-            _check(fn, getattr(lib(), fn)(*args, stream))
+            st = f(*args, stream)
+    if st != QLORA_OK:
+        raise QloraError(fn, st)
+
+
+def _at(t):
+    """A tensor's address for a ctypes pointer argument."""
+    return None if t is None else t.data_ptr()
+
+
+def _q4(w):
+    """The C view of an NF4Weight or Q4Weight, and its checked tensors."""
+    import torch
+    n = w.N * w.K
+    nb = n // 64
+    book, dq = (w.codebook, w.double_quant) if isinstance(w, Q4Weight) else ("nf4", True)
+    cb = CODEBOOKS[book] if book in CODEBOOKS else _codebook_id(book)
+    _is(w.codes, "w.codes", (n // 2,), torch.uint8)
+    if dq:
+        _is(w.absmax_q, "w.absmax_q", (nb,), torch.uint8)
+        _is(w.absmax_scale, "w.absmax_scale", ((nb + 255) // 256,), torch.float32)
+        q = w.absmax_q
+    else:
+        _is(w.absmax_scale, "w.absmax_scale", (nb,), torch.float32)
+        q = None
+    return (_Q4Weight(w.codes.data_ptr(), _at(q), w.absmax_scale.data_ptr(), w.N, w.K, cb,
+                      1 if dq else 0), w.codes, q, w.absmax_scale)
 
 
 def _drop(p, state):
-    """The C descriptor of dropout with probability p, and state's (name,
-    tensor) pairs.  state is an int64 [2] tensor {seed, offset} on the GPU (the
-    64-bit words as they are); it may be None when p is 0."""
+    """The C descriptor of dropout with probability p; state is an int64 [2]
+    tensor {seed, offset} on the GPU (the 64-bit words as they are) and may be
+    None when p is 0."""
     import torch
-    if state is not None:
-        _need(state, "state", (2,), torch.int64)
-    elif p != 0:
-        raise ValueError("state is required for p > 0")
-    return _Dropout(state.data_ptr() if state is not None else None, float(p)), [("state", state)]
+    if state is None:
+        if p != 0:
+            raise ValueError("state is required for p > 0")
+        return _Dropout(None, p)
+    _is(state, "state", (2,), torch.int64)
+    return _Dropout(state.data_ptr(), p)
 
 
 def _scratch(workspace, need, dev):
     """The caller's workspace if it is large enough, else one of need bytes."""
     import torch
     if workspace is not None:
-        _need(workspace, "workspace", (workspace.numel(),), torch.uint8)
-    if workspace is None or workspace.numel() < need:
-        return _ws(need, dev)
-    return workspace
+        _is(workspace, "workspace", (workspace.numel(),), torch.uint8)
+        if workspace.numel() >= need:
+            return workspace
+    return _ws(need, dev)
 
 
 def qlora_dropout(x, p: float, state, out=None):
@@ -638,15 +690,23 @@ def qlora_dropout(x, p: float, state, out=None):
     function of state (int64 [2] on the GPU: seed, offset) and the element's
     position.  The backward is the same call on the gradient; out may be x."""
     import torch
-    _need(x, "x", tuple(x.shape), torch.bfloat16)
-    if out is not None:
-        _need(out, "out", tuple(x.shape), torch.bfloat16)
-    d, named = _drop(p, state)
-    _on_gpu([("x", x), ("out", out)] + named)
+    _is(x, "x", x.shape, torch.bfloat16)
+    _maybe(out, "out", x.shape, torch.bfloat16)
+    d = _drop(p, state)
+    dev = _one_gpu("x state out", x, state, out)
     if out is None:
         out = torch.empty_like(x)
-    _call("qlora_dropout_apply", x.device, _ptr(x), x.numel(), ctypes.byref(d), _ptr(out))
+    _call("qlora_dropout_apply", dev, x.data_ptr(), x.numel(), ctypes.byref(d), out.data_ptr())
     return out
+
+
+def _rows(X, K):
+    import torch
+    if X.dim() != 2:
+        raise ValueError("X must be [M, K]")
+    M = X.shape[0]
+    _is(X, "X", (M, K), torch.bfloat16)
+    return M
 
 
 def qlora_linear_dropout_fwd(X, w, A=None, B=None, s: float = 1.0, p: float = 0.0, state=None,
@@ -655,27 +715,24 @@ def qlora_linear_dropout_fwd(X, w, A=None, B=None, s: float = 1.0, p: float = 0.
     with T = drop(X) . A.  w is an NF4Weight or a Q4Weight.  Returns (Y bf16
     [M,N], T fp32 [M,r])."""
     import torch
-    M = _x_rows(X, w.K)
-    w = _as_q4(w)
-    wt = _check_q4_weight(w)
+    M = _rows(X, w.K)
+    cw, *wt = _q4(w)
     r = _check_adapters(A, B, w)
-    d, named = _drop(p, state)
-    if Y is not None:
-        _need(Y, "Y", (M, w.N), torch.bfloat16)
-    if T is not None and r > 0:
-        _need(T, "T", (M, r), torch.float32)
-    _on_gpu([("X", X)] + wt + named + [("A", A), ("B", B), ("Y", Y), ("T", T if r > 0 else None),
-                                       ("workspace", workspace)])
-    dev = X.device
+    d = _drop(p, state)
+    _maybe(Y, "Y", (M, w.N), torch.bfloat16)
+    if r == 0:
+        T = None
+    _maybe(T, "T", (M, r), torch.float32)
+    need = lib().qlora_linear_dropout_fwd_workspace_bytes(M, w.N, w.K, r)
+    dev = _one_gpu("X w.codes w.absmax_q w.absmax_scale A B state Y T workspace", X, *wt, A, B,
+                   state, Y, T, workspace)
+    workspace = _scratch(workspace, need, dev)
     if Y is None:
         Y = torch.empty((M, w.N), dtype=torch.bfloat16, device=dev)
     if T is None and r > 0:
         T = torch.empty((M, r), dtype=torch.float32, device=dev)
-    need = lib().qlora_linear_dropout_fwd_workspace_bytes(M, w.N, w.K, r)
-    workspace = _scratch(workspace, need, dev)
-    cw = w._c()
-    _call("qlora_linear_dropout_fwd", dev, _ptr(X), M, ctypes.byref(cw), _ptr(A), _ptr(B), r,
-          float(s), ctypes.byref(d), _ptr(Y), _ptr(T), _ptr(workspace), need)
+    _call("qlora_linear_dropout_fwd", dev, X.data_ptr(), M, ctypes.byref(cw), _at(A), _at(B), r, s,
+          ctypes.byref(d), Y.data_ptr(), _at(T), _at(workspace), need)
     return Y, T
 
 
@@ -686,51 +743,54 @@ def qlora_linear_dropout_bwd(dY, X, w, A=None, B=None, s: float = 1.0, p: float 
     (dX bf16 [M,K] or None, dA bf16 [K,r], dB bf16 [r,N]); T None recomputes
     it."""
     import torch
-    M = _x_rows(X, w.K)
-    w = _as_q4(w)
-    wt = _check_q4_weight(w)
-    _need(dY, "dY", (M, w.N), torch.bfloat16)
+    M = _rows(X, w.K)
+    cw, *wt = _q4(w)
+    _is(dY, "dY", (M, w.N), torch.bfloat16)
     r = _check_adapters(A, B, w)
-    d, named = _drop(p, state)
-    if T is not None and r > 0:
-        _need(T, "T", (M, r), torch.float32)
-    if need_dx and dX is not None:
-        _need(dX, "dX", (M, w.K), torch.bfloat16)
-    if r > 0 and dA is not None:
-        _need(dA, "dA", (w.K, r), torch.bfloat16)
-    if r > 0 and dB is not None:
-        _need(dB, "dB", (r, w.N), torch.bfloat16)
-    _on_gpu([("X", X), ("dY", dY)] + wt + named +
-            [("A", A), ("B", B), ("T", T if r > 0 else None), ("dX", dX if need_dx else None),
-             ("dA", dA if r > 0 else None), ("dB", dB if r > 0 else None),
-             ("workspace", workspace)])
-    dev = X.device
-    if need_dx and dX is None:
-        dX = torch.empty((M, w.K), dtype=torch.bfloat16, device=dev)
-    if r > 0 and dA is None:
-        dA = torch.empty((w.K, r), dtype=torch.bfloat16, device=dev)
-    if r > 0 and dB is None:
-        dB = torch.empty((r, w.N), dtype=torch.bfloat16, device=dev)
-    need = lib().qlora_linear_dropout_bwd_workspace_bytes(M, w.N, w.K, r)
-    workspace = _scratch(workspace, need, dev)
-    cw = w._c()
-    _call("qlora_linear_dropout_bwd", dev, _ptr(dY), _ptr(X), M, ctypes.byref(cw), _ptr(A),
-          _ptr(B), r, float(s), ctypes.byref(d), _ptr(T if r > 0 else None),
-          _ptr(dX if need_dx else None), _ptr(dA if r > 0 else None),
-          _ptr(dB if r > 0 else None), _ptr(workspace), need)
-    return (dX if need_dx else None), dA, dB
+    d = _drop(p, state)
+    return _grads("qlora_linear_dropout_bwd", (), dY, X, M, w.N, w.K, cw, wt, A, B, r, s, d, state,
+                  T, need_dx, dX, dA, dB, (w.K, r), (r, w.N), workspace,
+                  lib().qlora_linear_dropout_bwd_workspace_bytes(M, w.N, w.K, r))
 
 
-def _grouped(X, offsets, w, E, A, B):
-    """Checks shared by the grouped calls: (M, N, r, w, named tensors)."""
+def _grads(fn, groups, dY, X, M, N, K, cw, wt, A, B, r, s, d, state, T, need_dx, dX, dA, dB,
+           shape_a, shape_b, workspace, need):
+    """The rest of a backward call: outputs, workspace, marshalling.  groups is
+    () or (offsets, E)."""
     import torch
-    M = _x_rows(X, w.K)
-    w = _as_q4(w)
-    named = [("X", X)] + _check_q4_weight(w)
+    if r == 0:
+        T = dA = dB = None
+    if not need_dx:
+        dX = None
+    _maybe(T, "T", (M, r), torch.float32)
+    _maybe(dX, "dX", (M, K), torch.bfloat16)
+    _maybe(dA, "dA", shape_a, torch.bfloat16)
+    _maybe(dB, "dB", shape_b, torch.bfloat16)
+    dev = _one_gpu("X dY w.codes w.absmax_q w.absmax_scale offsets A B state T dX dA dB workspace",
+                   X, dY, *wt, groups[0] if groups else None, A, B, state, T, dX, dA, dB,
+                   workspace)
+    workspace = _scratch(workspace, need, dev)
+    if need_dx and dX is None:
+        dX = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    if r > 0 and dA is None:
+        dA = torch.empty(shape_a, dtype=torch.bfloat16, device=dev)
+    if r > 0 and dB is None:
+        dB = torch.empty(shape_b, dtype=torch.bfloat16, device=dev)
+    where = (groups[0].data_ptr(), groups[1]) if groups else ()
+    _call(fn, dev, dY.data_ptr(), X.data_ptr(), M, *where, ctypes.byref(cw), _at(A), _at(B), r, s,
+          ctypes.byref(d), _at(T), _at(dX), _at(dA), _at(dB), _at(workspace), need)
+    return dX, dA, dB
+
+
+def _experts(X, offsets, w, E, A, B):
+    """Checks shared by the grouped calls: (M, N, r, C view, weight tensors)."""
+    import torch
+    M = _rows(X, w.K)
+    cw, *wt = _q4(w)
     if E < 1 or w.N % E:
         raise ValueError(f"w.N = {w.N} is not a multiple of E = {E}")
     N = w.N // E
-    _need(offsets, "offsets", (E + 1,), torch.int32)
+    _is(offsets, "offsets", (E + 1,), torch.int32)
     if A is None or B is None:
         if A is not None or B is not None:
             raise ValueError("A and B go together (both None selects r = 0)")
@@ -739,9 +799,9 @@ def _grouped(X, offsets, w, E, A, B):
         if A.dim() != 3:
             raise ValueError("A must be [E, K, r]")
         r = A.shape[2]
-        _need(A, "A", (E, w.K, r), torch.bfloat16)
-        _need(B, "B", (E, r, N), torch.bfloat16)
-    return M, N, r, w, named + [("offsets", offsets), ("A", A), ("B", B)]
+        _is(A, "A", (E, w.K, r), torch.bfloat16)
+        _is(B, "B", (E, r, N), torch.bfloat16)
+    return M, N, r, cw, wt
 
 
 def qlora_grouped_fwd(X, offsets, w, E: int, A=None, B=None, s: float = 1.0, p: float = 0.0,
@@ -752,23 +812,22 @@ def qlora_grouped_fwd(X, offsets, w, E: int, A=None, B=None, s: float = 1.0, p: 
     qlora_linear_dropout_fwd.  offsets is int32 [E+1] on the GPU.  Returns (Y
     bf16 [M,N], T fp32 [M,r]); rows outside all groups are left as they were."""
     import torch
-    M, N, r, w, named = _grouped(X, offsets, w, E, A, B)
-    d, dn = _drop(p, state)
-    if Y is not None:
-        _need(Y, "Y", (M, N), torch.bfloat16)
-    if T is not None and r > 0:
-        _need(T, "T", (M, r), torch.float32)
-    _on_gpu(named + dn + [("Y", Y), ("T", T if r > 0 else None), ("workspace", workspace)])
-    dev = X.device
+    M, N, r, cw, wt = _experts(X, offsets, w, E, A, B)
+    d = _drop(p, state)
+    _maybe(Y, "Y", (M, N), torch.bfloat16)
+    if r == 0:
+        T = None
+    _maybe(T, "T", (M, r), torch.float32)
+    need = lib().qlora_grouped_fwd_workspace_bytes(M, E, N, w.K, r)
+    dev = _one_gpu("X w.codes w.absmax_q w.absmax_scale offsets A B state Y T workspace", X, *wt,
+                   offsets, A, B, state, Y, T, workspace)
+    workspace = _scratch(workspace, need, dev)
     if Y is None:
         Y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     if T is None and r > 0:
         T = torch.empty((M, r), dtype=torch.float32, device=dev)
-    need = lib().qlora_grouped_fwd_workspace_bytes(M, E, N, w.K, r)
-    workspace = _scratch(workspace, need, dev)
-    cw = w._c()
-    _call("qlora_grouped_fwd", dev, _ptr(X), M, _ptr(offsets), E, ctypes.byref(cw), _ptr(A),
-          _ptr(B), r, float(s), ctypes.byref(d), _ptr(Y), _ptr(T), _ptr(workspace), need)
+    _call("qlora_grouped_fwd", dev, X.data_ptr(), M, offsets.data_ptr(), E, ctypes.byref(cw),
+          _at(A), _at(B), r, s, ctypes.byref(d), Y.data_ptr(), _at(T), _at(workspace), need)
     return Y, T
 
 
@@ -779,35 +838,12 @@ def qlora_grouped_bwd(dY, X, offsets, w, E: int, A=None, B=None, s: float = 1.0,
     dB bf16 [E,r,N]); T None recomputes it.  dA and dB are zero for an expert
     without rows."""
     import torch
-    M, N, r, w, named = _grouped(X, offsets, w, E, A, B)
-    _need(dY, "dY", (M, N), torch.bfloat16)
-    d, dn = _drop(p, state)
-    if T is not None and r > 0:
-        _need(T, "T", (M, r), torch.float32)
-    if need_dx and dX is not None:
-        _need(dX, "dX", (M, w.K), torch.bfloat16)
-    if r > 0 and dA is not None:
-        _need(dA, "dA", (E, w.K, r), torch.bfloat16)
-    if r > 0 and dB is not None:
-        _need(dB, "dB", (E, r, N), torch.bfloat16)
-    _on_gpu(named + dn + [("dY", dY), ("T", T if r > 0 else None),
-                          ("dX", dX if need_dx else None), ("dA", dA if r > 0 else None),
-                          ("dB", dB if r > 0 else None), ("workspace", workspace)])
-    dev = X.device
-    if need_dx and dX is None:
-        dX = torch.empty((M, w.K), dtype=torch.bfloat16, device=dev)
-    if r > 0 and dA is None:
-        dA = torch.empty((E, w.K, r), dtype=torch.bfloat16, device=dev)
-    if r > 0 and dB is None:
-        dB = torch.empty((E, r, N), dtype=torch.bfloat16, device=dev)
-    need = lib().qlora_grouped_bwd_workspace_bytes(M, E, N, w.K, r)
-    workspace = _scratch(workspace, need, dev)
-    cw = w._c()
-    _call("qlora_grouped_bwd", dev, _ptr(dY), _ptr(X), M, _ptr(offsets), E, ctypes.byref(cw),
-          _ptr(A), _ptr(B), r, float(s), ctypes.byref(d), _ptr(T if r > 0 else None),
-          _ptr(dX if need_dx else None), _ptr(dA if r > 0 else None),
-          _ptr(dB if r > 0 else None), _ptr(workspace), need)
-    return (dX if need_dx else None), dA, dB
+    M, N, r, cw, wt = _experts(X, offsets, w, E, A, B)
+    _is(dY, "dY", (M, N), torch.bfloat16)
+    d = _drop(p, state)
+    return _grads("qlora_grouped_bwd", (offsets, E), dY, X, M, N, w.K, cw, wt, A, B, r, s, d,
+                  state, T, need_dx, dX, dA, dB, (E, w.K, r), (E, r, N), workspace,
+                  lib().qlora_grouped_bwd_workspace_bytes(M, E, N, w.K, r))
 
 
 def qlora_expert_plan(ids, E: int, workspace=None):
@@ -816,16 +852,15 @@ def qlora_expert_plan(ids, E: int, workspace=None):
     tensors (offsets [E+1], order [n]: row -> slot or -1, inverse, of ids'
     shape: slot -> row or -1)."""
     import torch
-    _need(ids, "ids", tuple(ids.shape), torch.int32)
-    _on_gpu([("ids", ids), ("workspace", workspace)])
-    dev, n = ids.device, ids.numel()
+    _is(ids, "ids", ids.shape, torch.int32)
+    dev, n = _one_gpu("ids workspace", ids, workspace), ids.numel()
+    need = lib().qlora_expert_plan_workspace_bytes(n, E)
+    workspace = _scratch(workspace, need, dev)
     offsets = torch.empty(max(E, 0) + 1, dtype=torch.int32, device=dev)
     order = torch.empty(n, dtype=torch.int32, device=dev)
     inverse = torch.empty_like(ids)
-    need = lib().qlora_expert_plan_workspace_bytes(n, E)
-    workspace = _scratch(workspace, need, dev)
-    _call("qlora_expert_plan", dev, _ptr(ids), n, E, _ptr(offsets), _ptr(order), _ptr(inverse),
-          _ptr(workspace), need)
+    _call("qlora_expert_plan", dev, ids.data_ptr(), n, E, offsets.data_ptr(), order.data_ptr(),
+          inverse.data_ptr(), _at(workspace), need)
     return offsets, order, inverse
 
 
@@ -833,7 +868,7 @@ def _slots(inverse):
     import torch
     if inverse.dim() != 2:
         raise ValueError("inverse must be [tokens, topk]")
-    _need(inverse, "inverse", tuple(inverse.shape), torch.int32)
+    _is(inverse, "inverse", inverse.shape, torch.int32)
     return inverse.shape
 
 
@@ -846,13 +881,13 @@ def qlora_expert_gather(X, inverse, out=None):
     if X.dim() != 2:
         raise ValueError("X must be [tokens, K]")
     K = X.shape[1]
-    _need(X, "X", (tokens, K), torch.bfloat16)
-    if out is not None:
-        _need(out, "out", (tokens * topk, K), torch.bfloat16)
-    _on_gpu([("X", X), ("inverse", inverse), ("out", out)])
+    _is(X, "X", (tokens, K), torch.bfloat16)
+    _maybe(out, "out", (tokens * topk, K), torch.bfloat16)
+    dev = _one_gpu("X inverse out", X, inverse, out)
     if out is None:
-        out = torch.empty((tokens * topk, K), dtype=torch.bfloat16, device=X.device)
-    _call("qlora_expert_gather", X.device, _ptr(X), tokens, topk, K, _ptr(inverse), _ptr(out))
+        out = torch.empty((tokens * topk, K), dtype=torch.bfloat16, device=dev)
+    _call("qlora_expert_gather", dev, X.data_ptr(), tokens, topk, K, inverse.data_ptr(),
+          out.data_ptr())
     return out
 
 
@@ -865,16 +900,14 @@ def qlora_expert_combine(Y, inverse, weights=None, out=None):
     if Y.dim() != 2:
         raise ValueError("Y must be [tokens*topk, K]")
     K = Y.shape[1]
-    _need(Y, "Y", (tokens * topk, K), torch.bfloat16)
-    if weights is not None:
-        _need(weights, "weights", (tokens, topk), torch.float32)
-    if out is not None:
-        _need(out, "out", (tokens, K), torch.bfloat16)
-    _on_gpu([("Y", Y), ("inverse", inverse), ("weights", weights), ("out", out)])
+    _is(Y, "Y", (tokens * topk, K), torch.bfloat16)
+    _maybe(weights, "weights", (tokens, topk), torch.float32)
+    _maybe(out, "out", (tokens, K), torch.bfloat16)
+    dev = _one_gpu("Y inverse weights out", Y, inverse, weights, out)
     if out is None:
-        out = torch.empty((tokens, K), dtype=torch.bfloat16, device=Y.device)
-    _call("qlora_expert_combine", Y.device, _ptr(Y), tokens, topk, K, _ptr(inverse),
-          _ptr(weights), _ptr(out))
+        out = torch.empty((tokens, K), dtype=torch.bfloat16, device=dev)
+    _call("qlora_expert_combine", dev, Y.data_ptr(), tokens, topk, K, inverse.data_ptr(),
+          _at(weights), out.data_ptr())
     return out
 
 
@@ -888,21 +921,18 @@ def qlora_expert_combine_bwd(dOut, Y, inverse, weights, dY=None, dweights=None):
     if Y.dim() != 2:
         raise ValueError("Y must be [tokens*topk, K]")
     K = Y.shape[1]
-    _need(Y, "Y", (tokens * topk, K), torch.bfloat16)
-    _need(dOut, "dOut", (tokens, K), torch.bfloat16)
-    _need(weights, "weights", (tokens, topk), torch.float32)
-    if dY is not None:
-        _need(dY, "dY", (tokens * topk, K), torch.bfloat16)
-    if dweights is not None:
-        _need(dweights, "dweights", (tokens, topk), torch.float32)
-    _on_gpu([("dOut", dOut), ("Y", Y), ("inverse", inverse), ("weights", weights), ("dY", dY),
-             ("dweights", dweights)])
+    _is(Y, "Y", (tokens * topk, K), torch.bfloat16)
+    _is(dOut, "dOut", (tokens, K), torch.bfloat16)
+    _is(weights, "weights", (tokens, topk), torch.float32)
+    _maybe(dY, "dY", (tokens * topk, K), torch.bfloat16)
+    _maybe(dweights, "dweights", (tokens, topk), torch.float32)
+    dev = _one_gpu("dOut Y inverse weights dY dweights", dOut, Y, inverse, weights, dY, dweights)
     if dY is None:
         dY = torch.empty_like(Y)
     if dweights is None:
         dweights = torch.empty_like(weights)
-    _call("qlora_expert_combine_bwd", Y.device, _ptr(dOut), _ptr(Y), tokens, topk, K,
-          _ptr(inverse), _ptr(weights), _ptr(dY), _ptr(dweights))
+    _call("qlora_expert_combine_bwd", dev, dOut.data_ptr(), Y.data_ptr(), tokens, topk, K,
+          inverse.data_ptr(), weights.data_ptr(), dY.data_ptr(), dweights.data_ptr())
     return dY, dweights
 
 

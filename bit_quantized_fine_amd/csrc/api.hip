@@ -388,10 +388,11 @@ int check_experts(const qlora_q4_weight* w, int64_t M, int E) {
 
 size_t grouped_fwd_ws_bytes(int64_t M, int E, int64_t N, int64_t K, int r) {
   if (M == 0) return 0;
-  size_t f = grouped_down_ws_floats(M, E, K, r);
+  const size_t t = round_up(grouped_down_ws_floats(M, E, K, r) * sizeof(float), 256);
   const GemmSplit sp = grouped_fwd_split(M, E, N, K);
-  if (sp.splits > 1) f = std::max<size_t>(f, (size_t)sp.splits * M * N);
-  return round_up(f * sizeof(float), 256);
+  const size_t y = sp.splits > 1 ? round_up((size_t)sp.splits * M * N * sizeof(float), 256) : 0;
+  // T's partial sums are still read when the GEMM that adds them up writes its own
+  return grouped_fwd_folds_t(M, E) ? t + y : std::max(t, y);
 }
 
 size_t grouped_bwd_ws_bytes(int64_t M, int E, int64_t N, int64_t K, int r) {
@@ -896,11 +897,19 @@ int qlora_grouped_fwd(const uint16_t* X, int64_t M, const int32_t* offsets, int 
 
   const hipStream_t hs = static_cast<hipStream_t>(stream);
   float* ws = static_cast<float*>(workspace);
+  float* part = ws;
+  const bool fold = r > 0 && grouped_fwd_folds_t(M, E);
+  if (fold)
+    part = reinterpret_cast<float*>(
+        static_cast<char*>(workspace) +
+        round_up(grouped_down_ws_floats(M, E, w->K, r) * sizeof(float), 256));
+  int nz = 0;
   hipError_t e = hipSuccess;
-  if (r > 0) e = launch_grouped_down(X, M, offsets, E, w->K, A, r, T, ws, hs, dr);
+  if (r > 0)
+    e = launch_grouped_down(X, M, offsets, E, w->K, A, r, T, ws, hs, dr, fold ? &nz : nullptr);
   if (e == hipSuccess)
-    e = launch_grouped_fwd_gemm(X, M, offsets, E, q4_view(w), T, B, r, s, Y, ws,
-                                tables(w->codebook), hs);
+    e = launch_grouped_fwd_gemm(X, M, offsets, E, q4_view(w), nz > 0 ? ws : T, nz, dr.scale(), T,
+                                B, r, s, Y, part, tables(w->codebook), hs);
   return hip_status(e);
 }
 

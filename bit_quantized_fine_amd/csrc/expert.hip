@@ -193,14 +193,24 @@ __global__ __launch_bounds__(kRowThreads) void k_expert_combine(
   const int64_t t = blockIdx.x;
   for (int64_t c = 8 * threadIdx.x; c < K; c += 8 * kRowThreads) {
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < topk; ++j) {
-      const int64_t row = inverse[t * topk + j];
-      if (row < 0 || row >= n) continue;
-      const float w = weights ? weights[t * topk + j] : 1.f;
-      float y[8];
-      unpack8(*reinterpret_cast<const u32x4*>(Y + row * K + c), y);
+    for (int j0 = 0; j0 < topk; j0 += 4) {   // four rows' loads in flight
+      u32x4 v[4];
+      float w[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, y[i], acc[i]);
+      for (int i = 0; i < 4; ++i) {
+        const int j = j0 + i;
+        const int64_t row = j < topk ? inverse[t * topk + j] : -1;
+        const bool in = row >= 0 && row < n;   // a slot without a row adds 0 times 0
+        v[i] = in ? *reinterpret_cast<const u32x4*>(Y + row * K + c) : u32x4{0, 0, 0, 0};
+        w[i] = !in ? 0.f : (weights ? weights[t * topk + j] : 1.f);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float y[8];
+        unpack8(v[i], y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] = fmaf(w[i], y[k], acc[k]);
+      }
     }
     *reinterpret_cast<u32x4*>(out + t * K + c) = pack8(acc);
   }

@@ -1,0 +1,59 @@
+// Arguments of the grouped forward kernels and the dealing out of their tiles.
+#pragma once
+
+#include "group_tiles.hpp"
+
+namespace qnf4 {
+
+constexpr uint32_t kOffNone = 0x80000000u;   // a buffer offset past the end of every buffer
+
+struct ExpertArgs {
+  const uint16_t* X;
+  int64_t M;
+  const int* offsets;
+  int E;
+  const uint8_t* codes;
+  const uint8_t* absmax_q;
+  const float* absmax_scale;
+  int64_t N, K;
+  const float* T;     // [M][r], or (nz > 0) partial sums [nz][M][r] of it
+  int nz;
+  float tscale;       // of the partial sums
+  float* Tout;        // their sum goes here
+  const uint16_t* B;
+  int r;
+  float s;
+  uint16_t* Y;
+  int ptiles, qtiles, cps;
+  float* part;
+};
+
+__device__ __forceinline__ int xcd_remap_expert(int b, int total) {
+  const int n8 = total >> 3, rem = total & 7;
+  const int x = b & 7, i = b >> 3;
+  return x * n8 + min(x, rem) + i;
+}
+
+// The workgroup's tile: its token rows, weight row tile pt and split z of the
+// reduction; e = -1 when there is no work for it.  Only the tiles that the
+// groups have are dealt out over the XCDs (the grid holds the most that they
+// could have), so that none is left with the empty ones.
+template <int TQ>
+__device__ __forceinline__ GroupTile expert_deal(const ExpertArgs& a, GroupTiles<TQ>& groups,
+                                                 int& pt, int& z) {
+  const int splits = static_cast<int>(gridDim.x) / (a.ptiles * a.qtiles);
+  const int ntiles = a.ptiles * min(a.qtiles, groups.count());
+  const int work = ntiles * splits;
+  pt = z = 0;
+  if (static_cast<int>(blockIdx.x) >= work) return GroupTile{-1, 0, 0};
+  const int lin = xcd_remap_expert(blockIdx.x, work);
+  z = lin / ntiles;
+  const int tile = lin - z * ntiles, qt = tile / a.ptiles;
+  pt = tile - qt * a.ptiles;
+  return groups.find(qt);
+}
+
+// The few-token form (expert_few.hip); fills in the tiles.
+hipError_t launch_expert_few(ExpertArgs a, bool dq, const Nf4Tables& tb, hipStream_t stream);
+
+}  // namespace qnf4

@@ -21,9 +21,11 @@
 // The offsets are read on the GPU: the grid holds the most tiles the groups
 // could make, a workgroup finds its expert and rows in them, and the last tile
 // of a group runs the narrowest body that holds its rows.
+#include <algorithm>
 #include <type_traits>
 
 #include "device_common.hpp"
+#include "expert_args.hpp"
 #include "group_tiles.hpp"
 #include "kernels.hpp"
 #include "rank_tiles.hpp"
@@ -34,7 +36,6 @@ namespace {
 
 constexpr int EW = 8;            // waves
 constexpr int ET = 64 * EW;      // threads
-constexpr uint32_t kOffNone = 0x80000000u;   // past the end of every buffer
 
 template <int FR, int TB>
 struct ExpertTile {
@@ -46,6 +47,7 @@ struct ExpertTile {
   static constexpr int XBUF = TQ * PPR * 8;       // elements of one X buffer
   static constexpr int PIECES = TQ * PPR;
   static constexpr int PP = (PIECES + ET - 1) / ET;   // pieces a thread stages
+  static constexpr int D = 2;                     // code stages (128-k chunks)
   static constexpr int XST = TB > 8 ? 1 : 2;      // register stages of X
   static constexpr int MAIN = kRepTabBytes + 2 * XBUF * 2;
   static constexpr int TAIL = ROWS * 128 + TQ * 256;   // B tile, T hi and lo tiles
@@ -66,24 +68,6 @@ constexpr int expert_lds() {
   return lds;
 }
 
-struct ExpertArgs {
-  const uint16_t* X;
-  int64_t M;
-  const int* offsets;
-  int E;
-  const uint8_t* codes;
-  const uint8_t* absmax_q;
-  const float* absmax_scale;
-  int64_t N, K;
-  const float* T;
-  const uint16_t* B;
-  int r;
-  float s;
-  uint16_t* Y;
-  int ptiles, qtiles, cps;
-  float* part;
-};
-
 // Slot of 16-byte piece q of token row `row`.
 template <int PPR>
 __device__ __forceinline__ int xslot(int row, int q) {
@@ -95,7 +79,7 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
                                             int64_t mend, int pt, int z) {
   using Tile = ExpertTile<FR, TB>;
   constexpr int SUB = Tile::SUB, STEPS = Tile::STEPS, PPR = Tile::PPR, PP = Tile::PP;
-  constexpr int XST = Tile::XST;
+  constexpr int XST = Tile::XST, D = Tile::D;
   constexpr int GB = TB < 4 ? TB : 4, NG = TB / GB;   // token subtiles a group, groups
   constexpr int U = TB == 4 ? 2 : 1;                  // steps dequantized together
   uint16_t* const Xs = reinterpret_cast<uint16_t*>(dyn + kRepTabBytes);
@@ -117,7 +101,7 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
   const int64_t tile_rows = mend - q0 < Tile::TQ ? mend - q0 : Tile::TQ;
   const BufRes rx = make_bufres(a.X + q0 * K, static_cast<uint32_t>(tile_rows * K * 2));
 
-  // codes and constants of the lane's FR rows, two chunks in flight
+  // codes and constants of the lane's FR rows, D chunks in flight
   uint32_t cb[FR], eb[FR];
 #pragma unroll
   for (int f = 0; f < FR; ++f) {
@@ -125,9 +109,9 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
     cb[f] = static_cast<uint32_t>(n * (K / 2)) + 16u * g;        // + 64 c
     eb[f] = static_cast<uint32_t>(n * KB) + (g >> 1);            // + 2 c
   }
-  u32x4 cw[2][FR];
-  uint32_t ce[2][FR];
-  float cd[2][FR];
+  u32x4 cw[D][FR];
+  uint32_t ce[D][FR];
+  float cd[D][FR];
   auto load_codes = [&](int c, int st) {
     const bool live = c < nchunks;
     const bool blk = live && 2 * c + (g >> 1) < KB;   // the half chunk past K: constant 0
@@ -207,8 +191,8 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
                                            16 * b * PPR * 8);
   };
 
-  load_codes(c0, 0);
-  load_codes(c0 + 1, 1);
+#pragma unroll
+  for (int i = 0; i < D; ++i) load_codes(c0 + i, i);
   load_x(SUB * c0, 0);
   if constexpr (XST == 2) load_x(SUB * c0 + 1, 1);
   __syncthreads();   // the level table
@@ -230,9 +214,9 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
     constexpr int ST = decltype(stc)::value;
 #pragma unroll
     for (int h = 0; h < SUB; ++h) {
-      const int buf = SUB == 1 ? ST : h;
+      const int buf = SUB == 1 ? ST & 1 : h;
       const int t = SUB * c + h;
-      const int xs = XST == 2 ? (ST ^ 1) : 0;
+      const int xs = XST == 2 ? (ST + 1) & 1 : 0;
       u32x4 xf[2][GB];
 #pragma unroll
       for (int b = 0; b < GB; ++b) xf[0][b] = read_x(buf, 0, b);
@@ -242,7 +226,7 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
         const int i = k / NG;                      // step of the staging
         const int unit = (STEPS * h + i) / U;      // run of U steps of the chunk
         const bool first = k % (U * NG) == 0, last = k % (U * NG) == U * NG - 1;
-        const int nst = U * (unit + 1) < 4 ? ST : (ST ^ 1);   // codes of the next run
+        const int nst = U * (unit + 1) < 4 ? ST : (ST + 1) % D;   // codes of the next run
         if (first) {
 #pragma unroll
           for (int j = 0; j < U; ++j)
@@ -258,7 +242,7 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
           store_x(xs, buf ^ 1);
           load_x(XST == 2 ? t + 3 : t + 2, xs);
         }
-        if (first && unit == 4 / U - 1) load_codes(c + 2, ST);   // stage ST is used up
+        if (first && unit == 4 / U - 1) load_codes(c + D, ST);   // stage ST is used up
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int b = 0; b < GB; ++b)
@@ -277,8 +261,9 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
       __syncthreads();
     }
   };
-  // An odd chunk count adds one pass over a chunk past the end, all zeros.
-  for (int c = c0; c < nchunks; c += 2) {
+  // A chunk count that D does not divide adds passes over chunks past the end,
+  // all zeros.
+  for (int c = c0; c < nchunks; c += D) {
     chunk(c, std::integral_constant<int, 0>{});
     chunk(c + 1, std::integral_constant<int, 1>{});
   }
@@ -292,29 +277,45 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
     uint16_t* const tl = th + Tile::TQ * 64;
     const uint16_t* const Be = a.B + (int64_t)e * a.r * N;
     for (int j0 = 0; j0 < a.r; j0 += 64) {
+      // (all loads of the step before the first store, so that one latency
+      // serves them)
+      constexpr int BP = Tile::ROWS * 8 / ET;   // 16-byte pieces of B a thread
+      u32x4 bw[BP];
 #pragma unroll
-      for (int i = 0; i < Tile::ROWS * 8 / ET; ++i) {
+      for (int i = 0; i < BP; ++i) {
         const int idx = tid + ET * i, red = idx / (Tile::ROWS / 8), pc = idx % (Tile::ROWS / 8);
         const int64_t n = p0 + 8 * pc;
-        const u32x4 v = j0 + red < a.r && n < N ? ld16(Be + (int64_t)(j0 + red) * N + n)
-                                                : u32x4{0, 0, 0, 0};
-        st_lds16(bt + (pc / 16) * 64 * 128 + red * 128 + 8 * rm_slot<128>(red, pc % 16), v);
+        bw[i] = j0 + red < a.r && n < N ? ld16(Be + (int64_t)(j0 + red) * N + n)
+                                        : u32x4{0, 0, 0, 0};
       }
-      for (int idx = tid; idx < Tile::TQ * 8; idx += ET) {
-        const int row = idx / 8, q = idx % 8, j = j0 + 8 * q;
-        uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+      for (int idx = tid; idx < Tile::TQ * 16; idx += ET) {   // 4 ranks of a token
+        const int row = idx / 16, q = idx % 16, j = j0 + 4 * q;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
         if (q0 + row < mend && j < a.r) {
-          const float* src = a.T + (q0 + row) * a.r + j;
-          const f32x4 t0 = *reinterpret_cast<const f32x4*>(src) * a.s;
-          const f32x4 t1 = *reinterpret_cast<const f32x4*>(src + 4) * a.s;
-          split_bf16x2(t0.x, t0.y, hi[0], lo[0]);
-          split_bf16x2(t0.z, t0.w, hi[1], lo[1]);
-          split_bf16x2(t1.x, t1.y, hi[2], lo[2]);
-          split_bf16x2(t1.z, t1.w, hi[3], lo[3]);
+          const int64_t at = (q0 + row) * a.r + j;
+          const float* src = a.T + at;
+          if (a.nz > 0) {   // in split order
+#pragma unroll 16
+            for (int y = 0; y < a.nz; ++y)
+              v += *reinterpret_cast<const f32x4*>(src + y * a.M * a.r);
+            v *= a.tscale;
+            if (pt == 0) *reinterpret_cast<f32x4*>(a.Tout + at) = v;
+          } else {
+            v = *reinterpret_cast<const f32x4*>(src);
+          }
+          v *= a.s;
         }
-        const int o = (row * 8 + xslot<8>(row, q)) * 8;
-        st_lds16(th + o, u32x4{hi[0], hi[1], hi[2], hi[3]});
-        st_lds16(tl + o, u32x4{lo[0], lo[1], lo[2], lo[3]});
+        uint32_t h0, h1, l0, l1;
+        split_bf16x2(v.x, v.y, h0, l0);
+        split_bf16x2(v.z, v.w, h1, l1);
+        const int o = (row * 8 + xslot<8>(row, q >> 1)) * 8 + 4 * (q & 1);
+        *reinterpret_cast<u32x2*>(th + o) = u32x2{h0, h1};
+        *reinterpret_cast<u32x2*>(tl + o) = u32x2{l0, l1};
+      }
+#pragma unroll
+      for (int i = 0; i < BP; ++i) {
+        const int idx = tid + ET * i, red = idx / (Tile::ROWS / 8), pc = idx % (Tile::ROWS / 8);
+        st_lds16(bt + (pc / 16) * 64 * 128 + red * 128 + 8 * rm_slot<128>(red, pc % 16), bw[i]);
       }
       __syncthreads();
 #pragma unroll
@@ -363,30 +364,18 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
   }
 }
 
-__device__ __forceinline__ int xcd_remap_e(int b, int total) {
-  const int n8 = total >> 3, rem = total & 7;
-  const int x = b & 7, i = b >> 3;
-  return x * n8 + min(x, rem) + i;
-}
-
 }  // namespace
 
+// (Up to 32 tokens two workgroups fit a CU: 80 KB of LDS, 128 registers.)
 template <int FR, int TB, bool NODQ>
-__global__ __launch_bounds__(ET) void k_expert_fwd(ExpertArgs a, Nf4Tables tb) {
+__global__ __launch_bounds__(ET, TB <= 2 ? 4 : 2) void k_expert_fwd(ExpertArgs a, Nf4Tables tb) {
   // Dynamic LDS only: the level table sits at address 0.
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
-  build_rep_pair_table<ET>(reinterpret_cast<char*>(dyn), load_levels(tb), threadIdx.x);
   constexpr int TQ = 16 * TB;
-  // Only the tiles that the groups have are dealt out over the XCDs.
-  const int most = a.ptiles * a.qtiles;
-  const int splits = static_cast<int>(gridDim.x) / most;
-  const int ntiles = a.ptiles * min(a.qtiles, group_tile_count(a.offsets, a.E, a.M, TQ));
-  const int work = ntiles * splits;
-  if (static_cast<int>(blockIdx.x) >= work) return;
-  const int lin = xcd_remap_e(blockIdx.x, work);
-  const int z = lin / ntiles, tile = lin - z * ntiles;
-  const int qt = tile / a.ptiles, pt = tile - qt * a.ptiles;
-  const GroupTile gt = group_tile(a.offsets, a.E, a.M, TQ, qt);
+  GroupTiles<TQ> groups(a.offsets, a.E, a.M);
+  build_rep_pair_table<ET>(reinterpret_cast<char*>(dyn), load_levels(tb), threadIdx.x);
+  int pt, z;
+  const GroupTile gt = expert_deal(a, groups, pt, z);
   if (gt.e < 0) return;
   const int64_t rows = gt.end - gt.row0;
   constexpr int T1 = narrow1(TB), T2 = narrow2(TB);
@@ -421,22 +410,33 @@ hipError_t launch_variant(const ExpertArgs& a, const Nf4Tables& tb, int splits,
 }
 
 struct ExpertPlan {
-  int fr, tb, ptiles, qtiles;
+  int fr, tb, ptiles, qtiles;   // tb = 0: the few-token kernel, which plans itself
   GemmSplit sp;
 };
 
+// Rows up to which the few-token kernel is used.
+constexpr int64_t kFewRows = 16;
+
+// Token subtiles by the rows of an average expert, 256 weight rows a workgroup
+// if that leaves no CU idle (128 otherwise), and a split of K when there are
+// fewer workgroups than the CUs hold, of at least four chunks each.
 ExpertPlan plan_expert_fwd(int64_t M, int E, int64_t N, int64_t K) {
   ExpertPlan p;
+  if (M <= kFewRows) return ExpertPlan{0, 0, 0, 0, GemmSplit{1, 0}};
   const int64_t mean = (M + E - 1) / E;
-  p.tb = mean > 48 ? 12 : (mean > 8 ? 4 : 2);
+  p.tb = mean > 48 ? 12 : (mean > 16 ? 4 : 2);
+  const int64_t room = p.tb == 2 ? 512 : 256;
   p.qtiles = static_cast<int>(group_tile_bound(M, E, 16 * p.tb));
   p.fr = 2;
   p.ptiles = static_cast<int>((N + 255) / 256);
-  if (static_cast<int64_t>(p.ptiles) * p.qtiles < 256) {
+  if (static_cast<int64_t>(p.ptiles) * p.qtiles < room) {
     p.fr = 1;
     p.ptiles = static_cast<int>((N + 127) / 128);
   }
-  p.sp = gemm_split(static_cast<int64_t>(p.ptiles) * p.qtiles, (K + 127) / 128);
+  const int64_t tiles = static_cast<int64_t>(p.ptiles) * p.qtiles, chunks = (K + 127) / 128;
+  const int64_t want = std::max<int64_t>(1, std::min(room / tiles, chunks / 4));
+  p.sp.cps = static_cast<int>((chunks + want - 1) / want);
+  p.sp.splits = static_cast<int>((chunks + p.sp.cps - 1) / p.sp.cps);
   return p;
 }
 
@@ -446,16 +446,18 @@ GemmSplit grouped_fwd_split(int64_t M, int E, int64_t N, int64_t K) {
   return plan_expert_fwd(M, E, N, K).sp;
 }
 
+bool grouped_fwd_folds_t(int64_t M, int E) { return M <= 48 * static_cast<int64_t>(E); }
+
 hipError_t launch_grouped_fwd_gemm(const uint16_t* X, int64_t M, const int* offsets, int E,
-                                   const Nf4View& w, const float* T, const uint16_t* B, int r,
-                                   float s, uint16_t* Y, float* part, const Nf4Tables& tb,
-                                   hipStream_t stream) {
+                                   const Nf4View& w, const float* T, int nz, float tscale,
+                                   float* Tout, const uint16_t* B, int r, float s, uint16_t* Y,
+                                   float* part, const Nf4Tables& tb, hipStream_t stream) {
   const int64_t N = w.N / E;
   const ExpertPlan p = plan_expert_fwd(M, E, N, w.K);
   if (p.sp.splits > 1 && !part) return hipErrorInvalidValue;
-  const ExpertArgs a{X,    M, offsets,   E, w.codes,  w.absmax_q, w.absmax_scale, N,
-                     w.K,  T, B,         r, s,        Y,          p.ptiles,       p.qtiles,
-                     p.sp.cps, p.sp.splits > 1 ? part : nullptr};
+  const ExpertArgs a{X,   M,  offsets, E,    w.codes, w.absmax_q, w.absmax_scale, N,
+                     w.K, T,  nz,      tscale, Tout,  B,          r,              s,
+                     Y,   p.ptiles, p.qtiles, p.sp.cps, p.sp.splits > 1 ? part : nullptr};
   auto pick = [&](auto nodq) {
     constexpr bool ND = decltype(nodq)::value;
     if (p.fr == 2)
@@ -466,7 +468,8 @@ hipError_t launch_grouped_fwd_gemm(const uint16_t* X, int64_t M, const int* offs
   };
   auto launch = w.dq ? pick(std::false_type{}) : pick(std::true_type{});
   prof_begin(0, stream);
-  hipError_t e = launch(a, tb, p.sp.splits, stream);
+  hipError_t e = p.tb == 0 ? launch_expert_few(a, w.dq, tb, stream)
+                           : launch(a, tb, p.sp.splits, stream);
   if (e == hipSuccess && p.sp.splits > 1)
     e = launch_group_reduce(part, p.sp.splits, M, N, 1.f, offsets, E, nullptr, Y, stream);
   prof_end(0, stream);

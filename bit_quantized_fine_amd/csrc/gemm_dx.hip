@@ -115,6 +115,8 @@ __global__ __launch_bounds__(XT) void k_dx_gemm(
   const int li = lane & 15, g = lane >> 4;
   const int wc = wave % XWC, ks = wave / XWC;
   const int wt = wc % Tile::WT, wr = wc / Tile::WT;
+  // (grouped rows: the offsets are on their way while the table is built)
+  GroupTiles<XQ> groups(offsets, kExperts ? E : 0, M);
   if constexpr (kForm != kFormDense) build_rep_pair_table<XT>(tab, load_levels(tb), tid);
 
   // With a split reduction (few tiles), workgroup b takes row chunks
@@ -122,7 +124,7 @@ __global__ __launch_bounds__(XT) void k_dx_gemm(
   int ntiles = ptiles * qtiles, work = static_cast<int>(gridDim.x);
   if constexpr (kExperts) {   // only the tiles that the groups have
     const int splits = work / ntiles;
-    ntiles = ptiles * min(qtiles, group_tile_count(offsets, E, M, XQ));
+    ntiles = ptiles * min(qtiles, groups.count());
     work = min(work, ntiles * splits);
     if (static_cast<int>(blockIdx.x) >= work) return;
   }
@@ -133,7 +135,7 @@ __global__ __launch_bounds__(XT) void k_dx_gemm(
   int64_t q0 = (int64_t)qt * XQ, mend = M;   // the tile's tokens: q0 .. mend - 1 at most
   int64_t n0 = 0;                            // first row of W of the tile's expert
   if constexpr (kExperts) {
-    const GroupTile gt = group_tile(offsets, E, M, XQ, qt);
+    const GroupTile gt = groups.find(qt);
     if (gt.e < 0) return;
     q0 = gt.row0;
     mend = gt.end;

@@ -20,6 +20,7 @@ struct GroupTile {
   int end;    // end of the expert's rows
 };
 
+// Rows of expert e.
 __device__ __forceinline__ void group_range(const int* offsets, int64_t M, int e, int64_t& lo,
                                             int64_t& hi) {
   const int64_t a = offsets[e], b = offsets[e + 1];
@@ -27,52 +28,79 @@ __device__ __forceinline__ void group_range(const int* offsets, int64_t M, int e
   hi = b < lo ? lo : (b > M ? M : b);
 }
 
-// Number of tiles of tq rows.  Every lane of the wave takes one expert of 64
-// at a time; the result is wave-uniform.
-__device__ __forceinline__ int group_tile_count(const int* offsets, int E, int64_t M, int tq) {
-  const int lane = threadIdx.x & 63;
-  int n = 0;
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    if (e0 + lane < E) {
-      int64_t lo, hi;
-      group_range(offsets, M, e0 + lane, lo, hi);
-      n += static_cast<int>((hi - lo + tq - 1) / tq);
-    }
-  }
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) n += __shfl_xor(n, d);
-  return __builtin_amdgcn_readfirstlane(n);
+// Inclusive sum of v over the lanes of the wave.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast 15, 31
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
 }
 
-// Tile `slot` (wave-uniform) in expert order, e = -1 past the last one.
-__device__ __forceinline__ GroupTile group_tile(const int* offsets, int E, int64_t M, int tq,
-                                                int slot) {
-  const int lane = threadIdx.x & 63;
-  int e = -1, row0 = 0, end = 0, base = 0;
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    int64_t lo = 0, hi = 0;
-    if (e0 + lane < E) group_range(offsets, M, e0 + lane, lo, hi);
-    const int n = static_cast<int>((hi - lo + tq - 1) / tq);
-    int incl = n;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(incl, d);
-      if (lane >= d) incl += v;
-    }
-    const unsigned long long past = __ballot(base + incl > slot);
-    if (past != 0) {
-      const int l = __builtin_ctzll(past);
-      const int first = base + __builtin_amdgcn_readlane(incl - n, l);
-      e = e0 + l;
-      row0 = __builtin_amdgcn_readlane(static_cast<int>(lo), l) + (slot - first) * tq;
-      end = __builtin_amdgcn_readlane(static_cast<int>(hi), l);
-      break;
-    }
-    base += __builtin_amdgcn_readlane(incl, 63);
+// The tiles of tq rows, dealt out in expert order.  Every wave finds them by
+// itself: a lane takes one expert of 64 at a time.  The first 64 experts'
+// offsets are loaded at construction, so that a kernel can have them on their
+// way while it does something else; with no more than 64 they are loaded once.
+template <int TQ>
+class GroupTiles {
+ public:
+  __device__ __forceinline__ GroupTiles(const int* offsets, int E, int64_t M)
+      : offsets_(offsets), E_(E), M_(static_cast<int>(M)) {
+    load(0);
   }
-  return GroupTile{__builtin_amdgcn_readfirstlane(e), __builtin_amdgcn_readfirstlane(row0),
-                   __builtin_amdgcn_readfirstlane(end)};
-}
+
+  // Number of tiles (wave-uniform).
+  __device__ __forceinline__ int count() {
+    incl_ = wave_scan(tiles());
+    int n = __builtin_amdgcn_readlane(incl_, 63);
+    for (int e0 = 64; e0 < E_; e0 += 64) {
+      load(e0);
+      n += __builtin_amdgcn_readlane(wave_scan(tiles()), 63);
+    }
+    if (E_ > 64) {
+      load(0);
+      incl_ = wave_scan(tiles());
+    }
+    return n;
+  }
+
+  // Tile `slot` (wave-uniform); after count().
+  __device__ __forceinline__ GroupTile find(int slot) {
+    int base = 0;
+    for (int e0 = 0;; e0 += 64) {
+      const unsigned long long past = __ballot(base + incl_ > slot);
+      if (past != 0) {
+        const int l = __builtin_ctzll(past);
+        const int first = base + __builtin_amdgcn_readlane(incl_ - tiles(), l);
+        const int row0 = __builtin_amdgcn_readlane(lo_, l) + (slot - first) * TQ;
+        return GroupTile{__builtin_amdgcn_readfirstlane(e0 + l),
+                         __builtin_amdgcn_readfirstlane(row0),
+                         __builtin_amdgcn_readlane(hi_, l)};
+      }
+      if (e0 + 64 >= E_) return GroupTile{-1, 0, 0};
+      base += __builtin_amdgcn_readlane(incl_, 63);
+      load(e0 + 64);
+      incl_ = wave_scan(tiles());
+    }
+  }
+
+ private:
+  __device__ __forceinline__ void load(int e0) {
+    const int e = e0 + static_cast<int>(threadIdx.x & 63);
+    lo_ = hi_ = 0;
+    if (e < E_) {
+      lo_ = min(max(offsets_[e], 0), M_);
+      hi_ = min(max(offsets_[e + 1], lo_), M_);
+    }
+  }
+  __device__ __forceinline__ int tiles() const { return (hi_ - lo_ + TQ - 1) / TQ; }
+
+  const int* offsets_;
+  int E_, M_;
+  int lo_, hi_, incl_;
+};
 
 // Most tiles of tq rows that M rows of E experts can make.
 inline int64_t group_tile_bound(int64_t M, int E, int64_t tq) {

@@ -57,7 +57,9 @@ struct RowsJob {
 template <class LP, class LQ>
 __device__ __forceinline__ void rows_tile(const RowsJob& j, int x, int slot, int z, uint16_t* lds,
                                           int tid) {
-  const GroupTile gt = group_tile(j.offsets, j.E, j.M, RB_X, slot);
+  GroupTiles<RB_X> groups(j.offsets, j.E, j.M);
+  groups.count();
+  const GroupTile gt = groups.find(slot);
   if (gt.e < 0) return;
   const int64_t p0 = (int64_t)x * RB_R;
   const int kt0 = z * j.tps, kt1 = min(j.ntiles, kt0 + j.tps);
@@ -145,7 +147,8 @@ __global__ __launch_bounds__(256) void k_group_reduce(const float* part, int spl
   const int64_t row = i / cols;
   if (row < offsets[0] || row >= offsets[E]) return;
   f32x4 s = {0.f, 0.f, 0.f, 0.f};
-  for (int z = 0; z < splits; ++z)
+#pragma unroll 8
+  for (int z = 0; z < splits; ++z)   // (unrolled: the loads go out together)
     s += *reinterpret_cast<const f32x4*>(part + (int64_t)z * count + i);
   s *= scale;
   if constexpr (BF16) {
@@ -271,7 +274,7 @@ size_t grouped_rank_ws_floats(int64_t M, int E, int64_t N, int64_t K, int r) {
 
 hipError_t launch_grouped_down(const uint16_t* X, int64_t M, const int* offsets, int E, int64_t K,
                                const uint16_t* A, int r, float* T, float* ws, hipStream_t stream,
-                               const Drop& d) {
+                               const Drop& d, int* nz) {
   const RowsPlan p = plan_rows(M, E, K, r);
   auto kern = d.on() ? k_group_rows<Bf16RedMajor<RB_R>, Bf16Nat<RB_X, true>>
                      : k_group_rows<Bf16RedMajor<RB_R>, Bf16Nat<RB_X>>;
@@ -280,7 +283,9 @@ hipError_t launch_grouped_down(const uint16_t* X, int64_t M, const int* offsets,
                      rows_job(op(A, r, r, K), K * r, op(X, K, M, K), offsets, E, M, r, p,
                               d.scale(), p.splits > 1 ? ws : T, d));
   hipError_t e = hipGetLastError();
-  if (e == hipSuccess && p.splits > 1)
+  if (nz)
+    *nz = p.splits > 1 ? p.splits : 0;
+  else if (e == hipSuccess && p.splits > 1)
     e = launch_group_reduce(ws, p.splits, M, r, d.scale(), offsets, E, T, nullptr, stream);
   prof_end(4, stream);
   return e;

@@ -127,14 +127,18 @@ hipError_t launch_grad_a(const uint16_t* X, int64_t M, int64_t K, const float* G
 // and B [E][r][N].  Rows outside all groups are neither read nor written.
 // ---------------------------------------------------------------------------
 
-// Tokens a GEMM tile holds (256 or 64) for M rows of E experts.
+// Tokens a dX tile holds (256 or 64) for M rows of E experts.
 int grouped_tile(int64_t M, int E);
 GemmSplit grouped_fwd_split(int64_t M, int E, int64_t N, int64_t K);
 GemmSplit grouped_dx_split(int64_t M, int E, int64_t N, int64_t K);
+// T is final (nz = 0), or nz partial sums [nz][M][r] that the kernel adds up,
+// scales by tscale and writes to Tout: with few rows an expert
+// (grouped_fwd_folds_t) that costs less than a launch of its own.
+bool grouped_fwd_folds_t(int64_t M, int E);
 hipError_t launch_grouped_fwd_gemm(const uint16_t* X, int64_t M, const int* offsets, int E,
-                                   const Nf4View& w, const float* T, const uint16_t* B, int r,
-                                   float s, uint16_t* Y, float* part, const Nf4Tables& tb,
-                                   hipStream_t stream);
+                                   const Nf4View& w, const float* T, int nz, float tscale,
+                                   float* Tout, const uint16_t* B, int r, float s, uint16_t* Y,
+                                   float* part, const Nf4Tables& tb, hipStream_t stream);
 hipError_t launch_grouped_dx_gemm(const uint16_t* dY, int64_t M, const int* offsets, int E,
                                   const Nf4View& w, const float* G, const uint16_t* A, int r,
                                   float s, uint16_t* dX, float* part, const Nf4Tables& tb,
@@ -147,9 +151,11 @@ hipError_t launch_group_reduce(const float* part, int splits, int64_t M, int64_t
 // Floats of workspace of the four rank products, and those of T alone.
 size_t grouped_rank_ws_floats(int64_t M, int E, int64_t N, int64_t K, int r);
 size_t grouped_down_ws_floats(int64_t M, int E, int64_t K, int r);
+// T = scale . (mask X) . A_e.  With nz, a split product's partial sums stay in
+// ws and *nz is their number (0: T is final).
 hipError_t launch_grouped_down(const uint16_t* X, int64_t M, const int* offsets, int E, int64_t K,
                                const uint16_t* A, int r, float* T, float* ws, hipStream_t stream,
-                               const Drop& d);
+                               const Drop& d, int* nz = nullptr);
 hipError_t launch_grouped_grad_in_and_b(const uint16_t* dY, int64_t M, const int* offsets, int E,
                                         int64_t N, const uint16_t* B, const float* T, int r,
                                         float s, float* G, uint16_t* dB, float* ws,
