@@ -135,8 +135,8 @@ int hip_status(hipError_t e) { return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP
 
 // Forward workspace: the split-reduction partials of T, then (reusing the
 // same bytes once T is final) those of the GEMM when it splits its reduction.
-size_t fwd_ws_bytes(int64_t M, int64_t N, int64_t K, int r, bool drop = false) {
-  size_t f = lora_down_ws_floats(M, K, r, drop);
+size_t fwd_ws_bytes(int64_t M, int64_t N, int64_t K, int r) {
+  size_t f = lora_down_ws_floats(M, K, r);
   if (!decode_fits(M, K)) {
     const GemmSplit sp = fwd_gemm_split(M, N, K);
     if (sp.splits > 1) f = std::max<size_t>(f, (size_t)sp.splits * M * N);
@@ -146,10 +146,9 @@ size_t fwd_ws_bytes(int64_t M, int64_t N, int64_t K, int r, bool drop = false) {
 
 // Backward workspace: G [M][r] and the recomputed T [M][r] (r > 0), then the
 // partials of the rank products, whose bytes the dX GEMM's partials reuse.
-size_t bwd_ws_bytes(int64_t M, int64_t N, int64_t K, int r, bool drop = false) {
+size_t bwd_ws_bytes(int64_t M, int64_t N, int64_t K, int r) {
   const size_t mr = r > 0 ? round_up((size_t)M * r * sizeof(float), 256) : 0;
   size_t f = r > 0 ? rank_ws_floats(M, N, K, r) : 0;
-  if (drop) f = std::max(f, lora_down_ws_floats(M, K, r, true));
   const GemmSplit sp = dx_gemm_split(M, N, K);
   if (sp.splits > 1) f = std::max<size_t>(f, (size_t)sp.splits * M * K);
   return 2 * mr + round_up(f * sizeof(float), 256);
@@ -233,11 +232,11 @@ int fwd_impl(const uint16_t* X, int64_t M, const Nf4View& v, const Nf4Tables& tb
              float* ws, hipStream_t hs, const Drop& d = {}) {
   hipError_t e = hipSuccess;
   const bool decode = decode_fits(M, v.K);
-  if (decode && decode_folds_t(M, r) && !d.on()) {
+  if (decode && decode_folds_t(M, r)) {
     // T's partial sums are added up inside the decode kernel (no reduction
     // launch); its workgroup 0 writes T.
     int nz = 0;
-    e = launch_lora_down_partials(X, M, v.K, A, r, kMaxDownPartials, ws, &nz, hs);
+    e = launch_lora_down_partials(X, M, v.K, A, r, kMaxDownPartials, ws, &nz, hs, d);
     if (e == hipSuccess) e = launch_fwd_decode(X, M, v, ws, nz, T, B, r, s, Y, tb, hs);
     return hip_status(e);
   }
@@ -264,7 +263,7 @@ int bwd_impl(const uint16_t* dY, const uint16_t* X, int64_t M, const Nf4View& v,
       (r > 0 && (!aligned16(A) || !aligned16(B) || !aligned16(dA) || !aligned16(dB) ||
                  (T_saved && !aligned16(T_saved)))))
     return QLORA_ERR_ALIGN;
-  const size_t need = bwd_ws_bytes(M, v.N, v.K, r, d.on());
+  const size_t need = bwd_ws_bytes(M, v.N, v.K, r);
   if (need > 0 && (!workspace || workspace_bytes < need)) return QLORA_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return QLORA_ERR_ALIGN;
 
@@ -392,7 +391,7 @@ size_t grouped_fwd_ws_bytes(int64_t M, int E, int64_t N, int64_t K, int r) {
   const GemmSplit sp = grouped_fwd_split(M, E, N, K);
   const size_t y = sp.splits > 1 ? round_up((size_t)sp.splits * M * N * sizeof(float), 256) : 0;
   // T's partial sums are still read when the GEMM that adds them up writes its own
-  return grouped_fwd_folds_t(M, E) ? t + y : std::max(t, y);
+  return grouped_fwd_folds_t(M) ? t + y : std::max(t, y);
 }
 
 size_t grouped_bwd_ws_bytes(int64_t M, int E, int64_t N, int64_t K, int r) {
@@ -827,12 +826,12 @@ int qlora_dropout_apply(const uint16_t* x, int64_t n, const qlora_dropout* d, ui
 
 size_t qlora_linear_dropout_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int r) {
   if (M < 1 || N < 1 || K < 1 || r < 0) return 0;
-  return std::max(fwd_ws_bytes(M, N, K, r), fwd_ws_bytes(M, N, K, r, true));
+  return fwd_ws_bytes(M, N, K, r);
 }
 
 size_t qlora_linear_dropout_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int r) {
   if (M < 1 || N < 1 || K < 1 || r < 0) return 0;
-  return bwd_ws_bytes(M, N, K, r, true);
+  return bwd_ws_bytes(M, N, K, r);
 }
 
 int qlora_linear_dropout_fwd(const uint16_t* X, int64_t M, const qlora_q4_weight* w,
@@ -898,7 +897,7 @@ int qlora_grouped_fwd(const uint16_t* X, int64_t M, const int32_t* offsets, int 
   const hipStream_t hs = static_cast<hipStream_t>(stream);
   float* ws = static_cast<float*>(workspace);
   float* part = ws;
-  const bool fold = r > 0 && grouped_fwd_folds_t(M, E);
+  const bool fold = r > 0 && grouped_fwd_folds_t(M);
   if (fold)
     part = reinterpret_cast<float*>(
         static_cast<char*>(workspace) +

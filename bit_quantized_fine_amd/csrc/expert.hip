@@ -201,7 +201,8 @@ __global__ __launch_bounds__(kRowThreads) void k_expert_combine(
         const int j = j0 + i;
         const int64_t row = j < topk ? inverse[t * topk + j] : -1;
         const bool in = row >= 0 && row < n;   // a slot without a row adds 0 times 0
-        v[i] = in ? *reinterpret_cast<const u32x4*>(Y + row * K + c) : u32x4{0, 0, 0, 0};
+        v[i] = in ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(Y + row * K + c))
+                  : u32x4{0, 0, 0, 0};
         w[i] = !in ? 0.f : (weights ? weights[t * topk + j] : 1.f);
       }
 #pragma unroll

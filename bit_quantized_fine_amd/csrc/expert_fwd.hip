@@ -51,7 +51,9 @@ struct ExpertTile {
   static constexpr int XST = TB > 8 ? 1 : 2;      // register stages of X
   static constexpr int MAIN = kRepTabBytes + 2 * XBUF * 2;
   static constexpr int TAIL = ROWS * 128 + TQ * 256;   // B tile, T hi and lo tiles
-  static constexpr int LDS = MAIN > TAIL ? MAIN : TAIL;
+  static constexpr int YROW = ROWS + 8;                // a token row of the output tile
+  static constexpr int OUT = TQ * YROW * 2;
+  static constexpr int LDS = MAIN > TAIL ? (MAIN > OUT ? MAIN : OUT) : (TAIL > OUT ? TAIL : OUT);
 };
 
 // The narrower bodies a kernel of TB token subtiles holds (0: none): 12 -> 4,
@@ -288,29 +290,27 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
         bw[i] = j0 + red < a.r && n < N ? ld16(Be + (int64_t)(j0 + red) * N + n)
                                         : u32x4{0, 0, 0, 0};
       }
-      for (int idx = tid; idx < Tile::TQ * 16; idx += ET) {   // 4 ranks of a token
-        const int row = idx / 16, q = idx % 16, j = j0 + 4 * q;
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        if (q0 + row < mend && j < a.r) {
-          const int64_t at = (q0 + row) * a.r + j;
-          const float* src = a.T + at;
-          if (a.nz > 0) {   // in split order
-#pragma unroll 16
-            for (int y = 0; y < a.nz; ++y)
-              v += *reinterpret_cast<const f32x4*>(src + y * a.M * a.r);
-            v *= a.tscale;
-            if (pt == 0) *reinterpret_cast<f32x4*>(a.Tout + at) = v;
-          } else {
-            v = *reinterpret_cast<const f32x4*>(src);
-          }
-          v *= a.s;
+      constexpr int TP = (Tile::TQ * 16 + ET - 1) / ET;   // 4-rank pieces of T a thread
+      f32x4 tw[TP];
+#pragma unroll
+      for (int i = 0; i < TP; ++i) {
+        const int idx = tid + ET * i, row = idx / 16, j = j0 + 4 * (idx % 16);
+        tw[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (row < Tile::TQ && q0 + row < mend && j < a.r)
+          tw[i] = *reinterpret_cast<const f32x4*>(a.T + (q0 + row) * a.r + j);
+      }
+#pragma unroll
+      for (int i = 0; i < TP; ++i) {
+        const int idx = tid + ET * i, row = idx / 16, q = idx % 16;
+        if (row < Tile::TQ) {
+          const f32x4 v = tw[i] * a.s;
+          uint32_t h0, h1, l0, l1;
+          split_bf16x2(v.x, v.y, h0, l0);
+          split_bf16x2(v.z, v.w, h1, l1);
+          const int o = (row * 8 + xslot<8>(row, q >> 1)) * 8 + 4 * (q & 1);
+          *reinterpret_cast<u32x2*>(th + o) = u32x2{h0, h1};
+          *reinterpret_cast<u32x2*>(tl + o) = u32x2{l0, l1};
         }
-        uint32_t h0, h1, l0, l1;
-        split_bf16x2(v.x, v.y, h0, l0);
-        split_bf16x2(v.z, v.w, h1, l1);
-        const int o = (row * 8 + xslot<8>(row, q >> 1)) * 8 + 4 * (q & 1);
-        *reinterpret_cast<u32x2*>(th + o) = u32x2{h0, h1};
-        *reinterpret_cast<u32x2*>(tl + o) = u32x2{l0, l1};
       }
 #pragma unroll
       for (int i = 0; i < BP; ++i) {
@@ -343,24 +343,42 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
     }
   }
 
-  // Y[m, n..n+3] for the lane's 4 consecutive rows n of each subtile (bf16),
-  // or this split's fp32 partial sums part[z][m][n..n+3]
+  // This split's fp32 partial sums part[z][m][n..n+3] for the lane's 4
+  // consecutive rows n of each subtile, or Y: the bf16 tile goes through LDS
+  // (rows of ROWS + 8 values), so that a wave stores whole token rows of it
+  // instead of 32-byte pieces of 16 rows.
+  if (a.part) {
 #pragma unroll
-  for (int f = 0; f < FR; ++f) {
-    const int64_t n = p0 + 16 * (FR * wave + f) + 4 * g;
+    for (int f = 0; f < FR; ++f) {
+      const int64_t n = p0 + 16 * (FR * wave + f) + 4 * g;
 #pragma unroll
-    for (int b = 0; b < TB; ++b) {
-      const int64_t m = q0 + 16 * b + li;
-      if (m < mend && n < N) {
-        const f32x4 v = acc[f][b];
-        if (a.part) {
-          *reinterpret_cast<f32x4*>(a.part + ((int64_t)z * a.M + m) * N + n) = v;
-        } else {
-          *reinterpret_cast<u32x2*>(a.Y + m * N + n) =
-              u32x2{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
-        }
+      for (int b = 0; b < TB; ++b) {
+        const int64_t m = q0 + 16 * b + li;
+        if (m < mend && n < N)
+          *reinterpret_cast<f32x4*>(a.part + ((int64_t)z * a.M + m) * N + n) = acc[f][b];
       }
     }
+    return;
+  }
+  uint16_t* const ys = reinterpret_cast<uint16_t*>(dyn);
+  if (a.r == 0) __syncthreads();   // (the LoRA step ends with a barrier)
+#pragma unroll
+  for (int f = 0; f < FR; ++f)
+#pragma unroll
+    for (int b = 0; b < TB; ++b) {
+      const f32x4 v = acc[f][b];
+      *reinterpret_cast<u32x2*>(ys + (16 * b + li) * Tile::YROW + 16 * (FR * wave + f) + 4 * g) =
+          u32x2{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+    }
+  __syncthreads();
+  constexpr int YP = Tile::ROWS / 8;   // 16-byte pieces of a token row
+#pragma unroll
+  for (int i = 0; i < (Tile::TQ * YP + ET - 1) / ET; ++i) {
+    const int idx = tid + ET * i, row = idx / YP, pc = idx % YP;
+    const int64_t m = q0 + row, n = p0 + 8 * pc;
+    if (row < Tile::TQ && m < mend && n < N)
+      *reinterpret_cast<u32x4*>(a.Y + m * N + n) =
+          *reinterpret_cast<const u32x4*>(ys + row * Tile::YROW + 8 * pc);
   }
 }
 
@@ -416,6 +434,8 @@ struct ExpertPlan {
 
 // Rows up to which the few-token kernel is used.
 constexpr int64_t kFewRows = 16;
+// Rows of an average expert above which tiles are 192 tokens wide.
+constexpr int64_t kWideMean = 48;
 
 // Token subtiles by the rows of an average expert, 256 weight rows a workgroup
 // if that leaves no CU idle (128 otherwise), and a split of K when there are
@@ -424,7 +444,7 @@ ExpertPlan plan_expert_fwd(int64_t M, int E, int64_t N, int64_t K) {
   ExpertPlan p;
   if (M <= kFewRows) return ExpertPlan{0, 0, 0, 0, GemmSplit{1, 0}};
   const int64_t mean = (M + E - 1) / E;
-  p.tb = mean > 48 ? 12 : (mean > 16 ? 4 : 2);
+  p.tb = mean > kWideMean ? 12 : (mean > 16 ? 4 : 2);
   const int64_t room = p.tb == 2 ? 512 : 256;
   p.qtiles = static_cast<int>(group_tile_bound(M, E, 16 * p.tb));
   p.fr = 2;
@@ -446,7 +466,11 @@ GemmSplit grouped_fwd_split(int64_t M, int E, int64_t N, int64_t K) {
   return plan_expert_fwd(M, E, N, K).sp;
 }
 
-bool grouped_fwd_folds_t(int64_t M, int E) { return M <= 48 * static_cast<int64_t>(E); }
+// The few-token kernel adds up T's partial sums itself: every workgroup reads
+// those of its few rows.  With up to 32 tokens a tile that was 128 KB a
+// workgroup, and a launch of its own cost less (96 rows, 8 experts of 11008 x
+// 4096, r = 64: 80 against 85 us).
+bool grouped_fwd_folds_t(int64_t M) { return M <= kFewRows; }
 
 hipError_t launch_grouped_fwd_gemm(const uint16_t* X, int64_t M, const int* offsets, int E,
                                    const Nf4View& w, const float* T, int nz, float tscale,

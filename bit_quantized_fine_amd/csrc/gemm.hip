@@ -162,9 +162,14 @@ __global__ __launch_bounds__(256) void k_split_reduce_pair(ReduceJob a, ReduceJo
 constexpr int LDS_K = 128;             // k per slice
 constexpr int LDS_KS = LDS_K + 8;      // LDS row stride (elements)
 
+// With DROP, X is under the dropout mask: a lane forms the masks of the pieces
+// it multiplies while they are on their way, and the sums are scaled.
+template <bool DROP>
 __global__ __launch_bounds__(256) void k_lora_down_small(const uint16_t* __restrict__ X, int M,
                                                          int64_t K, const uint16_t* __restrict__ A,
-                                                         int r, int spw, float* __restrict__ ws) {
+                                                         int r, int spw, float* __restrict__ ws,
+                                                         const uint64_t* __restrict__ state,
+                                                         uint32_t thr, float scale) {
   __shared__ __attribute__((aligned(16))) uint16_t at[64 * LDS_KS];
   const int tid = threadIdx.x;
   const int wave = wave_id(), lane = tid & 63;
@@ -177,6 +182,8 @@ __global__ __launch_bounds__(256) void k_lora_down_small(const uint16_t* __restr
   // Slices run as a two-stage pipeline: the loads of slice sub + 1 are in
   // flight while slice sub is transposed and multiplied.
   u32x4 xf[2][LDS_K / 32];   // token fragments for the k32 steps of a slice
+  DropKey key{};
+  if constexpr (DROP) key = load_drop_key(state, thr);
   u32x4 rows[2][8];   // this thread's 8x8 patch of the slice's A rows
   for (int j0 = 0; j0 < r; j0 += 64) {
     // (buffer loads with out-of-range offsets instead of branches, so the
@@ -214,7 +221,12 @@ __global__ __launch_bounds__(256) void k_lora_down_small(const uint16_t* __restr
       for (int st = 0; st < LDS_K / 32; ++st) {
         const u32x4 af =
             *reinterpret_cast<const u32x4*>(at + (16 * wave + li) * LDS_KS + 32 * st + 8 * g);
-        acc = mfma16(af, xf[b][st], acc);
+        u32x4 x = xf[b][st];
+        if constexpr (DROP) {
+          const int k = (blockIdx.x * spw + sub) * LDS_K + 32 * st + 8 * g;
+          x &= keep_piece(key, static_cast<uint64_t>(li * K + k) / 8);
+        }
+        acc = mfma16(af, x, acc);
       }
       __syncthreads();
     };
@@ -224,6 +236,7 @@ __global__ __launch_bounds__(256) void k_lora_down_small(const uint16_t* __restr
       step(sub + 1, std::integral_constant<int, 1>{});
     }
     const int j = j0 + 16 * wave + 4 * g;
+    if constexpr (DROP) acc *= scale;
     if (m_ok && j < r)
       *reinterpret_cast<f32x4*>(ws + ((int64_t)blockIdx.x * M + li) * r + j) = acc;
   }
@@ -332,9 +345,9 @@ size_t rank_ws_floats(int64_t M, int64_t N, int64_t K, int r) {
   return m;
 }
 
-size_t lora_down_ws_floats(int64_t M, int64_t K, int r, bool drop) {
+size_t lora_down_ws_floats(int64_t M, int64_t K, int r) {
   if (r <= 0) return 0;
-  if (M <= 16 && !drop) return (size_t)lora_down_partial_count(K, kMaxDownPartials) * M * r;
+  if (M <= 16) return (size_t)lora_down_partial_count(K, kMaxDownPartials) * M * r;
   const Split t = choose_split(K, (r + RB_R - 1) / RB_R, (M + RB_X - 1) / RB_X);
   return (size_t)t.splits * M * r;
 }
@@ -346,23 +359,25 @@ int lora_down_partial_count(int64_t K, int maxp) {
 }
 
 hipError_t launch_lora_down_partials(const uint16_t* X, int64_t M, int64_t K, const uint16_t* A,
-                                     int r, int maxp, float* ws, int* nz, hipStream_t stream) {
+                                     int r, int maxp, float* ws, int* nz, hipStream_t stream,
+                                     const Drop& d) {
   if (maxp < 1 || maxp > kMaxDownPartials) return hipErrorInvalidValue;
   const int64_t slices = (K + LDS_K - 1) / LDS_K;
   const int spw = static_cast<int>((slices + maxp - 1) / maxp);
   *nz = lora_down_partial_count(K, maxp);
   prof_begin(4, stream);
-  hipLaunchKernelGGL(k_lora_down_small, dim3(*nz), dim3(256), 0, stream, X, (int)M, K, A, r, spw,
-                     ws);
+  hipLaunchKernelGGL(d.on() ? k_lora_down_small<true> : k_lora_down_small<false>, dim3(*nz),
+                     dim3(256), 0, stream, X, (int)M, K, A, r, spw, ws, d.state, d.thr, d.scale());
   prof_end(4, stream);
   return hipGetLastError();
 }
 
 hipError_t launch_lora_down(const uint16_t* X, int64_t M, int64_t K, const uint16_t* A,
                             int r, float* T, float* ws, hipStream_t stream, const Drop& d) {
-  if (M <= 16 && !d.on()) {
+  if (M <= 16) {
     int nz = 0;
-    hipError_t e = launch_lora_down_partials(X, M, K, A, r, kMaxDownPartials / 2, ws, &nz, stream);
+    hipError_t e =
+        launch_lora_down_partials(X, M, K, A, r, kMaxDownPartials / 2, ws, &nz, stream, d);
     if (e == hipSuccess) {
       prof_begin(4, stream);
       e = reduce<false>(ws, nz, M * r, 1.f, T, stream);

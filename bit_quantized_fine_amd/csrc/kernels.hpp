@@ -95,14 +95,16 @@ hipError_t launch_dx_gemm(const uint16_t* dY, int64_t M, const Nf4View& w,
 // Rank-r products with a split reduction; partials go to `ws`.
 size_t rank_ws_floats(int64_t M, int64_t N, int64_t K, int r);
 // The partials of T = X . A alone (the forward's rank product).
-size_t lora_down_ws_floats(int64_t M, int64_t K, int r, bool drop = false);
+size_t lora_down_ws_floats(int64_t M, int64_t K, int r);
 
 // Few-token LoRA down-projection: nz <= maxp fp32 partial sums [nz][M][r]
-// of T = X . A go to ws (nz returned); M <= 16, maxp <= kMaxDownPartials.
+// of T = X . A (with d on, scale . (mask X) . A) go to ws (nz returned);
+// M <= 16, maxp <= kMaxDownPartials.
 constexpr int kMaxDownPartials = 64;
 int lora_down_partial_count(int64_t K, int maxp);
 hipError_t launch_lora_down_partials(const uint16_t* X, int64_t M, int64_t K, const uint16_t* A,
-                                     int r, int maxp, float* ws, int* nz, hipStream_t stream);
+                                     int r, int maxp, float* ws, int* nz, hipStream_t stream,
+                                     const Drop& d = {});
 
 // T[M,r] = X . A (fp32 out); with d on, scale . (mask X) . A.
 hipError_t launch_lora_down(const uint16_t* X, int64_t M, int64_t K,
@@ -132,9 +134,8 @@ int grouped_tile(int64_t M, int E);
 GemmSplit grouped_fwd_split(int64_t M, int E, int64_t N, int64_t K);
 GemmSplit grouped_dx_split(int64_t M, int E, int64_t N, int64_t K);
 // T is final (nz = 0), or nz partial sums [nz][M][r] that the kernel adds up,
-// scales by tscale and writes to Tout: with few rows an expert
-// (grouped_fwd_folds_t) that costs less than a launch of its own.
-bool grouped_fwd_folds_t(int64_t M, int E);
+// scales by tscale and writes to Tout (grouped_fwd_folds_t: with few rows).
+bool grouped_fwd_folds_t(int64_t M);
 hipError_t launch_grouped_fwd_gemm(const uint16_t* X, int64_t M, const int* offsets, int E,
                                    const Nf4View& w, const float* T, int nz, float tscale,
                                    float* Tout, const uint16_t* B, int r, float s, uint16_t* Y,
