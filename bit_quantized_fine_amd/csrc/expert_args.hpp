@@ -24,33 +24,23 @@ struct ExpertArgs {
   int r;
   float s;
   uint16_t* Y;
-  int ptiles, qtiles, cps;
+  int ptiles, qtiles, splits, cps;
   float* part;
 };
 
-__device__ __forceinline__ int xcd_remap_expert(int b, int total) {
-  const int n8 = total >> 3, rem = total & 7;
-  const int x = b & 7, i = b >> 3;
-  return x * n8 + min(x, rem) + i;
-}
-
 // The workgroup's tile: its token rows, weight row tile pt and split z of the
 // reduction; e = -1 when there is no work for it.  Only the tiles that the
-// groups have are dealt out over the XCDs (the grid holds the most that they
-// could have), so that none is left with the empty ones.
+// groups have are dealt out (the grid holds the most that they could have).
 template <int TQ>
 __device__ __forceinline__ GroupTile expert_deal(const ExpertArgs& a, GroupTiles<TQ>& groups,
                                                  int& pt, int& z) {
-  const int splits = static_cast<int>(gridDim.x) / (a.ptiles * a.qtiles);
-  const int ntiles = a.ptiles * min(a.qtiles, groups.count());
-  const int work = ntiles * splits;
-  pt = z = 0;
-  if (static_cast<int>(blockIdx.x) >= work) return GroupTile{-1, 0, 0};
-  const int lin = xcd_remap_expert(blockIdx.x, work);
-  z = lin / ntiles;
-  const int tile = lin - z * ntiles, qt = tile / a.ptiles;
-  pt = tile - qt * a.ptiles;
-  return groups.find(qt);
+  const int slots = min(a.qtiles, groups.count());
+  const XcdTile t = xcd_deal(blockIdx.x, a.ptiles);
+  pt = t.pt;
+  z = 0;
+  if (t.v >= slots * a.splits) return GroupTile{-1, 0, 0};
+  z = t.v / slots;
+  return groups.find(t.v - z * slots);
 }
 
 // The few-token form (expert_few.hip); fills in the tiles.

@@ -209,7 +209,7 @@ hipError_t launch_few(const ExpertArgs& a, const Nf4Tables& tb, hipStream_t stre
       hipFuncSetAttribute(reinterpret_cast<const void*>(&k_expert_few<NODQ>),
                           hipFuncAttributeMaxDynamicSharedMemorySize, kFewLds);
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL((k_expert_few<NODQ>), dim3(a.ptiles * a.qtiles), dim3(FT), kFewLds, stream, a,
+  hipLaunchKernelGGL((k_expert_few<NODQ>), dim3(xcd_deal_grid(a.qtiles, a.ptiles)), dim3(FT), kFewLds, stream, a,
                      tb);
   return hipGetLastError();
 }
@@ -219,6 +219,7 @@ hipError_t launch_few(const ExpertArgs& a, const Nf4Tables& tb, hipStream_t stre
 hipError_t launch_expert_few(ExpertArgs a, bool dq, const Nf4Tables& tb, hipStream_t stream) {
   a.ptiles = static_cast<int>((a.N + FROWS - 1) / FROWS);
   a.qtiles = static_cast<int>(group_tile_bound(a.M, a.E, 16));
+  a.splits = 1;
   a.part = nullptr;
   return dq ? launch_few<false>(a, tb, stream) : launch_few<true>(a, tb, stream);
 }

@@ -415,15 +415,14 @@ __global__ __launch_bounds__(ET, TB <= 2 ? 4 : 2) void k_expert_fwd(ExpertArgs a
 namespace {
 
 template <int FR, int TB, bool NODQ>
-hipError_t launch_variant(const ExpertArgs& a, const Nf4Tables& tb, int splits,
-                          hipStream_t stream) {
+hipError_t launch_variant(const ExpertArgs& a, const Nf4Tables& tb, hipStream_t stream) {
   constexpr int kLds = expert_lds<FR, TB>();
   static const hipError_t attr =
       hipFuncSetAttribute(reinterpret_cast<const void*>(&k_expert_fwd<FR, TB, NODQ>),
                           hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL((k_expert_fwd<FR, TB, NODQ>), dim3(a.ptiles * a.qtiles * splits), dim3(ET),
-                     kLds, stream, a, tb);
+  hipLaunchKernelGGL((k_expert_fwd<FR, TB, NODQ>), dim3(xcd_deal_grid((int64_t)a.qtiles * a.splits, a.ptiles)),
+                     dim3(ET), kLds, stream, a, tb);
   return hipGetLastError();
 }
 
@@ -481,7 +480,7 @@ hipError_t launch_grouped_fwd_gemm(const uint16_t* X, int64_t M, const int* offs
   if (p.sp.splits > 1 && !part) return hipErrorInvalidValue;
   const ExpertArgs a{X,   M,  offsets, E,    w.codes, w.absmax_q, w.absmax_scale, N,
                      w.K, T,  nz,      tscale, Tout,  B,          r,              s,
-                     Y,   p.ptiles, p.qtiles, p.sp.cps, p.sp.splits > 1 ? part : nullptr};
+                     Y,   p.ptiles, p.qtiles, p.sp.splits, p.sp.cps, p.sp.splits > 1 ? part : nullptr};
   auto pick = [&](auto nodq) {
     constexpr bool ND = decltype(nodq)::value;
     if (p.fr == 2)
@@ -493,7 +492,7 @@ hipError_t launch_grouped_fwd_gemm(const uint16_t* X, int64_t M, const int* offs
   auto launch = w.dq ? pick(std::false_type{}) : pick(std::true_type{});
   prof_begin(0, stream);
   hipError_t e = p.tb == 0 ? launch_expert_few(a, w.dq, tb, stream)
-                           : launch(a, tb, p.sp.splits, stream);
+                           : launch(a, tb, stream);
   if (e == hipSuccess && p.sp.splits > 1)
     e = launch_group_reduce(part, p.sp.splits, M, N, 1.f, offsets, E, nullptr, Y, stream);
   prof_end(0, stream);

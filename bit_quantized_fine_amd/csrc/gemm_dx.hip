@@ -32,7 +32,8 @@
 //
 // kExperts instantiates it over token rows grouped by expert (see the forward
 // GEMM): the reduction runs over the rows of the tile's expert.  With kQ = 64
-// a tile is 64 tokens and the four wave columns split the 128 output columns.
+// a tile is 64 tokens and the four wave columns split the 128 output columns;
+// kQ = 128 lies between.
 //
 // kDrop is the backward of the layer whose adapter input was dropped out:
 // dX = dY . deq(W) + s . mask . (G . A^T), s holding the mask's scale.  The
@@ -64,7 +65,7 @@ constexpr int XYS = XN;          // LDS row stride of the dY tile (128 B, swizzl
 constexpr int XTB = 4;           // 16-token subtiles per wave
 constexpr int kXA = XN * XAS;    // elements of one weight tile buffer
 
-// A tile of kQ tokens (256 or 64).
+// A tile of kQ tokens (256, 128 or 64).
 template <int kQ>
 struct DxTile {
   static constexpr int WT = kQ / 64;              // token groups
@@ -91,22 +92,42 @@ typedef __attribute__((address_space(3))) v4i16 LdsV4i16;
 
 }  // namespace
 
+struct DxArgs {
+  const uint16_t* dY;
+  int64_t M;
+  const uint16_t* Wd;
+  const uint8_t* codes;
+  const uint8_t* absmax_q;
+  const float* absmax_scale;
+  int64_t N, K;
+  const float* G;
+  const uint16_t* Al;
+  int r;
+  float s;
+  uint16_t* dX;
+  int ptiles, qtiles, splits, cps;
+  float* part;
+  const int* offsets;
+  int E;
+  const uint64_t* state;
+  uint32_t thr;
+};
+
+// One tile: tokens q0 .. mend - 1 (kQ at most), columns 128 pt .., split z of
+// the reduction over the weight rows n0 .. n0 + N - 1 of expert e.
 template <int kForm, int kQ, bool kExperts, bool kDrop>
-__global__ __launch_bounds__(XT) void k_dx_gemm(
-    const uint16_t* __restrict__ dY, int64_t M, const uint16_t* __restrict__ Wd,
-    const uint8_t* __restrict__ codes,
-    const uint8_t* __restrict__ absmax_q, const float* __restrict__ absmax_scale,
-    int64_t N, int64_t K, const float* __restrict__ G, const uint16_t* __restrict__ Al,
-    int r, float s, uint16_t* __restrict__ dX, int ptiles, int qtiles, int cps,
-    float* __restrict__ part, Nf4Tables tb, const int* __restrict__ offsets, int E,
-    const uint64_t* __restrict__ state, uint32_t thr) {
+__device__ __forceinline__ void dx_tile(const DxArgs& args, uint8_t* dyn, int e, int64_t q0,
+                                        int64_t mend, int pt, int z) {
   using Tile = DxTile<kQ>;
   constexpr int XQ = kQ, XTA = Tile::TA, kXY = Tile::YTILE, XYPT = Tile::YPT;
-  // Dynamic LDS only (the level table sits at address 0): the replicated
-  // table, two weight tiles, two dY tiles; the table's bytes hold the
-  // accumulator exchange after the main loop.
-  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
-  char* tab = reinterpret_cast<char*>(dyn);
+  const uint16_t* const __restrict__ dY = args.dY;
+  const int64_t M = args.M, N = args.N, K = args.K;
+  const float* const __restrict__ G = args.G;
+  const int r = args.r, cps = args.cps;
+  const float s = args.s;
+  uint16_t* const __restrict__ dX = args.dX;
+  float* const __restrict__ part = args.part;
+  const uint16_t* const __restrict__ Al = args.Al + (kExperts ? (int64_t)e * K * r : 0);
   uint16_t* Ws = reinterpret_cast<uint16_t*>(dyn + kRepTabBytes);   // [2][XN][XAS]
   uint16_t* Ys = Ws + 2 * kXA;                                       // [2][XQ][XYS]
 
@@ -115,34 +136,9 @@ __global__ __launch_bounds__(XT) void k_dx_gemm(
   const int li = lane & 15, g = lane >> 4;
   const int wc = wave % XWC, ks = wave / XWC;
   const int wt = wc % Tile::WT, wr = wc / Tile::WT;
-  // (grouped rows: the offsets are on their way while the table is built)
-  GroupTiles<XQ> groups(offsets, kExperts ? E : 0, M);
-  if constexpr (kForm != kFormDense) build_rep_pair_table<XT>(tab, load_levels(tb), tid);
-
-  // With a split reduction (few tiles), workgroup b takes row chunks
-  // [z cps, (z + 1) cps) of its tile and writes fp32 partial sums.
-  int ntiles = ptiles * qtiles, work = static_cast<int>(gridDim.x);
-  if constexpr (kExperts) {   // only the tiles that the groups have
-    const int splits = work / ntiles;
-    ntiles = ptiles * min(qtiles, groups.count());
-    work = min(work, ntiles * splits);
-    if (static_cast<int>(blockIdx.x) >= work) return;
-  }
-  const int lin = xcd_remap_dx(blockIdx.x, work);
-  const int z = lin / ntiles, tile = lin - z * ntiles;
-  const int qt = tile / ptiles, pt = tile - qt * ptiles;
   const int64_t k0 = (int64_t)pt * XP;
-  int64_t q0 = (int64_t)qt * XQ, mend = M;   // the tile's tokens: q0 .. mend - 1 at most
-  int64_t n0 = 0;                            // first row of W of the tile's expert
-  if constexpr (kExperts) {
-    const GroupTile gt = groups.find(qt);
-    if (gt.e < 0) return;
-    q0 = gt.row0;
-    mend = gt.end;
-    n0 = (int64_t)gt.e * N;
-    Al += (int64_t)gt.e * K * r;
-  }
-  const int64_t NW = kExperts ? N * E : N;     // rows of W
+  const int64_t n0 = kExperts ? (int64_t)e * N : 0;
+  const int64_t NW = kExperts ? N * args.E : N;     // rows of W
   const int c0 = z * cps;
   // end of this split's row chunks
   const int nchunks = min(static_cast<int>((N + XN - 1) / XN), c0 + cps);
@@ -151,13 +147,13 @@ __global__ __launch_bounds__(XT) void k_dx_gemm(
   // Buffer descriptors: rows past W and tokens past the tile read as zero (a
   // row n >= N of an expert is the next one's; its dY columns read as zero).
   const uint32_t nb = static_cast<uint32_t>(NW * K / kBlock);
-  const BufRes rc = make_bufres(codes, static_cast<uint32_t>(NW * K / 2));
-  const BufRes re = make_bufres(absmax_q, nb);
+  const BufRes rc = make_bufres(args.codes, static_cast<uint32_t>(NW * K / 2));
+  const BufRes re = make_bufres(args.absmax_q, nb);
   // second-level scales, or one fp32 constant per block (kFormNoDq)
   const BufRes rd = make_bufres(
-      absmax_scale, (kForm == kFormNoDq ? nb : (nb + kGroup - 1) / kGroup) * 4u);
+      args.absmax_scale, (kForm == kFormNoDq ? nb : (nb + kGroup - 1) / kGroup) * 4u);
   // the bf16 weight (kFormDense; N K 2 < 2^31 bytes)
-  const BufRes rw = make_bufres(Wd, static_cast<uint32_t>(kForm == kFormDense ? N * K * 2 : 0));
+  const BufRes rw = make_bufres(args.Wd, static_cast<uint32_t>(kForm == kFormDense ? N * K * 2 : 0));
   // dY is addressed from the tile's first token (its 256 rows span less
   // than 2^31 bytes for N <= 2^22).  (A plain conditional, not min(): the
   // 64-bit min is opaque to the compiler's uniformity analysis and would put
@@ -399,7 +395,8 @@ __global__ __launch_bounds__(XT) void k_dx_gemm(
           for (int b = 0; b < XTB; ++b) low[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
         lora(std::integral_constant<int, K0 * TH>{}, std::integral_constant<int, TH>{}, low, 0,
              32);
-        const DropKey key = load_drop_key(state, thr);
+        const uint32_t thr = args.thr;
+        const DropKey key = load_drop_key(args.state, thr);
 #pragma unroll
         for (int b = 0; b < XTB; ++b) {
           const int64_t m = q0 + 64 * wt + 16 * b + li;
@@ -456,6 +453,49 @@ __global__ __launch_bounds__(XT) void k_dx_gemm(
   if (ks == 0) finish(std::integral_constant<int, 0>{}); else finish(std::integral_constant<int, 1>{});
 }
 
+// The largest body's LDS: that of kQ (the narrower bodies hold less).
+template <int kForm, int kQ, bool kExperts, bool kDrop>
+__global__ __launch_bounds__(XT) void k_dx_gemm(DxArgs args, Nf4Tables tb) {
+  // Dynamic LDS only (the level table sits at address 0): the replicated
+  // table, two weight tiles, two dY tiles; the table's bytes hold the
+  // accumulator exchange after the main loop.
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+  // (grouped rows: the offsets are on their way while the table is built)
+  GroupTiles<kQ> groups(args.offsets, kExperts ? args.E : 0, args.M);
+  if constexpr (kForm != kFormDense)
+    build_rep_pair_table<XT>(reinterpret_cast<char*>(dyn), load_levels(tb), threadIdx.x);
+
+  // With a split reduction (few tiles), a workgroup takes row chunks
+  // [z cps, (z + 1) cps) of its tile and writes fp32 partial sums.
+  if constexpr (kExperts) {   // only the tiles that the groups have
+    const int slots = min(args.qtiles, groups.count());
+    const XcdTile t = xcd_deal(blockIdx.x, args.ptiles);
+    if (t.v >= slots * args.splits) return;
+    const int z = t.v / slots, pt = t.pt;
+    const GroupTile gt = groups.find(t.v - z * slots);
+    if (gt.e < 0) return;
+    // the last tile of a group runs the narrowest body that holds its rows
+    const int rows = gt.end - gt.row0;
+    if constexpr (kQ == 256) {
+      if (rows <= 64) {
+        dx_tile<kForm, 64, true, kDrop>(args, dyn, gt.e, gt.row0, gt.end, pt, z);
+        return;
+      }
+      if (rows <= 128) {
+        dx_tile<kForm, 128, true, kDrop>(args, dyn, gt.e, gt.row0, gt.end, pt, z);
+        return;
+      }
+    }
+    dx_tile<kForm, kQ, true, kDrop>(args, dyn, gt.e, gt.row0, gt.end, pt, z);
+  } else {
+    const int ntiles = args.ptiles * args.qtiles;
+    const int lin = xcd_remap_dx(blockIdx.x, static_cast<int>(gridDim.x));
+    const int z = lin / ntiles, tile = lin - z * ntiles;
+    const int qt = tile / args.ptiles, pt = tile - qt * args.ptiles;
+    dx_tile<kForm, kQ, false, kDrop>(args, dyn, 0, (int64_t)qt * kQ, args.M, pt, z);
+  }
+}
+
 namespace {
 
 constexpr int kPlainQ = 256;   // tokens a tile without groups
@@ -472,10 +512,12 @@ hipError_t launch_dx_tiles(const uint16_t* dY, int64_t M, const Nf4View& w, int6
   if (attr != hipSuccess) return attr;
   if (sp.splits > 1 && !part) return hipErrorInvalidValue;
   const int ptiles = static_cast<int>((w.K + XP - 1) / XP);
-  hipLaunchKernelGGL((k_dx_gemm<kForm, kQ, kExperts, kDrop>), dim3(ptiles * qtiles * sp.splits),
-                     dim3(XT), kLds, stream, dY, M, w.dense, w.codes, w.absmax_q, w.absmax_scale,
-                     N, w.K, G, A, r, kDrop ? s * d.scale() : s, dX, ptiles, qtiles, sp.cps,
-                     sp.splits > 1 ? part : nullptr, tb, offsets, E, d.state, d.thr);
+  const DxArgs args{dY,  M, w.dense, w.codes, w.absmax_q, w.absmax_scale, N, w.K,
+                    G,   A, r,       kDrop ? s * d.scale() : s, dX, ptiles, qtiles, sp.splits, sp.cps,
+                    sp.splits > 1 ? part : nullptr, offsets, E, d.state, d.thr};
+  hipLaunchKernelGGL((k_dx_gemm<kForm, kQ, kExperts, kDrop>), dim3(kExperts ? xcd_deal_grid((int64_t)qtiles * sp.splits, ptiles)
+                                   : ptiles * qtiles * sp.splits),
+                     dim3(XT), kLds, stream, args, tb);
   return hipGetLastError();
 }
 

@@ -102,6 +102,30 @@ class GroupTiles {
   int lo_, hi_, incl_;
 };
 
+// Deals V token tiles x P weight tiles out to the eight XCDs (workgroup b runs on
+// XCD b % 8).  Of token tile v, XCD x takes weight tiles floor((x P + v % 8) / 8)
+// up to the next XCD's first, token tile after token tile: its workgroups share
+// few token tiles at a time and much the same weight tiles throughout, and over
+// every eight token tiles each XCD gets P tiles, full and partial ones mixed.
+// (Contiguous runs of all tiles gave some XCDs only full token tiles: one round
+// of workgroups more than the others.  All token tiles of one weight tile next
+// to each other read each XCD's tokens from beyond L2: 8% slower.)
+struct XcdTile {
+  int v, pt;   // v >= V: no work
+};
+__device__ __forceinline__ XcdTile xcd_deal(int b, int P) {
+  const int x = b & 7;
+  int i = b >> 3;
+  int v = 8 * (i / P);
+  i -= v / 8 * P;
+  for (int ph = 0;; ++ph) {
+    const int first = (x * P + ph) >> 3, n = (((x + 1) * P + ph) >> 3) - first;
+    if (i < n || ph == 7) return XcdTile{v + ph, first + i};
+    i -= n;
+  }
+}
+inline int xcd_deal_grid(int64_t V, int64_t P) { return static_cast<int>(8 * P * ((V + 7) / 8)); }
+
 // Most tiles of tq rows that M rows of E experts can make.
 inline int64_t group_tile_bound(int64_t M, int E, int64_t tq) {
   const int64_t groups = E < M ? E : M;

@@ -135,6 +135,22 @@ __global__ __launch_bounds__(NT) void k_group_grad(GradJob j) {
   grad_tile<HL, BP, BQ, LP, LQ>(j, blockIdx.x, lds, threadIdx.x);
 }
 
+// G's and dB's tiles in one launch (neither needs the other): workgroups
+// [0, nrows) are G's, so that the two share the machine.
+template <class LP, class LQ, int HL, int BP, int BQ, class LPG, class LQG>
+__global__ __launch_bounds__(NT) void k_group_pair(RowsJob a, GradJob b, int nrows) {
+  constexpr int LA = rank_lds<0, LP, LQ>(), LB = rank_lds<HL, LPG, LQG>();
+  __shared__ __attribute__((aligned(16))) uint16_t lds[LA > LB ? LA : LB];
+  const int blk = blockIdx.x;   // uniform: the branch is a scalar one
+  if (blk < nrows) {
+    const int per = a.px * a.slots;
+    const int z = blk / per, t = blk - z * per;
+    rows_tile<LP, LQ>(a, t % a.px, t / a.px, z, lds, threadIdx.x);
+  } else {
+    grad_tile<HL, BP, BQ, LPG, LQG>(b, blk - nrows, lds, threadIdx.x);
+  }
+}
+
 // out[m][c] = scale sum_z part[z][m][c] on rows [offsets[0], offsets[E]);
 // four columns a thread.
 template <bool BF16>
@@ -264,11 +280,11 @@ size_t grouped_down_ws_floats(int64_t M, int E, int64_t K, int r) {
 
 size_t grouped_rank_ws_floats(int64_t M, int E, int64_t N, int64_t K, int r) {
   if (r <= 0 || M <= 0) return 0;
-  size_t f = grouped_down_ws_floats(M, E, K, r);
-  f = std::max(f, grouped_down_ws_floats(M, E, N, r));
   const int sa = grad_splits(M, E, K, r), sb = grad_splits(M, E, N, r);
+  size_t gb = grouped_down_ws_floats(M, E, N, r);   // G's, and dB's beside them
+  if (sb > 1) gb += (size_t)sb * E * N * r;
+  size_t f = std::max(grouped_down_ws_floats(M, E, K, r), gb);
   if (sa > 1) f = std::max<size_t>(f, (size_t)sa * E * K * r);
-  if (sb > 1) f = std::max<size_t>(f, (size_t)sb * E * N * r);
   return f;
 }
 
@@ -295,28 +311,24 @@ hipError_t launch_grouped_grad_in_and_b(const uint16_t* dY, int64_t M, const int
                                         int64_t N, const uint16_t* B, const float* T, int r,
                                         float s, float* G, uint16_t* dB, float* ws,
                                         hipStream_t stream) {
-  hipError_t e = hipSuccess;
+  // G's partial sums, then dB's
+  RowsPlan p{1, 0, 1, 1, 1};
+  if (M > 0) p = plan_rows(M, E, N, r);
+  const int nrows = p.px * p.slots * p.splits, sb = grad_splits(M, E, N, r);
+  float* const wsb = ws + (p.splits > 1 ? (size_t)p.splits * M * r : 0);
+  const RowsJob jg = rows_job(op(B, N, r, N), (int64_t)r * N, op(dY, N, M, N), offsets, E, M, r, p,
+                              1.f, p.splits > 1 ? ws : G, {});
+  const GradJob jb = grad_job(op(dY, N, N, M), op(T, r, r, M), offsets, E, M, N, r, RB_X, RB_R, sb,
+                              s, dB, wsb, {});
   prof_begin(4, stream);
-  if (M > 0) {
-    const RowsPlan p = plan_rows(M, E, N, r);
-    hipLaunchKernelGGL((k_group_rows<Bf16Nat<RB_R>, Bf16Nat<RB_X>>),
-                       dim3(p.px * p.slots * p.splits), dim3(NT), 0, stream,
-                       rows_job(op(B, N, r, N), (int64_t)r * N, op(dY, N, M, N), offsets, E, M, r,
-                                p, 1.f, p.splits > 1 ? ws : G, {}));
-    e = hipGetLastError();
-    if (e == hipSuccess && p.splits > 1)
-      e = launch_group_reduce(ws, p.splits, M, r, 1.f, offsets, E, G, nullptr, stream);
-  }
-  if (e == hipSuccess) {
-    const int sb = grad_splits(M, E, N, r);
-    const GradJob j = grad_job(op(dY, N, N, M), op(T, r, r, M), offsets, E, M, N, r, RB_X, RB_R,
-                               sb, s, dB, ws, {});
-    hipLaunchKernelGGL((k_group_grad<2, RB_X, RB_R, Bf16RedMajor<RB_X>, F32RedMajor<RB_R>>),
-                       dim3(j.px * j.qy * E * sb), dim3(NT), 0, stream, j);
-    e = hipGetLastError();
-    if (e == hipSuccess && sb > 1)
-      e = launch_split_reduce_bf16(ws, sb, (int64_t)E * N * r, dB, stream, s);
-  }
+  hipLaunchKernelGGL((k_group_pair<Bf16Nat<RB_R>, Bf16Nat<RB_X>, 2, RB_X, RB_R,
+                                   Bf16RedMajor<RB_X>, F32RedMajor<RB_R>>),
+                     dim3(nrows + jb.px * jb.qy * E * sb), dim3(NT), 0, stream, jg, jb, nrows);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && p.splits > 1)
+    e = launch_group_reduce(ws, p.splits, M, r, 1.f, offsets, E, G, nullptr, stream);
+  if (e == hipSuccess && sb > 1)
+    e = launch_split_reduce_bf16(wsb, sb, (int64_t)E * N * r, dB, stream, s);
   prof_end(4, stream);
   return e;
 }
