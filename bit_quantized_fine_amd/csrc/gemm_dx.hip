@@ -377,8 +377,12 @@ __device__ __forceinline__ void dx_tile(const DxArgs& args, uint8_t* dyn, int e,
       for (int b = 0; b < XTB; ++b)
         xch[(((GIVE * XWC + wc) * TH + a) * XTB + b) * 64 + lane] = acc[GIVE * TH + a][b];
   };
-  // dX[m, k..k+3] for the lane's 4 consecutive columns k of each subtile
-  // (bf16), or this split's fp32 partial sums part[z][m][k..k+3]
+  // This split's fp32 partial sums part[z][m][k..k+3] for the lane's 4
+  // consecutive columns k of each subtile, or dX: the bf16 tile goes through
+  // LDS (rows of 128 + 8 values), so that a wave stores 256 bytes of a token row
+  // at a time instead of 32.
+  constexpr int kXRow = XP + 8;
+  uint16_t* const xs = reinterpret_cast<uint16_t*>(dyn);
   auto finish = [&](auto kc) {
     constexpr int K0 = decltype(kc)::value;
 #pragma unroll
@@ -430,22 +434,36 @@ __device__ __forceinline__ void dx_tile(const DxArgs& args, uint8_t* dyn, int e,
         }
       }
     }
+    const int col = 16 * (wr * XTA + K0 * TH) + 4 * g;   // of subtile a: + 16 a
+    if (part) {
 #pragma unroll
-    for (int a = 0; a < TH; ++a) {
-      const int64_t k = k0 + 16 * (wr * XTA + K0 * TH + a) + 4 * g;
+      for (int a = 0; a < TH; ++a)
+#pragma unroll
+        for (int b = 0; b < XTB; ++b) {
+          const int64_t m = q0 + 64 * wt + 16 * b + li;
+          if (m < mend && k0 + col + 16 * a < K)
+            *reinterpret_cast<f32x4*>(part + ((int64_t)z * M + m) * K + k0 + col + 16 * a) =
+                acc[K0 * TH + a][b];
+        }
+      return;
+    }
+    __syncthreads();   // every wave has taken its sums
+#pragma unroll
+    for (int a = 0; a < TH; ++a)
 #pragma unroll
       for (int b = 0; b < XTB; ++b) {
-        const int64_t m = q0 + 64 * wt + 16 * b + li;
-        if (m < mend && k < K) {
-          const f32x4 v = acc[K0 * TH + a][b];
-          if (part) {
-            *reinterpret_cast<f32x4*>(part + ((int64_t)z * M + m) * K + k) = v;
-          } else {
-            *reinterpret_cast<u32x2*>(dX + m * K + k) =
-                u32x2{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
-          }
-        }
+        const f32x4 v = acc[K0 * TH + a][b];
+        *reinterpret_cast<u32x2*>(xs + (64 * wt + 16 * b + li) * kXRow + col + 16 * a) =
+            u32x2{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
       }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < XQ * (XP / 8) / XT; ++i) {
+      const int idx = tid + XT * i, row = idx / (XP / 8), pc = idx % (XP / 8);
+      const int64_t m = q0 + row, k = k0 + 8 * pc;
+      if (m < mend && k < K)
+        *reinterpret_cast<u32x4*>(dX + m * K + k) =
+            *reinterpret_cast<const u32x4*>(xs + row * kXRow + 8 * pc);
     }
   };
   if (ks == 0) hand(std::integral_constant<int, 0>{}); else hand(std::integral_constant<int, 1>{});
