@@ -23,8 +23,9 @@ typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 // The generator's key and counter offset, the same for every lane.
 struct DropKey {
   uint32_t k0, k1, o0, o1;
-  u16x2 thr;   // the threshold in both halves
+  uint32_t thr;   // the threshold in both 16-bit halves
 };
+struct NoDropKey {};
 
 // state: {seed, offset} in device memory, so a captured graph draws another
 // mask on each replay when the caller advances the offset in between.
@@ -35,7 +36,7 @@ __device__ __forceinline__ DropKey load_drop_key(const uint64_t* state, uint32_t
   k.k1 = static_cast<uint32_t>(seed >> 32);
   k.o0 = static_cast<uint32_t>(off);
   k.o1 = static_cast<uint32_t>(off >> 32);
-  k.thr = u16x2{static_cast<unsigned short>(thr), static_cast<unsigned short>(thr)};
+  k.thr = thr | (thr << 16);
   return k;
 }
 
@@ -59,7 +60,8 @@ __device__ __forceinline__ u32x4 philox_piece(const DropKey& key, uint64_t piece
 
 // Two 16-bit halves -> 0xFFFF where kept (half >= thr), 0 where dropped.
 __device__ __forceinline__ uint32_t keep_bits(const DropKey& key, uint32_t w) {
-  const u16x2 d = __builtin_elementwise_sub_sat(key.thr, __builtin_bit_cast(u16x2, w));
+  const u16x2 d = __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, key.thr),
+                                               __builtin_bit_cast(u16x2, w));
   const u16x2 one = {1, 1};
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(d, one) - one);
 }

@@ -17,15 +17,16 @@ struct ExpertArgs {
   const float* absmax_scale;
   int64_t N, K;
   const float* T;     // [M][r], or (nz > 0) partial sums [nz][M][r] of it
-  int nz;
-  float tscale;       // of the partial sums
   float* Tout;        // their sum goes here
   const uint16_t* B;
-  int r;
-  float s;
   uint16_t* Y;
-  int ptiles, qtiles, splits, cps;
   float* part;
+  int nz, r;
+  int ptiles, qtiles, splits, cps;
+  // (last: fields used as vectors would take the ones behind them along into a
+  // private array)
+  float tscale;       // of T's partial sums
+  float s;
 };
 
 // The workgroup's tile: its token rows, weight row tile pt and split z of the

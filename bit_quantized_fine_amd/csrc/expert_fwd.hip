@@ -431,10 +431,18 @@ struct ExpertPlan {
   GemmSplit sp;
 };
 
-// Rows up to which the few-token kernel is used.
+// Rows up to which the few-token kernel is used: it streams the weights of the
+// experts that have rows faster than k_expert_fwd (8 experts of 4096 x 4096, r =
+// 16: 21 against 26 us at 4 rows, 30 against 32 at 16) until experts have more
+// rows than one MFMA column tile or X is read by too many workgroups (38 against
+// 33 us at 32 rows).
 constexpr int64_t kFewRows = 16;
-// Rows of an average expert above which tiles are 192 tokens wide.
-constexpr int64_t kWideMean = 48;
+// Rows of an average expert above which a tile holds 64 tokens, and 192 (the
+// narrower bodies take over in the last tile of a group).  Same experts, 32 /
+// 64 / 192 tokens a tile: 37 / 38 / 46 us at 192 rows, 49 / 46 / 48 at 256, 52 /
+// 48 / 48 at 384, 119 / 116 / 80 at 1024; 32 experts of 1024 x 2048: 29 / 31 / 35
+// us at 768 rows, 36 / 34 / 35 at 1024, 50 / 54 / 43 at 2048.
+constexpr int64_t kMidMean = 24, kWideMean = 40;
 
 // Token subtiles by the rows of an average expert, 256 weight rows a workgroup
 // if that leaves no CU idle (128 otherwise), and a split of K when there are
@@ -443,7 +451,7 @@ ExpertPlan plan_expert_fwd(int64_t M, int E, int64_t N, int64_t K) {
   ExpertPlan p;
   if (M <= kFewRows) return ExpertPlan{0, 0, 0, 0, GemmSplit{1, 0}};
   const int64_t mean = (M + E - 1) / E;
-  p.tb = mean > kWideMean ? 12 : (mean > 16 ? 4 : 2);
+  p.tb = mean > kWideMean ? 12 : (mean > kMidMean ? 4 : 2);
   const int64_t room = p.tb == 2 ? 512 : 256;
   p.qtiles = static_cast<int>(group_tile_bound(M, E, 16 * p.tb));
   p.fr = 2;
@@ -478,9 +486,9 @@ hipError_t launch_grouped_fwd_gemm(const uint16_t* X, int64_t M, const int* offs
   const int64_t N = w.N / E;
   const ExpertPlan p = plan_expert_fwd(M, E, N, w.K);
   if (p.sp.splits > 1 && !part) return hipErrorInvalidValue;
-  const ExpertArgs a{X,   M,  offsets, E,    w.codes, w.absmax_q, w.absmax_scale, N,
-                     w.K, T,  nz,      tscale, Tout,  B,          r,              s,
-                     Y,   p.ptiles, p.qtiles, p.sp.splits, p.sp.cps, p.sp.splits > 1 ? part : nullptr};
+  const ExpertArgs a{X, M, offsets, E, w.codes, w.absmax_q, w.absmax_scale, N, w.K, T, Tout, B, Y,
+                     p.sp.splits > 1 ? part : nullptr, nz, r, p.ptiles, p.qtiles, p.sp.splits,
+                     p.sp.cps, tscale, s};
   auto pick = [&](auto nodq) {
     constexpr bool ND = decltype(nodq)::value;
     if (p.fr == 2)

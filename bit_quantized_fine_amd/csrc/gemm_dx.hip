@@ -493,18 +493,15 @@ __global__ __launch_bounds__(XT) void k_dx_gemm(DxArgs args, Nf4Tables tb) {
     const GroupTile gt = groups.find(t.v - z * slots);
     if (gt.e < 0) return;
     // the last tile of a group runs the narrowest body that holds its rows
+    // (a launch of 64-token tiles was no faster at any number of rows: a backward
+    // of 8 experts of 4096 x 4096 took 78 / 78 us at 16 rows, 119 / 90 at 512)
     const int rows = gt.end - gt.row0;
-    if constexpr (kQ == 256) {
-      if (rows <= 64) {
-        dx_tile<kForm, 64, true, kDrop>(args, dyn, gt.e, gt.row0, gt.end, pt, z);
-        return;
-      }
-      if (rows <= 128) {
-        dx_tile<kForm, 128, true, kDrop>(args, dyn, gt.e, gt.row0, gt.end, pt, z);
-        return;
-      }
-    }
-    dx_tile<kForm, kQ, true, kDrop>(args, dyn, gt.e, gt.row0, gt.end, pt, z);
+    if (rows <= 64)
+      dx_tile<kForm, 64, true, kDrop>(args, dyn, gt.e, gt.row0, gt.end, pt, z);
+    else if (rows <= 128)
+      dx_tile<kForm, 128, true, kDrop>(args, dyn, gt.e, gt.row0, gt.end, pt, z);
+    else
+      dx_tile<kForm, kQ, true, kDrop>(args, dyn, gt.e, gt.row0, gt.end, pt, z);
   } else {
     const int ntiles = args.ptiles * args.qtiles;
     const int lin = xcd_remap_dx(blockIdx.x, static_cast<int>(gridDim.x));
@@ -516,7 +513,7 @@ __global__ __launch_bounds__(XT) void k_dx_gemm(DxArgs args, Nf4Tables tb) {
 
 namespace {
 
-constexpr int kPlainQ = 256;   // tokens a tile without groups
+constexpr int kTileQ = 256;   // tokens a tile
 
 template <int kForm, int kQ, bool kExperts, bool kDrop>
 hipError_t launch_dx_tiles(const uint16_t* dY, int64_t M, const Nf4View& w, int64_t N,
@@ -542,21 +539,21 @@ hipError_t launch_dx_tiles(const uint16_t* dY, int64_t M, const Nf4View& w, int6
 }  // namespace
 
 GemmSplit dx_gemm_split(int64_t M, int64_t N, int64_t K) {
-  return gemm_split((K + XP - 1) / XP * ((M + kPlainQ - 1) / kPlainQ), (N + XN - 1) / XN);
+  return gemm_split((K + XP - 1) / XP * ((M + kTileQ - 1) / kTileQ), (N + XN - 1) / XN);
 }
 
 hipError_t launch_dx_gemm(const uint16_t* dY, int64_t M, const Nf4View& w,
                           const float* G, const uint16_t* A, int r, float s,
                           uint16_t* dX, float* part, const Nf4Tables& tb, hipStream_t stream,
                           const Drop& d) {
-  const int qtiles = static_cast<int>((M + kPlainQ - 1) / kPlainQ);
+  const int qtiles = static_cast<int>((M + kTileQ - 1) / kTileQ);
   const GemmSplit sp = dx_gemm_split(M, w.N, w.K);
   if (w.dense && d.on()) return hipErrorInvalidValue;
-  auto launch = w.dense ? launch_dx_tiles<kFormDense, kPlainQ, false, false>
-                : d.on() ? (w.dq ? launch_dx_tiles<kFormDq, kPlainQ, false, true>
-                                 : launch_dx_tiles<kFormNoDq, kPlainQ, false, true>)
-                         : (w.dq ? launch_dx_tiles<kFormDq, kPlainQ, false, false>
-                                 : launch_dx_tiles<kFormNoDq, kPlainQ, false, false>);
+  auto launch = w.dense ? launch_dx_tiles<kFormDense, kTileQ, false, false>
+                : d.on() ? (w.dq ? launch_dx_tiles<kFormDq, kTileQ, false, true>
+                                 : launch_dx_tiles<kFormNoDq, kTileQ, false, true>)
+                         : (w.dq ? launch_dx_tiles<kFormDq, kTileQ, false, false>
+                                 : launch_dx_tiles<kFormNoDq, kTileQ, false, false>);
   prof_begin(1, stream);
   hipError_t e = launch(dY, M, w, w.N, G, A, r, s, dX, part, tb, stream, qtiles, sp, nullptr, 0, d);
   if (e == hipSuccess && sp.splits > 1)
@@ -566,7 +563,7 @@ hipError_t launch_dx_gemm(const uint16_t* dY, int64_t M, const Nf4View& w,
 }
 
 GemmSplit grouped_dx_split(int64_t M, int E, int64_t N, int64_t K) {
-  return gemm_split((K + XP - 1) / XP * group_tile_bound(M, E, grouped_tile(M, E)),
+  return gemm_split((K + XP - 1) / XP * group_tile_bound(M, E, kTileQ),
                     (N + XN - 1) / XN);
 }
 
@@ -575,18 +572,12 @@ hipError_t launch_grouped_dx_gemm(const uint16_t* dY, int64_t M, const int* offs
                                   float s, uint16_t* dX, float* part, const Nf4Tables& tb,
                                   hipStream_t stream, const Drop& d) {
   const int64_t N = w.N / E;
-  const int q = grouped_tile(M, E);
-  const int qtiles = static_cast<int>(group_tile_bound(M, E, q));
+  const int qtiles = static_cast<int>(group_tile_bound(M, E, kTileQ));
   const GemmSplit sp = grouped_dx_split(M, E, N, w.K);
-  auto pick = [&](auto qc) {
-    constexpr int Q = decltype(qc)::value;
-    return d.on() ? (w.dq ? launch_dx_tiles<kFormDq, Q, true, true>
-                          : launch_dx_tiles<kFormNoDq, Q, true, true>)
-                  : (w.dq ? launch_dx_tiles<kFormDq, Q, true, false>
-                          : launch_dx_tiles<kFormNoDq, Q, true, false>);
-  };
-  auto launch = q == 64 ? pick(std::integral_constant<int, 64>{})
-                        : pick(std::integral_constant<int, 256>{});
+  auto launch = d.on() ? (w.dq ? launch_dx_tiles<kFormDq, kTileQ, true, true>
+                               : launch_dx_tiles<kFormNoDq, kTileQ, true, true>)
+                       : (w.dq ? launch_dx_tiles<kFormDq, kTileQ, true, false>
+                               : launch_dx_tiles<kFormNoDq, kTileQ, true, false>);
   prof_begin(1, stream);
   hipError_t e = launch(dY, M, w, N, G, A, r, s, dX, part, tb, stream, qtiles, sp, offsets, E, d);
   if (e == hipSuccess && sp.splits > 1)

@@ -129,8 +129,6 @@ hipError_t launch_grad_a(const uint16_t* X, int64_t M, int64_t K, const float* G
 // and B [E][r][N].  Rows outside all groups are neither read nor written.
 // ---------------------------------------------------------------------------
 
-// Tokens a dX tile holds (256 or 64) for M rows of E experts.
-int grouped_tile(int64_t M, int E);
 GemmSplit grouped_fwd_split(int64_t M, int E, int64_t N, int64_t K);
 GemmSplit grouped_dx_split(int64_t M, int E, int64_t N, int64_t K);
 // T is final (nz = 0), or nz partial sums [nz][M][r] that the kernel adds up,

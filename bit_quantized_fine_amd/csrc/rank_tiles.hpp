@@ -4,6 +4,8 @@
 // loop and the stores of a tile of C[q, p] = sum_k P[p, k] . Q[q, k].
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "dropout.hpp"
 
@@ -18,8 +20,8 @@ struct OpParams {
   int64_t ld;      // leading dimension of the source array (elements)
   int64_t nrows;   // extent of the tile-row index
   int64_t nred;    // extent of the reduction index
-  float scale;     // fp32 sources: value = scale * src
   int64_t drow0;   // masked operands: row of the whole tensor that ptr points to
+  float scale;     // fp32 sources: value = scale * src
 };
 
 __device__ __forceinline__ u32x4 ld16(const void* p) {
@@ -50,7 +52,7 @@ struct Bf16Nat {   // element (row, k) = src[row * ld + k]
   OpParams o;
   int64_t row0;
   u32x4 r[CPT];
-  DropKey key;               // DROP only
+  std::conditional_t<DROP, DropKey, NoDropKey> key;
   u32x4 mask[DROP ? CPT : 1];
   __device__ void load(int kt, int tid) {
     const uint16_t* src = static_cast<const uint16_t*>(o.ptr);
@@ -124,7 +126,7 @@ struct Bf16RedMajor {   // element (row, k) = src[k * ld + row], bf16
   OpParams o;
   int64_t row0;
   u32x4 r[CPT];
-  DropKey key;               // DROP only
+  std::conditional_t<DROP, DropKey, NoDropKey> key;
   u32x4 mask[DROP ? CPT : 1];
   __device__ void load(int kt, int tid) {
     const uint16_t* src = static_cast<const uint16_t*>(o.ptr);
