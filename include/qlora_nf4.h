@@ -464,7 +464,8 @@ int qlora_linear_dropout_bwd(const uint16_t* dY, const uint16_t* X, int64_t M,
  * Backward, on each expert's rows: G = dY . B_e^T, dX = dY . deq(W_e) +
  * s . G . A_e^T (skipped if dX == NULL), dA_e = s . X^T . G, dB_e = s . T^T . dY,
  * with T_saved the forward's T or NULL to recompute it.
- * Other limits and errors as qlora_q4_linear_fwd / qlora_q4_linear_bwd.
+ * No output overlaps an input.  Other limits and errors as
+ * qlora_q4_linear_fwd / qlora_q4_linear_bwd.
  */
 size_t qlora_grouped_fwd_workspace_bytes(int64_t M, int E, int64_t N, int64_t K, int r);
 size_t qlora_grouped_bwd_workspace_bytes(int64_t M, int E, int64_t N, int64_t K, int r);
@@ -502,7 +503,8 @@ int qlora_grouped_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const in
  *   X, out, dOut [tokens, K], Xs, Y, dY [n, K] bf16, 16-byte aligned; the int32
  *   and fp32 vectors 4-byte aligned.  K % 8 == 0, 8 <= K <= 2^22,
  *   1 <= topk <= 64, 0 <= n <= 2^30.  inverse must name each row at most once
- *   (as the plan does); entries outside [0, n) count as -1.
+ *   (as the plan does); entries outside [0, n) count as -1.  No output overlaps
+ *   an input.
  * Errors: QLORA_ERR_EXPERT (E or topk), QLORA_ERR_SHAPE, QLORA_ERR_NULL,
  * QLORA_ERR_ALIGN, QLORA_ERR_WORKSPACE, QLORA_ERR_HIP.
  */
