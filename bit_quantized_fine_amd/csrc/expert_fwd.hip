@@ -9,14 +9,18 @@
 // chunk, and dword t of them, dequantized, is the lane's share of the 16 x 32
 // operand of step t (k = 32 g + 8 t .. + 7).  X is what the waves share: it is
 // staged through LDS in the same k order, double-buffered, one barrier a chunk,
-// its 16-byte pieces XOR-swizzled by row.  Per 128-k chunk and 256 rows the
-// LDS serves 128 KB of level lookups whatever TB is and 8 x 4 TB KB of X
-// reads, against 64 TB MFMAs a SIMD.
+// its 16-byte pieces XOR-swizzled by row; with 192 tokens it fills the 160 KB of
+// LDS together with the level table (half chunks, which need less, and two
+// barriers a chunk: 2% slower).  The operands of the next step are dequantized
+// while the MFMAs of the current one run.  X waits one or two chunks ahead in
+// registers.
 //
-// The operands of the next step are dequantized while the MFMAs of the current
-// one run.  X waits one or two chunks ahead in registers.  With TB = 16 a chunk's
-// X (64 KB twice) does not fit beside the level table, so it is staged as two
-// half chunks, steps 0-1 and steps 2-3.
+// Measured: 8 experts of 11008 x 4096, r = 64, 8192 rows: 755 us, 1.00
+// PFLOP/s where a large matrix product of the library reaches 1.38: bound by the
+// chip's power.  Of the loop's time the lookups take 19%, scaling and packing
+// 11%, X's reads 7% (timed without each).  The same experts with 96 rows: 67 us,
+// 2.7 TB/s of codes; 602 workgroups on 512 places, whose second round is short of
+// work.
 //
 // The offsets are read on the GPU: the grid holds the most tiles the groups
 // could make, a workgroup finds its expert and rows in them, and the last tile
@@ -41,9 +45,7 @@ template <int FR, int TB>
 struct ExpertTile {
   static constexpr int ROWS = 16 * FR * EW;       // weight rows
   static constexpr int TQ = 16 * TB;              // tokens
-  static constexpr int SUB = TB > 8 ? 2 : 1;      // X stagings of a 128-k chunk
-  static constexpr int STEPS = 4 / SUB;           // 32-k steps of one staging
-  static constexpr int PPR = 4 * STEPS;           // 16-byte pieces of a token row
+  static constexpr int PPR = 16;                  // 16-byte pieces of a token row's chunk
   static constexpr int XBUF = TQ * PPR * 8;       // elements of one X buffer
   static constexpr int PIECES = TQ * PPR;
   static constexpr int PP = (PIECES + ET - 1) / ET;   // pieces a thread stages
@@ -80,10 +82,9 @@ template <int FR, int TB, bool NODQ>
 __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, int e, int64_t q0,
                                             int64_t mend, int pt, int z) {
   using Tile = ExpertTile<FR, TB>;
-  constexpr int SUB = Tile::SUB, STEPS = Tile::STEPS, PPR = Tile::PPR, PP = Tile::PP;
+  constexpr int PPR = Tile::PPR, PP = Tile::PP;
   constexpr int XST = Tile::XST, D = Tile::D;
-  constexpr int GB = TB < 4 ? TB : 4, NG = TB / GB;   // token subtiles a group, groups
-  constexpr int U = TB == 4 ? 2 : 1;                  // steps dequantized together
+  constexpr int GB = TB >= 8 ? 2 : TB, NG = TB / GB;   // token subtiles a group, groups
   uint16_t* const Xs = reinterpret_cast<uint16_t*>(dyn + kRepTabBytes);
   const int tid = threadIdx.x;
   const int wave = wave_id(), lane = tid & 63;
@@ -131,24 +132,23 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
     }
   };
 
-  // X piece idx = tid + 512 j: token row idx / PPR, piece q = idx % PPR.  Piece q
-  // = g + 4 i is what lane group g takes at step i of the staging: k = 128 c +
-  // 8 (4 g + 2 h + i) .. + 7 (h: the half chunk).  In this order a 16-byte read,
-  // which the LDS serves in groups of 16 lanes of two g's, meets no bank twice;
-  // with q = 4 g + i it met every second one twice.
+  // X piece idx = tid + 512 j: token row idx / 16, piece q = idx % 16.  Piece q = g
+  // + 4 i is what lane group g takes at step i: k = 128 c + 8 (4 g + i) .. + 7.  In
+  // this order a 16-byte read, which the LDS serves in groups of 16 lanes of two
+  // g's, meets no bank twice; with q = 4 g + i it met every second one twice (784
+  // instead of 822 us for the 8192 rows above).
   // (A thread's pieces are whole rows apart, so they share q and the swizzle.)
   static_assert(ET % PPR == 0 && (ET / PPR) % 16 == 0, "piece rows apart");
   const int xrow = tid / PPR, xq = tid % PPR;
-  const int xcp = SUB == 1 ? xq : 4 * (xq >> 1) + (xq & 1);
+  const int xcp = 4 * (xq & 3) + (xq >> 2);
   const uint32_t xsrc = static_cast<uint32_t>(xrow * K32 + 8 * xcp) * 2u;
   const uint32_t xstep = static_cast<uint32_t>(ET / PPR * K32) * 2u;
   uint16_t* const xdst = Xs + (xrow * PPR + xslot<PPR>(xrow, xq)) * 8;
   const bool xlive = Tile::PIECES % ET == 0 || tid < Tile::PIECES;
   u32x4 xw[XST][PP];
-  auto load_x = [&](int t, int st) {   // staging t of this split (t = SUB c + h)
-    const int k0 = SUB == 1 ? 128 * t : 128 * (t >> 1) + 16 * (t & 1);
-    const bool ok = xlive && t < SUB * nchunks && k0 + 8 * xcp < K32;
-    const uint32_t o = ok ? xsrc + 2u * k0 : kOffNone;   // (+ j xstep < 2^31: stays past the end)
+  auto load_x = [&](int c, int st) {
+    const bool ok = xlive && c < nchunks && 128 * c + 8 * xcp < K32;
+    const uint32_t o = ok ? xsrc + 256u * c : kOffNone;   // (+ j xstep < 2^31: stays past the end)
 #pragma unroll
     for (int j = 0; j < PP; ++j) xw[st][j] = buf_load16(rx, o + j * xstep);
   };
@@ -166,7 +166,8 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
 #pragma unroll
     for (int b = 0; b < TB; ++b) acc[f][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // The level pairs of the 8 codes of step t, and bf16_rne(fl32(level * c)).
+  // The level pairs of the 8 codes of step t, and bf16_rne(fl32(level * c)) of a
+  // pair.
   struct Pairs {
     f32x2 v[4];
   };
@@ -176,92 +177,94 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
     return Pairs{{rep_lookup<0>(ta, w), rep_lookup<1>(ta, w), rep_lookup<2>(ta, w),
                   rep_lookup<3>(ta, w)}};
   };
-  auto scaled = [&](int st, int f, const Pairs& p) {
-    const float ch = NODQ ? cd[st][f] : static_cast<float>(ce[st][f]) * cd[st][f];
-    return u32x4{pack_bf16x2(p.v[0].x * ch, p.v[0].y * ch),
-                 pack_bf16x2(p.v[1].x * ch, p.v[1].y * ch),
-                 pack_bf16x2(p.v[2].x * ch, p.v[2].y * ch),
-                 pack_bf16x2(p.v[3].x * ch, p.v[3].y * ch)};
+  auto constant = [&](int st, int f) {
+    return NODQ ? cd[st][f] : static_cast<float>(ce[st][f]) * cd[st][f];
+  };
+  auto scaled = [&](const Pairs& p, int t, float ch) {
+    return pack_bf16x2(p.v[t].x * ch, p.v[t].y * ch);
   };
   // step i of the staging, token subtile b: token row 16 b + li, whose swizzle
   // is that of row li
   const uint16_t* const xsrow = Xs + li * PPR * 8;
-  const int xsw = PPR == 16 ? li : li >> 1;
   auto read_x = [&](int buf, int i, int b) {
-    const int q = SUB == 1 ? 4 * g + i : 2 * g + i;
-    return *reinterpret_cast<const u32x4*>(xsrow + 8 * (q ^ xsw) + buf * Tile::XBUF +
+    return *reinterpret_cast<const u32x4*>(xsrow + 8 * ((g + 4 * i) ^ li) + buf * Tile::XBUF +
                                            16 * b * PPR * 8);
   };
 
 #pragma unroll
   for (int i = 0; i < D; ++i) load_codes(c0 + i, i);
-  load_x(SUB * c0, 0);
-  if constexpr (XST == 2) load_x(SUB * c0 + 1, 1);
+  load_x(c0, 0);
+  if constexpr (XST == 2) load_x(c0 + 1, 1);
   __syncthreads();   // the level table
   store_x(0, 0);
-  if constexpr (XST == 2) load_x(SUB * c0 + 2, 0); else load_x(SUB * c0 + 1, 0);
-  u32x4 af[2][U][FR];   // operands of the current and the next U steps
+  load_x(c0 + XST, 0);
+  u32x4 af[2][FR];   // operands of the current and the next step
 #pragma unroll
-  for (int i = 0; i < U; ++i)
+  for (int f = 0; f < FR; ++f) {
+    const Pairs p = lookup(0, f, 0);
+    const float ch = constant(0, f);
 #pragma unroll
-    for (int f = 0; f < FR; ++f) af[0][i][f] = scaled(0, f, lookup(0, f, i));
+    for (int t = 0; t < 4; ++t) af[0][f][t] = scaled(p, t, ch);
+  }
   __syncthreads();
-  // Chunk c, codes in stage ST.  A staging's products run in groups of GB token
-  // subtiles of one step.  While a group's MFMAs run, the X operands of the next
-  // group and (at the first group of U steps) the level pairs of the next U
-  // steps are on their way from LDS; the pairs become operands behind the last
-  // group's MFMAs.  The scheduling barriers keep that order: left alone, the
-  // compiler issues a pair's two lookups next to their use and waits for each.
+  // Chunk c, codes in stage ST.  A step's products run in groups of GB token
+  // subtiles.  While a group's MFMAs run, the X operands of the next group and (at
+  // a step's first group) the level pairs of the next step are on their way from
+  // LDS; the pairs become operands one at a time between the later MFMAs, whose
+  // pipe they leave busy.  The scheduling barriers keep that order: left alone,
+  // the compiler issues a pair's two lookups next to their use and waits for each.
+  // Groups of 2 subtiles against 4 and 3: 754, 770 and 764 us (192-token tiles, 8
+  // experts of 11008 x 4096, 8192 rows); pairs scaled in one run behind a step's
+  // last group: 761.  All of it is within a few percent because the chip is at its
+  // power limit here: the main loop runs at 1.9 to 2.0 GHz, its MFMAs taking 62%
+  // of the cycles.
+  constexpr int SLOTS = TB * FR, PAIRS = 4 * FR, SLOT0 = SLOTS / 3;   // of a step
   auto chunk = [&](int c, auto stc) {
     constexpr int ST = decltype(stc)::value;
+    constexpr int buf = ST & 1, xs = XST == 2 ? (ST + 1) & 1 : 0;
+    u32x4 xf[2][GB];
 #pragma unroll
-    for (int h = 0; h < SUB; ++h) {
-      const int buf = SUB == 1 ? ST & 1 : h;
-      const int t = SUB * c + h;
-      const int xs = XST == 2 ? (ST + 1) & 1 : 0;
-      u32x4 xf[2][GB];
+    for (int b = 0; b < GB; ++b) xf[0][b] = read_x(buf, 0, b);
+    Pairs pr[FR];
+    float ch[FR];
 #pragma unroll
-      for (int b = 0; b < GB; ++b) xf[0][b] = read_x(buf, 0, b);
-      Pairs pr[U][FR];
+    for (int k = 0; k < 4 * NG; ++k) {
+      const int i = k / NG;                      // step of the chunk
+      const int nst = i < 3 ? ST : (ST + 1) % D;   // codes of the next step
+      if (k % NG == 0) {
 #pragma unroll
-      for (int k = 0; k < STEPS * NG; ++k) {
-        const int i = k / NG;                      // step of the staging
-        const int unit = (STEPS * h + i) / U;      // run of U steps of the chunk
-        const bool first = k % (U * NG) == 0, last = k % (U * NG) == U * NG - 1;
-        const int nst = U * (unit + 1) < 4 ? ST : (ST + 1) % D;   // codes of the next run
-        if (first) {
+        for (int f = 0; f < FR; ++f) pr[f] = lookup(nst, f, (i + 1) % 4);
+        if (i == 0 || i == 3) {
 #pragma unroll
-          for (int j = 0; j < U; ++j)
-#pragma unroll
-            for (int f = 0; f < FR; ++f) pr[j][f] = lookup(nst, f, (U * (unit + 1) + j) % 4);
-        }
-        if (k + 1 < STEPS * NG) {
-#pragma unroll
-          for (int b = 0; b < GB; ++b)
-            xf[(k + 1) & 1][b] = read_x(buf, (k + 1) / NG, GB * ((k + 1) % NG) + b);
-        }
-        if (k == 0) {   // X of the next staging, then the registers' next load
-          store_x(xs, buf ^ 1);
-          load_x(XST == 2 ? t + 3 : t + 2, xs);
-        }
-        if (first && unit == 4 / U - 1) load_codes(c + D, ST);   // stage ST is used up
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int b = 0; b < GB; ++b)
-#pragma unroll
-          for (int f = 0; f < FR; ++f)
-            acc[f][GB * (k % NG) + b] =
-                mfma16(af[unit & 1][i % U][f], xf[k & 1][b], acc[f][GB * (k % NG) + b]);
-        __builtin_amdgcn_sched_barrier(0);
-        if (last) {
-#pragma unroll
-          for (int j = 0; j < U; ++j)
-#pragma unroll
-            for (int f = 0; f < FR; ++f) af[(unit + 1) & 1][j][f] = scaled(nst, f, pr[j][f]);
+          for (int f = 0; f < FR; ++f) ch[f] = constant(nst, f);
         }
       }
-      __syncthreads();
+      if (k + 1 < 4 * NG) {
+#pragma unroll
+        for (int b = 0; b < GB; ++b)
+          xf[(k + 1) & 1][b] = read_x(buf, (k + 1) / NG, GB * ((k + 1) % NG) + b);
+      }
+      if (k == 0) {   // X of the next chunk, then the registers' next load
+        store_x(xs, buf ^ 1);
+        load_x(c + 1 + XST, xs);
+      }
+      if (k == 3 * NG) load_codes(c + D, ST);   // stage ST is used up
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int b = 0; b < GB; ++b)
+#pragma unroll
+        for (int f = 0; f < FR; ++f) {
+          acc[f][GB * (k % NG) + b] =
+              mfma16(af[i & 1][f], xf[k & 1][b], acc[f][GB * (k % NG) + b]);
+          const int slot = (k % NG * GB + b) * FR + f;
+#pragma unroll
+          for (int u = 0; u < PAIRS; ++u)
+            if (SLOT0 + u * (SLOTS - SLOT0) / PAIRS == slot)
+              af[(i + 1) & 1][u / 4][u % 4] = scaled(pr[u / 4], u % 4, ch[u / 4]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
     }
+    __syncthreads();
   };
   // A chunk count that D does not divide adds passes over chunks past the end,
   // all zeros.
@@ -439,9 +442,9 @@ struct ExpertPlan {
 constexpr int64_t kFewRows = 16;
 // Rows of an average expert above which a tile holds 64 tokens, and 192 (the
 // narrower bodies take over in the last tile of a group).  Same experts, 32 /
-// 64 / 192 tokens a tile: 37 / 38 / 46 us at 192 rows, 49 / 46 / 48 at 256, 52 /
-// 48 / 48 at 384, 119 / 116 / 80 at 1024; 32 experts of 1024 x 2048: 29 / 31 / 35
-// us at 768 rows, 36 / 34 / 35 at 1024, 50 / 54 / 43 at 2048.
+// 64 / 192 tokens a tile: 35 / 37 / 39 us at 192 rows, 51 / 38 / 40 at 256, 51 /
+// 40 / 40 at 320, 71 / 65 / 50 at 512; 32 experts of 1024 x 2048: 27 / 28 / 30 us
+// at 768 rows, 35 / 29 / 30 at 1024, 45 / 44 / 36 at 1536.
 constexpr int64_t kMidMean = 24, kWideMean = 40;
 
 // Token subtiles by the rows of an average expert, 256 weight rows a workgroup
