@@ -15,12 +15,11 @@
 // while the MFMAs of the current one run.  X waits one or two chunks ahead in
 // registers.
 //
-// Measured: 8 experts of 11008 x 4096, r = 64, 8192 rows: 755 us, 1.00
+// Measured: 8 experts of 11008 x 4096, r = 64, 8192 rows: 740 us, 1.02
 // PFLOP/s where a large matrix product of the library reaches 1.38: bound by the
 // chip's power.  Of the loop's time the lookups take 19%, scaling and packing
-// 11%, X's reads 7% (timed without each).  The same experts with 96 rows: 67 us,
-// 2.7 TB/s of codes; 602 workgroups on 512 places, whose second round is short of
-// work.
+// 11%, X's reads 7% (timed without each).  The same experts with 96 rows: 54 us,
+// 2.9 TB/s of codes.
 //
 // The offsets are read on the GPU: the grid holds the most tiles the groups
 // could make, a workgroup finds its expert and rows in them, and the last tile
@@ -49,7 +48,8 @@ struct ExpertTile {
   static constexpr int XBUF = TQ * PPR * 8;       // elements of one X buffer
   static constexpr int PIECES = TQ * PPR;
   static constexpr int PP = (PIECES + ET - 1) / ET;   // pieces a thread stages
-  static constexpr int D = 2;                     // code stages (128-k chunks)
+  static constexpr bool STREAM = FR == 1 && TB <= 2;   // bound by the stream of codes
+  static constexpr int D = STREAM ? 4 : 2;        // code stages (128-k chunks)
   static constexpr int XST = TB > 8 ? 1 : 2;      // register stages of X
   static constexpr int MAIN = kRepTabBytes + 2 * XBUF * 2;
   static constexpr int TAIL = ROWS * 128 + TQ * 256;   // B tile, T hi and lo tiles
@@ -99,7 +99,11 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
   // rows past W and tokens past the tile read as zero
   const uint32_t nb = static_cast<uint32_t>(NW * K / kBlock);
   const BufRes rc = make_bufres(a.codes, static_cast<uint32_t>(NW * K / 2));
-  const BufRes re = make_bufres(a.absmax_q, nb);
+  // (the windows below read whole aligned dwords of the 8-bit constants)
+  constexpr bool WIN = Tile::STREAM && !NODQ;
+  const uint32_t eoff =
+      WIN ? static_cast<uint32_t>(reinterpret_cast<uintptr_t>(a.absmax_q)) & 3u : 0u;
+  const BufRes re = make_bufres(a.absmax_q - eoff, WIN ? (eoff + nb + 3u) & ~3u : nb);
   const BufRes rd = make_bufres(a.absmax_scale, (NODQ ? nb : (nb + kGroup - 1) / kGroup) * 4u);
   const int64_t tile_rows = mend - q0 < Tile::TQ ? mend - q0 : Tile::TQ;
   const BufRes rx = make_bufres(a.X + q0 * K, static_cast<uint32_t>(tile_rows * K * 2));
@@ -123,12 +127,45 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
       cw[st][f] = buf_load16(rc, live ? cb[f] + 64u * c : kOffNone);
       const uint32_t b = eb[f] + 2u * c;
       if constexpr (NODQ) {
-        ce[st][f] = 1u;
         cd[st][f] = buf_load_f32(rd, blk ? b * 4u : kOffNone);
-      } else {
+      } else if constexpr (!WIN) {
         ce[st][f] = buf_load_u8(re, blk ? b : kOffNone);
         cd[st][f] = buf_load_f32(rd, blk ? (b / kGroup) * 4u : kOffNone);
       }
+    }
+  };
+
+  // Tiles of few tokens are bound by the code stream's vector memory instructions:
+  // without those of the constants, two a chunk and fragment, 96 rows of 8 experts
+  // of 11008 x 4096 took 61 us instead of 77.  So their constants come 16 chunks at
+  // a time, in five loads: lane group g holds the 8-bit constants of blocks 8 g ..
+  // + 7 of a window of 32 (three aligned dwords, shifted), every lane the window's
+  // two possible second-level scales, and a chunk takes its constants from the
+  // lanes that hold them: 67 us, and 65 with four chunks of codes in flight.  (With
+  // more registers in use, the window's spill or cost more than they save: 39
+  // against 38 us at 256 rows of 8 experts of 4096 x 4096.)
+  uint32_t wraw[FR][3], wlo[FR], whi[FR];
+  float dnext[FR][2], dlo[FR], dhi[FR];
+  auto window_load = [&](int w) {
+#pragma unroll
+    for (int f = 0; f < FR; ++f) {
+      const uint32_t b = eb[f] - (g >> 1) + 2u * c0 + 32u * w;   // first block of the window
+      const uint32_t at = (eoff + b + 8u * g) & ~3u;
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        wraw[f][i] = __builtin_amdgcn_raw_buffer_load_b32(re, at + 4u * i, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) dnext[f][i] = buf_load_f32(rd, (b / kGroup + i) * 4u);
+    }
+  };
+  auto window_take = [&]() {
+#pragma unroll
+    for (int f = 0; f < FR; ++f) {
+      const uint32_t sh = (eoff + eb[f] - (g >> 1) + 2u * c0) & 3u;
+      wlo[f] = __builtin_amdgcn_alignbyte(wraw[f][1], wraw[f][0], sh);
+      whi[f] = __builtin_amdgcn_alignbyte(wraw[f][2], wraw[f][1], sh);
+      dlo[f] = dnext[f][0];
+      dhi[f] = dnext[f][1];
     }
   };
 
@@ -177,8 +214,23 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
     return Pairs{{rep_lookup<0>(ta, w), rep_lookup<1>(ta, w), rep_lookup<2>(ta, w),
                   rep_lookup<3>(ta, w)}};
   };
-  auto constant = [&](int st, int f) {
-    return NODQ ? cd[st][f] : static_cast<float>(ce[st][f]) * cd[st][f];
+  // Constant of chunk c, codes in stage st, row fragment f (the half chunk past K:
+  // 0).
+  auto constant = [&](int c, int st, int f) {
+    if constexpr (NODQ) {
+      return cd[st][f];
+    } else if constexpr (!WIN) {
+      return static_cast<float>(ce[st][f]) * cd[st][f];
+    } else {
+      const int t = c - c0;
+      const uint32_t b = eb[f] + 2u * c, b0 = eb[f] - (g >> 1) + 2u * (c0 + (t & ~15));
+      const uint32_t lo = wlo[f], hi = whi[f];
+      const uint32_t q =
+          __builtin_amdgcn_ds_bpermute(4 * (li + 16 * ((t & 15) >> 2)), (t & 2) ? hi : lo);
+      const float e = static_cast<float>((q >> (16 * (t & 1) + 8 * (g >> 1))) & 255u);
+      const float d0 = dlo[f], d1 = dhi[f];
+      return 2 * c + (g >> 1) < KB ? e * (b / kGroup == b0 / kGroup ? d0 : d1) : 0.f;
+    }
   };
   auto scaled = [&](const Pairs& p, int t, float ch) {
     return pack_bf16x2(p.v[t].x * ch, p.v[t].y * ch);
@@ -193,18 +245,24 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
 
 #pragma unroll
   for (int i = 0; i < D; ++i) load_codes(c0 + i, i);
+  if constexpr (WIN) window_load(0);
   load_x(c0, 0);
   if constexpr (XST == 2) load_x(c0 + 1, 1);
   __syncthreads();   // the level table
   store_x(0, 0);
   load_x(c0 + XST, 0);
+  if constexpr (WIN) {
+    window_take();
+    window_load(1);
+  }
   u32x4 af[2][FR];   // operands of the current and the next step
+  float ch[FR];      // constants of the codes that are next to be scaled
 #pragma unroll
   for (int f = 0; f < FR; ++f) {
     const Pairs p = lookup(0, f, 0);
-    const float ch = constant(0, f);
+    ch[f] = constant(c0, 0, f);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) af[0][f][t] = scaled(p, t, ch);
+    for (int t = 0; t < 4; ++t) af[0][f][t] = scaled(p, t, ch[f]);
   }
   __syncthreads();
   // Chunk c, codes in stage ST.  A step's products run in groups of GB token
@@ -226,7 +284,6 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
 #pragma unroll
     for (int b = 0; b < GB; ++b) xf[0][b] = read_x(buf, 0, b);
     Pairs pr[FR];
-    float ch[FR];
 #pragma unroll
     for (int k = 0; k < 4 * NG; ++k) {
       const int i = k / NG;                      // step of the chunk
@@ -234,9 +291,15 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
       if (k % NG == 0) {
 #pragma unroll
         for (int f = 0; f < FR; ++f) pr[f] = lookup(nst, f, (i + 1) % 4);
-        if (i == 0 || i == 3) {
+        if (i == 3) {
+          if constexpr (WIN) {
+            if (((c + 1 - c0) & 15) == 0) {
+              window_take();
+              window_load(((c + 1 - c0) >> 4) + 1);
+            }
+          }
 #pragma unroll
-          for (int f = 0; f < FR; ++f) ch[f] = constant(nst, f);
+          for (int f = 0; f < FR; ++f) ch[f] = constant(c + 1, nst, f);
         }
       }
       if (k + 1 < 4 * NG) {
@@ -271,6 +334,10 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
   for (int c = c0; c < nchunks; c += D) {
     chunk(c, std::integral_constant<int, 0>{});
     chunk(c + 1, std::integral_constant<int, 1>{});
+    if constexpr (D == 4) {
+      chunk(c + 2, std::integral_constant<int, 2>{});
+      chunk(c + 3, std::integral_constant<int, 3>{});
+    }
   }
 
   // LoRA update (the first split only): 64 ranks at a time, the B tile [64

@@ -28,6 +28,11 @@ EDGES = [
     ([17], 128, 128, 16, {}),
     ([16, 17, 32, 33, 1, 15, 31, 34], 264, 192, 24, dict(dq=False)),
     ([24] * 40, 4096, 64, 8, {}),                         # 256 weight rows a workgroup
+    # the same, constants in windows of 2048 columns: split inside and between them
+    ([17, 3], 256, 64 * 67, 8, {}),
+    ([16, 17, 0, 9], 256, 64 * 130, 16, dict(p=0.1)),
+    ([20, 25], 128, 128 * 40, 8, dict(book="fp4")),
+    ([20] * 200, 128, 64 * 34, 8, {}),                    # not split
     # 64 tokens a tile
     ([64, 65, 16, 17, 33, 32, 1, 48], 264, 192, 16, dict(dq=False, p=0.1)),
     ([31, 33] * 32, 2048, 128, 8, dict(p=0.1)),           # 256 weight rows a workgroup
@@ -165,6 +170,25 @@ def test_two_graphs_share_a_workspace():
         torch.cuda.synchronize()
         for a, b in zip(want[i], outs[i]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("sizes", [[2, 3], [20, 15], [40, 90]])
+@pytest.mark.parametrize("shift", [1, 2, 3])
+def test_constants_at_any_address(sizes, shift):
+    """The 8-bit constants may start at any byte."""
+    need_gpu()
+    say(f"constants {shift} bytes off, sizes={sizes}")
+    g = Grouped(sizes, 256, 64 * 35, 16, seed=6)
+    want = g.check()
+    buf = torch.full((g.w.absmax_q.numel() + 8,), 0xFF, dtype=torch.uint8, device=dev())
+    moved = buf[shift:shift + g.w.absmax_q.numel()]
+    moved.copy_(g.w.absmax_q)
+    g.w = g.w._replace(absmax_q=moved)
+    Y, T = g.fwd()
+    out = (Y, T) + g.bwd(T)
+    torch.cuda.synchronize()
+    for a, b in zip(want, out):
+        assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("tokens", [8, 100])
