@@ -1,7 +1,9 @@
-// Arguments of the grouped forward kernels and the dealing out of their tiles.
+// Arguments of the kernels of the layer grouped by expert and the dealing out of
+// their tiles.  (expert_dx.hip takes dY for X, G for T, A for B and dX for Y.)
 #pragma once
 
 #include "group_tiles.hpp"
+#include "kernels.hpp"
 
 namespace qnf4 {
 
@@ -27,6 +29,8 @@ struct ExpertArgs {
   // private array)
   float tscale;       // of T's partial sums
   float s;
+  const uint64_t* state;   // dropout (dX only)
+  uint32_t thr;
 };
 
 // The workgroup's tile: its token rows, weight row tile pt and split z of the
@@ -46,5 +50,12 @@ __device__ __forceinline__ GroupTile expert_deal(const ExpertArgs& a, GroupTiles
 
 // The few-token form (expert_few.hip); fills in the tiles.
 hipError_t launch_expert_few(ExpertArgs a, bool dq, const Nf4Tables& tb, hipStream_t stream);
+
+// dX for many rows (expert_dx.hip), without a split reduction.
+bool expert_dx_fits(int64_t M, int E, int64_t K);
+hipError_t launch_expert_dx(const uint16_t* dY, int64_t M, const int* offsets, int E,
+                            const Nf4View& w, const float* G, const uint16_t* A, int r, float s,
+                            uint16_t* dX, const Nf4Tables& tb, hipStream_t stream,
+                            const Drop& d);
 
 }  // namespace qnf4

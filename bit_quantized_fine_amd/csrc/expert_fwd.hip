@@ -558,7 +558,7 @@ hipError_t launch_grouped_fwd_gemm(const uint16_t* X, int64_t M, const int* offs
   if (p.sp.splits > 1 && !part) return hipErrorInvalidValue;
   const ExpertArgs a{X, M, offsets, E, w.codes, w.absmax_q, w.absmax_scale, N, w.K, T, Tout, B, Y,
                      p.sp.splits > 1 ? part : nullptr, nz, r, p.ptiles, p.qtiles, p.sp.splits,
-                     p.sp.cps, tscale, s};
+                     p.sp.cps, tscale, s, nullptr, 0};
   auto pick = [&](auto nodq) {
     constexpr bool ND = decltype(nodq)::value;
     if (p.fr == 2)

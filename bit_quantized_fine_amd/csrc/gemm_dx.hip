@@ -33,7 +33,8 @@
 // kExperts instantiates it over token rows grouped by expert (see the forward
 // GEMM): the reduction runs over the rows of the tile's expert.  With kQ = 64
 // a tile is 64 tokens and the four wave columns split the 128 output columns;
-// kQ = 128 lies between.
+// kQ = 128 lies between.  It serves the calls of few tiles, whose reduction it can
+// split; with enough tiles to fill the machine expert_dx.hip is faster.
 //
 // kDrop is the backward of the layer whose adapter input was dropped out:
 // dX = dY . deq(W) + s . mask . (G . A^T), s holding the mask's scale.  The
@@ -47,6 +48,7 @@
 
 #include "device_common.hpp"
 #include "dropout.hpp"
+#include "expert_args.hpp"
 #include "group_tiles.hpp"
 #include "kernels.hpp"
 
@@ -579,7 +581,10 @@ hipError_t launch_grouped_dx_gemm(const uint16_t* dY, int64_t M, const int* offs
                        : (w.dq ? launch_dx_tiles<kFormDq, kTileQ, true, false>
                                : launch_dx_tiles<kFormNoDq, kTileQ, true, false>);
   prof_begin(1, stream);
-  hipError_t e = launch(dY, M, w, N, G, A, r, s, dX, part, tb, stream, qtiles, sp, offsets, E, d);
+  hipError_t e =
+      sp.splits == 1 && expert_dx_fits(M, E, w.K)
+          ? launch_expert_dx(dY, M, offsets, E, w, G, A, r, s, dX, tb, stream, d)
+          : launch(dY, M, w, N, G, A, r, s, dX, part, tb, stream, qtiles, sp, offsets, E, d);
   if (e == hipSuccess && sp.splits > 1)
     e = launch_group_reduce(part, sp.splits, M, w.K, 1.f, offsets, E, nullptr, dX, stream);
   prof_end(1, stream);

@@ -53,6 +53,43 @@ def test_edges(sizes, N, K, r, kw):
     Grouped(sizes, N, K, r, seed=len(sizes) + N + K + r, **kw).check()
 
 
+MANY = [
+    # many rows and columns: dX in tiles of 256 columns x 192 tokens
+    ([300, 200, 64, 129, 65], 256, 64 * 161, 16, dict(before=3, behind=5)),
+    ([193, 1, 0, 400, 128], 72, 10240, 72, dict(dq=False)),
+    ([100] * 4, 8, 64 * 260, 8, dict(dq=False, book="int4")),
+    ([150] * 3, 200, 64 * 257, 0, dict(dq=False)),
+    ([260] * 3, 128, 16384, 256, dict(book="fp4")),
+    ([1, 700, 0, 63], 192, 256 * 64, 40, dict(x_kind="shifted")),
+    ([300, 200, 64, 129, 65], 256, 64 * 161, 16, dict(p=0.2)),
+]
+
+
+@pytest.mark.parametrize("sizes,N,K,r,kw", MANY)
+def test_many_rows_and_columns(sizes, N, K, r, kw):
+    need_gpu()
+    say(f"grouped many sizes={sizes} N={N} K={K} r={r} {kw}")
+    Grouped(sizes, N, K, r, seed=len(sizes) + N + K + r, **kw).check()
+
+
+def test_many_rows_with_a_poisoned_expert():
+    """NaN constants, activations and gradients of one expert leave the others'
+    dX as it was."""
+    need_gpu()
+    say("poisoned expert, many rows")
+    g = Grouped([200, 150, 130, 90], 8, 64 * 260, 8, dq=False, seed=3)
+    _, T, dX, dA, dB = g.check()
+    own = slice(int(g.off[1]), int(g.off[2]))
+    n = g.N * g.K // 64
+    g.w.absmax_scale[n:2 * n] = float("nan")
+    g.dY[own] = float("nan")
+    g.A[1] = float("inf")
+    dX2, dA2, dB2 = g.bwd(T)
+    torch.cuda.synchronize()
+    assert torch.equal(dX[:own.start], dX2[:own.start])
+    assert torch.equal(dX[own.stop:], dX2[own.stop:]) and torch.isnan(dX2[own]).all()
+
+
 @pytest.mark.parametrize("sizes", [[3, 5, 2], [20, 11, 30], [70, 100, 60]])
 def test_nan_and_infinity_stay_with_their_expert(sizes):
     """NaN in one expert's activations, infinity in its gradients and NaN in its
