@@ -24,6 +24,9 @@ EDGES = [
     ([0] * 69 + [3], 64, 256, 32, dict(book="fp4")),
     ([1, 0, 0, 1], 8, 64 * 130, 40, dict(dq=False, behind=14)),   # no more rows than the bound
     ([7, 2], 1032, 448, 0, dict(dq=False, book="int4")),
+    ([4, 5, 0, 3, 2, 1], 264, 64 * 9, 24, dict(dq=False, p=0.2)),   # around four rows
+    ([4], 64, 64 * 35, 8, dict(dq=False, before=1, behind=2)),
+    ([3, 4, 4, 4], 128, 64 * 34, 16, {}),
     # 32 tokens a tile
     ([17], 128, 128, 16, {}),
     ([16, 17, 32, 33, 1, 15, 31, 34], 264, 192, 24, dict(dq=False)),
