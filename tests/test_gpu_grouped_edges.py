@@ -269,3 +269,43 @@ def test_padded_batch_and_repeated_choices(tokens):
     assert torch.equal(Y[two[:, 0].long()], Y[two[:, 1].long()])
     assert torch.equal(out[2::4], Y[two[:, 0].long()])
     assert torch.equal(dw[2::4, 0], dw[2::4, 1])
+
+
+@pytest.mark.parametrize("rows", [12, 600])
+def test_the_most_experts(rows):
+    """1024 experts, most of them without a row."""
+    need_gpu()
+    say(f"1024 experts, {rows} rows")
+    rng = np.random.default_rng(rows)
+    sizes = [0] * 1024
+    for e in rng.integers(0, 1024, rows):
+        sizes[e] += 1
+    Grouped(sizes, 8, 128, 8, dq=False, seed=rows, behind=3).check()
+
+
+@pytest.mark.parametrize("sizes", [[3, 2], [50, 40]])
+def test_adapter_gradients_alone(sizes):
+    """need_dx = False computes the same dA and dB; without adapters nothing is
+    left to do."""
+    need_gpu()
+    say(f"no dX, sizes={sizes}")
+    g = Grouped(sizes, 256, 256, 16, p=0.1, seed=2)
+    Y, T, dX, dA, dB = g.check()
+    none, dA2, dB2 = q.qlora_grouped_bwd(g.dY, g.X, g.offsets, g.w, g.E, T=T, need_dx=False,
+                                         **g.kw())
+    torch.cuda.synchronize()
+    assert none is None and torch.equal(dA, dA2) and torch.equal(dB, dB2)
+    assert q.qlora_grouped_bwd(g.dY, g.X, g.offsets, g.w, g.E, need_dx=False) == (None, None, None)
+
+
+def test_probabilities_at_the_ends():
+    """p below half a 65536th keeps everything; p next to 1 drops all but one
+    16-bit value of 65536, whose elements are scaled by 65536."""
+    need_gpu()
+    say("p next to 0 and 1")
+    from expert_util import state
+    x = torch.ones(1 << 20, dtype=torch.bfloat16, device=dev())
+    assert torch.equal(q.qlora_dropout(x, 1e-6, state()), x)
+    y = q.qlora_dropout(x, 0.9999999, state())
+    keep = od.halves(x.numel(), SEED, OFFSET) == 65535
+    np.testing.assert_array_equal(y.float().cpu().numpy(), 65536.0 * keep)
