@@ -9,6 +9,13 @@
 // writes zeros.  The partial sums of a split reduction are added in split
 // order by a second launch (deterministic); without a split the result is
 // written at once.
+//
+// With r = 64 and 8192 rows on 8 experts, T over 4096 columns takes 31 us, G and dB
+// for 4096 columns 42 us and dA for 11008 columns 64 us (2.8 TB/s of X): bound by
+// the traffic between L2 and the CUs, where the fp32 factor is read again by each
+// of dA's column tiles, and by the largest expert's reductions.  (Largest experts
+// first: 0.6% of the backward, less than the search cost other sizes; workgroups
+// for two rounds instead of one: no change.)
 #include <algorithm>
 #include <type_traits>
 

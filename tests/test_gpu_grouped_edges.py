@@ -309,3 +309,61 @@ def test_probabilities_at_the_ends():
     y = q.qlora_dropout(x, 0.9999999, state())
     keep = od.halves(x.numel(), SEED, OFFSET) == 65535
     np.testing.assert_array_equal(y.float().cpu().numpy(), 65536.0 * keep)
+
+
+def test_layer_with_dropout_in_a_graph():
+    """Forward and backward of one layer, captured: every replay draws the mask of
+    its state and equals the eager calls on it."""
+    need_gpu()
+    say("layer with dropout in a graph")
+    from expert_util import state
+    for M in (7, 90):
+        g = Grouped([M], 256, 512, 16, p=0.3, seed=M)
+        st = g.state
+        def step():
+            Y, T = q.qlora_linear_dropout_fwd(g.X, g.w, g.A[0], g.B[0], g.s, g.p, st)
+            return (Y, T) + q.qlora_linear_dropout_bwd(g.dY, g.X, g.w, g.A[0], g.B[0], g.s, g.p, st,
+                                                       T=T)
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+            st[1] += 1
+        st.copy_(state(5, 100))
+        seen = []
+        for i in range(4):
+            graph.replay()
+            got = [t.clone() for t in out]
+            st.copy_(state(5, 100 + i))
+            want = step()
+            st.copy_(state(5, 101 + i))
+            torch.cuda.synchronize()
+            for a, b in zip(got, want):
+                assert torch.equal(a, b)
+            seen.append(got[1])
+        assert not torch.equal(seen[0], seen[1])
+
+
+def test_exchange_past_32_bits():
+    """Token rows of more than 2^32 elements (8 GiB), there and back."""
+    need_gpu()
+    tokens, K = 2 ** 16 + 40, 2 ** 16
+    say(f"exchange tokens={tokens} K={K}")
+    X = torch.empty((tokens, K), dtype=torch.bfloat16, device=dev())
+    X.copy_(torch.arange(tokens, device=dev()).remainder(251).to(torch.bfloat16)[:, None])
+    X[:, 3] = torch.arange(tokens, device=dev()).remainder(127).to(torch.bfloat16)
+    inv = torch.arange(tokens - 1, -1, -1, dtype=torch.int32, device=dev())[:, None]
+    Xs = q.qlora_expert_gather(X, inv)
+    for t in (0, 1, 39, tokens // 2, tokens - 41, tokens - 1):
+        assert torch.equal(Xs[tokens - 1 - t], X[t])
+    w = torch.full((tokens, 1), 2.0, device=dev())
+    out = q.qlora_expert_combine(Xs, inv, w)
+    dY, dw = q.qlora_expert_combine_bwd(X, Xs, inv, w)
+    torch.cuda.synchronize()
+    for t in (0, 1, 39, tokens // 2, tokens - 41, tokens - 1):
+        assert torch.equal(out[t], 2 * X[t]) and torch.equal(dY[tokens - 1 - t], 2 * X[t])
+        v = float(t % 251)
+        want = (K - 1) * v * v + float(t % 127) ** 2
+        # sums of K products of 16 significant bits in fp32
+        assert abs(float(dw[t]) - want) <= K * 2.0 ** -24 * want
