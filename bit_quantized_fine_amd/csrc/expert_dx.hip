@@ -402,9 +402,16 @@ hipError_t launch_tiles(const ExpertArgs& a, const Nf4Tables& tb, hipStream_t st
 // split its reduction: 8 experts of 4096 x 4096 with 1024 rows (208 tiles at most)
 // 105 / 88 us, with 2048 rows (288 tiles) 119 / 163; 32 experts of 2048 x 1024 with
 // 4096 rows (212) 74 / 68, with 8192 rows (296) 86 / 117; 64 experts of 1024 x 2048
-// with 128 rows (512) 53 / 71.
+// with 128 rows (512) 53 / 71.  With up to 4 experts next to all tiles are full ones, and
+// the rounds that 256 CUs need for them count; a round of this kernel's takes 1.28
+// times as long as one of the other's 128 columns x 256 tokens.  One expert of
+// 11008 x 4096, 3900 rows of X (2 rounds of either): 550 / 460 us; 4096 x
+// 11008, 2048 rows (2 rounds / 3): 255 / 289.
 bool expert_dx_fits(int64_t M, int E, int64_t K) {
-  return (K + VK - 1) / VK * group_tile_bound(M, E, 16 * VTB) >= 256;
+  const int64_t tiles = (K + VK - 1) / VK * group_tile_bound(M, E, 16 * VTB);
+  if (tiles < 256 || E > 4) return tiles >= 256;
+  const int64_t other = (K + 127) / 128 * group_tile_bound(M, E, 256);
+  return 128 * ((tiles + 255) / 256) <= 100 * ((other + 255) / 256);
 }
 
 hipError_t launch_expert_dx(const uint16_t* dY, int64_t M, const int* offsets, int E,

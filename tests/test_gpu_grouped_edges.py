@@ -65,6 +65,9 @@ MANY = [
     ([260] * 3, 128, 16384, 256, dict(book="fp4")),
     ([1, 700, 0, 63], 192, 256 * 64, 40, dict(x_kind="shifted")),
     ([300, 200, 64, 129, 65], 256, 64 * 161, 16, dict(p=0.2)),
+    ([600], 8, 16384, 8, dict(dq=False, p=0.1)),        # one expert: rounds decide
+    ([700], 8, 11008, 8, dict(dq=False)),
+    ([380, 1], 8, 32768, 8, dict(dq=False)),
 ]
 
 
