@@ -248,8 +248,8 @@ hipError_t launch_few(const ExpertArgs& a, const Nf4Tables& tb, hipStream_t stre
       hipFuncSetAttribute(reinterpret_cast<const void*>(&k_expert_few<NODQ>),
                           hipFuncAttributeMaxDynamicSharedMemorySize, kFewLds);
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL((k_expert_few<NODQ>), dim3(xcd_deal_grid(a.qtiles, a.ptiles)), dim3(FT), kFewLds, stream, a,
-                     tb);
+  hipLaunchKernelGGL((k_expert_few<NODQ>), dim3(xcd_deal_grid(a.qtiles, a.ptiles)), dim3(FT),
+                     kFewLds, stream, a, tb);
   return hipGetLastError();
 }
 

@@ -491,8 +491,8 @@ hipError_t launch_variant(const ExpertArgs& a, const Nf4Tables& tb, hipStream_t 
       hipFuncSetAttribute(reinterpret_cast<const void*>(&k_expert_fwd<FR, TB, NODQ>),
                           hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL((k_expert_fwd<FR, TB, NODQ>), dim3(xcd_deal_grid((int64_t)a.qtiles * a.splits, a.ptiles)),
-                     dim3(ET), kLds, stream, a, tb);
+  const dim3 grid(xcd_deal_grid((int64_t)a.qtiles * a.splits, a.ptiles));
+  hipLaunchKernelGGL((k_expert_fwd<FR, TB, NODQ>), grid, dim3(ET), kLds, stream, a, tb);
   return hipGetLastError();
 }
 

@@ -532,9 +532,10 @@ hipError_t launch_dx_tiles(const uint16_t* dY, int64_t M, const Nf4View& w, int6
   const DxArgs args{dY,  M, w.dense, w.codes, w.absmax_q, w.absmax_scale, N, w.K,
                     G,   A, r,       kDrop ? s * d.scale() : s, dX, ptiles, qtiles, sp.splits, sp.cps,
                     sp.splits > 1 ? part : nullptr, offsets, E, d.state, d.thr};
-  hipLaunchKernelGGL((k_dx_gemm<kForm, kQ, kExperts, kDrop>), dim3(kExperts ? xcd_deal_grid((int64_t)qtiles * sp.splits, ptiles)
-                                   : ptiles * qtiles * sp.splits),
-                     dim3(XT), kLds, stream, args, tb);
+  const dim3 grid(kExperts ? xcd_deal_grid((int64_t)qtiles * sp.splits, ptiles)
+                           : ptiles * qtiles * sp.splits);
+  hipLaunchKernelGGL((k_dx_gemm<kForm, kQ, kExperts, kDrop>), grid, dim3(XT), kLds, stream, args,
+                     tb);
   return hipGetLastError();
 }
 
