@@ -613,12 +613,13 @@ def _maybe(t, name, shape, dtype):
 def _one_gpu(names, *tensors):
     """The GPU of all tensors given (None where an argument is absent); names
     holds theirs, separated by spaces."""
-    dev = None
+    dev = index = None
     for t in tensors:
         if t is not None:
+            i = t.get_device()   # -1: not on a GPU
             if dev is None:
-                dev = t.device
-            if t.device != dev or dev.type != "cuda":
+                dev, index = t.device, i
+            if i != index or i < 0:
                 _on_gpu(zip(names.split(), tensors))
     return dev
 
