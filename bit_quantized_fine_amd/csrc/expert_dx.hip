@@ -254,7 +254,8 @@ __device__ __forceinline__ void dx_expert_tile(const ExpertArgs& a, uint8_t* dyn
   }
 
   // LoRA update: 64 ranks at a time, the A tile [VK][64] and s . G as bf16 hi and lo
-  // tiles [TQ][64], all in swizzled 128-byte rows.
+  // tiles [TQ][64], all in swizzled 128-byte rows.  (The two halves keep 16 of the
+  // fp32 value's 24 bits, of which the bf16 result keeps 8.)
   f32x4 low[DROP ? 2 : 1][DROP ? TB : 1];
   if constexpr (DROP) {
 #pragma unroll

@@ -342,7 +342,8 @@ __device__ __forceinline__ void expert_tile(const ExpertArgs& a, uint8_t* dyn, i
 
   // LoRA update (the first split only): 64 ranks at a time, the B tile [64
   // ranks][ROWS] as it lies in memory, read with transposing loads, and s . T as
-  // bf16 hi and lo tiles [TQ][64], swizzled like half-chunk X rows.
+  // bf16 hi and lo tiles [TQ][64] in swizzled 128-byte rows.  (The two halves keep
+  // 16 of the fp32 value's 24 bits, of which the bf16 result keeps 8.)
   if (a.r > 0 && z == 0) {
     uint16_t* const bt = reinterpret_cast<uint16_t*>(dyn);
     uint16_t* const th = bt + Tile::ROWS * 64;
