@@ -565,10 +565,10 @@ hipError_t launch_decode_variant(const uint16_t* X, int64_t M, const Nf4View& w,
                                  int nz, float* Tout, const uint16_t* B, int r, float s,
                                  uint16_t* Y, const Nf4Tables& tb, hipStream_t stream, int ldt,
                                  int ldb, int ldy, int ksl = 0) {
-  // allow the largest dynamic LDS (once per variant)
-  static const hipError_t attr = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(&k_fwd_decode<D, XP, FR, NODQ, SL>),
-      hipFuncAttributeMaxDynamicSharedMemorySize, kDecLdsMax);
+  // allow the largest dynamic LDS (once per variant and device)
+  static LdsLimit lds;
+  const hipError_t attr = lds.raise(
+      reinterpret_cast<const void*>(&k_fwd_decode<D, XP, FR, NODQ, SL>), kDecLdsMax);
   if (attr != hipSuccess) return attr;
   if (SL && ksl != 1024) return hipErrorInvalidValue;
   const DecLds L(M, w.K, r, XP > 0, FR, ksl, SL ? 2 : 1);

@@ -308,10 +308,10 @@ int qlora_expert_plan(const int32_t* ids, int64_t n, int E, int32_t* offsets, in
     if (hipGetLastError() != hipSuccess) return QLORA_ERR_HIP;
   }
   // static and dynamic LDS together exceed the default limit for large E
-  static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&k_plan_place),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kPlanWaves * kMaxE * 4);
-  if (attr != hipSuccess) return QLORA_ERR_HIP;
+  static LdsLimit lds;
+  if (lds.raise(reinterpret_cast<const void*>(&k_plan_place), kPlanWaves * kMaxE * 4) !=
+      hipSuccess)
+    return QLORA_ERR_HIP;
   hipLaunchKernelGGL(k_plan_place, dim3(nb), dim3(kPlanThreads), kPlanWaves * E * sizeof(int), st,
                      ids, n, E, chunk, counts, offsets, order, inverse);
   return hip_status(hipGetLastError());

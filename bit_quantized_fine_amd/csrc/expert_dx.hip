@@ -388,9 +388,8 @@ template <bool NODQ, bool DROP>
 hipError_t launch_tiles(const ExpertArgs& a, const Nf4Tables& tb, hipStream_t stream) {
   constexpr int kLds = VTile<VTB>::LDS;
   static_assert(kLds >= VTile<8>::LDS && kLds >= VTile<4>::LDS, "the widest body's LDS");
-  static const hipError_t attr = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(&k_expert_dx<NODQ, DROP>),
-      hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  static LdsLimit lds;
+  const hipError_t attr = lds.raise(reinterpret_cast<const void*>(&k_expert_dx<NODQ, DROP>), kLds);
   if (attr != hipSuccess) return attr;
   hipLaunchKernelGGL((k_expert_dx<NODQ, DROP>), dim3(xcd_deal_grid(a.qtiles, a.ptiles)), dim3(VT), kLds,
                      stream, a, tb);

@@ -244,9 +244,8 @@ namespace {
 
 template <bool NODQ>
 hipError_t launch_few(const ExpertArgs& a, const Nf4Tables& tb, hipStream_t stream) {
-  static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&k_expert_few<NODQ>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kFewLds);
+  static LdsLimit lds;
+  const hipError_t attr = lds.raise(reinterpret_cast<const void*>(&k_expert_few<NODQ>), kFewLds);
   if (attr != hipSuccess) return attr;
   hipLaunchKernelGGL((k_expert_few<NODQ>), dim3(xcd_deal_grid(a.qtiles, a.ptiles)), dim3(FT),
                      kFewLds, stream, a, tb);

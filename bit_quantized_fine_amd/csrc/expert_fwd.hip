@@ -488,9 +488,9 @@ namespace {
 template <int FR, int TB, bool NODQ>
 hipError_t launch_variant(const ExpertArgs& a, const Nf4Tables& tb, hipStream_t stream) {
   constexpr int kLds = expert_lds<FR, TB>();
-  static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&k_expert_fwd<FR, TB, NODQ>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  static LdsLimit lds;
+  const hipError_t attr =
+      lds.raise(reinterpret_cast<const void*>(&k_expert_fwd<FR, TB, NODQ>), kLds);
   if (attr != hipSuccess) return attr;
   const dim3 grid(xcd_deal_grid((int64_t)a.qtiles * a.splits, a.ptiles));
   hipLaunchKernelGGL((k_expert_fwd<FR, TB, NODQ>), grid, dim3(ET), kLds, stream, a, tb);

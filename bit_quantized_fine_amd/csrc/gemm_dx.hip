@@ -526,9 +526,9 @@ hipError_t launch_dx_tiles(const uint16_t* dY, int64_t M, const Nf4View& w, int6
                            float* part, const Nf4Tables& tb, hipStream_t stream, int qtiles,
                            const GemmSplit& sp, const int* offsets, int E, const Drop& d) {
   constexpr int kLds = DxTile<kQ>::LDS;
-  static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&k_dx_gemm<kForm, kQ, kExperts, kDrop>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  static LdsLimit lds;
+  const hipError_t attr = lds.raise(
+      reinterpret_cast<const void*>(&k_dx_gemm<kForm, kQ, kExperts, kDrop>), kLds);
   if (attr != hipSuccess) return attr;
   if (sp.splits > 1 && !part) return hipErrorInvalidValue;
   const int ptiles = static_cast<int>((w.K + XP - 1) / XP);

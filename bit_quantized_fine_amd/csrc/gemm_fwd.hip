@@ -394,17 +394,12 @@ hipError_t launch_fwd_gemm(const uint16_t* X, int64_t M, const Nf4View& w,
                             const float* T, const uint16_t* B, int r, float s,
                             uint16_t* Y, float* part, const Nf4Tables& tb, hipStream_t stream,
                             int ldt, int64_t seg_rows) {
-  static const hipError_t attr[3] = {
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&k_fwd_gemm<kFormDq>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kFwdLds),
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&k_fwd_gemm<kFormNoDq>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kFwdLds),
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&k_fwd_gemm<kFormDense>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kFwdLds)};
   const int form = w.dense ? kFormDense : (w.dq ? kFormDq : kFormNoDq);
-  if (attr[form] != hipSuccess) return attr[form];
   decltype(&k_fwd_gemm<kFormDq>) kern =
       form == kFormDense ? k_fwd_gemm<kFormDense> : (form == kFormNoDq ? k_fwd_gemm<kFormNoDq> : k_fwd_gemm<kFormDq>);
+  static LdsLimit lds[3];
+  const hipError_t attr = lds[form].raise(reinterpret_cast<const void*>(kern), kFwdLds);
+  if (attr != hipSuccess) return attr;
   const int ptiles = static_cast<int>((w.N + GP - 1) / GP);
   const int qtiles = static_cast<int>((M + GQ - 1) / GQ);
   const GemmSplit sp = fwd_gemm_split(M, w.N, w.K);

@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace qnf4 {
 
 struct Nf4Tables;
@@ -40,6 +42,26 @@ struct Drop {
   uint32_t thr = 0;
   bool on() const { return thr > 0; }
   float scale() const { return 65536.f / static_cast<float>(65536u - thr); }
+};
+
+// Dynamic LDS past what a launch may use by default.  The limit belongs to a
+// kernel on one device, so it is raised the first time a launcher runs with
+// that device current (once each; a static of the launcher keeps the devices).
+class LdsLimit {
+ public:
+  hipError_t raise(const void* kernel, int bytes) {
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;   // (no bit: each time)
+    if (done_.load(std::memory_order_relaxed) & bit) return hipSuccess;
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess) done_.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};
 };
 
 // Profiling hook: the launchers call these around the launches of one
