@@ -15,6 +15,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPieces = 4;   // 16-byte pieces a thread, kThreads apart
+// Workgroups lie in rows of this many along y (a launch holds fewer than 2^32
+// threads along x).
+constexpr int64_t kRowBlocks = int64_t(1) << 23;
 
 __device__ __forceinline__ uint32_t drop_pair(uint32_t x, uint32_t keep, float scale) {
   return pack_bf16x2(bf16_lo_to_f32(x) * scale, bf16_hi_to_f32(x) * scale) & keep;
@@ -28,7 +31,8 @@ __global__ __launch_bounds__(kThreads) void k_dropout(const uint16_t* x, int64_t
   DropKey key{};   // thr = 0 keeps everything, and state may be null
   if (thr > 0) key = load_drop_key(state, thr);
   const int64_t whole = n / 8;
-  const int64_t p0 = (int64_t)blockIdx.x * (kThreads * kPieces) + threadIdx.x;
+  const int64_t p0 =
+      ((int64_t)blockIdx.y * kRowBlocks + blockIdx.x) * (kThreads * kPieces) + threadIdx.x;
   u32x4 v[kPieces];
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
@@ -60,9 +64,11 @@ __global__ __launch_bounds__(kThreads) void k_dropout(const uint16_t* x, int64_t
 
 hipError_t launch_dropout(const uint16_t* x, int64_t n, const Drop& d, uint16_t* y,
                           hipStream_t stream) {
-  const int64_t per = 8 * kThreads * kPieces;
-  hipLaunchKernelGGL(k_dropout, dim3(static_cast<unsigned>(n / per + 1)), dim3(kThreads), 0,
-                     stream, x, n, d.state, d.thr, d.scale(), y);
+  const int64_t blocks = n / (8 * kThreads * kPieces) + 1;
+  const dim3 grid(static_cast<unsigned>(blocks < kRowBlocks ? blocks : kRowBlocks),
+                  static_cast<unsigned>((blocks + kRowBlocks - 1) / kRowBlocks));
+  hipLaunchKernelGGL(k_dropout, grid, dim3(kThreads), 0, stream, x, n, d.state, d.thr, d.scale(),
+                     y);
   return hipGetLastError();
 }
 

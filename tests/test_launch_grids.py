@@ -22,11 +22,19 @@ for n in (1, 1 << 24, 1 << 30):
 print(json.dumps(out))
 """
 
+DROPOUT = """
+out = []
+for n in (1, 1 << 24, (1 << 36) - 1, 1 << 36, (1 << 36) + 1, (1 << 37) - 8192, 1 << 37, 3 << 37):
+    st = [L.qlora_dropout_apply(P, n, drop(0.1), P, None)]
+    out.append((n, st, [l[0] for l in launches()]))
+print(json.dumps(out))
+"""
 
-@pytest.mark.parametrize("calls", [ROWS], ids=["exchange"])
+
+@pytest.mark.parametrize("calls", [ROWS, DROPOUT], ids=["exchange", "dropout"])
 def test_grids_of_admitted_sizes(tmp_path, calls):
     got = run(tmp_path, calls)
-    assert len(got) > 10
+    assert len(got) > 7
     for *size, status, threads in got:
         assert all(s == 0 for s in status), size
         assert len(threads) >= len(status) and max(threads) < 2 ** 32, (size, threads)
