@@ -373,16 +373,19 @@ int check_dropout(const qlora_dropout* d, Drop* out) {
 constexpr int kMaxExperts = 1024;
 
 // Limits of the expert layout: each expert's rows start at a group of 256
-// block constants (so they are a weight of their own), and the grids fit.
-int check_experts(const qlora_q4_weight* w, int64_t M, int E) {
+// block constants (so they are a weight of their own), and every launch holds
+// fewer than 2^32 threads.
+int check_experts(const qlora_q4_weight* w, int64_t M, int E, int r, bool back) {
   if (E < 1 || E > kMaxExperts || w->N % E != 0) return QLORA_ERR_EXPERT;
   const int64_t N = w->N / E;
   if (N % 8 != 0) return QLORA_ERR_SHAPE;
   if (w->double_quant && (N * w->K / kBlock) % kGroup != 0) return QLORA_ERR_EXPERT;
   if (M < 0 || M > INT32_MAX) return QLORA_ERR_SHAPE;
-  const int64_t wide = (std::max(N, w->K) + 127) / 128;
-  if (group_tile_bound(M, E, 64) > (int64_t(1) << 30) / wide) return QLORA_ERR_SHAPE;
-  return QLORA_OK;
+  if (M == 0) return QLORA_OK;
+  const int64_t threads = std::max(grouped_rank_threads(M, E, N, w->K, r),
+                                   back ? grouped_dx_threads(M, E, N, w->K)
+                                        : grouped_fwd_threads(M, E, N, w->K));
+  return threads < int64_t(1) << 32 ? QLORA_OK : QLORA_ERR_SHAPE;
 }
 
 size_t grouped_fwd_ws_bytes(int64_t M, int E, int64_t N, int64_t K, int r) {
@@ -880,7 +883,7 @@ int qlora_grouped_fwd(const uint16_t* X, int64_t M, const int32_t* offsets, int 
   int st = check_q4_weight(w);
   if (st) return st;
   if ((st = check_rank(r))) return st;
-  if ((st = check_experts(w, M, E))) return st;
+  if ((st = check_experts(w, M, E, r, false))) return st;
   Drop dr;
   if ((st = check_dropout(d, &dr))) return st;
   if (!offsets || (r > 0 && (!A || !B))) return QLORA_ERR_NULL;
@@ -920,7 +923,7 @@ int qlora_grouped_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const in
   int st = check_q4_weight(w);
   if (st) return st;
   if ((st = check_rank(r))) return st;
-  if ((st = check_experts(w, M, E))) return st;
+  if ((st = check_experts(w, M, E, r, true))) return st;
   Drop dr;
   if ((st = check_dropout(d, &dr))) return st;
   if (!offsets || (r > 0 && (!A || !B || !dA || !dB))) return QLORA_ERR_NULL;

@@ -49,10 +49,12 @@ __device__ __forceinline__ GroupTile expert_deal(const ExpertArgs& a, GroupTiles
 }
 
 // The few-token form (expert_few.hip); fills in the tiles.
+int64_t expert_few_threads(int64_t M, int E, int64_t N);
 hipError_t launch_expert_few(ExpertArgs a, bool dq, const Nf4Tables& tb, hipStream_t stream);
 
 // dX for many rows (expert_dx.hip), without a split reduction.
 bool expert_dx_fits(int64_t M, int E, int64_t K);
+int64_t expert_dx_threads(int64_t M, int E, int64_t K);
 hipError_t launch_expert_dx(const uint16_t* dY, int64_t M, const int* offsets, int E,
                             const Nf4View& w, const float* G, const uint16_t* A, int r, float s,
                             uint16_t* dX, const Nf4Tables& tb, hipStream_t stream,

@@ -391,7 +391,8 @@ hipError_t launch_tiles(const ExpertArgs& a, const Nf4Tables& tb, hipStream_t st
   static LdsLimit lds;
   const hipError_t attr = lds.raise(reinterpret_cast<const void*>(&k_expert_dx<NODQ, DROP>), kLds);
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL((k_expert_dx<NODQ, DROP>), dim3(xcd_deal_grid(a.qtiles, a.ptiles)), dim3(VT), kLds,
+  hipLaunchKernelGGL((k_expert_dx<NODQ, DROP>),
+                     dim3(static_cast<unsigned>(xcd_deal_grid(a.qtiles, a.ptiles))), dim3(VT), kLds,
                      stream, a, tb);
   return hipGetLastError();
 }
@@ -412,6 +413,10 @@ bool expert_dx_fits(int64_t M, int E, int64_t K) {
   if (tiles < 256 || E > 4) return tiles >= 256;
   const int64_t other = (K + 127) / 128 * group_tile_bound(M, E, 256);
   return 128 * ((tiles + 255) / 256) <= 100 * ((other + 255) / 256);
+}
+
+int64_t expert_dx_threads(int64_t M, int E, int64_t K) {
+  return VT * xcd_deal_grid(group_tile_bound(M, E, 16 * VTB), (K + VK - 1) / VK);
 }
 
 hipError_t launch_expert_dx(const uint16_t* dY, int64_t M, const int* offsets, int E,

@@ -247,12 +247,16 @@ hipError_t launch_few(const ExpertArgs& a, const Nf4Tables& tb, hipStream_t stre
   static LdsLimit lds;
   const hipError_t attr = lds.raise(reinterpret_cast<const void*>(&k_expert_few<NODQ>), kFewLds);
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL((k_expert_few<NODQ>), dim3(xcd_deal_grid(a.qtiles, a.ptiles)), dim3(FT),
-                     kFewLds, stream, a, tb);
+  hipLaunchKernelGGL((k_expert_few<NODQ>), dim3(static_cast<unsigned>(xcd_deal_grid(a.qtiles, a.ptiles))),
+                     dim3(FT), kFewLds, stream, a, tb);
   return hipGetLastError();
 }
 
 }  // namespace
+
+int64_t expert_few_threads(int64_t M, int E, int64_t N) {
+  return FT * xcd_deal_grid(group_tile_bound(M, E, 16), (N + FROWS - 1) / FROWS);
+}
 
 hipError_t launch_expert_few(ExpertArgs a, bool dq, const Nf4Tables& tb, hipStream_t stream) {
   a.ptiles = static_cast<int>((a.N + FROWS - 1) / FROWS);

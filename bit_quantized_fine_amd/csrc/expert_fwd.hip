@@ -492,7 +492,8 @@ hipError_t launch_variant(const ExpertArgs& a, const Nf4Tables& tb, hipStream_t 
   const hipError_t attr =
       lds.raise(reinterpret_cast<const void*>(&k_expert_fwd<FR, TB, NODQ>), kLds);
   if (attr != hipSuccess) return attr;
-  const dim3 grid(xcd_deal_grid((int64_t)a.qtiles * a.splits, a.ptiles));
+  const dim3 grid(
+      static_cast<unsigned>(xcd_deal_grid((int64_t)a.qtiles * a.splits, a.ptiles)));
   hipLaunchKernelGGL((k_expert_fwd<FR, TB, NODQ>), grid, dim3(ET), kLds, stream, a, tb);
   return hipGetLastError();
 }
@@ -542,6 +543,12 @@ ExpertPlan plan_expert_fwd(int64_t M, int E, int64_t N, int64_t K) {
 
 GemmSplit grouped_fwd_split(int64_t M, int E, int64_t N, int64_t K) {
   return plan_expert_fwd(M, E, N, K).sp;
+}
+
+int64_t grouped_fwd_threads(int64_t M, int E, int64_t N, int64_t K) {
+  const ExpertPlan p = plan_expert_fwd(M, E, N, K);
+  return p.tb == 0 ? expert_few_threads(M, E, N)
+                   : ET * xcd_deal_grid((int64_t)p.qtiles * p.sp.splits, p.ptiles);
 }
 
 // The few-token kernel adds up T's partial sums itself: every workgroup reads

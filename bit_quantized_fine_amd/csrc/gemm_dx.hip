@@ -535,7 +535,8 @@ hipError_t launch_dx_tiles(const uint16_t* dY, int64_t M, const Nf4View& w, int6
   const DxArgs args{dY,  M, w.dense, w.codes, w.absmax_q, w.absmax_scale, N, w.K,
                     G,   A, r,       kDrop ? s * d.scale() : s, dX, ptiles, qtiles, sp.splits, sp.cps,
                     sp.splits > 1 ? part : nullptr, offsets, E, d.state, d.thr};
-  const dim3 grid(kExperts ? xcd_deal_grid((int64_t)qtiles * sp.splits, ptiles)
+  const dim3 grid(kExperts ? static_cast<unsigned>(
+                                 xcd_deal_grid((int64_t)qtiles * sp.splits, ptiles))
                            : ptiles * qtiles * sp.splits);
   hipLaunchKernelGGL((k_dx_gemm<kForm, kQ, kExperts, kDrop>), grid, dim3(XT), kLds, stream, args,
                      tb);
@@ -571,6 +572,12 @@ hipError_t launch_dx_gemm(const uint16_t* dY, int64_t M, const Nf4View& w,
 GemmSplit grouped_dx_split(int64_t M, int E, int64_t N, int64_t K) {
   return gemm_split((K + XP - 1) / XP * group_tile_bound(M, E, kTileQ),
                     (N + XN - 1) / XN);
+}
+
+int64_t grouped_dx_threads(int64_t M, int E, int64_t N, int64_t K) {
+  const GemmSplit sp = grouped_dx_split(M, E, N, K);
+  if (sp.splits == 1 && expert_dx_fits(M, E, K)) return expert_dx_threads(M, E, K);
+  return XT * xcd_deal_grid(group_tile_bound(M, E, kTileQ) * sp.splits, (K + XP - 1) / XP);
 }
 
 hipError_t launch_grouped_dx_gemm(const uint16_t* dY, int64_t M, const int* offsets, int E,

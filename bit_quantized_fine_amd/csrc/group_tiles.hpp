@@ -124,7 +124,7 @@ __device__ __forceinline__ XcdTile xcd_deal(int b, int P) {
     i -= n;
   }
 }
-inline int xcd_deal_grid(int64_t V, int64_t P) { return static_cast<int>(8 * P * ((V + 7) / 8)); }
+inline int64_t xcd_deal_grid(int64_t V, int64_t P) { return 8 * P * ((V + 7) / 8); }
 
 // Most tiles of tq rows that M rows of E experts can make.
 inline int64_t group_tile_bound(int64_t M, int E, int64_t tq) {

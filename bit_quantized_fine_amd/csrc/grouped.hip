@@ -296,6 +296,18 @@ size_t grouped_rank_ws_floats(int64_t M, int E, int64_t N, int64_t K, int r) {
   return f;
 }
 
+int64_t grouped_rank_threads(int64_t M, int E, int64_t N, int64_t K, int r) {
+  if (r <= 0 || M <= 0) return 0;
+  auto rows = [&](int64_t nred) {
+    const RowsPlan p = plan_rows(M, E, nred, r);
+    return (int64_t)p.px * p.slots * p.splits;
+  };
+  auto grad = [&](int64_t len) {
+    return cdiv(len, RB_X) * cdiv(r, RB_R) * E * grad_splits(M, E, len, r);
+  };
+  return NT * std::max(rows(K), std::max(rows(N) + grad(N), grad(K)));
+}
+
 hipError_t launch_grouped_down(const uint16_t* X, int64_t M, const int* offsets, int E, int64_t K,
                                const uint16_t* A, int r, float* T, float* ws, hipStream_t stream,
                                const Drop& d, int* nz) {

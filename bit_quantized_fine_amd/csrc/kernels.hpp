@@ -164,6 +164,10 @@ hipError_t launch_grouped_dx_gemm(const uint16_t* dY, int64_t M, const int* offs
                                   const Nf4View& w, const float* G, const uint16_t* A, int r,
                                   float s, uint16_t* dX, float* part, const Nf4Tables& tb,
                                   hipStream_t stream, const Drop& d);
+// Threads of the largest launch: of the forward GEMM, of dX and of the rank products.
+int64_t grouped_fwd_threads(int64_t M, int E, int64_t N, int64_t K);
+int64_t grouped_dx_threads(int64_t M, int E, int64_t N, int64_t K);
+int64_t grouped_rank_threads(int64_t M, int E, int64_t N, int64_t K, int r);
 // out[m][i] = scale * sum_z part[z][m][i] for the rows of the groups; exactly
 // one of f32 and bf16 is the output.
 hipError_t launch_group_reduce(const float* part, int splits, int64_t M, int64_t cols, float scale,

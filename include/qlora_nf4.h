@@ -459,6 +459,8 @@ int qlora_linear_dropout_bwd(const uint16_t* dY, const uint16_t* X, int64_t M,
  *   A  [E, K, r], B [E, r, N] bf16, dA and dB of the same shapes: zero for an
  *      expert without rows.  r = 0 (A, B, T, dA, dB may be NULL): base only.
  *   0 <= M < 2^31; M = 0 is allowed (X, Y, dY, dX, T may then be NULL).
+ *      QLORA_ERR_SHAPE also where a launch would hold 2^32 threads, which takes
+ *      1.6e9 rows at N, K <= 256 (r <= 64) and more memory than a GPU's elsewhere.
  *   d: dropout on the adapters' input as in qlora_linear_dropout_*, the
  *      mask being that of X [M, K]; NULL for none.
  * Backward, on each expert's rows: G = dY . B_e^T, dX = dY . deq(W_e) +
