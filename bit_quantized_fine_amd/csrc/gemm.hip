@@ -60,7 +60,9 @@ __device__ __forceinline__ void rank_tile(const RankJob& j, int x, int y, int z,
 template <int BP, int BQ, class LP, class LQ, int HL>
 __global__ __launch_bounds__(NT) void k_rank(RankJob j) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[RankKind<BP, BQ, LP, LQ, HL>::LDS];
-  rank_tile<BP, BQ, LP, LQ, HL>(j, blockIdx.x, blockIdx.y, blockIdx.z, lds, threadIdx.x);
+  // (the long axis along x: y and z take 65536 workgroups only; all three in x cost
+  // two divisions and 0.3 us a launch)
+  rank_tile<BP, BQ, LP, LQ, HL>(j, blockIdx.y, blockIdx.x, blockIdx.z, lds, threadIdx.x);
 }
 
 // Two independent products in one launch (workgroups [0, a.nblk) run the
@@ -390,7 +392,7 @@ hipError_t launch_lora_down(const uint16_t* X, int64_t M, int64_t K, const uint1
   auto kern = d.on() ? k_rank<RB_R, RB_X, Bf16RedMajor<RB_R>, Bf16Nat<RB_X, true>, 0>
                      : k_rank<RB_R, RB_X, Bf16RedMajor<RB_R>, Bf16Nat<RB_X>, 0>;
   prof_begin(4, stream);
-  hipLaunchKernelGGL(kern, dim3(pt, qt, sp.splits), dim3(NT), 0, stream,
+  hipLaunchKernelGGL(kern, dim3(qt, pt, sp.splits), dim3(NT), 0, stream,
                      job(op(A, r, r, K), op(X, K, M, K), sp, ws, r, M, pt, qt, d));
   hipError_t e = hipGetLastError();
   if (e == hipSuccess) e = reduce<false>(ws, sp.splits, M * r, d.scale(), T, stream);
@@ -439,7 +441,7 @@ hipError_t launch_grad_a(const uint16_t* X, int64_t M, int64_t K, const float* G
   auto kern = d.on() ? k_rank<RB_R, RB_X, F32RedMajor<RB_R>, Bf16RedMajor<RB_X, true>, 1>
                      : k_rank<RB_R, RB_X, F32RedMajor<RB_R>, Bf16RedMajor<RB_X>, 1>;
   prof_begin(4, stream);
-  hipLaunchKernelGGL(kern, dim3(pt, qt, sp.splits), dim3(NT), 0, stream,
+  hipLaunchKernelGGL(kern, dim3(qt, pt, sp.splits), dim3(NT), 0, stream,
                      job(op(G, r, r, M), op(X, K, K, M), sp, ws, r, K, pt, qt, d));
   hipError_t e = hipGetLastError();
   if (e == hipSuccess) e = reduce<true>(ws, sp.splits, K * r, s * d.scale(), dA, stream);

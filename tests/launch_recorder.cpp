@@ -16,6 +16,7 @@ struct Dim {
 struct Launch {
   int device;
   uint64_t threads_x;   // gridDim.x * blockDim.x
+  uint64_t blocks_yz;   // the larger of gridDim.y and gridDim.z
   uint64_t lds;         // dynamic, bytes
   uint64_t allowed;     // the kernel's limit on the device, 0 when never set
 };
@@ -57,7 +58,7 @@ int __hipPopCallConfiguration(Dim* grid, Dim* block, size_t* lds, void** stream)
 }
 int hipLaunchKernel(const void* f, Dim grid, Dim block, void**, size_t lds, void*) {
   const auto it = limits.find({current, f});
-  launches.push_back({current, uint64_t(grid.x) * block.x, lds,
+  launches.push_back({current, uint64_t(grid.x) * block.x, grid.y > grid.z ? grid.y : grid.z, lds,
                       it == limits.end() ? 0 : it->second});
   return 0;
 }
@@ -66,6 +67,7 @@ void recorder_device(int d) { current = d; }
 int recorder_count() { return static_cast<int>(launches.size()); }
 void recorder_clear() { launches.clear(); }
 uint64_t recorder_threads_x(int i) { return launches[i].threads_x; }
+uint64_t recorder_blocks_yz(int i) { return launches[i].blocks_yz; }
 uint64_t recorder_lds(int i) { return launches[i].lds; }
 uint64_t recorder_allowed(int i) { return launches[i].allowed; }
 }

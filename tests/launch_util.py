@@ -16,7 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 HEAD = """
 import ctypes, json, sys
 rec = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)
-for name in ("threads_x", "lds", "allowed"):
+for name in ("threads_x", "blocks_yz", "lds", "allowed"):
     getattr(rec, "recorder_" + name).restype = ctypes.c_uint64
 import bit_quantized_fine_amd as q
 L = q.lib()
@@ -28,6 +28,9 @@ def weight(N, K, dq=1, book=0):
 
 def drop(p):
     return ctypes.byref(q._Dropout(1 << 20, p))
+
+def blocks_yz():
+    return [rec.recorder_blocks_yz(i) for i in range(rec.recorder_count())]
 
 def launches():
     n = rec.recorder_count()

@@ -1,5 +1,5 @@
 """Every size that a call admits can be launched: HIP takes fewer than 2^32 threads
-along x in one launch."""
+along x in one launch, and the GPU's limit along y and z is 65536 workgroups."""
 import pytest
 
 from launch_util import run
@@ -49,8 +49,24 @@ for E, N, K in ((1, 8, 64), (1, 256, 64), (4, 264, 64), (1024, 8, 64), (1, 8, 25
 print(json.dumps(out))
 """
 
+LAYER = """
+out = []
+for M in (1, 16, 17, 2048, 1 << 23, (1 << 23) + 200, 1 << 24, 1 << 28):
+    for N, K, r in ((8, 64, 8), (8, 64, 256), (4096, 4096, 64), (8, 1 << 22, 8), (1 << 22, 64, 8)):
+        if M * (2 * (N + K) + 8 * r) > 288 << 30:   # (T and its partial sums)
+            continue
+        for d in (None, drop(0.1)):
+            st = [L.qlora_linear_dropout_fwd(P, M, weight(N, K), P, P, r, 1.0, d, P, P, P, BIG, None),
+                  L.qlora_linear_dropout_bwd(P, P, M, weight(N, K), P, P, r, 1.0, d, None, P, P, P, P,
+                                             BIG, None)]
+            yz = max(blocks_yz())
+            out.append((M, N, K, r, yz, st, [l[0] for l in launches()]))
+            assert yz <= 65536, (M, N, K, r, yz)
+print(json.dumps(out))
+"""
 
-@pytest.mark.parametrize("calls", [ROWS, DROPOUT, GROUPED], ids=["exchange", "dropout", "grouped"])
+
+@pytest.mark.parametrize("calls", [ROWS, DROPOUT, GROUPED, LAYER], ids=["exchange", "dropout", "grouped", "layer"])
 def test_grids_of_admitted_sizes(tmp_path, calls):
     got = run(tmp_path, calls)
     assert len(got) > 7
