@@ -18,6 +18,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import sys
 import time
 
@@ -52,6 +53,16 @@ def kernel_source_hash(kernel):
     return h.hexdigest()[:16]
 
 
+def traffic_kernel(name):
+    """The key in KERNEL_SOURCES of a dispatched kernel's name, or None: the instance
+    that the training step runs has 0 as its first template argument (NF4 with double
+    quantization) and none of the variants (experts, dropout) switched on."""
+    m = re.search(r"\b(k_\w+)<0(?:, ([^<>]*))?>", name)
+    if m is None or m.group(1) not in KERNEL_SOURCES or "true" in (m.group(2) or ""):
+        return None
+    return m.group(1)
+
+
 def write_traffic(fetch_dir, write_dir, copy_mib, source_note, path=None):
     """profiles/traffic.json from two rocprofv3 counter runs of the same
     command (FETCH_SIZE, then WRITE_SIZE), each with a calibration copy of
@@ -67,8 +78,7 @@ def write_traffic(fetch_dir, write_dir, copy_mib, source_note, path=None):
                 if r["Counter_Name"] != counter:
                     continue
                 name = r["Kernel_Name"]
-                key = ("neg" if "neg_kernel" in name else
-                       next((k for k in KERNEL_SOURCES if f"{k}<0>" in name), None))
+                key = "neg" if "neg_kernel" in name else traffic_kernel(name)
                 if key:
                     agg.setdefault(key, []).append(float(r["Counter_Value"]))
         if "neg" not in agg:
