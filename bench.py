@@ -40,7 +40,8 @@ def log(*a):
 # stored counter reading is used only while these files are unchanged.
 KERNEL_SOURCES = {
     "k_fwd_gemm": ("gemm_fwd.hip", "device_common.hpp", "kernels.hpp"),
-    "k_dx_gemm": ("gemm_dx.hip", "device_common.hpp", "kernels.hpp"),
+    "k_dx_gemm": ("gemm_dx.hip", "device_common.hpp", "dropout.hpp", "expert_args.hpp",
+                  "group_tiles.hpp", "kernels.hpp"),
 }
 
 

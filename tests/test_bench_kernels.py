@@ -39,3 +39,18 @@ def test_the_training_steps_instance_is_recorded(tmp_path, kernel):
     assert set(out) == {kernel}
     assert out[kernel]["dispatches"] == 1
     assert out[kernel]["bytes_per_launch"] == pytest.approx(200 * 1024)
+
+
+@pytest.mark.parametrize("kernel", sorted(bench.KERNEL_SOURCES))
+def test_a_stored_reading_depends_on_every_source_of_its_kernel(kernel):
+    """The hash covers the kernel's file and whatever of this library it includes,
+    directly or not."""
+    files, todo = set(), [bench.KERNEL_SOURCES[kernel][0]]
+    while todo:
+        f = todo.pop()
+        if f in files:
+            continue
+        files.add(f)
+        with open(os.path.join(CSRC, f)) as fh:
+            todo += re.findall(r'^#include "(\w+\.hpp)"', fh.read(), re.M)
+    assert files == set(bench.KERNEL_SOURCES[kernel])
