@@ -3,8 +3,8 @@
 // wrote them), so the host only knows an upper bound of the tiles and every
 // workgroup finds its own tile here.
 //
-// Offsets are clamped to [0, M] and a group that ends before it starts is
-// empty, so offsets the caller got wrong cannot lead outside the buffers.
+// Offsets are clamped to [0, M] and a group that ends before it starts has no
+// tiles, so offsets the caller got wrong cannot lead outside the buffers.
 #pragma once
 
 #include "device_common.hpp"

@@ -447,9 +447,9 @@ int qlora_linear_dropout_bwd(const uint16_t* dY, const uint16_t* X, int64_t M,
  *   X [M, K], Y, dY [M, N] bf16, T [M, r] fp32, dX [M, K] bf16.
  *   offsets  int32 [E+1] in device memory (4-byte aligned), ascending, within
  *      [0, M]; a group may be empty.  The library reads them on the GPU only.
- *      Offsets outside [0, M] are clamped to it and a group that ends before
- *      it starts is empty; which rows overlapping groups leave is undefined,
- *      but nothing outside the buffers is touched.
+ *      Offsets outside [0, M] are clamped to it.  Where they do not ascend,
+ *      which rows of the outputs are written, and with what, is undefined, but
+ *      nothing outside the buffers is touched.
  *   Rows outside all groups (before offsets[0], from offsets[E] on) are not
  *      read, and their rows of Y, T and dX are left as they were.
  *   w  [E*N, K]: the experts' weights one after the other, quantized as one
