@@ -49,7 +49,9 @@ __device__ __forceinline__ float bf16_hi_to_f32(uint32_t packed) {
 }
 
 // Split fp32 values a, b into bf16 hi parts and bf16 lo parts (v - hi),
-// so that hi + lo carries ~16 significant bits of v.
+// so that hi + lo carries ~16 significant bits of v.  The fp32 factors T and G
+// enter their MFMAs this way: 2^-16 relative, where the bf16 results that they go
+// into are rounded by 2^-8, for two products where three would keep all 24 bits.
 __device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& hi,
                                              uint32_t& lo) {
   hi = pack_bf16x2(a, b);

@@ -23,7 +23,9 @@
 // Measured: 8 experts of 4096 x 11008, r = 64, 8192 rows, the whole backward: 903
 // us against 1030 with the kernel that passes dequantized weights through LDS
 // (gemm_dx.hip), 1003 against 1107 with dropout (whose second set of sums spills
-// some addresses).  Bound like the forward by the chip's power.
+// some addresses); 876 to 892 and 966 on other cards.  Bound by the chip's power and
+// by its own instructions: for as many MFMAs as the forward the kernel is busy for
+// 11% more cycles, with twice the scalar and 1.17 times the LDS instructions.
 #include <algorithm>
 #include <type_traits>
 
@@ -399,15 +401,15 @@ hipError_t launch_tiles(const ExpertArgs& a, const Nf4Tables& tb, hipStream_t st
 
 }  // namespace
 
-// Whole backwards with this kernel / with the other, which has narrower tiles and can
-// split its reduction: 8 experts of 4096 x 4096 with 1024 rows (208 tiles at most)
-// 105 / 88 us, with 2048 rows (288 tiles) 119 / 163; 32 experts of 2048 x 1024 with
-// 4096 rows (212) 74 / 68, with 8192 rows (296) 86 / 117; 64 experts of 1024 x 2048
-// with 128 rows (512) 53 / 71.  With up to 4 experts next to all tiles are full ones, and
+// Whole backwards (r = 64) with this kernel / with the other, which has narrower tiles
+// and can split its reduction: 8 experts of 4096 x 4096 with 1024 rows (208 tiles at
+// most) 111 / 96 us, with 2048 rows (288 tiles) 126 / 157; 32 experts of 2048 x 1024
+// with 4096 rows (212) 85 / 81, with 8192 rows (296) 96 / 128; 64 experts of 1024 x
+// 2048 with 128 rows (512) 61 / 80.  With up to 4 experts next to all tiles are full ones, and
 // the rounds that 256 CUs need for them count; a round of this kernel's takes 1.28
 // times as long as one of the other's 128 columns x 256 tokens.  One expert of
-// 11008 x 4096, 3900 rows of X (2 rounds of either): 550 / 460 us; 4096 x
-// 11008, 2048 rows (2 rounds / 3): 255 / 289.
+// 11008 x 4096, 3900 rows of X (2 rounds of either): 528 / 442 us; 4096 x
+// 11008, 2048 rows (2 rounds / 3): 233 / 269.
 bool expert_dx_fits(int64_t M, int E, int64_t K) {
   const int64_t tiles = (K + VK - 1) / VK * group_tile_bound(M, E, 16 * VTB);
   if (tiles < 256 || E > 4) return tiles >= 256;

@@ -15,11 +15,12 @@
 // while the MFMAs of the current one run.  X waits one or two chunks ahead in
 // registers.
 //
-// Measured: 8 experts of 11008 x 4096, r = 64, 8192 rows: 740 us, 1.02
-// PFLOP/s where a large matrix product of the library reaches 1.38: bound by the
-// chip's power.  Of the loop's time the lookups take 19%, scaling and packing
-// 11%, X's reads 7% (timed without each).  The same experts with 96 rows: 54 us,
-// 2.9 TB/s of codes.
+// Measured: 8 experts of 11008 x 4096, r = 64, 8192 rows: 765 to 785 us for the whole
+// forward on most cards (740 on the best), 0.96 to 0.99 PFLOP/s where a large matrix
+// product of the library reaches 1.38: bound by the chip's power.  Of the loop's
+// time the lookups take 19%, scaling and packing 11%, X's reads 7% (timed without
+// each).  96 rows on seven of the same experts: 57 us for this kernel, 2.8 TB/s of
+// codes (67 us with T's two launches).
 //
 // The offsets are read on the GPU: the grid holds the most tiles the groups
 // could make, a workgroup finds its expert and rows in them, and the last tile
@@ -503,11 +504,12 @@ struct ExpertPlan {
   GemmSplit sp;
 };
 
-// Rows up to which the few-token kernel is used: it streams the weights of the
-// experts that have rows faster than k_expert_fwd (8 experts of 4096 x 4096, r =
-// 16: 21 against 26 us at 4 rows, 30 against 32 at 16) until experts have more
-// rows than one MFMA column tile or X is read by too many workgroups (38 against
-// 33 us at 32 rows).
+// Rows up to which the few-token kernel is used.  It streams the weights of few
+// experts faster than k_expert_fwd: 8 experts of 4096 x 4096, r = 16, 4 rows on three
+// of them 20 against 25 us, 16 rows on one 19 against 26, on three or four 22.6
+// against 26.  With rows on all eight it is the slower one (31 against 30 us at 8
+// rows, 32 against 30 at 16), but the host does not know how many have any.  At 32
+// rows an expert can have more than one MFMA column tile, and it takes 36 against 31.
 constexpr int64_t kFewRows = 16;
 // Rows of an average expert above which a tile holds 64 tokens, and 192 (the
 // narrower bodies take over in the last tile of a group).  Same experts, 32 /

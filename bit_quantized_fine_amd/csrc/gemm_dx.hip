@@ -30,8 +30,8 @@
 // stores them where the dequantized values would go.  kFormNoDq reads one
 // fp32 constant per block (codes without double quantization).
 //
-// kExperts instantiates it over token rows grouped by expert (see the forward
-// GEMM): the reduction runs over the rows of the tile's expert.  With kQ = 64
+// kExperts instantiates it over token rows grouped by expert (as expert_fwd.hip is):
+// the reduction runs over the rows of the tile's expert.  With kQ = 64
 // a tile is 64 tokens and the four wave columns split the 128 output columns;
 // kQ = 128 lies between.  It serves the calls of few tiles, whose reduction it can
 // split; with enough tiles to fill the machine expert_dx.hip is faster.
@@ -498,8 +498,9 @@ __global__ __launch_bounds__(XT) void k_dx_gemm(DxArgs args, Nf4Tables tb) {
     const GroupTile gt = groups.find(t.v - z * slots);
     if (gt.e < 0) return;
     // the last tile of a group runs the narrowest body that holds its rows
-    // (a launch of 64-token tiles was no faster at any number of rows: a backward
-    // of 8 experts of 4096 x 4096 took 78 / 78 us at 16 rows, 119 / 90 at 512)
+    // (a launch of 64-token tiles is no faster at any number of rows: a backward of 8
+    // experts of 4096 x 4096, r = 64, takes 58 / 59 us at 16 and 128 rows, 112 / 74
+    // at 512 uneven ones)
     const int rows = gt.end - gt.row0;
     if (rows <= 64)
       dx_tile<kForm, 64, true, kDrop>(args, dyn, gt.e, gt.row0, gt.end, pt, z);
