@@ -127,6 +127,14 @@ int check_rank(int r) {
   return QLORA_OK;
 }
 
+// Every launch over M rows holds fewer than 2^32 threads: the reductions of T and
+// of G with dB take one for four values, a GEMM 512 for 128 x 256 outputs.
+int check_rows(int64_t M, int64_t cols, int64_t N, int r) {
+  if (M < 1 || M > (int64_t(1) << 40)) return QLORA_ERR_SHAPE;
+  if (r > 0 && M + N > ((int64_t(1) << 34) - 4096) / r) return QLORA_ERR_SHAPE;
+  return (cols + 127) / 128 * ((M + 255) / 256) < int64_t(1) << 23 ? QLORA_OK : QLORA_ERR_SHAPE;
+}
+
 Nf4View view(const qlora_nf4_weight* w) {
   return Nf4View{w->codes, w->absmax_q, w->absmax_scale, w->N, w->K};
 }
@@ -161,7 +169,8 @@ int check_fwd_rest(const uint16_t* X, int64_t M, int64_t N, const uint16_t* A, c
   if (st) return st;
   if (!X || !Y) return QLORA_ERR_NULL;
   if (r > 0 && (!A || !B || !T)) return QLORA_ERR_NULL;
-  if (M < 1 || N % 8 != 0) return QLORA_ERR_SHAPE;
+  if (N % 8 != 0) return QLORA_ERR_SHAPE;
+  if ((st = check_rows(M, N, N, r))) return st;
   if (!aligned16(X) || !aligned16(Y) || (r > 0 && (!aligned16(A) || !aligned16(B) || !aligned16(T))))
     return QLORA_ERR_ALIGN;
   return QLORA_OK;
@@ -258,7 +267,8 @@ int bwd_impl(const uint16_t* dY, const uint16_t* X, int64_t M, const Nf4View& v,
   if (st) return st;
   if (!dY || !X) return QLORA_ERR_NULL;
   if (r > 0 && (!A || !B || !dA || !dB)) return QLORA_ERR_NULL;
-  if (M < 1 || v.N % 8 != 0) return QLORA_ERR_SHAPE;
+  if (v.N % 8 != 0) return QLORA_ERR_SHAPE;
+  if ((st = check_rows(M, std::max(v.N, v.K), v.N, r))) return st;
   if (!aligned16(dY) || !aligned16(X) || (dX && !aligned16(dX)) ||
       (r > 0 && (!aligned16(A) || !aligned16(B) || !aligned16(dA) || !aligned16(dB) ||
                  (T_saved && !aligned16(T_saved)))))
@@ -625,7 +635,7 @@ int qlora_lora16_fwd(const uint16_t* X, int64_t M, const uint16_t* W, int64_t N,
   if ((st = check_rank(r))) return st;
   if (!X || !Y) return QLORA_ERR_NULL;
   if (r > 0 && (!A || !B || !T)) return QLORA_ERR_NULL;
-  if (M < 1) return QLORA_ERR_SHAPE;
+  if ((st = check_rows(M, N, N, r))) return st;
   if (!aligned16(X) || !aligned16(Y) || (r > 0 && (!aligned16(A) || !aligned16(B) || !aligned16(T))))
     return QLORA_ERR_ALIGN;
   const size_t need = dense_fwd_ws_bytes(M, N, K, r);
@@ -741,6 +751,7 @@ int qlora_block_fwd(const uint16_t* X, int64_t M, const qlora_nf4_weight* w, int
   if (st) return st;
   if (r == 0) return QLORA_ERR_RANK;
   if ((st = check_block(w, S, r))) return st;
+  if ((st = check_rows(M, w->N, w->N, S * r))) return st;
   const int64_t nseg = w->N / S;
   const int rt = S * r;
   const size_t need = block_fwd_ws_bytes(M, S, nseg, w->K, r);
@@ -780,7 +791,7 @@ int qlora_block_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const qlor
   if (r == 0) return QLORA_ERR_RANK;
   if ((st = check_block(w, S, r))) return st;
   if (!dY || !X || !A || !B || !dA || !dB) return QLORA_ERR_NULL;
-  if (M < 1) return QLORA_ERR_SHAPE;
+  if ((st = check_rows(M, std::max(w->N, w->K), w->N, S * r))) return st;
   if (!aligned16(dY) || !aligned16(X) || (dX && !aligned16(dX)) || !aligned16(A) ||
       !aligned16(B) || !aligned16(dA) || !aligned16(dB) || (T_saved && !aligned16(T_saved)))
     return QLORA_ERR_ALIGN;

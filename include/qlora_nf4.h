@@ -68,7 +68,10 @@ typedef enum {
   QLORA_OK = 0,
   QLORA_ERR_NULL = 1,       /* a required pointer is NULL */
   QLORA_ERR_SHAPE = 2,      /* M < 1, N < 1, K < 64, K % 64 != 0, N % 8 != 0
-                               (fwd/bwd), N > 2^22, K > 2^22 or N*K > 2^32 */
+                               (fwd/bwd), N > 2^22, K > 2^22 or N*K > 2^32; or
+                               so many rows that a launch would hold 2^32
+                               threads: (M + N)*r > 2^34 - 4096, or 2^23 tiles
+                               of 256 rows x 128 columns of Y or dX */
   QLORA_ERR_RANK = 3,       /* r outside [0, 256] or r % 8 != 0 */
   QLORA_ERR_ALIGN = 4,      /* a device pointer is not 16-byte aligned */
   QLORA_ERR_HIP = 5,        /* a HIP runtime call or kernel launch failed */
@@ -211,8 +214,9 @@ size_t qlora_linear_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int r);
  *      kept for the backward pass.
  *   workspace: device, at least qlora_linear_fwd_workspace_bytes() bytes
  *      (may be NULL when that is 0).
- * Accumulation is fp32; Y is rounded to bf16 once.  M >= 1, N % 8 == 0,
- * r % 8 == 0 (QLORA_ERR_SHAPE / QLORA_ERR_RANK otherwise).
+ * Accumulation is fp32; Y is rounded to bf16 once.  M >= 1 (and no more than a
+ * launch takes), N % 8 == 0, r % 8 == 0 (QLORA_ERR_SHAPE / QLORA_ERR_RANK
+ * otherwise).
  */
 int qlora_linear_fwd(const uint16_t* X, int64_t M, const qlora_nf4_weight* w,
                      const uint16_t* A, const uint16_t* B, int r, float s,

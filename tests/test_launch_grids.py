@@ -51,7 +51,7 @@ print(json.dumps(out))
 
 LAYER = """
 out = []
-for M in (1, 16, 17, 2048, 1 << 23, (1 << 23) + 200, 1 << 24, 1 << 28):
+for M in (1, 16, 17, 2048, 1 << 23, (1 << 23) + 200, 1 << 24, 1 << 26, 1 << 28):
     for N, K, r in ((8, 64, 8), (8, 64, 256), (4096, 4096, 64), (8, 1 << 22, 8), (1 << 22, 64, 8)):
         if M * (2 * (N + K) + 8 * r) > 288 << 30:   # (T and its partial sums)
             continue
@@ -59,8 +59,9 @@ for M in (1, 16, 17, 2048, 1 << 23, (1 << 23) + 200, 1 << 24, 1 << 28):
             st = [L.qlora_linear_dropout_fwd(P, M, weight(N, K), P, P, r, 1.0, d, P, P, P, BIG, None),
                   L.qlora_linear_dropout_bwd(P, P, M, weight(N, K), P, P, r, 1.0, d, None, P, P, P, P,
                                              BIG, None)]
-            yz = max(blocks_yz())
-            out.append((M, N, K, r, yz, st, [l[0] for l in launches()]))
+            yz = max(blocks_yz(), default=0)
+            out.append((M, N, K, r, yz, [s for s in st if M < 1 << 26 or s != 2],
+                        [l[0] for l in launches()]))
             assert yz <= 65536, (M, N, K, r, yz)
 print(json.dumps(out))
 """
