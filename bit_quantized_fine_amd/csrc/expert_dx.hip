@@ -23,7 +23,7 @@
 // Measured: 8 experts of 4096 x 11008, r = 64, 8192 rows, the whole backward: 903
 // us against 1030 with the kernel that passes dequantized weights through LDS
 // (gemm_dx.hip), 1003 against 1107 with dropout (whose second set of sums spills
-// some addresses); 876 to 892 and 966 on other cards.  Bound by the chip's power and
+// some addresses); 854 to 892 and 966 on other cards.  Bound by the chip's power and
 // by its own instructions: for as many MFMAs as the forward the kernel is busy for
 // 11% more cycles, with twice the scalar and 1.17 times the LDS instructions.
 #include <algorithm>
