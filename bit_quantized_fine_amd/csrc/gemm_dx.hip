@@ -146,8 +146,11 @@ __device__ __forceinline__ void dx_tile(const DxArgs& args, uint8_t* dyn, int e,
   const int nchunks = min(static_cast<int>((N + XN - 1) / XN), c0 + cps);
   const int KB = static_cast<int>(K / kBlock);
 
-  // Buffer descriptors: rows past W and tokens past the tile read as zero.
-  const uint32_t nb = static_cast<uint32_t>(NW * K / kBlock);
+  // Buffer descriptors: rows past W and tokens past the tile read as zero.  A row
+  // n >= N of an expert is the next one's: its dY columns read as zero, and the
+  // constants' buffers end with the expert's (whole groups of them), as zero times
+  // one that is not finite, or whose weight is not in bf16, would be NaN.
+  const uint32_t nb = static_cast<uint32_t>((n0 + N) * KB);
   const BufRes rc = make_bufres(args.codes, static_cast<uint32_t>(NW * K / 2));
   const BufRes re = make_bufres(args.absmax_q, nb);
   // second-level scales, or one fp32 constant per block (kFormNoDq)
@@ -182,20 +185,16 @@ __device__ __forceinline__ void dx_tile(const DxArgs& args, uint8_t* dyn, int e,
       ww[st][1] = buf_load16(rw, live ? o + 16u : 0x80000000u);
     } else {
       const uint32_t blk = dblk + static_cast<uint32_t>(c * XN * KB);
-      // A row n >= N of an expert is the next one's: its dY columns read as zero,
-      // and so do its constants, as zero times one that is not finite (or whose
-      // weight is not, in bf16) would be NaN.
-      const bool own = live && (!kExperts || c * XN + dr < static_cast<int>(N));
       cw[st] = __builtin_bit_cast(
           u32x2, __builtin_amdgcn_raw_buffer_load_b64(
                      rc, live ? dcode + static_cast<uint32_t>(c * XN) * static_cast<uint32_t>(K / 2)
                               : 0x80000000u, 0, 0));
       if constexpr (kForm == kFormNoDq) {   // e = 1, d = the block's absmax
         ce[st] = 1u;
-        cd[st] = buf_load_f32(rd, own ? blk * 4u : 0x80000000u);
+        cd[st] = buf_load_f32(rd, live ? blk * 4u : 0x80000000u);
       } else {
-        ce[st] = buf_load_u8(re, own ? blk : 0x80000000u);
-        cd[st] = buf_load_f32(rd, own ? (blk / kGroup) * 4u : 0x80000000u);
+        ce[st] = buf_load_u8(re, live ? blk : 0x80000000u);
+        cd[st] = buf_load_f32(rd, live ? (blk / kGroup) * 4u : 0x80000000u);
       }
     }
   };
