@@ -455,9 +455,9 @@ def run(st):
     if kind == "norm":
         if case["back"]:
             return q.qlora_rms_norm_bwd(st["dy"], st["h"], st["rstd"], st["g"], dres=st["dres"])
-        h, y, rstd, y8 = q.qlora_rms_norm_fwd(st["x"], st["g"], residual=st["residual"], eps=EPS,
-                                              act8=case["act8"])
-        return (h, y, rstd, q.qlora_act8_unpack(y8)) if case["act8"] else (h, y, rstd)
+        out = q.qlora_rms_norm_fwd(st["x"], st["g"], residual=st["residual"], eps=EPS,
+                                   act8=case["act8"])
+        return out[:3] + (q.qlora_act8_unpack(out[3]),) if case["act8"] else out
     if kind == "act8":
         x8 = q.qlora_act8_pack(st["x"])
         return q.qlora_act8_unpack(x8), x8.scales
