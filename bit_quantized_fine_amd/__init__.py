@@ -19,6 +19,7 @@ QLORA_OK = 0
 QLORA_ERR_SCRATCH = 7
 QLORA_ERR_FORMAT = 8
 CODEBOOKS = {"nf4": 0, "int4": 1, "fp4": 2}   # qlora_codebook of the header
+SCORES = {"softmax": 0, "sigmoid": 1}         # qlora_score of the header
 NOALLOC_SCRATCH_BYTES = 32 << 20   # QLORA_NOALLOC_SCRATCH_BYTES of the header
 _lib = None
 
@@ -38,6 +39,16 @@ class _Q4Weight(ctypes.Structure):
 
 class _Dropout(ctypes.Structure):
     _fields_ = [("state", ctypes.c_void_p), ("p", ctypes.c_float)]
+
+
+class _Act8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class _RouterConfig(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("topk", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class _AdamWConfig(ctypes.Structure):
@@ -172,6 +183,40 @@ _SIGS = {
     "qlora_expert_combine_bwd": (ctypes.c_int, [
         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int64,
         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "qlora_act8_pack": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.POINTER(_Act8), ctypes.c_void_p]),
+    "qlora_act8_unpack": (ctypes.c_int, [
+        ctypes.POINTER(_Act8), ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]),
+    "qlora_linear_act8_bwd_workspace_bytes": (ctypes.c_size_t, [
+        ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
+    "qlora_grouped_act8_bwd_workspace_bytes": (ctypes.c_size_t, [
+        ctypes.c_int64, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
+    "qlora_linear_act8_bwd": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.POINTER(_Act8), ctypes.c_int64, ctypes.POINTER(_Q4Weight),
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.POINTER(_Dropout),
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_size_t, ctypes.c_void_p]),
+    "qlora_grouped_act8_bwd": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.POINTER(_Act8), ctypes.c_int64, ctypes.c_void_p, ctypes.c_int,
+        ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(_Q4Weight),
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.POINTER(_Dropout),
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_size_t, ctypes.c_void_p]),
+    "qlora_rms_norm_fwd": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+        ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.POINTER(_Act8), ctypes.c_void_p]),
+    "qlora_rms_norm_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
+    "qlora_rms_norm_bwd": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qlora_router_fwd": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p,
+        ctypes.POINTER(_RouterConfig), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "qlora_router_bwd": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64,
+        ctypes.c_int, ctypes.POINTER(_RouterConfig), ctypes.c_void_p, ctypes.c_void_p]),
     "qlora_adamw_step": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                         ctypes.c_void_p, ctypes.c_int64,
                                         ctypes.POINTER(_AdamWConfig), ctypes.c_int64,
@@ -755,9 +800,10 @@ def qlora_linear_dropout_bwd(dY, X, w, A=None, B=None, s: float = 1.0, p: float 
 
 
 def _grads(fn, groups, dY, X, M, N, K, cw, wt, A, B, r, s, d, state, T, need_dx, dX, dA, dB,
-           shape_a, shape_b, workspace, need):
+           shape_a, shape_b, workspace, need, kept=None):
     """The rest of a backward call: outputs, workspace, marshalling.  groups is
-    () or (offsets, E)."""
+    () or (offsets, E).  With an 8-bit checkpoint in X's place, kept is (its C
+    view, constants, further arguments, order or None) and X its codes."""
     import torch
     if r == 0:
         T = dA = dB = None
@@ -767,9 +813,14 @@ def _grads(fn, groups, dY, X, M, N, K, cw, wt, A, B, r, s, d, state, T, need_dx,
     _maybe(dX, "dX", (M, K), torch.bfloat16)
     _maybe(dA, "dA", shape_a, torch.bfloat16)
     _maybe(dB, "dB", shape_b, torch.bfloat16)
-    dev = _one_gpu("X dY w.codes w.absmax_q w.absmax_scale offsets A B state T dX dA dB workspace",
-                   X, dY, *wt, groups[0] if groups else None, A, B, state, T, dX, dA, dB,
-                   workspace)
+    names = "X dY w.codes w.absmax_q w.absmax_scale offsets A B state T dX dA dB workspace"
+    tensors = (X, dY, *wt, groups[0] if groups else None, A, B, state, T, dX, dA, dB, workspace)
+    if kept is None:
+        dev, x = _one_gpu(names, *tensors), (X.data_ptr(),)
+    else:
+        x8, scales, more, order = kept
+        dev = _one_gpu("x8.codes" + names[1:] + " x8.scales order", *tensors, scales, order)
+        x = (ctypes.byref(x8), *more)
     workspace = _scratch(workspace, need, dev)
     if need_dx and dX is None:
         dX = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
@@ -778,15 +829,20 @@ def _grads(fn, groups, dY, X, M, N, K, cw, wt, A, B, r, s, d, state, T, need_dx,
     if r > 0 and dB is None:
         dB = torch.empty(shape_b, dtype=torch.bfloat16, device=dev)
     where = (groups[0].data_ptr(), groups[1]) if groups else ()
-    _call(fn, dev, dY.data_ptr(), X.data_ptr(), M, *where, ctypes.byref(cw), _at(A), _at(B), r, s,
+    _call(fn, dev, dY.data_ptr(), *x, M, *where, ctypes.byref(cw), _at(A), _at(B), r, s,
           ctypes.byref(d), _at(T), _at(dX), _at(dA), _at(dB), _at(workspace), need)
     return dX, dA, dB
 
 
 def _experts(X, offsets, w, E, A, B):
     """Checks shared by the grouped calls: (M, N, r, C view, weight tensors)."""
-    import torch
     M = _rows(X, w.K)
+    return (M, *_expert_layers(offsets, w, E, A, B))
+
+
+def _expert_layers(offsets, w, E, A, B):
+    """The same without X: (N, r, C view, weight tensors)."""
+    import torch
     cw, *wt = _q4(w)
     if E < 1 or w.N % E:
         raise ValueError(f"w.N = {w.N} is not a multiple of E = {E}")
@@ -802,7 +858,7 @@ def _experts(X, offsets, w, E, A, B):
         r = A.shape[2]
         _is(A, "A", (E, w.K, r), torch.bfloat16)
         _is(B, "B", (E, r, N), torch.bfloat16)
-    return M, N, r, cw, wt
+    return N, r, cw, wt
 
 
 def qlora_grouped_fwd(X, offsets, w, E: int, A=None, B=None, s: float = 1.0, p: float = 0.0,
@@ -935,6 +991,256 @@ def qlora_expert_combine_bwd(dOut, Y, inverse, weights, dY=None, dweights=None):
     _call("qlora_expert_combine_bwd", dev, dOut.data_ptr(), Y.data_ptr(), tokens, topk, K,
           inverse.data_ptr(), weights.data_ptr(), dY.data_ptr(), dweights.data_ptr())
     return dY, dweights
+
+
+# ---------------------------------------------------------------------------
+# Activations in 8 bits and the backward pass from them, the norm in front of a
+# layer, and the routing to experts.
+# ---------------------------------------------------------------------------
+
+class Act8(NamedTuple):
+    """Activations [M, K] as an 8-bit checkpoint: one signed byte a value and one
+    fp32 constant for each 64 of a row."""
+    codes: "torch.Tensor"    # int8 [M, K]
+    scales: "torch.Tensor"   # float32 [M, K/64]
+
+    def _c(self) -> _Act8:
+        return _Act8(self.codes.data_ptr(), self.scales.data_ptr())
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + 4 * self.scales.numel()
+
+
+def _empty_act8(M, K, dev):
+    import torch
+    return Act8(torch.empty((M, K), dtype=torch.int8, device=dev),
+                torch.empty((M, K // 64), dtype=torch.float32, device=dev))
+
+
+def _check_act8(x8, name, M=None, K=None):
+    """(M, K) of a checkpoint (of the given sizes)."""
+    import torch
+    if x8 is None:
+        raise ValueError(f"{name} is required")
+    if x8.codes.dim() != 2:
+        raise ValueError(f"{name}.codes must be [M, K]")
+    M, K = x8.codes.shape[0] if M is None else M, x8.codes.shape[1] if K is None else K
+    if K % 64:
+        raise ValueError(f"{name}: K = {K} is not a multiple of 64")
+    _is(x8.codes, name + ".codes", (M, K), torch.int8)
+    _is(x8.scales, name + ".scales", (M, K // 64), torch.float32)
+    return M, K
+
+
+def _matrix(t, name):
+    import torch
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be two-dimensional")
+    _is(t, name, t.shape, torch.bfloat16)
+    return t.shape
+
+
+def qlora_act8_pack(X, out: Optional[Act8] = None) -> Act8:
+    """The 8-bit checkpoint of X (bf16 [M, K], K % 64 == 0): blocks of 64 values
+    along a row, codes rint(x / c) with c = max |x| / 127."""
+    M, K = _matrix(X, "X")
+    if K % 64:
+        raise ValueError(f"K = {K} is not a multiple of 64")
+    if out is None:
+        dev = _one_gpu("X", X)
+        out = _empty_act8(M, K, dev)
+    else:
+        _check_act8(out, "out", M, K)
+        dev = _one_gpu("X out.codes out.scales", X, out.codes, out.scales)
+    _call("qlora_act8_pack", dev, X.data_ptr(), M, K, ctypes.byref(out._c()))
+    return out
+
+
+def qlora_act8_unpack(x8: Act8, out=None):
+    """The values (bf16 [M, K]) of an 8-bit checkpoint."""
+    import torch
+    M, K = _check_act8(x8, "x8")
+    _maybe(out, "out", (M, K), torch.bfloat16)
+    dev = _one_gpu("x8.codes x8.scales out", x8.codes, x8.scales, out)
+    if out is None:
+        out = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    _call("qlora_act8_unpack", dev, ctypes.byref(x8._c()), M, K, out.data_ptr())
+    return out
+
+
+def qlora_linear_act8_bwd(dY, x8: Act8, w, A=None, B=None, s: float = 1.0, p: float = 0.0,
+                          state=None, T=None, need_dx: bool = True, dX=None, dA=None, dB=None,
+                          workspace=None):
+    """qlora_linear_dropout_bwd from an 8-bit checkpoint of the layer's input:
+    (dX bf16 [M,K] or None, dA bf16 [K,r], dB bf16 [r,N])."""
+    import torch
+    M, K = _check_act8(x8, "x8", K=w.K)
+    cw, *wt = _q4(w)
+    _is(dY, "dY", (M, w.N), torch.bfloat16)
+    r = _check_adapters(A, B, w)
+    d = _drop(p, state)
+    return _grads("qlora_linear_act8_bwd", (), dY, x8.codes, M, w.N, K, cw, wt, A, B, r, s, d,
+                  state, T, need_dx, dX, dA, dB, (K, r), (r, w.N), workspace,
+                  lib().qlora_linear_act8_bwd_workspace_bytes(M, w.N, K, r),
+                  (x8._c(), x8.scales, (), None))
+
+
+def qlora_grouped_act8_bwd(dY, x8: Act8, offsets, w, E: int, A=None, B=None, s: float = 1.0,
+                           p: float = 0.0, state=None, order=None, topk: int = 1, T=None,
+                           need_dx: bool = True, dX=None, dA=None, dB=None, workspace=None):
+    """qlora_grouped_bwd from an 8-bit checkpoint.  Without an order, x8 holds the
+    rows of the grouped input; with order (int32 [M], as qlora_expert_plan gives
+    it) it holds the tokens' rows, each once, and row i of the grouped input is
+    row order[i] // topk of it.  Returns (dX bf16 [M,K] or None, dA bf16
+    [E,K,r], dB bf16 [E,r,N])."""
+    import torch
+    if dY.dim() != 2:
+        raise ValueError("dY must be [M, N]")
+    M = dY.shape[0]
+    tokens, K = _check_act8(x8, "x8", None if order is not None else M, w.K)
+    _maybe(order, "order", (M,), torch.int32)
+    N, r, cw, wt = _expert_layers(offsets, w, E, A, B)
+    _is(dY, "dY", (M, N), torch.bfloat16)
+    d = _drop(p, state)
+    return _grads("qlora_grouped_act8_bwd", (offsets, E), dY, x8.codes, M, N, K, cw, wt, A, B, r,
+                  s, d, state, T, need_dx, dX, dA, dB, (E, K, r), (E, r, N), workspace,
+                  lib().qlora_grouped_act8_bwd_workspace_bytes(M, E, N, K, r),
+                  (x8._c(), x8.scales, (tokens, _at(order), topk), order))
+
+
+def _norm_weight(g, K):
+    """1 if g [K] is fp32, 0 if bf16."""
+    import torch
+    fp32 = g.dtype is torch.float32
+    _is(g, "g", (K,), torch.float32 if fp32 else torch.bfloat16)
+    return int(fp32)
+
+
+def qlora_rms_norm_fwd(x, g, residual=None, eps: float = 1e-5, act8=False, h=None, y=None,
+                       rstd=None):
+    """h = x + residual (x itself without one), y = h / rms(h) * g: (h bf16 [M,K],
+    y bf16 [M,K], rstd fp32 [M]), and with act8 (True, or an Act8 to write to)
+    the 8-bit checkpoint of y too.  g is fp32 or bf16 [K]; h may be x or
+    residual."""
+    import torch
+    M, K = _matrix(x, "x")
+    g32 = _norm_weight(g, K)
+    _maybe(residual, "residual", (M, K), torch.bfloat16)
+    if residual is None:
+        if h is not None and h is not x:
+            raise ValueError("without a residual h is x")
+        h = x
+    else:
+        _maybe(h, "h", (M, K), torch.bfloat16)
+    _maybe(y, "y", (M, K), torch.bfloat16)
+    _maybe(rstd, "rstd", (M,), torch.float32)
+    keep = act8 is not False and act8 is not None
+    out = act8 if keep and act8 is not True else None
+    if keep and K % 64:
+        raise ValueError(f"K = {K} is not a multiple of 64")
+    if out is not None:
+        _check_act8(out, "act8", M, K)
+    dev = _one_gpu("x g residual h y rstd act8.codes act8.scales", x, g, residual, h, y, rstd,
+                   *(out if out is not None else (None, None)))
+    if h is None:
+        h = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    if y is None:
+        y = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    if rstd is None:
+        rstd = torch.empty(M, dtype=torch.float32, device=dev)
+    if keep and out is None:
+        out = _empty_act8(M, K, dev)
+    _call("qlora_rms_norm_fwd", dev, x.data_ptr(), _at(residual), g.data_ptr(), g32, M, K, eps,
+          h.data_ptr(), y.data_ptr(), rstd.data_ptr(), ctypes.byref(out._c()) if keep else None)
+    return (h, y, rstd, out) if keep else (h, y, rstd)
+
+
+def qlora_rms_norm_bwd(dy, h, rstd, g, dres=None, need_dg: bool = True, dx=None, dg=None,
+                       workspace=None):
+    """Backward of qlora_rms_norm_fwd: (dx bf16 [M,K], the gradient of x and of the
+    residual, with dres, the gradient that reaches h from elsewhere, added; dg of
+    g's type [K], or None without need_dg).  dx may be dres."""
+    import torch
+    M, K = _matrix(h, "h")
+    g32 = _norm_weight(g, K)
+    _is(dy, "dy", (M, K), torch.bfloat16)
+    _is(rstd, "rstd", (M,), torch.float32)
+    _maybe(dres, "dres", (M, K), torch.bfloat16)
+    _maybe(dx, "dx", (M, K), torch.bfloat16)
+    if not need_dg:
+        dg = None
+    _maybe(dg, "dg", (K,), g.dtype)
+    need = lib().qlora_rms_norm_bwd_workspace_bytes(M, K) if need_dg else 0
+    dev = _one_gpu("h dy rstd g dres dx dg workspace", h, dy, rstd, g, dres, dx, dg, workspace)
+    workspace = _scratch(workspace, need, dev)
+    if dx is None:
+        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    if need_dg and dg is None:
+        dg = torch.empty(K, dtype=g.dtype, device=dev)
+    _call("qlora_rms_norm_bwd", dev, dy.data_ptr(), _at(dres), h.data_ptr(), rstd.data_ptr(),
+          g.data_ptr(), g32, M, K, dx.data_ptr(), _at(dg), _at(workspace), need)
+    return dx, dg
+
+
+def _router(logits, topk, score, groups, top_groups, group_top, renorm, scale):
+    """(tokens, E, 1 for fp32 logits, the C configuration)."""
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits must be [tokens, E]")
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
+    fp32 = logits.dtype is torch.float32
+    _is(logits, "logits", logits.shape, torch.float32 if fp32 else torch.bfloat16)
+    return (*logits.shape, int(fp32),
+            _RouterConfig(SCORES[score], topk, groups, top_groups, group_top,
+                          1 if renorm else 0, scale))
+
+
+def qlora_router_fwd(logits, topk: int, score: str = "softmax", bias=None, groups: int = 1,
+                     top_groups: int = 1, group_top: int = 1, renorm: bool = True,
+                     scale: float = 1.0, ids=None, weights=None):
+    """The topk experts of every token, best first, and their weights: (ids int32
+    [tokens, topk], weights fp32 [tokens, topk]).  logits are fp32 or bf16
+    [tokens, E]; score is "softmax" or "sigmoid"; bias (fp32 [E]) takes part in
+    the choice alone; of `groups` equal groups of experts the top_groups with the
+    best sum of their group_top (1 or 2) best experts stay; renorm divides the
+    weights by their sum.  Experts with a logit of -inf are not chosen; a slot
+    left over has id -1 and weight 0."""
+    import torch
+    tokens, E, fp32, cfg = _router(logits, topk, score, groups, top_groups, group_top, renorm,
+                                   scale)
+    _maybe(bias, "bias", (E,), torch.float32)
+    _maybe(ids, "ids", (tokens, topk), torch.int32)
+    _maybe(weights, "weights", (tokens, topk), torch.float32)
+    dev = _one_gpu("logits bias ids weights", logits, bias, ids, weights)
+    if ids is None:
+        ids = torch.empty((tokens, max(topk, 0)), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((tokens, max(topk, 0)), dtype=torch.float32, device=dev)
+    _call("qlora_router_fwd", dev, logits.data_ptr(), fp32, tokens, E, _at(bias),
+          ctypes.byref(cfg), ids.data_ptr(), weights.data_ptr())
+    return ids, weights
+
+
+def qlora_router_bwd(dweights, logits, ids, score: str = "softmax", renorm: bool = True,
+                     scale: float = 1.0, dlogits=None):
+    """The gradient of the logits (of their type, [tokens, E]) from that of the
+    weights (fp32 [tokens, topk]), the choice held fixed: ids, score, renorm and
+    scale are those of qlora_router_fwd."""
+    import torch
+    if ids.dim() != 2:
+        raise ValueError("ids must be [tokens, topk]")
+    topk = ids.shape[1]
+    tokens, E, fp32, cfg = _router(logits, topk, score, 1, 1, 1, renorm, scale)
+    _is(ids, "ids", (tokens, topk), torch.int32)
+    _is(dweights, "dweights", (tokens, topk), torch.float32)
+    _maybe(dlogits, "dlogits", logits.shape, logits.dtype)
+    dev = _one_gpu("logits dweights ids dlogits", logits, dweights, ids, dlogits)
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    _call("qlora_router_bwd", dev, dweights.data_ptr(), logits.data_ptr(), fp32, ids.data_ptr(),
+          tokens, E, ctypes.byref(cfg), dlogits.data_ptr())
+    return dlogits
 
 
 def _addr(x):

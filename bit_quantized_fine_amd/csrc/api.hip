@@ -111,6 +111,7 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 constexpr int64_t kMaxK = int64_t(1) << 22;        // weight columns (in features)
 constexpr int64_t kMaxN = int64_t(1) << 22;        // weight rows (out features)
 constexpr int64_t kMaxElems = int64_t(1) << 32;    // N * K of one weight
+constexpr int64_t kMaxActs = int64_t(1) << 40;     // M * K of a checkpoint
 
 int check_weight(const qlora_nf4_weight* w) {
   if (!w || !w->codes || !w->absmax_q || !w->absmax_scale) return QLORA_ERR_NULL;
@@ -259,13 +260,14 @@ int fwd_impl(const uint16_t* X, int64_t M, const Nf4View& v, const Nf4Tables& tb
 }
 
 // The backward once the weight is checked (either form); ws as bwd_ws_bytes.
+// With x8, X is held as a checkpoint whose pointers are checked (X unused).
 int bwd_impl(const uint16_t* dY, const uint16_t* X, int64_t M, const Nf4View& v,
              const Nf4Tables& tb, const uint16_t* A, const uint16_t* B, int r, float s, const float* T_saved,
              uint16_t* dX, uint16_t* dA, uint16_t* dB, void* workspace, size_t workspace_bytes,
-             hipStream_t hs, const Drop& d = {}) {
+             hipStream_t hs, const Drop& d = {}, const Act8View* x8 = nullptr) {
   int st = check_rank(r);
   if (st) return st;
-  if (!dY || !X) return QLORA_ERR_NULL;
+  if (!dY || (!X && !x8)) return QLORA_ERR_NULL;
   if (r > 0 && (!A || !B || !dA || !dB)) return QLORA_ERR_NULL;
   if (v.N % 8 != 0) return QLORA_ERR_SHAPE;
   if ((st = check_rows(M, std::max(v.N, v.K), v.N, r))) return st;
@@ -287,11 +289,14 @@ int bwd_impl(const uint16_t* dY, const uint16_t* X, int64_t M, const Nf4View& v,
     float* Tr = reinterpret_cast<float*>(base + mr);
     const float* T = T_saved;
     if (!T) {
-      e = launch_lora_down(X, M, v.K, A, r, Tr, part, hs, d);
+      e = x8 ? launch_lora_down_act8(*x8, M, v.K, A, r, Tr, part, hs, d)
+             : launch_lora_down(X, M, v.K, A, r, Tr, part, hs, d);
       T = Tr;
     }
     if (e == hipSuccess) e = launch_grad_in_and_b(dY, M, v.N, B, T, r, s, G, dB, part, hs);
-    if (e == hipSuccess) e = launch_grad_a(X, M, v.K, G, r, s, dA, part, hs, d);
+    if (e == hipSuccess)
+      e = x8 ? launch_grad_a_act8(*x8, M, v.K, G, r, s, dA, part, hs, d)
+             : launch_grad_a(X, M, v.K, G, r, s, dA, part, hs, d);
     if (e != hipSuccess) return QLORA_ERR_HIP;
   }
   if (dX) e = launch_dx_gemm(dY, M, v, G, A, r, s, dX, part, tb, hs, r > 0 ? d : Drop{});
@@ -381,6 +386,16 @@ int check_dropout(const qlora_dropout* d, Drop* out) {
 }
 
 constexpr int kMaxExperts = 1024;
+
+// A checkpoint of M rows of K values.
+int check_act8(const qlora_act8* x8, int64_t M, int64_t K) {
+  if (K < kBlock || K % kBlock != 0 || K > kMaxK || M < 0 || M > kMaxActs / K)
+    return QLORA_ERR_SHAPE;
+  if (!x8) return QLORA_ERR_NULL;
+  if (M > 0 && (!x8->codes || !x8->scales)) return QLORA_ERR_NULL;
+  if (!aligned16(x8->codes) || !aligned16(x8->scales)) return QLORA_ERR_ALIGN;
+  return QLORA_OK;
+}
 
 // Limits of the expert layout: each expert's rows start at a group of 256
 // block constants (so they are a weight of their own), and every launch holds
@@ -512,7 +527,8 @@ const char* qlora_status_string(int status) {
       return "unknown codebook or constant format (codebook 0..2, double_quant 0 or 1)";
     case QLORA_ERR_EXPERT:
       return "invalid expert layout (need 1<=E<=1024 dividing the weight's rows, whole groups of "
-             "256 block constants per expert with double quantization, 1<=topk<=64)";
+             "256 block constants per expert with double quantization, 1<=topk<=64, a router's "
+             "configuration within its limits)";
     case QLORA_ERR_DROPOUT: return "dropout probability outside [0, 1)";
     default: return "unknown status";
   }
@@ -926,11 +942,16 @@ int qlora_grouped_fwd(const uint16_t* X, int64_t M, const int32_t* offsets, int 
   return hip_status(e);
 }
 
-int qlora_grouped_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const int32_t* offsets,
-                      int E, const qlora_q4_weight* w, const uint16_t* A, const uint16_t* B,
-                      int r, float s, const qlora_dropout* d, const float* T_saved, uint16_t* dX,
-                      uint16_t* dA, uint16_t* dB, void* workspace, size_t workspace_bytes,
-                      qlora_stream_t stream) {
+}  // extern "C"
+
+namespace {
+
+// The grouped backward, with X or a checkpoint x8 whose pointers are checked.
+int grouped_bwd_impl(const uint16_t* dY, const uint16_t* X, const Act8View* x8, int64_t M,
+                     const int32_t* offsets, int E, const qlora_q4_weight* w, const uint16_t* A,
+                     const uint16_t* B, int r, float s, const qlora_dropout* d,
+                     const float* T_saved, uint16_t* dX, uint16_t* dA, uint16_t* dB,
+                     void* workspace, size_t workspace_bytes, qlora_stream_t stream) {
   int st = check_q4_weight(w);
   if (st) return st;
   if ((st = check_rank(r))) return st;
@@ -938,7 +959,7 @@ int qlora_grouped_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const in
   Drop dr;
   if ((st = check_dropout(d, &dr))) return st;
   if (!offsets || (r > 0 && (!A || !B || !dA || !dB))) return QLORA_ERR_NULL;
-  if (M > 0 && (!dY || !X)) return QLORA_ERR_NULL;
+  if (M > 0 && (!dY || (!X && !x8))) return QLORA_ERR_NULL;
   if (!aligned16(dY) || !aligned16(X) || !aligned16(dX) ||
       (reinterpret_cast<uintptr_t>(offsets) & 3u) ||
       (r > 0 && (!aligned16(A) || !aligned16(B) || !aligned16(dA) || !aligned16(dB) ||
@@ -959,18 +980,95 @@ int qlora_grouped_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const in
   if (r > 0) {
     const float* T = T_saved;
     if (!T && M > 0) {
-      e = launch_grouped_down(X, M, offsets, E, w->K, A, r, Tr, part, hs, dr);
+      e = x8 ? launch_grouped_down_act8(*x8, M, offsets, E, w->K, A, r, Tr, part, hs, dr)
+             : launch_grouped_down(X, M, offsets, E, w->K, A, r, Tr, part, hs, dr);
       T = Tr;
     }
     if (e == hipSuccess)
       e = launch_grouped_grad_in_and_b(dY, M, offsets, E, N, B, T, r, s, G, dB, part, hs);
     if (e == hipSuccess)
-      e = launch_grouped_grad_a(X, M, offsets, E, w->K, G, r, s, dA, part, hs, dr);
+      e = x8 ? launch_grouped_grad_a_act8(*x8, M, offsets, E, w->K, G, r, s, dA, part, hs, dr)
+             : launch_grouped_grad_a(X, M, offsets, E, w->K, G, r, s, dA, part, hs, dr);
   }
   if (e == hipSuccess && dX && M > 0)
     e = launch_grouped_dx_gemm(dY, M, offsets, E, q4_view(w), G, A, r, s, dX, part,
                                tables(w->codebook), hs, r > 0 ? dr : Drop{});
   return hip_status(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+int qlora_grouped_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const int32_t* offsets,
+                      int E, const qlora_q4_weight* w, const uint16_t* A, const uint16_t* B,
+                      int r, float s, const qlora_dropout* d, const float* T_saved, uint16_t* dX,
+                      uint16_t* dA, uint16_t* dB, void* workspace, size_t workspace_bytes,
+                      qlora_stream_t stream) {
+  return grouped_bwd_impl(dY, X, nullptr, M, offsets, E, w, A, B, r, s, d, T_saved, dX, dA, dB,
+                          workspace, workspace_bytes, stream);
+}
+
+int qlora_act8_pack(const uint16_t* X, int64_t M, int64_t K, const qlora_act8* x8,
+                    qlora_stream_t stream) {
+  const int st = check_act8(x8, M, K);
+  if (st) return st;
+  if (M == 0) return QLORA_OK;
+  if (!X) return QLORA_ERR_NULL;
+  if (!aligned16(X)) return QLORA_ERR_ALIGN;
+  return hip_status(launch_act8_pack(X, M * K, x8->codes, x8->scales,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+int qlora_act8_unpack(const qlora_act8* x8, int64_t M, int64_t K, uint16_t* X,
+                      qlora_stream_t stream) {
+  const int st = check_act8(x8, M, K);
+  if (st) return st;
+  if (M == 0) return QLORA_OK;
+  if (!X) return QLORA_ERR_NULL;
+  if (!aligned16(X)) return QLORA_ERR_ALIGN;
+  return hip_status(launch_act8_unpack(x8->codes, x8->scales, M * K, X,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+size_t qlora_linear_act8_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int r) {
+  return qlora_linear_dropout_bwd_workspace_bytes(M, N, K, r);
+}
+
+size_t qlora_grouped_act8_bwd_workspace_bytes(int64_t M, int E, int64_t N, int64_t K, int r) {
+  return qlora_grouped_bwd_workspace_bytes(M, E, N, K, r);
+}
+
+int qlora_linear_act8_bwd(const uint16_t* dY, const qlora_act8* x8, int64_t M,
+                          const qlora_q4_weight* w, const uint16_t* A, const uint16_t* B, int r,
+                          float s, const qlora_dropout* d, const float* T_saved, uint16_t* dX,
+                          uint16_t* dA, uint16_t* dB, void* workspace, size_t workspace_bytes,
+                          qlora_stream_t stream) {
+  int st = check_q4_weight(w);
+  if (st) return st;
+  if ((st = check_act8(x8, M, w->K))) return st;
+  Drop dr;
+  if ((st = check_dropout(d, &dr))) return st;
+  const Act8View v{x8->codes, x8->scales, M};
+  return bwd_impl(dY, nullptr, M, q4_view(w), tables(w->codebook), A, B, r, s, T_saved, dX, dA, dB,
+                  workspace, workspace_bytes, static_cast<hipStream_t>(stream), dr, &v);
+}
+
+int qlora_grouped_act8_bwd(const uint16_t* dY, const qlora_act8* x8, int64_t tokens,
+                           const int32_t* order, int topk, int64_t M, const int32_t* offsets,
+                           int E, const qlora_q4_weight* w, const uint16_t* A, const uint16_t* B,
+                           int r, float s, const qlora_dropout* d, const float* T_saved,
+                           uint16_t* dX, uint16_t* dA, uint16_t* dB, void* workspace,
+                           size_t workspace_bytes, qlora_stream_t stream) {
+  int st = check_q4_weight(w);
+  if (st) return st;
+  if (topk < 1 || topk > 64) return QLORA_ERR_EXPERT;
+  if (tokens > INT32_MAX || (!order && tokens != M)) return QLORA_ERR_SHAPE;
+  if ((st = check_act8(x8, tokens, w->K))) return st;
+  if (reinterpret_cast<uintptr_t>(order) & 3u) return QLORA_ERR_ALIGN;
+  const Act8View v{x8->codes, x8->scales, tokens, order, topk};
+  return grouped_bwd_impl(dY, nullptr, &v, M, offsets, E, w, A, B, r, s, d, T_saved, dX, dA, dB,
+                          workspace, workspace_bytes, stream);
 }
 
 int qlora_profile_enable(int enable) {

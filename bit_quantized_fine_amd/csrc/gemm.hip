@@ -32,9 +32,11 @@ struct RankKind {
   static constexpr int LDS = 2 * (LP::TILE + LQ::TILE + XT);   // bf16 elements
 };
 
-// One product: tile (x, y) of C and reduction split z.
-struct RankJob {
-  OpParams po, qo;
+// One product: tile (x, y) of C and reduction split z.  QP: the form of Q.
+template <class QP>
+struct RankJobOf {
+  OpParams po;
+  QP qo;
   int ntiles, tps;
   float* ws;
   int64_t P, Q;
@@ -42,9 +44,10 @@ struct RankJob {
   const uint64_t* state;   // Q under the dropout mask: the generator's state
   uint32_t thr;            // and threshold
 };
+using RankJob = RankJobOf<OpParams>;
 
 template <int BP, int BQ, class LP, class LQ, int HL>
-__device__ __forceinline__ void rank_tile(const RankJob& j, int x, int y, int z, uint16_t* lds,
+__device__ __forceinline__ void rank_tile(const RankJobOf<typename LQ::Par>& j, int x, int y, int z, uint16_t* lds,
                                           int tid) {
   const int64_t p0 = (int64_t)x * BP, q0 = (int64_t)y * BQ;
   const int kt0 = z * j.tps, kt1 = min(j.ntiles, kt0 + j.tps);
@@ -58,7 +61,7 @@ __device__ __forceinline__ void rank_tile(const RankJob& j, int x, int y, int z,
 }
 
 template <int BP, int BQ, class LP, class LQ, int HL>
-__global__ __launch_bounds__(NT) void k_rank(RankJob j) {
+__global__ __launch_bounds__(NT) void k_rank(RankJobOf<typename LQ::Par> j) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[RankKind<BP, BQ, LP, LQ, HL>::LDS];
   // (the long axis along x: y and z take 65536 workgroups only; all three in x cost
   // two divisions and 0.3 us a launch)
@@ -279,9 +282,10 @@ Split choose_split(int64_t nred, int64_t ptiles, int64_t qtiles) {
   return s;
 }
 
-RankJob job(const OpParams& po, const OpParams& qo, const Split& sp, float* ws, int64_t P,
-            int64_t Q, int64_t px, int64_t qy, const Drop& d = {}) {
-  RankJob j;
+template <class QP>
+RankJobOf<QP> job(const OpParams& po, const QP& qo, const Split& sp, float* ws, int64_t P,
+                  int64_t Q, int64_t px, int64_t qy, const Drop& d = {}) {
+  RankJobOf<QP> j;
   j.po = po;
   j.qo = qo;
   j.ntiles = sp.ntiles;
@@ -443,6 +447,40 @@ hipError_t launch_grad_a(const uint16_t* X, int64_t M, int64_t K, const float* G
   prof_begin(4, stream);
   hipLaunchKernelGGL(kern, dim3(qt, pt, sp.splits), dim3(NT), 0, stream,
                      job(op(G, r, r, M), op(X, K, K, M), sp, ws, r, K, pt, qt, d));
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess) e = reduce<true>(ws, sp.splits, K * r, s * d.scale(), dA, stream);
+  prof_end(4, stream);
+  return e;
+}
+
+// T and dA with X held as an 8-bit checkpoint: the tiles and splits of the bf16
+// products (T's at any M: the few-token kernel reads bf16 rows), so that the sums
+// are those of the unpacked values, in the same order.
+hipError_t launch_lora_down_act8(const Act8View& x8, int64_t M, int64_t K, const uint16_t* A,
+                                 int r, float* T, float* ws, hipStream_t stream, const Drop& d) {
+  const int64_t pt = (r + RB_R - 1) / RB_R, qt = (M + RB_X - 1) / RB_X;
+  const Split sp = choose_split(K, pt, qt);
+  auto kern = d.on() ? k_rank<RB_R, RB_X, Bf16RedMajor<RB_R>, Act8Nat<RB_X, true>, 0>
+                     : k_rank<RB_R, RB_X, Bf16RedMajor<RB_R>, Act8Nat<RB_X, false>, 0>;
+  prof_begin(4, stream);
+  hipLaunchKernelGGL(kern, dim3(qt, pt, sp.splits), dim3(NT), 0, stream,
+                     job(op(A, r, r, K), act8_op(x8, K, M, K), sp, ws, r, M, pt, qt, d));
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess) e = reduce<false>(ws, sp.splits, M * r, d.scale(), T, stream);
+  prof_end(4, stream);
+  return e;
+}
+
+hipError_t launch_grad_a_act8(const Act8View& x8, int64_t M, int64_t K, const float* G, int r,
+                              float s, uint16_t* dA, float* ws, hipStream_t stream,
+                              const Drop& d) {
+  const int64_t pt = (r + RB_R - 1) / RB_R, qt = (K + RB_X - 1) / RB_X;
+  const Split sp = choose_split(M, pt, qt);
+  auto kern = d.on() ? k_rank<RB_R, RB_X, F32RedMajor<RB_R>, Act8RedMajor<RB_X, true>, 1>
+                     : k_rank<RB_R, RB_X, F32RedMajor<RB_R>, Act8RedMajor<RB_X, false>, 1>;
+  prof_begin(4, stream);
+  hipLaunchKernelGGL(kern, dim3(qt, pt, sp.splits), dim3(NT), 0, stream,
+                     job(op(G, r, r, M), act8_op(x8, K, K, M), sp, ws, r, K, pt, qt, d));
   hipError_t e = hipGetLastError();
   if (e == hipSuccess) e = reduce<true>(ws, sp.splits, K * r, s * d.scale(), dA, stream);
   prof_end(4, stream);

@@ -44,11 +44,13 @@ __device__ __forceinline__ void scale_acc(Mma<BP, BQ>& mma, float scale) {
     for (int j = 0; j < Mma<BP, BQ>::TQ; ++j) mma.acc[i][j] *= scale;
 }
 
-// C[m, j] = scale sum_k P_e[j, k] Q[m, k] on the rows m of every expert e.
-struct RowsJob {
+// C[m, j] = scale sum_k P_e[j, k] Q[m, k] on the rows m of every expert e.  QP:
+// the form of Q.
+template <class QP>
+struct RowsJobOf {
   OpParams po;        // P of expert 0
   int64_t pstride;    // elements from one expert's P to the next
-  OpParams qo;        // Q [M][reduction]
+  QP qo;              // Q [M][reduction]
   const int* offsets;
   int E;
   int64_t M;
@@ -65,9 +67,10 @@ struct RowsJob {
   // with 2 tokens each (4096 x 4096) took 17.2 us where it now takes 4.6.
   float scale;
 };
+using RowsJob = RowsJobOf<OpParams>;
 
 template <class LP, class LQ>
-__device__ __forceinline__ void rows_tile(const RowsJob& j, int x, int slot, int z, uint16_t* lds,
+__device__ __forceinline__ void rows_tile(const RowsJobOf<typename LQ::Par>& j, int x, int slot, int z, uint16_t* lds,
                                           int tid) {
   GroupTiles<RB_X> groups(j.offsets, j.E, j.M);
   groups.count();
@@ -88,7 +91,7 @@ __device__ __forceinline__ void rows_tile(const RowsJob& j, int x, int slot, int
 }
 
 template <class LP, class LQ>
-__global__ __launch_bounds__(NT) void k_group_rows(RowsJob j) {
+__global__ __launch_bounds__(NT) void k_group_rows(RowsJobOf<typename LQ::Par> j) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[rank_lds<0, LP, LQ>()];
   const int per = j.px * j.slots;
   const int z = blockIdx.x / per, t = blockIdx.x - z * per;
@@ -97,8 +100,10 @@ __global__ __launch_bounds__(NT) void k_group_rows(RowsJob j) {
 
 // C_e[q, p] = scale sum_m P[m, p] Q[m, q] over the rows m of expert e; HL
 // names the fp32 operand (1: P, 2: Q).
-struct GradJob {
-  OpParams po, qo;    // [M][P] and [M][Q], reduction-major
+template <class QP>
+struct GradJobOf {
+  OpParams po;        // [M][P] and [M][Q], reduction-major
+  QP qo;
   const int* offsets;
   int E;
   int64_t M, P, Q;
@@ -109,9 +114,22 @@ struct GradJob {
   uint32_t thr;
   float scale;        // last, as in RowsJob
 };
+using GradJob = GradJobOf<OpParams>;
+
+// Rows lo .. hi - 1 of an operand of `bytes`-byte elements, or of a checkpoint.
+__device__ __forceinline__ OpParams operand_rows(const OpParams& o, int64_t lo, int64_t hi,
+                                                 int bytes) {
+  return OpParams{static_cast<const char*>(o.ptr) + lo * o.ld * bytes, o.ld, o.nrows, hi - lo, lo,
+                  o.scale};
+}
+__device__ __forceinline__ Act8Params operand_rows(Act8Params o, int64_t lo, int64_t hi, int) {
+  o.nred = hi - lo;
+  o.drow0 = lo;
+  return o;
+}
 
 template <int HL, int BP, int BQ, class LP, class LQ>
-__device__ __forceinline__ void grad_tile(const GradJob& j, int blk, uint16_t* lds, int tid) {
+__device__ __forceinline__ void grad_tile(const GradJobOf<typename LQ::Par>& j, int blk, uint16_t* lds, int tid) {
   const int x = blk % j.px, y = (blk / j.px) % j.qy;
   const int ez = blk / (j.px * j.qy), e = ez % j.E, z = ez / j.E;
   int64_t lo, hi;
@@ -122,13 +140,8 @@ __device__ __forceinline__ void grad_tile(const GradJob& j, int blk, uint16_t* l
   const int64_t p0 = (int64_t)x * BP, q0 = (int64_t)y * BQ;
   Mma<BP, BQ> mma;
   mma.zero();
-  // the expert's rows of an operand of 2- or 4-byte elements
-  auto rows = [&](const OpParams& o, int bytes) {
-    return OpParams{static_cast<const char*>(o.ptr) + lo * o.ld * bytes, o.ld, o.nrows, hi - lo,
-                    lo, o.scale};
-  };
-  LP lp{rows(j.po, HL == 1 ? 4 : 2), p0};
-  LQ lq{rows(j.qo, HL == 2 ? 4 : 2), q0};
+  LP lp{operand_rows(j.po, lo, hi, HL == 1 ? 4 : 2), p0};
+  LQ lq{operand_rows(j.qo, lo, hi, HL == 2 ? 4 : 2), q0};
   if constexpr (LQ::kDrop) lq.key = load_drop_key(j.state, j.thr);
   run_tiles<BP, BQ, HL, 2>(lp, lq, kt0, kt1, mma, lds, tid);
   if (j.splits == 1) {
@@ -140,7 +153,7 @@ __device__ __forceinline__ void grad_tile(const GradJob& j, int blk, uint16_t* l
 }
 
 template <int HL, int BP, int BQ, class LP, class LQ>
-__global__ __launch_bounds__(NT) void k_group_grad(GradJob j) {
+__global__ __launch_bounds__(NT) void k_group_grad(GradJobOf<typename LQ::Par> j) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[rank_lds<HL, LP, LQ>()];
   grad_tile<HL, BP, BQ, LP, LQ>(j, blockIdx.x, lds, threadIdx.x);
 }
@@ -221,10 +234,11 @@ int grad_splits(int64_t M, int E, int64_t len, int r) {
   return static_cast<int>(std::max<int64_t>(1, std::min(256 / tiles, steps / 4)));
 }
 
-RowsJob rows_job(const OpParams& po, int64_t pstride, const OpParams& qo, const int* offsets,
-                 int E, int64_t M, int r, const RowsPlan& p, float scale, float* out,
-                 const Drop& d) {
-  RowsJob j{};
+template <class QP>
+RowsJobOf<QP> rows_job(const OpParams& po, int64_t pstride, const QP& qo, const int* offsets,
+                       int E, int64_t M, int r, const RowsPlan& p, float scale, float* out,
+                       const Drop& d) {
+  RowsJobOf<QP> j{};
   j.po = po;
   j.pstride = pstride;
   j.qo = qo;
@@ -243,10 +257,11 @@ RowsJob rows_job(const OpParams& po, int64_t pstride, const OpParams& qo, const 
   return j;
 }
 
-GradJob grad_job(const OpParams& po, const OpParams& qo, const int* offsets, int E, int64_t M,
-                 int64_t P, int64_t Q, int bp, int bq, int splits, float scale, uint16_t* out,
-                 float* ws, const Drop& d) {
-  GradJob j{};
+template <class QP>
+GradJobOf<QP> grad_job(const OpParams& po, const QP& qo, const int* offsets, int E, int64_t M,
+                       int64_t P, int64_t Q, int bp, int bq, int splits, float scale,
+                       uint16_t* out, float* ws, const Drop& d) {
+  GradJobOf<QP> j{};
   j.po = po;
   j.qo = qo;
   j.offsets = offsets;
@@ -362,6 +377,42 @@ hipError_t launch_grouped_grad_a(const uint16_t* X, int64_t M, const int* offset
   auto kern = d.on()
       ? k_group_grad<1, RB_R, RB_X, F32RedMajor<RB_R>, Bf16RedMajor<RB_X, true>>
       : k_group_grad<1, RB_R, RB_X, F32RedMajor<RB_R>, Bf16RedMajor<RB_X>>;
+  prof_begin(4, stream);
+  hipLaunchKernelGGL(kern, dim3(j.px * j.qy * E * sa), dim3(NT), 0, stream, j);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && sa > 1)
+    e = launch_split_reduce_bf16(ws, sa, (int64_t)E * K * r, dA, stream, s * d.scale());
+  prof_end(4, stream);
+  return e;
+}
+
+// T and dA with X held as an 8-bit checkpoint.
+hipError_t launch_grouped_down_act8(const Act8View& x8, int64_t M, const int* offsets, int E,
+                                    int64_t K, const uint16_t* A, int r, float* T, float* ws,
+                                    hipStream_t stream, const Drop& d) {
+  const RowsPlan p = plan_rows(M, E, K, r);
+  auto kern = d.on() ? k_group_rows<Bf16RedMajor<RB_R>, Act8Nat<RB_X, true>>
+                     : k_group_rows<Bf16RedMajor<RB_R>, Act8Nat<RB_X, false>>;
+  prof_begin(4, stream);
+  hipLaunchKernelGGL(kern, dim3(p.px * p.slots * p.splits), dim3(NT), 0, stream,
+                     rows_job(op(A, r, r, K), K * r, act8_op(x8, K, M, K), offsets, E, M, r, p,
+                              d.scale(), p.splits > 1 ? ws : T, d));
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && p.splits > 1)
+    e = launch_group_reduce(ws, p.splits, M, r, d.scale(), offsets, E, T, nullptr, stream);
+  prof_end(4, stream);
+  return e;
+}
+
+hipError_t launch_grouped_grad_a_act8(const Act8View& x8, int64_t M, const int* offsets, int E,
+                                      int64_t K, const float* G, int r, float s, uint16_t* dA,
+                                      float* ws, hipStream_t stream, const Drop& d) {
+  const int sa = grad_splits(M, E, K, r);
+  const auto j = grad_job(op(G, r, r, M), act8_op(x8, K, K, M), offsets, E, M, r, K, RB_R, RB_X,
+                          sa, s * d.scale(), dA, ws, d);
+  auto kern = d.on()
+      ? k_group_grad<1, RB_R, RB_X, F32RedMajor<RB_R>, Act8RedMajor<RB_X, true>>
+      : k_group_grad<1, RB_R, RB_X, F32RedMajor<RB_R>, Act8RedMajor<RB_X, false>>;
   prof_begin(4, stream);
   hipLaunchKernelGGL(kern, dim3(j.px * j.qy * E * sa), dim3(NT), 0, stream, j);
   hipError_t e = hipGetLastError();

@@ -44,6 +44,16 @@ struct Drop {
   float scale() const { return 65536.f / static_cast<float>(65536u - thr); }
 };
 
+// Activations [tokens, K] held as an 8-bit checkpoint (act8.hpp).  With an
+// order, row i of the call's X is token order[i] / topk.
+struct Act8View {
+  const int8_t* codes;
+  const float* scales;
+  int64_t tokens;
+  const int* order = nullptr;
+  int topk = 1;
+};
+
 // Dynamic LDS past what a launch may use by default.  The limit belongs to a
 // kernel on one device, so it is raised the first time a launcher runs with
 // that device current (once each; a static of the launcher keeps the devices).
@@ -188,6 +198,26 @@ hipError_t launch_grouped_grad_in_and_b(const uint16_t* dY, int64_t M, const int
 hipError_t launch_grouped_grad_a(const uint16_t* X, int64_t M, const int* offsets, int E,
                                  int64_t K, const float* G, int r, float s, uint16_t* dA,
                                  float* ws, hipStream_t stream, const Drop& d);
+
+// T and dA with X held as an 8-bit checkpoint: as launch_lora_down and
+// launch_grad_a (workspace of rank_ws_floats), and as the grouped ones above.
+hipError_t launch_lora_down_act8(const Act8View& x8, int64_t M, int64_t K, const uint16_t* A,
+                                 int r, float* T, float* ws, hipStream_t stream, const Drop& d);
+hipError_t launch_grad_a_act8(const Act8View& x8, int64_t M, int64_t K, const float* G, int r,
+                              float s, uint16_t* dA, float* ws, hipStream_t stream,
+                              const Drop& d);
+hipError_t launch_grouped_down_act8(const Act8View& x8, int64_t M, const int* offsets, int E,
+                                    int64_t K, const uint16_t* A, int r, float* T, float* ws,
+                                    hipStream_t stream, const Drop& d);
+hipError_t launch_grouped_grad_a_act8(const Act8View& x8, int64_t M, const int* offsets, int E,
+                                      int64_t K, const float* G, int r, float s, uint16_t* dA,
+                                      float* ws, hipStream_t stream, const Drop& d);
+
+// n bf16 values (n % 64 == 0, rows of whole blocks) to codes and constants, and back.
+hipError_t launch_act8_pack(const uint16_t* x, int64_t n, int8_t* codes, float* scales,
+                            hipStream_t stream);
+hipError_t launch_act8_unpack(const int8_t* codes, const float* scales, int64_t n, uint16_t* x,
+                              hipStream_t stream);
 
 // y[i] = mask scale x[i] (bf16, n elements; y may be x).
 hipError_t launch_dropout(const uint16_t* x, int64_t n, const Drop& d, uint16_t* y,

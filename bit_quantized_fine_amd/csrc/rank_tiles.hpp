@@ -6,8 +6,10 @@
 
 #include <type_traits>
 
+#include "act8.hpp"
 #include "device_common.hpp"
 #include "dropout.hpp"
+#include "kernels.hpp"
 
 namespace qnf4 {
 
@@ -23,6 +25,51 @@ struct OpParams {
   int64_t drow0;   // masked operands: row of the whole tensor that ptr points to
   float scale;     // fp32 sources: value = scale * src
 };
+
+// An operand held as an 8-bit checkpoint (act8.hpp), rows of ld values.  Row i of
+// the operand is row drow0 + i of the call's X and, with an order, the token
+// order[drow0 + i] / topk of the checkpoint; a token outside [0, tokens) is a
+// row of zeros.
+struct Act8Params {
+  const int8_t* codes;
+  const float* scales;
+  const int* order;       // may be null: token = row
+  uint32_t topk_mul;      // the quotient by topk as a multiplication and a shift,
+  int topk_shift;         // topk_shift < 0: topk = 1
+  int64_t tokens;
+  int64_t ld;
+  int64_t nrows;
+  int64_t nred;
+  int64_t drow0;
+  // Exact for slots below 2^31: with topk <= 2^shift < 2 topk, topk_mul = ceil(2^(31 +
+  // shift) / topk) is off by less than one, so the quotient is by less than
+  // 2^31 / 2^(31 + shift) <= 1 / topk.
+  __device__ int64_t token(int64_t i) const {
+    if (!order) return drow0 + i;
+    const uint32_t slot = static_cast<uint32_t>(order[drow0 + i]);
+    if (slot >> 31) return -1;
+    const uint32_t t = topk_shift < 0 ? slot : __umulhi(slot, topk_mul) >> (topk_shift - 1);
+    return t < tokens ? static_cast<int64_t>(t) : int64_t(-1);
+  }
+};
+
+inline Act8Params act8_op(const Act8View& x8, int64_t K, int64_t nrows, int64_t nred) {
+  Act8Params o{};
+  o.codes = x8.codes;
+  o.scales = x8.scales;
+  o.order = x8.order;
+  o.topk_shift = -1;
+  if (x8.topk > 1) {
+    o.topk_shift = 32 - __builtin_clz(static_cast<uint32_t>(x8.topk - 1));
+    const uint64_t one = uint64_t(1) << (31 + o.topk_shift);
+    o.topk_mul = static_cast<uint32_t>((one + x8.topk - 1) / x8.topk);
+  }
+  o.tokens = x8.tokens;
+  o.ld = K;
+  o.nrows = nrows;
+  o.nred = nred;
+  return o;
+}
 
 __device__ __forceinline__ u32x4 ld16(const void* p) {
   return *reinterpret_cast<const u32x4*>(p);
@@ -41,6 +88,7 @@ __device__ __forceinline__ void st_lds16(uint16_t* p, u32x4 v) {
 
 template <int ROWS, bool DROP = false>
 struct Bf16Nat {   // element (row, k) = src[row * ld + k]
+  using Par = OpParams;
   static constexpr bool kDrop = DROP;
   static constexpr int TILE = ROWS * LDS_STRIDE;
   __device__ static u32x4 frag(const uint16_t* tile, int c0, int ks, int lane) {
@@ -119,6 +167,7 @@ __device__ __forceinline__ u32x4 rm_frag(const uint16_t* tile, int c0, int ks, i
 
 template <int COLS, bool DROP = false>
 struct Bf16RedMajor {   // element (row, k) = src[k * ld + row], bf16
+  using Par = OpParams;
   static constexpr bool kDrop = DROP;
   static constexpr int TILE = BK * COLS;
   static constexpr int PCS = COLS / 8;                 // 16-byte pieces per tile row
@@ -157,6 +206,7 @@ struct Bf16RedMajor {   // element (row, k) = src[k * ld + row], bf16
 
 template <int COLS>
 struct F32RedMajor {    // element (row, k) = scale * src[k * ld + row], fp32 -> bf16 hi, lo
+  using Par = OpParams;
   static constexpr bool kDrop = false;
   static constexpr int TILE = BK * COLS;
   static constexpr int QCS = COLS / 4;                 // 4-float pieces per tile row
@@ -188,6 +238,109 @@ struct F32RedMajor {    // element (row, k) = scale * src[k * ld + row], fp32 ->
   }
   __device__ static u32x4 frag(const uint16_t* tile, int c0, int ks, int lane) {
     return rm_frag<COLS>(tile, c0, ks, lane);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// The same operands held as an 8-bit checkpoint: 16 codes a load and one
+// constant, made bf16 values when they are stored to LDS, in the tile layouts
+// of the bf16 loaders, so that a product gives the bits it would give on the
+// unpacked values.
+// ---------------------------------------------------------------------------
+
+template <int ROWS, bool DROP>
+struct Act8Nat {   // element (row, k) = value(row, k)
+  using Par = Act8Params;
+  static constexpr bool kDrop = DROP;
+  static constexpr int TILE = ROWS * LDS_STRIDE;
+  static constexpr int PCS = BK / 16;
+  static constexpr int CPT = ROWS * PCS / NT;
+  __device__ static u32x4 frag(const uint16_t* tile, int c0, int ks, int lane) {
+    return Bf16Nat<ROWS>::frag(tile, c0, ks, lane);
+  }
+  Act8Params o;
+  int64_t row0;
+  u32x4 r[CPT];
+  float c[CPT];
+  std::conditional_t<DROP, DropKey, NoDropKey> key;
+  u32x4 mask[DROP ? 2 * CPT : 1];
+  int64_t tok[CPT];   // a thread's rows are the same in every tile
+  bool have = false;
+  __device__ void load(int kt, int tid) {
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int idx = tid + i * NT, row = idx / PCS, pc = idx % PCS;
+      const int64_t gr = row0 + row, gk = (int64_t)kt * BK + 16 * pc;
+      if (!have) tok[i] = gr < o.nrows ? o.token(gr) : -1;
+      const bool ok = tok[i] >= 0 && gk < o.nred;
+      r[i] = ok ? ld16(o.codes + tok[i] * o.ld + gk) : u32x4{0, 0, 0, 0};
+      c[i] = ok ? o.scales[tok[i] * (o.ld / kBlock) + gk / kBlock] : 0.f;
+      if constexpr (DROP) {
+        const uint64_t piece = static_cast<uint64_t>((o.drow0 + gr) * o.ld + gk) / 8;
+        mask[2 * i] = keep_piece(key, piece);
+        mask[2 * i + 1] = keep_piece(key, piece + 1);
+      }
+    }
+    have = true;
+  }
+  __device__ void store(uint16_t* lds, int tid) {
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int idx = tid + i * NT, row = idx / PCS, pc = idx % PCS;
+      u32x4 a = act8_values(r[i].x, r[i].y, c[i]), b = act8_values(r[i].z, r[i].w, c[i]);
+      if constexpr (DROP) {
+        a &= mask[2 * i];
+        b &= mask[2 * i + 1];
+      }
+      st_lds16(lds + row * LDS_STRIDE + 16 * pc, a);
+      st_lds16(lds + row * LDS_STRIDE + 16 * pc + 8, b);
+    }
+  }
+};
+
+template <int COLS, bool DROP>
+struct Act8RedMajor {   // element (row, k) = value(k, row)
+  using Par = Act8Params;
+  static constexpr bool kDrop = DROP;
+  static constexpr int TILE = BK * COLS;
+  static constexpr int PCS = COLS / 16;
+  static constexpr int CPT = BK * PCS / NT;
+  __device__ static u32x4 frag(const uint16_t* tile, int c0, int ks, int lane) {
+    return rm_frag<COLS>(tile, c0, ks, lane);
+  }
+  Act8Params o;
+  int64_t row0;
+  u32x4 r[CPT];
+  float c[CPT];
+  std::conditional_t<DROP, DropKey, NoDropKey> key;
+  u32x4 mask[DROP ? 2 * CPT : 1];
+  __device__ void load(int kt, int tid) {
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int idx = tid + i * NT, red = idx / PCS, pc = idx % PCS;
+      const int64_t gk = (int64_t)kt * BK + red, gr = row0 + 16 * pc;
+      const int64_t tok = gk < o.nred && gr < o.nrows ? o.token(gk) : -1;
+      r[i] = tok >= 0 ? ld16(o.codes + tok * o.ld + gr) : u32x4{0, 0, 0, 0};
+      c[i] = tok >= 0 ? o.scales[tok * (o.ld / kBlock) + gr / kBlock] : 0.f;
+      if constexpr (DROP) {
+        const uint64_t piece = static_cast<uint64_t>((o.drow0 + gk) * o.ld + gr) / 8;
+        mask[2 * i] = keep_piece(key, piece);
+        mask[2 * i + 1] = keep_piece(key, piece + 1);
+      }
+    }
+  }
+  __device__ void store(uint16_t* lds, int tid) {
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int idx = tid + i * NT, red = idx / PCS, pc = idx % PCS;
+      u32x4 a = act8_values(r[i].x, r[i].y, c[i]), b = act8_values(r[i].z, r[i].w, c[i]);
+      if constexpr (DROP) {
+        a &= mask[2 * i];
+        b &= mask[2 * i + 1];
+      }
+      st_lds16(lds + red * COLS + 8 * rm_slot<COLS>(red, 2 * pc), a);
+      st_lds16(lds + red * COLS + 8 * rm_slot<COLS>(red, 2 * pc + 1), b);
+    }
   }
 };
 

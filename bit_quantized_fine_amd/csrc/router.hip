@@ -1,0 +1,480 @@
+// Routing of tokens to experts: scores, the choice of the topk best, their
+// weights, and the gradient of the weights back to the logits.
+//
+// A wave takes one token; lane l holds experts l EPL .. l EPL + EPL - 1, so that
+// among equal values the lowest lane's first one is the lowest index.  Values
+// are compared as integers of the same order: the logits' 32 bits where no bias
+// is given (a softmax or sigmoid keeps their order), else the 64 bits of p +
+// bias, formed in 64 bits: the scores of 256 experts lie about 2^-8 apart, so in
+// 32 bits about one token in 10^4 would get an order that depends on how its
+// scores were rounded.  A round of the choice is the wave's largest value by six
+// lane moves, and a ballot for its owner.
+//
+// Weights and gradients are formed in 64 bits too, where they cost one lane's
+// work a slot: what is left of 1 - p where one expert takes nearly all would
+// lose its bits in 32.
+#include <algorithm>
+#include <cmath>
+
+#include "device_common.hpp"
+#include "kernels.hpp"
+#include "qlora_nf4.h"
+
+namespace qnf4 {
+
+namespace {
+
+constexpr int kWaves = 4;          // tokens a workgroup
+constexpr int kMaxE = 1024;
+constexpr int kMaxTopk = 64;
+constexpr int kMaxGroups = 64;
+// Workgroups lie in rows of this many along y (a launch holds fewer than 2^32
+// threads along x).
+constexpr int64_t kRowBlocks = int64_t(1) << 23;
+
+struct Router {
+  const void* logits;
+  int64_t tokens;
+  int E;
+  const float* bias;      // may be null
+  int topk;
+  int sigmoid, renorm;
+  float scale;
+  int choose_groups;      // 0: every group stays
+  int groups, top_groups, group_top;
+  int gs;                 // experts of a group
+  uint32_t gs_mul;        // e / gs = e gs_mul >> 20
+  int gshift;             // log2 of the lanes that share a group
+  int* ids;
+  float* weights;
+  const float* dweights;
+  void* dlogits;
+};
+
+__device__ __forceinline__ int read_lane(int v, int lane) {
+  return __builtin_amdgcn_readlane(v, lane);
+}
+__device__ __forceinline__ float read_lane(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+__device__ __forceinline__ double read_lane(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), lane);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// Largest value over the wave (zero where no lane has a larger one).
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  auto step = [&](auto moved) { v = max(v, static_cast<uint32_t>(moved)); };
+  step(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x111, 0xF, 0xF, false));   // row_shr 1
+  step(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x112, 0xF, 0xF, false));
+  step(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x114, 0xF, 0xF, false));
+  step(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x118, 0xF, 0xF, false));
+  step(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x142, 0xA, 0xF, false));   // row_bcast 15
+  step(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x143, 0xC, 0xF, false));   // row_bcast 31
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+  const uint32_t hi = wave_max(static_cast<uint32_t>(v >> 32));
+  const uint32_t lo =
+      wave_max(static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+// Integers in the order of the values; 0 for an expert that is not to be
+// chosen (-inf or NaN).  v + 0 makes -0 equal to 0.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.f);
+  return v > -__builtin_inff() ? b ^ ((b >> 31) ? ~0u : 0x80000000u) : 0u;
+}
+__device__ __forceinline__ uint64_t order_key(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);
+  return v > -__builtin_inf() ? b ^ ((b >> 63) ? ~0ull : 1ull << 63) : 0ull;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __builtin_bit_cast(float, (k >> 31) ? k ^ 0x80000000u : ~k);
+}
+
+template <class L>
+__device__ __forceinline__ float to_f32(L v) {
+  if constexpr (sizeof(L) == 2)
+    return bf16_lo_to_f32(v);
+  else
+    return v;
+}
+
+// sigma(x) = exp(min(x, 0)) / (1 + exp(-|x|)): neither factor overflows.
+__device__ __forceinline__ double sigmoid64(double x) {
+  return exp(min(x, 0.0)) / (1.0 + exp(-fabs(x)));
+}
+
+// A token's logits: lane l holds experts l EPL ...; -inf past E.
+template <int EPL, class L>
+struct Logits {
+  float x[EPL];
+  float top;    // the largest, -inf without any
+  bool bad;     // a NaN or +inf among them
+  __device__ void load(const L* row, int E, int lane) {
+    uint32_t k = 0;
+    bool b = false;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = lane * EPL + i;
+      x[i] = e < E ? to_f32(row[e]) : -__builtin_inff();
+      b |= !(x[i] < __builtin_inff());
+      k = max(k, order_key(x[i]));
+    }
+    bad = __builtin_amdgcn_ballot_w64(b) != 0;
+    k = wave_max(k);
+    top = k ? key_value(k) : -__builtin_inff();
+  }
+  // sum over the experts of exp(x - top), which this lane's d[i] receive
+  __device__ double exps(double* d) const {
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      d[i] = x[i] > -__builtin_inff() ? exp(static_cast<double>(x[i]) - static_cast<double>(top)) : 0.0;
+      s += d[i];
+    }
+    return wave_sum(s);
+  }
+};
+
+// The topk largest keys in order: lane j gets expert and logit of slot j
+// (id -1: none left).
+template <int EPL, class Key>
+__device__ __forceinline__ void choose(Key* k, const float* x, int topk, int lane, int& id,
+                                       float& lx) {
+  Key cur = k[0];
+#pragma unroll
+  for (int i = 1; i < EPL; ++i) cur = max(cur, k[i]);
+  id = -1;
+  lx = 0.f;
+  for (int j = 0; j < topk; ++j) {
+    const Key m = wave_max(cur);
+    if (m == 0) break;   // uniform
+    const int who = __builtin_ctzll(__builtin_amdgcn_ballot_w64(cur == m));
+    int e = 0;
+    float v = 0.f;
+    if (lane == who) {
+      bool found = false;
+      cur = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        if (!found && k[i] == m) {
+          found = true;
+          e = lane * EPL + i;
+          v = x[i];
+          k[i] = 0;
+        }
+        cur = max(cur, k[i]);
+      }
+    }
+    const int we = read_lane(e, who);
+    const float wv = read_lane(v, who);
+    if (lane == j) {
+      id = we;
+      lx = wv;
+    }
+  }
+}
+
+// Relative weights u of the chosen (0 for lanes without one), for the
+// renormalised forms: exp(x - m), times 1 / (1 + exp(-|x|)) for a sigmoid, whose
+// factor exp(min(x, 0)) is the one shifted by m.
+__device__ __forceinline__ double relative_weight(const Router& a, bool live, float lx) {
+  const float v = a.sigmoid ? min(lx, 0.f) : lx;
+  const float m = key_value(wave_max(live ? order_key(v) : 0u));
+  if (!live) return 0.0;
+  const double u = exp(static_cast<double>(v) - static_cast<double>(m));
+  return a.sigmoid ? u / (1.0 + exp(-fabs(static_cast<double>(lx)))) : u;
+}
+
+__device__ __forceinline__ int64_t wave_token() {
+  return ((int64_t)blockIdx.y * kRowBlocks + blockIdx.x) * kWaves + wave_id();
+}
+
+}  // namespace
+
+template <int EPL, class L>
+__global__ __launch_bounds__(64 * kWaves) void k_router_fwd(Router a) {
+  extern __shared__ double lds[];   // [kWaves][E] where groups are chosen
+  const int lane = threadIdx.x & 63;
+  const int64_t token = wave_token();
+  const bool in = token < a.tokens;
+  // (a wave without a token repeats the last one, for the barriers)
+  const int64_t t = in ? token : a.tokens - 1;
+  Logits<EPL, L> l;
+  l.load(static_cast<const L*>(a.logits) + t * a.E, a.E, lane);
+
+  double p[EPL], sum = 0.0;   // p: scores where they rank, exps otherwise unused
+  const bool sums = a.choose_groups && a.group_top == 2;
+  if (a.bias || sums) {
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) p[i] = sigmoid64(l.x[i]);
+    } else {
+      sum = l.exps(p);
+      const double r = sum > 0.0 ? 1.0 / sum : 0.0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) p[i] *= r;
+    }
+  }
+  double rank[EPL];   // with a bias
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = lane * EPL + i;
+      rank[i] = e < a.E && l.x[i] > -__builtin_inff()
+                    ? p[i] + static_cast<double>(a.bias[e]) : -__builtin_inf();
+    }
+  }
+  uint64_t keep = ~0ull;   // bit (group << gshift): the group stays
+  if (a.choose_groups) {
+    double* mine = lds + (int64_t)wave_id() * a.E;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = lane * EPL + i;
+      double v = a.bias ? rank[i] : (sums ? p[i] : static_cast<double>(l.x[i]));
+      if (!(l.x[i] > -__builtin_inff()) || !(v > -__builtin_inf())) v = -__builtin_inf();
+      if (e < a.E) mine[e] = v;
+    }
+    __syncthreads();
+    // the two best of a group, by the lanes that share it
+    const int g = lane >> a.gshift, sub = lane & ((1 << a.gshift) - 1);
+    double t1 = -__builtin_inf(), t2 = t1;
+    if (g < a.groups)
+      for (int j = sub; j < a.gs; j += 1 << a.gshift) {
+        const double v = mine[g * a.gs + j];
+        t2 = v > t1 ? t1 : max(t2, v);
+        t1 = max(t1, v);
+      }
+    for (int d = 1; d < 1 << a.gshift; d <<= 1) {
+      const double o1 = __shfl_xor(t1, d), o2 = __shfl_xor(t2, d);
+      t2 = max(min(t1, o1), max(t2, o2));
+      t1 = max(t1, o1);
+    }
+    const bool any = t1 > -__builtin_inf();
+    const double score = a.group_top == 2 && t2 > -__builtin_inf() ? t1 + t2 : t1;
+    int better = 0;
+    for (int q = 0; q < a.groups; ++q) {
+      const double o = read_lane(score, q << a.gshift);
+      better += o > score || (o == score && q < g);
+    }
+    keep = __builtin_amdgcn_ballot_w64(g < a.groups && sub == 0 && any && better < a.top_groups);
+  }
+  auto stays = [&](int i) {
+    if (!a.choose_groups) return true;
+    const int e = lane * EPL + i;
+    return e < a.E && ((keep >> (((e * a.gs_mul) >> 20) << a.gshift)) & 1) != 0;
+  };
+  int id;
+  float lx;
+  if (a.bias) {
+    uint64_t k[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) k[i] = stays(i) ? order_key(rank[i]) : 0ull;
+    choose<EPL, uint64_t>(k, l.x, a.topk, lane, id, lx);
+  } else {
+    uint32_t k[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) k[i] = stays(i) ? order_key(l.x[i]) : 0u;
+    choose<EPL, uint32_t>(k, l.x, a.topk, lane, id, lx);
+  }
+  const bool live = id >= 0;
+  double w;
+  if (a.renorm) {
+    w = relative_weight(a, live, lx);
+    const double total = wave_sum(w);
+    w = live ? w / total : 0.0;
+  } else if (a.sigmoid) {
+    w = live ? sigmoid64(lx) : 0.0;
+  } else {
+    if (sum == 0.0) sum = l.exps(p);
+    w = live ? exp(static_cast<double>(lx) - static_cast<double>(l.top)) / sum : 0.0;
+  }
+  if (in && lane < a.topk) {
+    a.ids[t * a.topk + lane] = id;
+    a.weights[t * a.topk + lane] =
+        l.bad && live ? __builtin_nanf("") : static_cast<float>(static_cast<double>(a.scale) * w);
+  }
+}
+
+// dlogits of one token.  Lane j holds slot j; sums over the slots run in their
+// order in every lane.
+template <int EPL, class L>
+__global__ __launch_bounds__(64 * kWaves) void k_router_bwd(Router a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = wave_token();
+  if (t >= a.tokens) return;
+  const L* row = static_cast<const L*>(a.logits) + t * a.E;
+  Logits<EPL, L> l;
+  l.load(row, a.E, lane);
+  int id = -1;
+  double dw = 0.0;
+  float lx = 0.f;
+  if (lane < a.topk) {
+    id = a.ids[t * a.topk + lane];
+    if (id < 0 || id >= a.E) id = -1;
+    if (id >= 0) {
+      lx = to_f32(row[id]);
+      if (!(lx > -__builtin_inff()) && lx == lx) id = -1;   // -inf: never chosen
+    }
+    if (id >= 0) dw = static_cast<double>(a.dweights[t * a.topk + lane]);
+  }
+  const bool live = id >= 0;
+  double d = 0.0;       // of this slot's expert
+  double s = 0.0;       // softmax without renorm: sum p dw
+  double p[EPL], r = 0.0;
+  if (a.renorm) {
+    const double u = relative_weight(a, live, lx), total = wave_sum(u);
+    const double q = live ? u / total : 0.0;
+    // q_i sum_j q_j (dw_i - dw_j): no difference of nearly equal sums
+    double v = 0.0;
+    for (int j = 0; j < a.topk; ++j) v += read_lane(q, j) * (dw - read_lane(dw, j));
+    d = q * v;
+    if (a.sigmoid) d *= sigmoid64(-static_cast<double>(lx));
+  } else if (a.sigmoid) {
+    d = live ? dw * sigmoid64(lx) * sigmoid64(-static_cast<double>(lx)) : 0.0;
+  } else {
+    r = 1.0 / l.exps(p);
+    d = live ? dw * exp(static_cast<double>(lx) - static_cast<double>(l.top)) * r : 0.0;
+    for (int j = 0; j < a.topk; ++j) s += read_lane(d, j);
+  }
+  double out[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    out[i] = !a.renorm && !a.sigmoid && l.x[i] > -__builtin_inff() ? -p[i] * r * s : 0.0;
+  for (int j = 0; j < a.topk; ++j) {
+    const int e = read_lane(live ? id : -1, j) - lane * EPL;
+    const double v = read_lane(d, j);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) out[i] += e == i ? v : 0.0;
+  }
+  L* dst = static_cast<L*>(a.dlogits) + t * a.E;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane * EPL + i;
+    const float v = l.bad ? __builtin_nanf("")
+                          : static_cast<float>(static_cast<double>(a.scale) * out[i]);
+    if (e < a.E) {
+      if constexpr (sizeof(L) == 2)
+        dst[e] = static_cast<L>(pack_bf16x2(v, 0.f));
+      else
+        dst[e] = v;
+    }
+  }
+}
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int check_router(int64_t tokens, int E, const qlora_router_config* c) {
+  if (!c) return QLORA_ERR_NULL;
+  if (E < 1 || E > kMaxE || c->topk < 1 || c->topk > kMaxTopk) return QLORA_ERR_EXPERT;
+  if (c->groups < 1 || c->groups > kMaxGroups || E % c->groups != 0 || c->top_groups < 1 ||
+      c->top_groups > c->groups || c->group_top < 1 || c->group_top > 2)
+    return QLORA_ERR_EXPERT;
+  if (c->topk > E / c->groups * c->top_groups) return QLORA_ERR_EXPERT;
+  if ((c->score != QLORA_SCORE_SOFTMAX && c->score != QLORA_SCORE_SIGMOID) ||
+      (c->renorm != 0 && c->renorm != 1))
+    return QLORA_ERR_EXPERT;
+  if (!std::isfinite(c->scale)) return QLORA_ERR_EXPERT;
+  if (tokens < 0 || tokens > (int64_t(1) << 30) / c->topk) return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+
+Router router(const void* logits, int64_t tokens, int E, const qlora_router_config* c) {
+  Router a{};
+  a.logits = logits;
+  a.tokens = tokens;
+  a.E = E;
+  a.topk = c->topk;
+  a.sigmoid = c->score == QLORA_SCORE_SIGMOID;
+  a.renorm = c->renorm;
+  a.scale = c->scale;
+  a.choose_groups = c->top_groups < c->groups;
+  a.groups = c->groups;
+  a.top_groups = c->top_groups;
+  a.group_top = c->group_top;
+  a.gs = E / c->groups;
+  // (e < 1024 and gs < 1024: e gs < 2^20, so the quotient is exact)
+  a.gs_mul = ((1u << 20) + a.gs - 1) / a.gs;
+  while ((c->groups << (a.gshift + 1)) <= 64) ++a.gshift;
+  return a;
+}
+
+template <bool BACK, int EPL, class L>
+hipError_t launch(const Router& a, hipStream_t st) {
+  const int64_t blocks = (a.tokens + kWaves - 1) / kWaves;
+  const dim3 grid(static_cast<unsigned>(std::min(blocks, kRowBlocks)),
+                  static_cast<unsigned>((blocks + kRowBlocks - 1) / kRowBlocks));
+  if constexpr (BACK)
+    hipLaunchKernelGGL((k_router_bwd<EPL, L>), grid, dim3(64 * kWaves), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_router_fwd<EPL, L>), grid, dim3(64 * kWaves),
+                       a.choose_groups ? kWaves * a.E * sizeof(double) : 0, st, a);
+  return hipGetLastError();
+}
+
+template <bool BACK, class L>
+int dispatch(const Router& a, hipStream_t st) {
+  hipError_t e;
+  if (a.E <= 64) e = launch<BACK, 1, L>(a, st);
+  else if (a.E <= 128) e = launch<BACK, 2, L>(a, st);
+  else if (a.E <= 256) e = launch<BACK, 4, L>(a, st);
+  else if (a.E <= 512) e = launch<BACK, 8, L>(a, st);
+  else e = launch<BACK, 16, L>(a, st);
+  return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP;
+}
+
+}  // namespace
+
+}  // namespace qnf4
+
+using namespace qnf4;
+
+extern "C" {
+
+int qlora_router_fwd(const void* logits, int logits_fp32, int64_t tokens, int E,
+                     const float* bias, const qlora_router_config* cfg, int32_t* ids,
+                     float* weights, qlora_stream_t stream) {
+  const int st = check_router(tokens, E, cfg);
+  if (st) return st;
+  if (tokens > 0 && (!logits || !ids || !weights)) return QLORA_ERR_NULL;
+  if (!aligned(logits, 16) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+    return QLORA_ERR_ALIGN;
+  if (tokens == 0) return QLORA_OK;
+  Router a = router(logits, tokens, E, cfg);
+  a.bias = bias;
+  a.ids = ids;
+  a.weights = weights;
+  const hipStream_t hs = static_cast<hipStream_t>(stream);
+  return logits_fp32 ? dispatch<false, float>(a, hs) : dispatch<false, uint16_t>(a, hs);
+}
+
+int qlora_router_bwd(const float* dweights, const void* logits, int logits_fp32,
+                     const int32_t* ids, int64_t tokens, int E, const qlora_router_config* cfg,
+                     void* dlogits, qlora_stream_t stream) {
+  const int st = check_router(tokens, E, cfg);
+  if (st) return st;
+  if (tokens > 0 && (!dweights || !logits || !ids || !dlogits)) return QLORA_ERR_NULL;
+  if (!aligned(logits, 16) || !aligned(dlogits, 16) || !aligned(ids, 4) || !aligned(dweights, 4))
+    return QLORA_ERR_ALIGN;
+  if (tokens == 0) return QLORA_OK;
+  Router a = router(logits, tokens, E, cfg);
+  a.ids = const_cast<int32_t*>(ids);
+  a.dweights = dweights;
+  a.dlogits = dlogits;
+  const hipStream_t hs = static_cast<hipStream_t>(stream);
+  return logits_fp32 ? dispatch<true, float>(a, hs) : dispatch<true, uint16_t>(a, hs);
+}
+
+}  // extern "C"

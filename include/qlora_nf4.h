@@ -80,10 +80,11 @@ typedef enum {
                                QLORA_NOALLOC_SCRATCH_BYTES of workspace */
   QLORA_ERR_FORMAT = 8,     /* qlora_q4_*: unknown codebook, or double_quant
                                not 0 or 1 */
-  QLORA_ERR_EXPERT = 9,     /* qlora_grouped_*, qlora_expert_*: E outside
-                               [1, 1024] or not dividing the weight's rows, an
-                               expert that is not whole groups of 256 block
-                               constants, topk outside [1, 64] */
+  QLORA_ERR_EXPERT = 9,     /* qlora_grouped_*, qlora_expert_*, qlora_router_*:
+                               E outside [1, 1024] or not dividing the weight's
+                               rows, an expert that is not whole groups of 256
+                               block constants, topk outside [1, 64], a router's
+                               configuration outside its limits */
   QLORA_ERR_DROPOUT = 10    /* dropout probability outside [0, 1) */
 } qlora_status;
 
@@ -526,6 +527,148 @@ int qlora_expert_combine(const uint16_t* Y, int64_t tokens, int topk, int64_t K,
 int qlora_expert_combine_bwd(const uint16_t* dOut, const uint16_t* Y, int64_t tokens, int topk,
                              int64_t K, const int32_t* inverse, const float* weights,
                              uint16_t* dY, float* dweights, qlora_stream_t stream);
+
+/*
+ * 8-bit checkpoints of activations.  The base weight is frozen, so a layer's
+ * backward reads its input X for the adapter's gradient dA (and a recomputed T)
+ * alone; kept in 8 bits, X takes 8.5 bits a value until then instead of 16.
+ *
+ * Format, for X [M, K] bf16 with K % 64 == 0: blocks of 64 consecutive values of
+ * a row, amax the largest magnitude of a block,
+ *   scales [M, K/64] fp32: c = fl32(amax / 127)
+ *   codes  [M, K]    int8: rint(fl32(x / c)), ties to even, -127 .. 127
+ *                    (0 where c = 0)
+ *   value = bf16_rne(fl32(code * c))
+ * A block that holds a NaN or an infinity gets c = NaN and codes 0, so that all
+ * of it comes back as NaN.  codes and scales 16-byte aligned; K >= 64,
+ * K <= 2^22, M >= 0, M*K <= 2^40 (QLORA_ERR_SHAPE otherwise); M = 0 is allowed.
+ *
+ * qlora_act8_pack writes the checkpoint of X, qlora_act8_unpack its values.
+ */
+typedef struct {
+  int8_t* codes;
+  float* scales;
+} qlora_act8;
+
+int qlora_act8_pack(const uint16_t* X, int64_t M, int64_t K, const qlora_act8* x8,
+                    qlora_stream_t stream);
+int qlora_act8_unpack(const qlora_act8* x8, int64_t M, int64_t K, uint16_t* X,
+                      qlora_stream_t stream);
+
+/*
+ * The layer's backward from a checkpoint of its input.
+ *
+ * qlora_linear_act8_bwd: qlora_linear_dropout_bwd with X held in x8 [M, K]; the
+ *   results are bit for bit those of that call on the values of qlora_act8_unpack
+ *   (T_saved NULL recomputes T from them; with M <= 16 it then agrees within
+ *   rounding only, as the sums run in another order).
+ * qlora_grouped_act8_bwd: qlora_grouped_bwd with X held in x8.
+ *   order NULL: x8 holds the rows of X (tokens = M).
+ *   order [M] int32 (as qlora_expert_plan gives it, 4-byte aligned): x8 holds
+ *     the tokens' rows [tokens, K], each once, and row i of the call's X is row
+ *     order[i] / topk of it (1 <= topk <= 64, QLORA_ERR_EXPERT otherwise; tokens
+ *     < 2^31).  An order that leads outside [0, tokens) is a row of zeros.
+ * Dropout, other arguments, limits, workspaces and errors as those calls, and
+ * the checkpoint's own.
+ */
+size_t qlora_linear_act8_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int r);
+size_t qlora_grouped_act8_bwd_workspace_bytes(int64_t M, int E, int64_t N, int64_t K, int r);
+int qlora_linear_act8_bwd(const uint16_t* dY, const qlora_act8* x8, int64_t M,
+                          const qlora_q4_weight* w, const uint16_t* A, const uint16_t* B, int r,
+                          float s, const qlora_dropout* d, const float* T_saved, uint16_t* dX,
+                          uint16_t* dA, uint16_t* dB, void* workspace, size_t workspace_bytes,
+                          qlora_stream_t stream);
+int qlora_grouped_act8_bwd(const uint16_t* dY, const qlora_act8* x8, int64_t tokens,
+                           const int32_t* order, int topk, int64_t M, const int32_t* offsets,
+                           int E, const qlora_q4_weight* w, const uint16_t* A, const uint16_t* B,
+                           int r, float s, const qlora_dropout* d, const float* T_saved,
+                           uint16_t* dX, uint16_t* dA, uint16_t* dB, void* workspace,
+                           size_t workspace_bytes, qlora_stream_t stream);
+
+/*
+ * Root-mean-square norm in front of a layer, with the residual's addition and
+ * the checkpoint of its output:
+ *   h = bf16_rne(x + residual),  rstd = 1 / sqrt(mean_k h^2 + eps),
+ *   y = bf16_rne(h * rstd * g)
+ *   x, residual, h, y [M, K] bf16; rstd [M] fp32 (kept for the backward pass).
+ *   g   [K]: bf16, or fp32 with g_fp32 != 0.
+ *   residual NULL: h is x, and the argument h is not used (may be NULL).
+ *   h may be x or residual (in place); y overlaps nothing.
+ *   y8  NULL, or where the checkpoint of y goes (then K % 64 == 0).
+ * Squares are summed in fp32.  K % 8 == 0, 8 <= K <= 2^22, M >= 0, M*K <= 2^40,
+ * eps > 0 and finite (QLORA_ERR_SHAPE otherwise); M = 0 is allowed.  All
+ * buffers 16-byte aligned.
+ *
+ * Backward, with dy the gradient of y and dres that of h from elsewhere (the
+ * residual stream; NULL for none):
+ *   n = h rstd,  c = mean_k(dy g n),  dx = bf16_rne(dres + rstd (dy g - n c)),
+ *   dg = sum over the rows of dy n (of g's type; skipped if NULL, zeros for M = 0)
+ * dx is the gradient of x and of residual alike; it may be dres (in place) and
+ * overlaps nothing else.  Results do not depend on the order in which anything
+ * runs.  Workspace: qlora_rms_norm_bwd_workspace_bytes(M, K) bytes, none needed
+ * without dg.
+ */
+int qlora_rms_norm_fwd(const uint16_t* x, const uint16_t* residual, const void* g, int g_fp32,
+                       int64_t M, int64_t K, float eps, uint16_t* h, uint16_t* y, float* rstd,
+                       const qlora_act8* y8, qlora_stream_t stream);
+size_t qlora_rms_norm_bwd_workspace_bytes(int64_t M, int64_t K);
+int qlora_rms_norm_bwd(const uint16_t* dy, const uint16_t* dres, const uint16_t* h,
+                       const float* rstd, const void* g, int g_fp32, int64_t M, int64_t K,
+                       uint16_t* dx, void* dg, void* workspace, size_t workspace_bytes,
+                       qlora_stream_t stream);
+
+/*
+ * Routing of tokens to experts: from a token's logits [E] its topk experts and
+ * their weights, as qlora_expert_plan (ids) and qlora_expert_combine (weights)
+ * take them, and from the gradient of the weights (dweights of
+ * qlora_expert_combine_bwd) that of the logits.
+ *   logits [tokens, E] bf16, or fp32 with logits_fp32 != 0; 16-byte aligned.
+ *   score: p = softmax over the token's experts, or the sigmoid of each logit.
+ *   bias [E] fp32 or NULL (kept for balance: it takes part in the choice, not in
+ *     the weights, and gets no gradient).
+ *   Choice: experts rank by p + bias, formed in 64 bits; without a bias by the
+ *     logit (the same order, and apart where two scores round to one).  With
+ *     top_groups < groups, the experts form `groups` equal groups in order, a
+ *     group's score is the sum of its group_top (1 or 2) best ranks (of its best
+ *     p where no bias is given), and the experts of the top_groups best
+ *     groups stay.  The topk best experts, best first.  Ties, of experts and of
+ *     groups, go to the lower index.
+ *   ids [tokens, topk] int32, weights [tokens, topk] fp32: p, or p over the sum
+ *     of the chosen p with renorm = 1, times scale.
+ *   An expert whose logit or rank is -inf (masked) or NaN is not chosen, and a
+ *     group with no other experts neither; slots left over get id -1 (no row in
+ *     qlora_expert_plan) and weight 0.  A token with a NaN or +inf logit gets
+ *     NaN weights in the slots taken and NaN gradients.
+ *   Backward, ids as the forward gave them: with u = p, or p over the sum of the
+ *     chosen p, weights = scale u(logits) is differentiated with the choice held
+ *     fixed; dlogits [tokens, E] has the logits' type.  A slot whose id is
+ *     outside [0, E) counts as not taken.
+ *   1 <= E <= 1024, 1 <= topk <= 64, groups in [1, 64] divides E,
+ *   1 <= top_groups <= groups, topk <= top_groups E / groups, scale finite
+ *   (QLORA_ERR_EXPERT otherwise); 0 <= tokens, tokens*topk <= 2^30
+ *   (QLORA_ERR_SHAPE).  No output overlaps an input.
+ */
+typedef enum {
+  QLORA_SCORE_SOFTMAX = 0,
+  QLORA_SCORE_SIGMOID = 1
+} qlora_score;
+
+typedef struct {
+  int32_t score;        /* qlora_score */
+  int32_t topk;
+  int32_t groups;
+  int32_t top_groups;
+  int32_t group_top;
+  int32_t renorm;       /* 1 or 0 */
+  float scale;
+} qlora_router_config;
+
+int qlora_router_fwd(const void* logits, int logits_fp32, int64_t tokens, int E,
+                     const float* bias, const qlora_router_config* cfg, int32_t* ids,
+                     float* weights, qlora_stream_t stream);
+int qlora_router_bwd(const float* dweights, const void* logits, int logits_fp32,
+                     const int32_t* ids, int64_t tokens, int E, const qlora_router_config* cfg,
+                     void* dlogits, qlora_stream_t stream);
 
 /*
  * Optimizer step on the adapters, and its state paged between HBM and host

@@ -1,0 +1,221 @@
+"""GPU parity of the routing to experts: ids exactly those of a float64 choice,
+weights and gradients within half a step of their type."""
+import numpy as np
+import pytest
+
+import bit_quantized_fine_amd as q
+from expert_util import within
+from gpu_util import dev, need_gpu, say, torch
+from oracle import router as orr
+
+pytestmark = pytest.mark.gpu
+
+# one rounding of a 64-bit value to fp32 (and to bf16 after it), 64-bit error besides
+F32, BF16 = 1.001 * 2.0 ** -24, 2.0 ** -8 + 2.0 ** -23
+
+CASES = [
+    # tokens, E, topk, score, bias, groups, top_groups, group_top, renorm, fp32
+    (1, 1, 1, "softmax", False, 1, 1, 1, True, True),
+    (3, 8, 2, "softmax", False, 1, 1, 1, True, False),
+    (5, 8, 8, "softmax", False, 1, 1, 1, False, True),
+    (7, 7, 3, "sigmoid", False, 1, 1, 1, False, False),
+    (33, 64, 6, "softmax", True, 1, 1, 1, True, True),
+    (20, 65, 4, "sigmoid", True, 1, 1, 1, True, True),
+    (64, 100, 10, "softmax", False, 4, 2, 1, False, True),
+    (31, 128, 8, "softmax", False, 8, 3, 2, True, True),
+    (50, 256, 8, "sigmoid", True, 8, 4, 2, True, True),
+    (50, 256, 8, "sigmoid", True, 8, 4, 2, False, False),
+    (9, 160, 6, "softmax", True, 8, 3, 1, False, False),
+    (6, 63, 5, "sigmoid", True, 21, 5, 2, True, True),
+    (6, 64, 3, "softmax", True, 64, 9, 1, True, True),
+    (10, 320, 12, "softmax", True, 5, 2, 2, True, True),
+    (4, 512, 64, "softmax", False, 1, 1, 1, True, True),
+    (5, 1000, 64, "sigmoid", True, 10, 3, 2, True, False),
+    (3, 1024, 33, "softmax", False, 32, 7, 2, False, True),
+    (3, 1024, 64, "softmax", True, 1, 1, 1, False, True),
+]
+
+
+def _logits(rng, tokens, E, fp32, kind):
+    x = 2 * rng.standard_normal((tokens, E)) + rng.standard_normal(E)
+    if kind == "ties":          # few different values, both zeros
+        x = rng.integers(-2, 3, (tokens, E)) * 0.5
+        x[x == 0] = rng.choice([0.0, -0.0], int((x == 0).sum()))
+    elif kind == "masked":
+        x[rng.random(x.shape) < 0.5] = -np.inf
+        x[::3] = -np.inf        # rows that the mask leaves empty
+        x[1::3, : E // 2] = np.finfo(np.float32).min if fp32 else -3.3895313892515355e38
+    elif kind == "wide":
+        x *= 60.0
+    t = torch.from_numpy(x.astype(np.float32)).to(dev())
+    t = t if fp32 else t.bfloat16()
+    return t, t.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("kind", ["normal", "ties", "masked", "wide"])
+@pytest.mark.parametrize("tokens,E,topk,score,bias,groups,tg,gt,renorm,fp32", CASES)
+def test_router(tokens, E, topk, score, bias, groups, tg, gt, renorm, fp32, kind):
+    need_gpu()
+    say(f"router tokens={tokens} E={E} topk={topk} {score} bias={bias} groups={groups}/{tg}/{gt} "
+        f"renorm={renorm} fp32={fp32} {kind}")
+    if kind in ("ties", "wide") and tg < groups and gt == 2:
+        # sums of two scores: equal ones are rounded apart, or not, as they are formed
+        kind = "normal"
+    rng = np.random.default_rng(E + topk)
+    t, x = _logits(rng, tokens, E, fp32, kind)
+    b = None
+    if bias:
+        b = torch.from_numpy((0.05 * rng.standard_normal(E)).astype(np.float32)).to(dev())
+        if kind == "ties":
+            b = torch.zeros_like(b)     # equal logits stay equal
+    kw = dict(score=score, renorm=renorm, scale=2.5)
+    ids, w = q.qlora_router_fwd(t, topk, bias=b, groups=groups, top_groups=tg, group_top=gt, **kw)
+    dw = torch.from_numpy(rng.standard_normal((tokens, topk)).astype(np.float32)).to(dev())
+    dl = q.qlora_router_bwd(dw, t, ids, **kw)
+    torch.cuda.synchronize()
+    wid, ww = orr.fwd(x, topk, score, None if b is None else b.double().cpu().numpy(), groups, tg,
+                      gt, renorm, 2.5)
+    np.testing.assert_array_equal(ids.cpu().numpy(), wid)
+    within("weights", w, ww, F32 * np.abs(ww) + 2.0 ** -149)
+    assert dl.dtype == t.dtype
+    want, mag = orr.bwd(dw.double().cpu().numpy(), x, wid, score, renorm, 2.5)
+    bound = (F32 if fp32 else BF16) * np.abs(want) + 1e-13 * mag + (2.0 ** -149 if fp32 else 2.0 ** -133)
+    if score == "softmax" and not renorm:
+        # p_e (dw_e - sum_j p_j dw_j) in 64 bits, here and in the reference: p is off by
+        # (E / 64 + 8 for the sum's additions) 2^-53, at most 24 2^-53, of itself, the sum over
+        # j by topk 2^-53 more, each times |dw|; where p_e is next to 1 this is what is left
+        bound += 2.5 * 2 * (topk + 24) * 2.0 ** -53 * np.abs(dw.double().cpu().numpy()).max(
+            axis=1, keepdims=True)
+    within("dlogits", dl, want, bound)
+
+
+def test_many_tokens():
+    """A batch of 8192 tokens and 256 experts: every id, in the order of 64 bits."""
+    need_gpu()
+    say("router, 8192 x 256")
+    g = torch.Generator(device=dev()).manual_seed(0)
+    x = 2 * torch.randn(8192, 256, generator=g, device=dev())
+    b = 0.05 * torch.randn(256, generator=g, device=dev())
+    ids, w = q.qlora_router_fwd(x, 8, "sigmoid", b, groups=8, top_groups=4, group_top=2)
+    torch.cuda.synchronize()
+    rank = 1 / (1 + np.exp(-x.double().cpu().numpy())) + b.double().cpu().numpy()
+    two = np.sort(rank.reshape(8192, 8, 32), axis=2)[:, :, -2:].sum(axis=2)
+    stay = np.argsort(-two, axis=1, kind="stable")[:, :4]
+    keep = np.zeros((8192, 8), bool)
+    np.put_along_axis(keep, stay, True, 1)
+    rank[~np.repeat(keep, 32, axis=1)] = -np.inf
+    np.testing.assert_array_equal(ids.cpu().numpy(),
+                                  np.argsort(-rank, axis=1, kind="stable")[:, :8])
+    np.testing.assert_allclose(w.sum(dim=1).cpu().numpy(), 1, rtol=8 * 2.0 ** -24)
+
+
+def test_gradient_of_a_sure_choice():
+    """Where one expert takes all but 1e-6, the gradient keeps its digits."""
+    need_gpu()
+    say("router, sure choices")
+    x = np.zeros((4, 8), np.float32)
+    x[:, 0] = [14.0, 20.0, 40.0, 80.0]
+    t = torch.from_numpy(x).to(dev())
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            ids, _ = q.qlora_router_fwd(t, 2, score, renorm=renorm)
+            dw = torch.tensor([[1.0, -0.5]] * 4, device=dev())
+            dl = q.qlora_router_bwd(dw, t, ids, score, renorm)
+            torch.cuda.synchronize()
+            want, mag = orr.bwd(dw.double().cpu().numpy(), x.astype(np.float64), ids.cpu().numpy(), score,
+                                renorm)
+            # 1 - p to 2^-53, where p is within 1e-6 of 1
+            within("dlogits", dl, want, F32 * np.abs(want) + 4e-16 + 2.0 ** -149)
+
+
+def test_bad_logits_show():
+    """NaN and +inf make a token's weights and gradients NaN; its ids stay within
+    the experts and apart, and other tokens are as without them."""
+    need_gpu()
+    say("router, NaN logits")
+    for E, groups in ((8, 1), (96, 4), (512, 8)):
+        t = torch.randn(9, E, device=dev())
+        clean = t.clone()
+        t[2, 3], t[5, 0], t[7] = float("nan"), float("inf"), float("nan")
+        for score in ("softmax", "sigmoid"):
+            for bias in (None, torch.randn(E, device=dev())):
+                for renorm in (True, False):
+                    cfg = dict(score=score, renorm=renorm)
+                    kw = dict(bias=bias, groups=groups, top_groups=max(1, groups // 2), **cfg)
+                    ids, w = q.qlora_router_fwd(t, 3, **kw)
+                    ids0, w0 = q.qlora_router_fwd(clean, 3, **kw)
+                    dw = torch.ones_like(w)
+                    dl = q.qlora_router_bwd(dw, t, ids, **cfg)
+                    dl0 = q.qlora_router_bwd(dw, clean, ids0, **cfg)
+                    torch.cuda.synchronize()
+                    bad = torch.tensor([2, 5, 7], device=dev())
+                    good = torch.tensor([0, 1, 3, 4, 6, 8], device=dev())
+                    assert torch.equal(ids[good], ids0[good]) and torch.equal(w[good], w0[good])
+                    assert torch.equal(dl[good], dl0[good])
+                    assert (ids >= -1).all() and (ids < E).all() and (ids[7] == -1).all()
+                    for row in (2, 5):
+                        assert len(set(ids[row].tolist())) == 3 and 3 not in ids[2].tolist()
+                        assert torch.isnan(w[row][ids[row] >= 0]).all()
+                    assert torch.isnan(dl[bad]).all() and not w[7].any()
+
+
+def test_ids_of_the_callers_own():
+    """Backward: ids outside the experts are slots not taken, the same expert twice
+    adds up, and a masked expert named by an id has no gradient."""
+    need_gpu()
+    say("router, ids of the caller's own")
+    x = torch.randn(5, 12, device=dev())
+    x[4, 2] = -float("inf")
+    ids = torch.tensor([[3, 3, 1], [-1, 5, 12], [-2 ** 31, 2 ** 31 - 1, -1], [0, 11, 0], [2, 1, 4]],
+                       dtype=torch.int32, device=dev())
+    dw = torch.randn(5, 3, device=dev())
+    norm = np.where((ids.cpu().numpy() < 0) | (ids.cpu().numpy() >= 12), -1, ids.cpu().numpy())
+    norm[4, 0] = -1
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            dl = q.qlora_router_bwd(dw, x, ids, score, renorm)
+            torch.cuda.synchronize()
+            want, mag = orr.bwd(dw.double().cpu().numpy(), x.double().cpu().numpy(), norm, score,
+                                renorm)
+            within("dlogits", dl, want, F32 * np.abs(want) + 1e-13 * mag + 2.0 ** -149)
+
+
+def test_guards_streams_and_graph():
+    """Nothing around the outputs changes; another stream and replays of a graph
+    give the same bits as eager calls."""
+    need_gpu()
+    say("router in a graph")
+    T, E, k = 301, 72, 5
+    x, b = torch.randn(T, E, device=dev()), 0.1 * torch.randn(E, device=dev())
+    dw = torch.randn(T, k, device=dev())
+    I = torch.full((T + 2, k), 7, dtype=torch.int32, device=dev())
+    W, D = torch.full((T + 2, k), 7.0, device=dev()), torch.full((T + 4, E), 7.0, device=dev())
+    q.qlora_router_fwd(x, k, bias=b, groups=9, top_groups=4, ids=I[1:-1], weights=W[1:-1])
+    q.qlora_router_bwd(dw, x, I[1:-1], dlogits=D[2:-2])
+    torch.cuda.synchronize()
+    assert (I[0] == 7).all() and (I[-1] == 7).all() and (W[0] == 7).all() and (W[-1] == 7).all()
+    assert (D[:2] == 7).all() and (D[-2:] == 7).all()
+
+    def step():
+        ids, w = q.qlora_router_fwd(x, k, bias=b, groups=9, top_groups=4)
+        return ids, w, q.qlora_router_bwd(dw, x, ids)
+    first = step()
+    torch.cuda.synchronize()
+    assert torch.equal(first[0], I[1:-1]) and torch.equal(first[2], D[2:-2])
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        other = step()
+    side.synchronize()
+    assert all(torch.equal(u, v) for u, v in zip(first, other))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        x.copy_(torch.randn(T, E, device=dev()))
+        graph.replay()
+        a = [t.clone() for t in got]
+        e = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(a, e))
+    ids, w = q.qlora_router_fwd(x[:0], k)
+    assert ids.shape == (0, k) and q.qlora_router_bwd(dw[:0], x[:0], ids).shape == (0, E)
