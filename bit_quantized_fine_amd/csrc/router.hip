@@ -44,7 +44,8 @@ struct Router {
   int groups, top_groups, group_top;
   int gs;                 // experts of a group
   uint32_t gs_mul;        // e / gs = e gs_mul >> 20
-  int gshift;             // log2 of the lanes that share a group
+  int gshift;             // log2 of the lanes that share a group in LDS
+  int glanes;             // lanes that hold one whole group each, or 0
   int* ids;
   float* weights;
   const float* dweights;
@@ -81,10 +82,50 @@ __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
       wave_max(static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
   return static_cast<uint64_t>(hi) << 32 | lo;
 }
+// v moved across lanes (zero where there is no lane to take it from).
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, ROWS, 0xF, false);
+  const uint32_t hi =
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+// Sum over the wave, always in the same order.
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  v += dpp_f64<0x111>(v);        // row_shr 1, 2, 4, 8
+  v += dpp_f64<0x112>(v);
+  v += dpp_f64<0x114>(v);
+  v += dpp_f64<0x118>(v);
+  v += dpp_f64<0x142, 0xA>(v);   // row_bcast 15, 31
+  v += dpp_f64<0x143, 0xC>(v);
+  return read_lane(v, 63);
+}
+
+// exp(x) for x <= 0, to about one unit in the last place of 64 bits: x = n ln 2 +
+// r with |r| <= ln 2 / 2 (W. Cody, W. Waite, "Software Manual for the Elementary
+// Functions": ln 2 as a part of 32 bits, whose product with n is exact, and the
+// rest), and the series of exp(r) to r^13 / 13!, which leaves out less than 2^-57.
+__device__ __forceinline__ double exp_neg(double x) {
+  x = max(x, -800.0);   // 0 from about -745 on (-inf too)
+  const double n = __builtin_rint(x * 1.4426950408889634074);
+  double r = fma(n, -0x1.62e42feep-1, x);
+  r = fma(n, -0x1.a39ef35793c76p-33, r);
+  double p = 1.0 / 6227020800.0;
+  p = fma(p, r, 1.0 / 479001600.0);
+  p = fma(p, r, 1.0 / 39916800.0);
+  p = fma(p, r, 1.0 / 3628800.0);
+  p = fma(p, r, 1.0 / 362880.0);
+  p = fma(p, r, 1.0 / 40320.0);
+  p = fma(p, r, 1.0 / 5040.0);
+  p = fma(p, r, 1.0 / 720.0);
+  p = fma(p, r, 1.0 / 120.0);
+  p = fma(p, r, 1.0 / 24.0);
+  p = fma(p, r, 1.0 / 6.0);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return __builtin_amdgcn_ldexp(p, static_cast<int>(n));
 }
 
 // Integers in the order of the values; 0 for an expert that is not to be
@@ -109,9 +150,10 @@ __device__ __forceinline__ float to_f32(L v) {
     return v;
 }
 
-// sigma(x) = exp(min(x, 0)) / (1 + exp(-|x|)): neither factor overflows.
+// sigma(x) = exp(min(x, 0)) / (1 + exp(-|x|))
 __device__ __forceinline__ double sigmoid64(double x) {
-  return exp(min(x, 0.0)) / (1.0 + exp(-fabs(x)));
+  const double t = exp_neg(-fabs(x));
+  return (x > 0.0 ? 1.0 : t) / (1.0 + t);
 }
 
 // A token's logits: lane l holds experts l EPL ...; -inf past E.
@@ -123,10 +165,19 @@ struct Logits {
   __device__ void load(const L* row, int E, int lane) {
     uint32_t k = 0;
     bool b = false;
+    const int e0 = lane * EPL;
+    if (E % EPL == 0) {   // a lane's experts are one aligned piece, whole or absent
+      constexpr int kAlign = EPL * sizeof(L) < 16 ? EPL * sizeof(L) : 16;
+      L v[EPL];
+      if (e0 < E) __builtin_memcpy(v, __builtin_assume_aligned(row + e0, kAlign), sizeof(v));
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) x[i] = e0 < E ? to_f32(v[i]) : -__builtin_inff();
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) x[i] = e0 + i < E ? to_f32(row[e0 + i]) : -__builtin_inff();
+    }
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int e = lane * EPL + i;
-      x[i] = e < E ? to_f32(row[e]) : -__builtin_inff();
       b |= !(x[i] < __builtin_inff());
       k = max(k, order_key(x[i]));
     }
@@ -139,50 +190,112 @@ struct Logits {
     double s = 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      d[i] = x[i] > -__builtin_inff() ? exp(static_cast<double>(x[i]) - static_cast<double>(top)) : 0.0;
+      d[i] = x[i] > -__builtin_inff() ? exp_neg(static_cast<double>(x[i]) - static_cast<double>(top))
+                                      : 0.0;
       s += d[i];
     }
     return wave_sum(s);
   }
 };
 
-// The topk largest keys in order: lane j gets expert and logit of slot j
-// (id -1: none left).
+// The lane with the wave's largest key, the lowest of several; -1 if all are 0.
+// Where the high words of 64 bits decide (all but about one round in 10^4), the low
+// ones are not looked at.
+__device__ __forceinline__ int best_lane(uint32_t k) {
+  const uint32_t m = wave_max(k);
+  return m ? __builtin_ctzll(__builtin_amdgcn_ballot_w64(k == m)) : -1;
+}
+__device__ __forceinline__ int best_lane(uint64_t k) {
+  const uint32_t hi = static_cast<uint32_t>(k >> 32), lo = static_cast<uint32_t>(k);
+  const uint32_t m = wave_max(hi);
+  if (m == 0) return -1;   // (a key that is not 0 has its high word)
+  uint64_t at = __builtin_amdgcn_ballot_w64(hi == m);
+  if (at & (at - 1)) {
+    const uint32_t l = wave_max(hi == m ? lo : 0u);
+    at = __builtin_amdgcn_ballot_w64(hi == m && lo == l);
+  }
+  return __builtin_ctzll(at);
+}
+
+// The topk largest keys in order: lane j gets the expert of slot j, -1 if none is
+// left.  Up to eight keys a lane are sorted first, so that a round only moves the
+// winner's up: neighbours change places where the second is larger, which
+// leaves equal ones in their order.
 template <int EPL, class Key>
-__device__ __forceinline__ void choose(Key* k, const float* x, int topk, int lane, int& id,
-                                       float& lx) {
-  Key cur = k[0];
+__device__ __forceinline__ int choose(Key* k, int topk, int lane) {
+  int id = -1;
+  if constexpr (EPL <= 8) {
+    int at[EPL];
 #pragma unroll
-  for (int i = 1; i < EPL; ++i) cur = max(cur, k[i]);
-  id = -1;
-  lx = 0.f;
-  for (int j = 0; j < topk; ++j) {
-    const Key m = wave_max(cur);
-    if (m == 0) break;   // uniform
-    const int who = __builtin_ctzll(__builtin_amdgcn_ballot_w64(cur == m));
-    int e = 0;
-    float v = 0.f;
-    if (lane == who) {
-      bool found = false;
-      cur = 0;
+    for (int i = 0; i < EPL; ++i) at[i] = lane * EPL + i;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        if (!found && k[i] == m) {
-          found = true;
-          e = lane * EPL + i;
-          v = x[i];
-          k[i] = 0;
+    for (int n = 0; n < EPL; ++n)
+#pragma unroll
+      for (int i = n & 1; i + 1 < EPL; i += 2) {
+        const bool swap = k[i] < k[i + 1];
+        const Key hi = swap ? k[i + 1] : k[i], lo = swap ? k[i] : k[i + 1];
+        const int ih = swap ? at[i + 1] : at[i], il = swap ? at[i] : at[i + 1];
+        k[i] = hi;
+        k[i + 1] = lo;
+        at[i] = ih;
+        at[i + 1] = il;
+      }
+    for (int j = 0; j < topk; ++j) {
+      const int who = best_lane(k[0]);
+      if (who < 0) break;   // uniform
+      const int e = read_lane(at[0], who);
+      if (lane == j) id = e;
+      if (lane == who) {
+#pragma unroll
+        for (int i = 0; i + 1 < EPL; ++i) {
+          k[i] = k[i + 1];
+          at[i] = at[i + 1];
         }
-        cur = max(cur, k[i]);
+        k[EPL - 1] = 0;
       }
     }
-    const int we = read_lane(e, who);
-    const float wv = read_lane(v, who);
-    if (lane == j) {
-      id = we;
-      lx = wv;
+  } else {
+    Key cur = k[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) cur = max(cur, k[i]);
+    for (int j = 0; j < topk; ++j) {
+      const int who = best_lane(cur);
+      if (who < 0) break;   // uniform
+      int e = 0;
+      if (lane == who) {
+        const Key m = cur;
+        bool found = false;
+        cur = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          if (!found && k[i] == m) {
+            found = true;
+            e = lane * EPL + i;
+            k[i] = 0;
+          }
+          cur = max(cur, k[i]);
+        }
+      }
+      e = read_lane(e, who);
+      if (lane == j) id = e;
     }
   }
+  return id;
+}
+
+// The two largest of all values that the lanes of a group hold (groups of 1 << n
+// lanes, n <= 4), in all of them.
+template <int CTRL>
+__device__ __forceinline__ void merge_two(double& t1, double& t2) {
+  const double o1 = dpp_f64<CTRL>(t1), o2 = dpp_f64<CTRL>(t2);
+  t2 = max(min(t1, o1), max(t2, o2));
+  t1 = max(t1, o1);
+}
+__device__ __forceinline__ void two_best_of_lanes(double& t1, double& t2, int lanes) {
+  if (lanes > 1) merge_two<0xB1>(t1, t2);    // quad_perm 1,0,3,2
+  if (lanes > 2) merge_two<0x4E>(t1, t2);    // quad_perm 2,3,0,1
+  if (lanes > 4) merge_two<0x141>(t1, t2);   // row_half_mirror
+  if (lanes > 8) merge_two<0x140>(t1, t2);   // row_mirror
 }
 
 // Relative weights u of the chosen (0 for lanes without one), for the
@@ -192,8 +305,8 @@ __device__ __forceinline__ double relative_weight(const Router& a, bool live, fl
   const float v = a.sigmoid ? min(lx, 0.f) : lx;
   const float m = key_value(wave_max(live ? order_key(v) : 0u));
   if (!live) return 0.0;
-  const double u = exp(static_cast<double>(v) - static_cast<double>(m));
-  return a.sigmoid ? u / (1.0 + exp(-fabs(static_cast<double>(lx)))) : u;
+  const double u = exp_neg(static_cast<double>(v) - static_cast<double>(m));
+  return a.sigmoid ? u / (1.0 + exp_neg(-fabs(static_cast<double>(lx)))) : u;
 }
 
 __device__ __forceinline__ int64_t wave_token() {
@@ -235,58 +348,80 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_fwd(Router a) {
                     ? p[i] + static_cast<double>(a.bias[e]) : -__builtin_inf();
     }
   }
-  uint64_t keep = ~0ull;   // bit (group << gshift): the group stays
+  bool mine_stay = true;   // this lane's group, where a lane holds one
+  uint64_t keep = 0;       // else bit (group << gshift): the group stays
   if (a.choose_groups) {
-    double* mine = lds + (int64_t)wave_id() * a.E;
+    double v[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int e = lane * EPL + i;
-      double v = a.bias ? rank[i] : (sums ? p[i] : static_cast<double>(l.x[i]));
-      if (!(l.x[i] > -__builtin_inff()) || !(v > -__builtin_inf())) v = -__builtin_inf();
-      if (e < a.E) mine[e] = v;
+      v[i] = a.bias ? rank[i] : (sums ? p[i] : static_cast<double>(l.x[i]));
+      if (!(l.x[i] > -__builtin_inff()) || !(v[i] > -__builtin_inf())) v[i] = -__builtin_inf();
     }
-    __syncthreads();
-    // the two best of a group, by the lanes that share it
-    const int g = lane >> a.gshift, sub = lane & ((1 << a.gshift) - 1);
     double t1 = -__builtin_inf(), t2 = t1;
-    if (g < a.groups)
-      for (int j = sub; j < a.gs; j += 1 << a.gshift) {
-        const double v = mine[g * a.gs + j];
-        t2 = v > t1 ? t1 : max(t2, v);
-        t1 = max(t1, v);
+    auto add = [&](double u) {
+      t2 = max(t2, min(t1, u));
+      t1 = max(t1, u);
+    };
+    int g, sub, lanes;   // this lane's group, its place among the group's lanes, their number
+    if (a.glanes) {
+      lanes = a.glanes;
+      g = lane / lanes;
+      sub = lane & (lanes - 1);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) add(v[i]);
+      two_best_of_lanes(t1, t2, lanes);
+    } else {
+      lanes = 1 << a.gshift;
+      g = lane >> a.gshift;
+      sub = lane & (lanes - 1);
+      double* mine = lds + (int64_t)wave_id() * a.E;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (lane * EPL + i < a.E) mine[lane * EPL + i] = v[i];
+      __syncthreads();   // (uniform over the workgroup)
+      if (g < a.groups)
+        for (int j = sub; j < a.gs; j += lanes) add(mine[g * a.gs + j]);
+      for (int d = 1; d < lanes; d <<= 1) {
+        const double o1 = __shfl_xor(t1, d), o2 = __shfl_xor(t2, d);
+        t2 = max(min(t1, o1), max(t2, o2));
+        t1 = max(t1, o1);
       }
-    for (int d = 1; d < 1 << a.gshift; d <<= 1) {
-      const double o1 = __shfl_xor(t1, d), o2 = __shfl_xor(t2, d);
-      t2 = max(min(t1, o1), max(t2, o2));
-      t1 = max(t1, o1);
     }
-    const bool any = t1 > -__builtin_inf();
     const double score = a.group_top == 2 && t2 > -__builtin_inf() ? t1 + t2 : t1;
-    int better = 0;
-    for (int q = 0; q < a.groups; ++q) {
-      const double o = read_lane(score, q << a.gshift);
-      better += o > score || (o == score && q < g);
+    int better = 0;   // groups ahead of this lane's
+    if (lanes >= a.groups) {   // each of a group's lanes looks at one other group
+      const double o = __shfl(score, sub * lanes);
+      const uint64_t ahead = __builtin_amdgcn_ballot_w64(
+          sub < a.groups && (o > score || (o == score && sub < g)));
+      better = __builtin_popcountll((ahead >> (lane - sub)) & ((2ull << (lanes - 1)) - 1));
+    } else {
+      for (int q = 0; q < a.groups; ++q) {
+        const double o = read_lane(score, q * lanes);
+        better += o > score || (o == score && q < g);
+      }
     }
-    keep = __builtin_amdgcn_ballot_w64(g < a.groups && sub == 0 && any && better < a.top_groups);
+    mine_stay = g < a.groups && t1 > -__builtin_inf() && better < a.top_groups;
+    if (!a.glanes) keep = __builtin_amdgcn_ballot_w64(mine_stay && sub == 0);
   }
   auto stays = [&](int i) {
-    if (!a.choose_groups) return true;
+    if (!a.choose_groups || a.glanes) return mine_stay;
     const int e = lane * EPL + i;
     return e < a.E && ((keep >> (((e * a.gs_mul) >> 20) << a.gshift)) & 1) != 0;
   };
   int id;
-  float lx;
   if (a.bias) {
     uint64_t k[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) k[i] = stays(i) ? order_key(rank[i]) : 0ull;
-    choose<EPL, uint64_t>(k, l.x, a.topk, lane, id, lx);
+    id = choose<EPL, uint64_t>(k, a.topk, lane);
   } else {
     uint32_t k[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) k[i] = stays(i) ? order_key(l.x[i]) : 0u;
-    choose<EPL, uint32_t>(k, l.x, a.topk, lane, id, lx);
+    id = choose<EPL, uint32_t>(k, a.topk, lane);
   }
+  const float lx =
+      id >= 0 ? to_f32(static_cast<const L*>(a.logits)[t * a.E + id]) : 0.f;
   const bool live = id >= 0;
   double w;
   if (a.renorm) {
@@ -297,7 +432,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_fwd(Router a) {
     w = live ? sigmoid64(lx) : 0.0;
   } else {
     if (sum == 0.0) sum = l.exps(p);
-    w = live ? exp(static_cast<double>(lx) - static_cast<double>(l.top)) / sum : 0.0;
+    w = live ? exp_neg(static_cast<double>(lx) - static_cast<double>(l.top)) / sum : 0.0;
   }
   if (in && lane < a.topk) {
     a.ids[t * a.topk + lane] = id;
@@ -344,7 +479,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_bwd(Router a) {
     d = live ? dw * sigmoid64(lx) * sigmoid64(-static_cast<double>(lx)) : 0.0;
   } else {
     r = 1.0 / l.exps(p);
-    d = live ? dw * exp(static_cast<double>(lx) - static_cast<double>(l.top)) * r : 0.0;
+    d = live ? dw * exp_neg(static_cast<double>(lx) - static_cast<double>(l.top)) * r : 0.0;
     for (int j = 0; j < a.topk; ++j) s += read_lane(d, j);
   }
   double out[EPL];
@@ -391,6 +526,13 @@ int check_router(int64_t tokens, int E, const qlora_router_config* c) {
   return QLORA_OK;
 }
 
+// Experts a lane holds: 1, 2, 4, 8 or 16.
+int lane_experts(int E) {
+  int n = 1;
+  while (64 * n < E) n *= 2;
+  return n;
+}
+
 Router router(const void* logits, int64_t tokens, int E, const qlora_router_config* c) {
   Router a{};
   a.logits = logits;
@@ -408,8 +550,13 @@ Router router(const void* logits, int64_t tokens, int E, const qlora_router_conf
   // (e < 1024 and gs < 1024: e gs < 2^20, so the quotient is exact)
   a.gs_mul = ((1u << 20) + a.gs - 1) / a.gs;
   while ((c->groups << (a.gshift + 1)) <= 64) ++a.gshift;
+  // whole groups in 1, 2, 4, 8 or 16 lanes: no way through LDS
+  const int per = lane_experts(E);
+  for (int n = 1; n <= 16; n *= 2)
+    if (a.gs == n * per) a.glanes = n;
   return a;
 }
+
 
 template <bool BACK, int EPL, class L>
 hipError_t launch(const Router& a, hipStream_t st) {
@@ -420,18 +567,20 @@ hipError_t launch(const Router& a, hipStream_t st) {
     hipLaunchKernelGGL((k_router_bwd<EPL, L>), grid, dim3(64 * kWaves), 0, st, a);
   else
     hipLaunchKernelGGL((k_router_fwd<EPL, L>), grid, dim3(64 * kWaves),
-                       a.choose_groups ? kWaves * a.E * sizeof(double) : 0, st, a);
+                       a.choose_groups && !a.glanes ? kWaves * a.E * sizeof(double) : 0, st, a);
   return hipGetLastError();
 }
 
 template <bool BACK, class L>
 int dispatch(const Router& a, hipStream_t st) {
   hipError_t e;
-  if (a.E <= 64) e = launch<BACK, 1, L>(a, st);
-  else if (a.E <= 128) e = launch<BACK, 2, L>(a, st);
-  else if (a.E <= 256) e = launch<BACK, 4, L>(a, st);
-  else if (a.E <= 512) e = launch<BACK, 8, L>(a, st);
-  else e = launch<BACK, 16, L>(a, st);
+  switch (lane_experts(a.E)) {
+    case 1: e = launch<BACK, 1, L>(a, st); break;
+    case 2: e = launch<BACK, 2, L>(a, st); break;
+    case 4: e = launch<BACK, 4, L>(a, st); break;
+    case 8: e = launch<BACK, 8, L>(a, st); break;
+    default: e = launch<BACK, 16, L>(a, st);
+  }
   return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP;
 }
 
