@@ -106,27 +106,33 @@ __device__ __forceinline__ double wave_sum(double v) {
 // r with |r| <= ln 2 / 2 (W. Cody, W. Waite, "Software Manual for the Elementary
 // Functions": ln 2 as a part of 32 bits, whose product with n is exact, and the
 // rest), and the series of exp(r) to r^13 / 13!, which leaves out less than 2^-57.
-__device__ __forceinline__ double exp_neg(double x) {
-  x = max(x, -800.0);   // 0 from about -745 on (-inf too)
-  const double n = __builtin_rint(x * 1.4426950408889634074);
-  double r = fma(n, -0x1.62e42feep-1, x);
-  r = fma(n, -0x1.a39ef35793c76p-33, r);
-  double p = 1.0 / 6227020800.0;
-  p = fma(p, r, 1.0 / 479001600.0);
-  p = fma(p, r, 1.0 / 39916800.0);
-  p = fma(p, r, 1.0 / 3628800.0);
-  p = fma(p, r, 1.0 / 362880.0);
-  p = fma(p, r, 1.0 / 40320.0);
-  p = fma(p, r, 1.0 / 5040.0);
-  p = fma(p, r, 1.0 / 720.0);
-  p = fma(p, r, 1.0 / 120.0);
-  p = fma(p, r, 1.0 / 24.0);
-  p = fma(p, r, 1.0 / 6.0);
-  p = fma(p, r, 0.5);
-  p = fma(p, r, 1.0);
-  p = fma(p, r, 1.0);
-  return __builtin_amdgcn_ldexp(p, static_cast<int>(n));
-}
+// The coefficients are held in scalar registers (the empty asm puts them there): a
+// step is then one fma that reads its coefficient, where the compiler else copies
+// each into vector registers first, three instructions a step.
+struct Exp {
+  double c[12];   // 1 / 13!, ..., 1 / 2!
+  __device__ __forceinline__ Exp() {
+    double f = 6227020800.0;
+#pragma unroll
+    for (int i = 0; i < 12; ++i) {
+      c[i] = 1.0 / f;
+      asm("" : "+s"(c[i]));
+      f /= 13 - i;   // (exact)
+    }
+  }
+  __device__ __forceinline__ double operator()(double x) const {
+    x = max(x, -800.0);   // 0 from about -745 on (-inf too)
+    const double n = __builtin_rint(x * 1.4426950408889634074);
+    double r = fma(n, -0x1.62e42feep-1, x);
+    r = fma(n, -0x1.a39ef35793c76p-33, r);
+    double p = c[0];
+#pragma unroll
+    for (int i = 1; i < 12; ++i) p = fma(p, r, c[i]);
+    p = fma(p, r, 1.0);
+    p = fma(p, r, 1.0);
+    return __builtin_amdgcn_ldexp(p, static_cast<int>(n));
+  }
+};
 
 // Integers in the order of the values; 0 for an expert that is not to be
 // chosen (-inf or NaN).  v + 0 makes -0 equal to 0.
@@ -151,7 +157,7 @@ __device__ __forceinline__ float to_f32(L v) {
 }
 
 // sigma(x) = exp(min(x, 0)) / (1 + exp(-|x|))
-__device__ __forceinline__ double sigmoid64(double x) {
+__device__ __forceinline__ double sigmoid64(const Exp& exp_neg, double x) {
   const double t = exp_neg(-fabs(x));
   return (x > 0.0 ? 1.0 : t) / (1.0 + t);
 }
@@ -186,7 +192,7 @@ struct Logits {
     top = k ? key_value(k) : -__builtin_inff();
   }
   // sum over the experts of exp(x - top), which this lane's d[i] receive
-  __device__ double exps(double* d) const {
+  __device__ double exps(const Exp& exp_neg, double* d) const {
     double s = 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -301,7 +307,8 @@ __device__ __forceinline__ void two_best_of_lanes(double& t1, double& t2, int la
 // Relative weights u of the chosen (0 for lanes without one), for the
 // renormalised forms: exp(x - m), times 1 / (1 + exp(-|x|)) for a sigmoid, whose
 // factor exp(min(x, 0)) is the one shifted by m.
-__device__ __forceinline__ double relative_weight(const Router& a, bool live, float lx) {
+__device__ __forceinline__ double relative_weight(const Router& a, const Exp& exp_neg, bool live,
+                                                  float lx) {
   const float v = a.sigmoid ? min(lx, 0.f) : lx;
   const float m = key_value(wave_max(live ? order_key(v) : 0u));
   if (!live) return 0.0;
@@ -326,14 +333,15 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_fwd(Router a) {
   Logits<EPL, L> l;
   l.load(static_cast<const L*>(a.logits) + t * a.E, a.E, lane);
 
+  const Exp exp_neg;
   double p[EPL], sum = 0.0;   // p: scores where they rank, exps otherwise unused
   const bool sums = a.choose_groups && a.group_top == 2;
   if (a.bias || sums) {
     if (a.sigmoid) {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) p[i] = sigmoid64(l.x[i]);
+      for (int i = 0; i < EPL; ++i) p[i] = sigmoid64(exp_neg, l.x[i]);
     } else {
-      sum = l.exps(p);
+      sum = l.exps(exp_neg, p);
       const double r = sum > 0.0 ? 1.0 / sum : 0.0;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) p[i] *= r;
@@ -425,13 +433,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_fwd(Router a) {
   const bool live = id >= 0;
   double w;
   if (a.renorm) {
-    w = relative_weight(a, live, lx);
+    w = relative_weight(a, exp_neg, live, lx);
     const double total = wave_sum(w);
     w = live ? w / total : 0.0;
   } else if (a.sigmoid) {
-    w = live ? sigmoid64(lx) : 0.0;
+    w = live ? sigmoid64(exp_neg, lx) : 0.0;
   } else {
-    if (sum == 0.0) sum = l.exps(p);
+    if (sum == 0.0) sum = l.exps(exp_neg, p);
     w = live ? exp_neg(static_cast<double>(lx) - static_cast<double>(l.top)) / sum : 0.0;
   }
   if (in && lane < a.topk) {
@@ -464,21 +472,22 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_bwd(Router a) {
     if (id >= 0) dw = static_cast<double>(a.dweights[t * a.topk + lane]);
   }
   const bool live = id >= 0;
+  const Exp exp_neg;
   double d = 0.0;       // of this slot's expert
   double s = 0.0;       // softmax without renorm: sum p dw
   double p[EPL], r = 0.0;
   if (a.renorm) {
-    const double u = relative_weight(a, live, lx), total = wave_sum(u);
+    const double u = relative_weight(a, exp_neg, live, lx), total = wave_sum(u);
     const double q = live ? u / total : 0.0;
     // q_i sum_j q_j (dw_i - dw_j): no difference of nearly equal sums
     double v = 0.0;
     for (int j = 0; j < a.topk; ++j) v += read_lane(q, j) * (dw - read_lane(dw, j));
     d = q * v;
-    if (a.sigmoid) d *= sigmoid64(-static_cast<double>(lx));
+    if (a.sigmoid) d *= sigmoid64(exp_neg, -static_cast<double>(lx));
   } else if (a.sigmoid) {
-    d = live ? dw * sigmoid64(lx) * sigmoid64(-static_cast<double>(lx)) : 0.0;
+    d = live ? dw * sigmoid64(exp_neg, lx) * sigmoid64(exp_neg, -static_cast<double>(lx)) : 0.0;
   } else {
-    r = 1.0 / l.exps(p);
+    r = 1.0 / l.exps(exp_neg, p);
     d = live ? dw * exp_neg(static_cast<double>(lx) - static_cast<double>(l.top)) * r : 0.0;
     for (int j = 0; j < a.topk; ++j) s += read_lane(d, j);
   }
