@@ -9,6 +9,7 @@ If the shared library has not been built, every entry point raises; there is
 no fallback implementation.
 """
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional, Tuple
 
@@ -1011,10 +1012,10 @@ class Act8(NamedTuple):
         return self.codes.numel() + 4 * self.scales.numel()
 
 
-def _empty_act8(M, K, dev):
+def _new_act8(X, shape):
     import torch
-    return Act8(torch.empty((M, K), dtype=torch.int8, device=dev),
-                torch.empty((M, K // 64), dtype=torch.float32, device=dev))
+    return Act8(torch.empty_like(X, dtype=torch.int8),
+                X.new_empty((shape[0], shape[1] // 64), dtype=torch.float32))
 
 
 def _check_act8(x8, name, M=None, K=None):
@@ -1033,22 +1034,25 @@ def _check_act8(x8, name, M=None, K=None):
 
 
 def _matrix(t, name):
+    """The shape of a bf16 matrix."""
     import torch
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be two-dimensional")
-    _is(t, name, t.shape, torch.bfloat16)
-    return t.shape
+    if t.dtype is not torch.bfloat16 or not t.is_contiguous():
+        _need(t, name, shape, torch.bfloat16)
+    return shape
 
 
 def qlora_act8_pack(X, out: Optional[Act8] = None) -> Act8:
     """The 8-bit checkpoint of X (bf16 [M, K], K % 64 == 0): blocks of 64 values
     along a row, codes rint(x / c) with c = max |x| / 127."""
-    M, K = _matrix(X, "X")
+    M, K = shape = _matrix(X, "X")
     if K % 64:
         raise ValueError(f"K = {K} is not a multiple of 64")
     if out is None:
         dev = _one_gpu("X", X)
-        out = _empty_act8(M, K, dev)
+        out = _new_act8(X, shape)
     else:
         _check_act8(out, "out", M, K)
         dev = _one_gpu("X out.codes out.scales", X, out.codes, out.scales)
@@ -1060,10 +1064,11 @@ def qlora_act8_unpack(x8: Act8, out=None):
     """The values (bf16 [M, K]) of an 8-bit checkpoint."""
     import torch
     M, K = _check_act8(x8, "x8")
-    _maybe(out, "out", (M, K), torch.bfloat16)
+    if out is not None:
+        _is(out, "out", (M, K), torch.bfloat16)
     dev = _one_gpu("x8.codes x8.scales out", x8.codes, x8.scales, out)
     if out is None:
-        out = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(x8.codes, dtype=torch.bfloat16)
     _call("qlora_act8_unpack", dev, ctypes.byref(x8._c()), M, K, out.data_ptr())
     return out
 
@@ -1111,9 +1116,11 @@ def qlora_grouped_act8_bwd(dY, x8: Act8, offsets, w, E: int, A=None, B=None, s: 
 def _norm_weight(g, K):
     """1 if g [K] is fp32, 0 if bf16."""
     import torch
-    fp32 = g.dtype is torch.float32
-    _is(g, "g", (K,), torch.float32 if fp32 else torch.bfloat16)
-    return int(fp32)
+    if g.dtype is torch.float32:
+        _is(g, "g", (K,), torch.float32)
+        return 1
+    _is(g, "g", (K,), torch.bfloat16)
+    return 0
 
 
 def qlora_rms_norm_fwd(x, g, residual=None, eps: float = 1e-5, act8=False, h=None, y=None,
@@ -1123,36 +1130,44 @@ def qlora_rms_norm_fwd(x, g, residual=None, eps: float = 1e-5, act8=False, h=Non
     the 8-bit checkpoint of y too.  g is fp32 or bf16 [K]; h may be x or
     residual."""
     import torch
-    M, K = _matrix(x, "x")
+    M, K = shape = _matrix(x, "x")
     g32 = _norm_weight(g, K)
-    _maybe(residual, "residual", (M, K), torch.bfloat16)
-    if residual is None:
-        if h is not None and h is not x:
-            raise ValueError("without a residual h is x")
+    if residual is not None:
+        _is(residual, "residual", shape, torch.bfloat16)
+    elif h is None or h is x:
         h = x
     else:
-        _maybe(h, "h", (M, K), torch.bfloat16)
-    _maybe(y, "y", (M, K), torch.bfloat16)
-    _maybe(rstd, "rstd", (M,), torch.float32)
+        raise ValueError("without a residual h is x")
+    if h is not None:
+        _is(h, "h", shape, torch.bfloat16)
+    if y is not None:
+        _is(y, "y", shape, torch.bfloat16)
+    if rstd is not None:
+        _is(rstd, "rstd", (M,), torch.float32)
     keep = act8 is not False and act8 is not None
-    out = act8 if keep and act8 is not True else None
-    if keep and K % 64:
-        raise ValueError(f"K = {K} is not a multiple of 64")
-    if out is not None:
-        _check_act8(out, "act8", M, K)
-    dev = _one_gpu("x g residual h y rstd act8.codes act8.scales", x, g, residual, h, y, rstd,
-                   *(out if out is not None else (None, None)))
+    if keep:
+        if K % 64:
+            raise ValueError(f"K = {K} is not a multiple of 64")
+        if act8 is not True:
+            _check_act8(act8, "act8", M, K)
+    out = act8 if keep and act8 is not True else (None, None)
+    dev = _one_gpu("x g residual h y rstd act8.codes act8.scales", x, g, residual, h, y, rstd, *out)
     if h is None:
-        h = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        h = torch.empty_like(x)
     if y is None:
-        y = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        y = torch.empty_like(x)
     if rstd is None:
-        rstd = torch.empty(M, dtype=torch.float32, device=dev)
-    if keep and out is None:
-        out = _empty_act8(M, K, dev)
+        rstd = x.new_empty(M, dtype=torch.float32)
+    if keep and act8 is True:
+        out = _new_act8(x, shape)
     _call("qlora_rms_norm_fwd", dev, x.data_ptr(), _at(residual), g.data_ptr(), g32, M, K, eps,
           h.data_ptr(), y.data_ptr(), rstd.data_ptr(), ctypes.byref(out._c()) if keep else None)
     return (h, y, rstd, out) if keep else (h, y, rstd)
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_bwd_need(M, K):
+    return lib().qlora_rms_norm_bwd_workspace_bytes(M, K)
 
 
 def qlora_rms_norm_bwd(dy, h, rstd, g, dres=None, need_dg: bool = True, dx=None, dg=None,
@@ -1161,39 +1176,49 @@ def qlora_rms_norm_bwd(dy, h, rstd, g, dres=None, need_dg: bool = True, dx=None,
     residual, with dres, the gradient that reaches h from elsewhere, added; dg of
     g's type [K], or None without need_dg).  dx may be dres."""
     import torch
-    M, K = _matrix(h, "h")
+    M, K = shape = _matrix(h, "h")
     g32 = _norm_weight(g, K)
-    _is(dy, "dy", (M, K), torch.bfloat16)
+    _is(dy, "dy", shape, torch.bfloat16)
     _is(rstd, "rstd", (M,), torch.float32)
-    _maybe(dres, "dres", (M, K), torch.bfloat16)
-    _maybe(dx, "dx", (M, K), torch.bfloat16)
-    if not need_dg:
+    if dres is not None:
+        _is(dres, "dres", shape, torch.bfloat16)
+    if dx is not None:
+        _is(dx, "dx", shape, torch.bfloat16)
+    need = 0
+    if need_dg:
+        need = _norm_bwd_need(M, K)
+        if dg is not None:
+            _is(dg, "dg", (K,), g.dtype)
+    else:
         dg = None
-    _maybe(dg, "dg", (K,), g.dtype)
-    need = lib().qlora_rms_norm_bwd_workspace_bytes(M, K) if need_dg else 0
     dev = _one_gpu("h dy rstd g dres dx dg workspace", h, dy, rstd, g, dres, dx, dg, workspace)
-    workspace = _scratch(workspace, need, dev)
+    if need or workspace is not None:
+        workspace = _scratch(workspace, need, dev)
     if dx is None:
-        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        dx = torch.empty_like(h)
     if need_dg and dg is None:
-        dg = torch.empty(K, dtype=g.dtype, device=dev)
+        dg = torch.empty_like(g)
     _call("qlora_rms_norm_bwd", dev, dy.data_ptr(), _at(dres), h.data_ptr(), rstd.data_ptr(),
           g.data_ptr(), g32, M, K, dx.data_ptr(), _at(dg), _at(workspace), need)
     return dx, dg
 
 
-def _router(logits, topk, score, groups, top_groups, group_top, renorm, scale):
-    """(tokens, E, 1 for fp32 logits, the C configuration)."""
+def _logits(logits):
+    """(tokens, E, 1 for fp32 or 0 for bf16)."""
     import torch
-    if logits.dim() != 2:
+    shape = logits.shape
+    if len(shape) != 2:
         raise ValueError("logits must be [tokens, E]")
+    fp32 = logits.dtype is torch.float32
+    if not (fp32 or logits.dtype is torch.bfloat16) or not logits.is_contiguous():
+        _need(logits, "logits", shape, torch.float32 if fp32 else torch.bfloat16)
+    return shape[0], shape[1], 1 if fp32 else 0
+
+
+def _score(score):
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
-    fp32 = logits.dtype is torch.float32
-    _is(logits, "logits", logits.shape, torch.float32 if fp32 else torch.bfloat16)
-    return (*logits.shape, int(fp32),
-            _RouterConfig(SCORES[score], topk, groups, top_groups, group_top,
-                          1 if renorm else 0, scale))
+    return SCORES[score]
 
 
 def qlora_router_fwd(logits, topk: int, score: str = "softmax", bias=None, groups: int = 1,
@@ -1207,16 +1232,20 @@ def qlora_router_fwd(logits, topk: int, score: str = "softmax", bias=None, group
     weights by their sum.  Experts with a logit of -inf are not chosen; a slot
     left over has id -1 and weight 0."""
     import torch
-    tokens, E, fp32, cfg = _router(logits, topk, score, groups, top_groups, group_top, renorm,
-                                   scale)
-    _maybe(bias, "bias", (E,), torch.float32)
-    _maybe(ids, "ids", (tokens, topk), torch.int32)
-    _maybe(weights, "weights", (tokens, topk), torch.float32)
+    tokens, E, fp32 = _logits(logits)
+    cfg = _RouterConfig(_score(score), topk, groups, top_groups, group_top, 1 if renorm else 0,
+                        scale)
+    if bias is not None:
+        _is(bias, "bias", (E,), torch.float32)
+    if ids is not None:
+        _is(ids, "ids", (tokens, topk), torch.int32)
+    if weights is not None:
+        _is(weights, "weights", (tokens, topk), torch.float32)
     dev = _one_gpu("logits bias ids weights", logits, bias, ids, weights)
     if ids is None:
-        ids = torch.empty((tokens, max(topk, 0)), dtype=torch.int32, device=dev)
+        ids = logits.new_empty((tokens, max(topk, 0)), dtype=torch.int32)
     if weights is None:
-        weights = torch.empty((tokens, max(topk, 0)), dtype=torch.float32, device=dev)
+        weights = torch.empty_like(ids, dtype=torch.float32)
     _call("qlora_router_fwd", dev, logits.data_ptr(), fp32, tokens, E, _at(bias),
           ctypes.byref(cfg), ids.data_ptr(), weights.data_ptr())
     return ids, weights
@@ -1228,13 +1257,16 @@ def qlora_router_bwd(dweights, logits, ids, score: str = "softmax", renorm: bool
     weights (fp32 [tokens, topk]), the choice held fixed: ids, score, renorm and
     scale are those of qlora_router_fwd."""
     import torch
-    if ids.dim() != 2:
+    tokens, E, fp32 = _logits(logits)
+    shape = ids.shape
+    if len(shape) != 2:
         raise ValueError("ids must be [tokens, topk]")
-    topk = ids.shape[1]
-    tokens, E, fp32, cfg = _router(logits, topk, score, 1, 1, 1, renorm, scale)
+    topk = shape[1]
     _is(ids, "ids", (tokens, topk), torch.int32)
-    _is(dweights, "dweights", (tokens, topk), torch.float32)
-    _maybe(dlogits, "dlogits", logits.shape, logits.dtype)
+    _is(dweights, "dweights", shape, torch.float32)
+    if dlogits is not None:
+        _is(dlogits, "dlogits", logits.shape, logits.dtype)
+    cfg = _RouterConfig(_score(score), topk, 1, 1, 1, 1 if renorm else 0, scale)
     dev = _one_gpu("logits dweights ids dlogits", logits, dweights, ids, dlogits)
     if dlogits is None:
         dlogits = torch.empty_like(logits)
