@@ -105,10 +105,24 @@ __device__ __forceinline__ uint32_t max_over8(uint32_t v) {
   return dpp_max_u32<0x141>(max_over4(v));          // row_half_mirror
 }
 
-// Eight codes (two dwords) -> eight values as bf16 pairs.
+// Eight codes (two dwords) -> eight values as bf16 pairs.  With 128 added to a
+// code (its sign bit flipped) one instruction makes a byte a float, and one fma
+// takes 128 c off again: u c - 128 c is code c before its one rounding.  Where 128 c
+// overflows (a block whose largest value is the largest of bf16), the codes are
+// extended instead, an instruction more each.
 __device__ __forceinline__ u32x4 act8_values(uint32_t a, uint32_t b, float c) {
+  const float off = -128.f * c;
+  if (__builtin_amdgcn_ballot_w64(off == -__builtin_inff()) != 0) {
+    auto f = [&](uint32_t w, int i) {
+      return static_cast<float>(static_cast<int8_t>(w >> (8 * i))) * c;
+    };
+    return u32x4{pack_bf16x2(f(a, 0), f(a, 1)), pack_bf16x2(f(a, 2), f(a, 3)),
+                 pack_bf16x2(f(b, 0), f(b, 1)), pack_bf16x2(f(b, 2), f(b, 3))};
+  }
+  a ^= 0x80808080u;
+  b ^= 0x80808080u;
   auto f = [&](uint32_t w, int i) {
-    return static_cast<float>(static_cast<int8_t>(w >> (8 * i))) * c;
+    return fmaf(static_cast<float>((w >> (8 * i)) & 0xFFu), c, off);
   };
   return u32x4{pack_bf16x2(f(a, 0), f(a, 1)), pack_bf16x2(f(a, 2), f(a, 3)),
                pack_bf16x2(f(b, 0), f(b, 1)), pack_bf16x2(f(b, 2), f(b, 3))};

@@ -34,7 +34,7 @@ struct RankKind {
 
 // One product: tile (x, y) of C and reduction split z.  QP: the form of Q.
 template <class QP>
-struct RankJobOf {
+struct RankJobBase {
   OpParams po;
   QP qo;
   int ntiles, tps;
@@ -44,11 +44,21 @@ struct RankJobOf {
   const uint64_t* state;   // Q under the dropout mask: the generator's state
   uint32_t thr;            // and threshold
 };
+template <class QP>
+struct RankJobOf : RankJobBase<QP> {};
+// With X as a checkpoint, a product of one split goes to out (bf16 or fp32 [Q][P])
+// at once, scaled, without a reduction launch.
+template <>
+struct RankJobOf<Act8Params> : RankJobBase<Act8Params> {
+  void* out = nullptr;
+  float scale = 1.f;
+  bool out_bf16 = false;
+};
 using RankJob = RankJobOf<OpParams>;
 
 template <int BP, int BQ, class LP, class LQ, int HL>
-__device__ __forceinline__ void rank_tile(const RankJobOf<typename LQ::Par>& j, int x, int y, int z, uint16_t* lds,
-                                          int tid) {
+__device__ __forceinline__ void rank_tile(const RankJobOf<typename LQ::Par>& j, int x, int y,
+                                          int z, uint16_t* lds, int tid) {
   const int64_t p0 = (int64_t)x * BP, q0 = (int64_t)y * BQ;
   const int kt0 = z * j.tps, kt1 = min(j.ntiles, kt0 + j.tps);
   Mma<BP, BQ> mma;
@@ -57,6 +67,21 @@ __device__ __forceinline__ void rank_tile(const RankJobOf<typename LQ::Par>& j, 
   LQ lq{j.qo, q0};
   if constexpr (LQ::kDrop) lq.key = load_drop_key(j.state, j.thr);
   run_tiles<BP, BQ, HL, 2>(lp, lq, kt0, kt1, mma, lds, tid);
+  if constexpr (std::is_same_v<typename LQ::Par, Act8Params>) {
+    if (j.out) {
+      // (x + 0, then the scale: the bits of a reduction over one split)
+#pragma unroll
+      for (int a = 0; a < Mma<BP, BQ>::TP; ++a)
+#pragma unroll
+        for (int b = 0; b < Mma<BP, BQ>::TQ; ++b)
+          mma.acc[a][b] = (mma.acc[a][b] + f32x4{0.f, 0.f, 0.f, 0.f}) * j.scale;
+      if (j.out_bf16)
+        store_bf16(mma, static_cast<uint16_t*>(j.out), j.P, p0, q0, j.P, j.Q, tid);
+      else
+        store_f32(mma, static_cast<float*>(j.out), j.P, p0, q0, j.P, j.Q, tid);
+      return;
+    }
+  }
   store_f32(mma, j.ws + (int64_t)z * j.P * j.Q, j.P, p0, q0, j.P, j.Q, tid);
 }
 
@@ -462,11 +487,15 @@ hipError_t launch_lora_down_act8(const Act8View& x8, int64_t M, int64_t K, const
   const Split sp = choose_split(K, pt, qt);
   auto kern = d.on() ? k_rank<RB_R, RB_X, Bf16RedMajor<RB_R>, Act8Nat<RB_X, true>, 0>
                      : k_rank<RB_R, RB_X, Bf16RedMajor<RB_R>, Act8Nat<RB_X, false>, 0>;
+  auto j = job(op(A, r, r, K), act8_op(x8, K, M, K), sp, ws, r, M, pt, qt, d);
+  if (sp.splits == 1) {
+    j.out = T;
+    j.scale = d.scale();
+  }
   prof_begin(4, stream);
-  hipLaunchKernelGGL(kern, dim3(qt, pt, sp.splits), dim3(NT), 0, stream,
-                     job(op(A, r, r, K), act8_op(x8, K, M, K), sp, ws, r, M, pt, qt, d));
+  hipLaunchKernelGGL(kern, dim3(qt, pt, sp.splits), dim3(NT), 0, stream, j);
   hipError_t e = hipGetLastError();
-  if (e == hipSuccess) e = reduce<false>(ws, sp.splits, M * r, d.scale(), T, stream);
+  if (e == hipSuccess && sp.splits > 1) e = reduce<false>(ws, sp.splits, M * r, d.scale(), T, stream);
   prof_end(4, stream);
   return e;
 }
@@ -474,15 +503,20 @@ hipError_t launch_lora_down_act8(const Act8View& x8, int64_t M, int64_t K, const
 hipError_t launch_grad_a_act8(const Act8View& x8, int64_t M, int64_t K, const float* G, int r,
                               float s, uint16_t* dA, float* ws, hipStream_t stream,
                               const Drop& d) {
-  const int64_t pt = (r + RB_R - 1) / RB_R, qt = (K + RB_X - 1) / RB_X;
-  const Split sp = choose_split(M, pt, qt);
-  auto kern = d.on() ? k_rank<RB_R, RB_X, F32RedMajor<RB_R>, Act8RedMajor<RB_X, true>, 1>
-                     : k_rank<RB_R, RB_X, F32RedMajor<RB_R>, Act8RedMajor<RB_X, false>, 1>;
+  const Split sp = choose_split(M, (r + RB_R - 1) / RB_R, (K + RB_X - 1) / RB_X);
+  const int64_t pt = (r + RB_R - 1) / RB_R, qt = (K + RB_X8 - 1) / RB_X8;
+  auto kern = d.on() ? k_rank<RB_R, RB_X8, F32RedMajor<RB_R>, Act8RedMajor<RB_X8, true>, 1>
+                     : k_rank<RB_R, RB_X8, F32RedMajor<RB_R>, Act8RedMajor<RB_X8, false>, 1>;
+  auto j = job(op(G, r, r, M), act8_op(x8, K, K, M), sp, ws, r, K, pt, qt, d);
+  if (sp.splits == 1) {
+    j.out = dA;
+    j.scale = s * d.scale();
+    j.out_bf16 = true;
+  }
   prof_begin(4, stream);
-  hipLaunchKernelGGL(kern, dim3(qt, pt, sp.splits), dim3(NT), 0, stream,
-                     job(op(G, r, r, M), act8_op(x8, K, K, M), sp, ws, r, K, pt, qt, d));
+  hipLaunchKernelGGL(kern, dim3(qt, pt, sp.splits), dim3(NT), 0, stream, j);
   hipError_t e = hipGetLastError();
-  if (e == hipSuccess) e = reduce<true>(ws, sp.splits, K * r, s * d.scale(), dA, stream);
+  if (e == hipSuccess && sp.splits > 1) e = reduce<true>(ws, sp.splits, K * r, s * d.scale(), dA, stream);
   prof_end(4, stream);
   return e;
 }

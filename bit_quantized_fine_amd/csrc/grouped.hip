@@ -408,11 +408,11 @@ hipError_t launch_grouped_grad_a_act8(const Act8View& x8, int64_t M, const int* 
                                       int64_t K, const float* G, int r, float s, uint16_t* dA,
                                       float* ws, hipStream_t stream, const Drop& d) {
   const int sa = grad_splits(M, E, K, r);
-  const auto j = grad_job(op(G, r, r, M), act8_op(x8, K, K, M), offsets, E, M, r, K, RB_R, RB_X,
+  const auto j = grad_job(op(G, r, r, M), act8_op(x8, K, K, M), offsets, E, M, r, K, RB_R, RB_X8,
                           sa, s * d.scale(), dA, ws, d);
   auto kern = d.on()
-      ? k_group_grad<1, RB_R, RB_X, F32RedMajor<RB_R>, Act8RedMajor<RB_X, true>>
-      : k_group_grad<1, RB_R, RB_X, F32RedMajor<RB_R>, Act8RedMajor<RB_X, false>>;
+      ? k_group_grad<1, RB_R, RB_X8, F32RedMajor<RB_R>, Act8RedMajor<RB_X8, true>>
+      : k_group_grad<1, RB_R, RB_X8, F32RedMajor<RB_R>, Act8RedMajor<RB_X8, false>>;
   prof_begin(4, stream);
   hipLaunchKernelGGL(kern, dim3(j.px * j.qy * E * sa), dim3(NT), 0, stream, j);
   hipError_t e = hipGetLastError();

@@ -16,6 +16,7 @@ namespace qnf4 {
 constexpr int BK = 64;              // reduction elements per tile
 constexpr int LDS_STRIDE = BK + 8;  // bf16 per LDS row: 144 B, spreads rows over banks
 constexpr int NT = 256;             // threads per workgroup (4 waves)
+constexpr int RB_X8 = 64;           // columns of a tile of dA from a checkpoint
 
 struct OpParams {
   const void* ptr;
