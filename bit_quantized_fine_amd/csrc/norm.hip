@@ -54,8 +54,9 @@ struct NormBwd {
   int64_t M, K;
   uint16_t* dx;
   void* dg;                   // may be null
-  float* part;                // [parts][K] sums of dy n, or null: none or by columns
+  float* part;                // sums of dy n that a second launch adds up, or null
   int64_t row_blocks;         // workgroups for rows; the rest add up columns
+  int64_t run_rows;           // rows of a run of those
   int g_fp32;
 };
 
@@ -223,14 +224,20 @@ __global__ __launch_bounds__(row_threads<TPR>()) void k_rms_fwd(NormFwd a) {
 
 namespace {
 
-// Sums of dy n down 128 columns: 16 threads a row, 16 rows at a time.
+// Sums of dy n down 128 columns, of the rows from a run's first on: 16 threads a
+// row, THREADS / 16 rows at a time.  With more runs than one they go to part.
+template <int THREADS>
 __device__ __forceinline__ void dg_columns(const NormBwd& a, int64_t block, float* lds) {
-  const int t = threadIdx.x & 15, seg = threadIdx.x >> 4, segs = blockDim.x >> 4;
+  constexpr int segs = THREADS / 16;
+  const int t = threadIdx.x & 15, seg = threadIdx.x >> 4;
+  const int64_t ncols = (a.K + 127) / 128, run = block / ncols;
+  block -= run * ncols;
+  const int64_t r0 = run * a.run_rows, r1 = min(a.M, r0 + a.run_rows);
   const int64_t c = 128 * block + 8 * t;
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (c < a.K) {
 #pragma unroll 4
-    for (int64_t row = seg; row < a.M; row += segs) {
+    for (int64_t row = r0 + seg; row < r1; row += segs) {
       const F8 d = unpack8(ld8(a.dy + row * a.K + c)), h = unpack8(ld8(a.h + row * a.K + c));
       const float rstd = a.rstd[row];
 #pragma unroll
@@ -245,7 +252,9 @@ __device__ __forceinline__ void dg_columns(const NormBwd& a, int64_t block, floa
     float v = 0.f;
     for (int j = 0; j < segs; ++j)
       v += lds[(16 * j + (threadIdx.x >> 3)) * 9 + (threadIdx.x & 7)];
-    if (a.g_fp32)
+    if (a.part)
+      a.part[run * a.K + col] = v;
+    else if (a.g_fp32)
       static_cast<float*>(a.dg)[col] = v;
     else
       static_cast<uint16_t*>(a.dg)[col] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
@@ -274,11 +283,16 @@ template <int TPR, int P>
 __global__ __launch_bounds__(row_threads<TPR>()) void k_rms_bwd(NormBwd a) {
   constexpr int NTHR = row_threads<TPR>(), RPB = NTHR / TPR;
   __shared__ float red[2][TPR / 64];
-  __shared__ float cols[256 * 9];
+  // for the sums of columns, or of the waves that take a row each
+  constexpr int kWaveSums = RPB > 1 ? RPB * 512 * P : 0;
+  __shared__ __attribute__((aligned(16))) float
+      cols[P == 0 ? 1 : (kWaveSums > NTHR * 9 ? kWaveSums : NTHR * 9)];
   const int64_t block = block_index();
-  if (block >= a.row_blocks) {   // uniform
-    if constexpr (NTHR == 256) dg_columns(a, block - a.row_blocks, cols);
-    return;
+  if constexpr (P > 0) {
+    if (block >= a.row_blocks) {   // uniform
+      dg_columns<NTHR>(a, block - a.row_blocks, cols);
+      return;
+    }
   }
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const F8 zero{};
@@ -288,44 +302,73 @@ __global__ __launch_bounds__(row_threads<TPR>()) void k_rms_bwd(NormBwd a) {
     for (int p = 0; p < P; ++p)
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[p][i] = 0.f;
-    int turn = 0;
-    for (int64_t row = block * RPB + sub; row < a.M; row += a.row_blocks * RPB, turn ^= 1) {
+    // the next row's loads are on their way while this one is summed and written
+    struct Row {
       u32x4 h[P], dy[P], dr[P];
-      const float rstd = a.rstd[row];
+      float rstd;
+    };
+    auto load = [&](Row& v, int64_t row) {
+      v.rstd = a.rstd[row];
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int64_t c = 8 * (p * TPR + t), i = row * a.K + c;
         const bool in = c < a.K;
-        h[p] = in ? ld8(a.h + i) : u32x4{0, 0, 0, 0};
-        dy[p] = in ? ld8(a.dy + i) : u32x4{0, 0, 0, 0};
-        dr[p] = in && a.dres ? ld8(a.dres + i) : u32x4{0, 0, 0, 0};
+        v.h[p] = in ? ld8(a.h + i) : u32x4{0, 0, 0, 0};
+        v.dy[p] = in ? ld8(a.dy + i) : u32x4{0, 0, 0, 0};
+        v.dr[p] = in && a.dres ? ld8(a.dres + i) : u32x4{0, 0, 0, 0};
       }
+    };
+    const int64_t step = a.row_blocks * RPB;
+    int64_t row = block * RPB + sub;
+    Row now, next;
+    if (row < a.M) load(now, row);
+    for (int turn = 0; row < a.M; row += step, turn ^= 1) {
+      if (row + step < a.M) load(next, row + step);
       float s = 0.f;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int64_t c = 8 * (p * TPR + t);
-        if (c < a.K) s = norm_dot(unpack8(h[p]), unpack8(dy[p]), load_g(a.g, a.g_fp32, c), rstd, s);
+        if (c < a.K)
+          s = norm_dot(unpack8(now.h[p]), unpack8(now.dy[p]), load_g(a.g, a.g_fp32, c), now.rstd, s);
       }
       const float mean = row_sum<TPR>(s, red[turn]) / static_cast<float>(a.K);
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int64_t c = 8 * (p * TPR + t);
         if (c >= a.K) continue;
-        const F8 fh = unpack8(h[p]), fd = unpack8(dy[p]);
+        const F8 fh = unpack8(now.h[p]), fd = unpack8(now.dy[p]);
         st8(a.dx + row * a.K + c,
-            norm_dx(fh, fd, load_g(a.g, a.g_fp32, c), rstd, mean, unpack8(dr[p])));
+            norm_dx(fh, fd, load_g(a.g, a.g_fp32, c), now.rstd, mean, unpack8(now.dr[p])));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[p][i] = fmaf(fd.v[i], fh.v[i] * rstd, acc[p][i]);
+        for (int i = 0; i < 8; ++i)
+          acc[p][i] = fmaf(fd.v[i], fh.v[i] * now.rstd, acc[p][i]);
       }
+      now = next;
     }
     if (a.part) {
-      float* out = a.part + (block * RPB + sub) * a.K;
+      float* out = a.part + block * a.K;
+      if constexpr (RPB > 1) {   // the rows' waves, added up in order
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int64_t c = 8 * (p * TPR + t);
-        if (c >= a.K) continue;
-        *reinterpret_cast<f32x4*>(out + c) = f32x4{acc[p][0], acc[p][1], acc[p][2], acc[p][3]};
-        *reinterpret_cast<f32x4*>(out + c + 4) = f32x4{acc[p][4], acc[p][5], acc[p][6], acc[p][7]};
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int i = 0; i < 8; i += 4)
+            *reinterpret_cast<f32x4*>(cols + 8 * (p * TPR + t) + i + sub * 512 * P) =
+                f32x4{acc[p][i], acc[p][i + 1], acc[p][i + 2], acc[p][i + 3]};
+        __syncthreads();
+        for (int c = 4 * threadIdx.x; c < a.K; c += 4 * NTHR) {
+          f32x4 v = *reinterpret_cast<const f32x4*>(cols + c);
+#pragma unroll
+          for (int w = 1; w < RPB; ++w) v += *reinterpret_cast<const f32x4*>(cols + c + w * 512 * P);
+          *reinterpret_cast<f32x4*>(out + c) = v;
+        }
+      } else {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const int64_t c = 8 * (p * TPR + t);
+          if (c >= a.K) continue;
+          *reinterpret_cast<f32x4*>(out + c) = f32x4{acc[p][0], acc[p][1], acc[p][2], acc[p][3]};
+          *reinterpret_cast<f32x4*>(out + c + 4) = f32x4{acc[p][4], acc[p][5], acc[p][6], acc[p][7]};
+        }
       }
     }
   } else {
@@ -347,33 +390,39 @@ __global__ __launch_bounds__(row_threads<TPR>()) void k_rms_bwd(NormBwd a) {
 // Whole columns alone, for rows too long for the kernel above to add them up.
 __global__ __launch_bounds__(256) void k_rms_dg_columns(NormBwd a) {
   __shared__ float cols[256 * 9];
-  dg_columns(a, block_index(), cols);
+  dg_columns<256>(a, block_index(), cols);
 }
 
-// dg[c] = sum_p part[p][c]: 64 columns a workgroup, 16 runs of the parts, four
+// dg[c] = sum_p part[p][c]: 64 columns a workgroup, 64 runs of the parts, four
 // columns a thread.
-__global__ __launch_bounds__(256) void k_rms_dg(const float* part, int64_t parts, int64_t K,
-                                                void* dg, int g_fp32) {
-  __shared__ f32x4 sums[16][17];
+__global__ __launch_bounds__(1024) void k_rms_dg(const float* part, int64_t parts, int64_t K,
+                                                 void* dg, int g_fp32) {
+  __shared__ f32x4 sums[64][17];
   const int t = threadIdx.x & 15, seg = threadIdx.x >> 4;
   const int64_t c = 64 * (int64_t)blockIdx.x + 4 * t;
-  const int64_t per = (parts + 15) / 16, p0 = seg * per, p1 = min(parts, p0 + per);
+  const int64_t per = (parts + 63) / 64, p0 = min(parts, seg * per), p1 = min(parts, p0 + per);
   f32x4 s = {0.f, 0.f, 0.f, 0.f};
   if (c < K) {
-#pragma unroll 8
+#pragma unroll 4
     for (int64_t p = p0; p < p1; ++p) s += *reinterpret_cast<const f32x4*>(part + p * K + c);
   }
   sums[seg][t] = s;
   __syncthreads();
-  if (seg == 0 && c < K) {
-    f32x4 v = sums[0][t];
+  if (seg < 8) {
 #pragma unroll
-    for (int j = 1; j < 16; ++j) v += sums[j][t];
+    for (int j = 8; j < 64; j += 8) s += sums[seg + j][t];
+  }
+  __syncthreads();
+  if (seg < 8) sums[seg][t] = s;
+  __syncthreads();
+  if (seg == 0 && c < K) {
+#pragma unroll
+    for (int j = 1; j < 8; ++j) s += sums[j][t];
     if (g_fp32)
-      *reinterpret_cast<f32x4*>(static_cast<float*>(dg) + c) = v;
+      *reinterpret_cast<f32x4*>(static_cast<float*>(dg) + c) = s;
     else
       *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(dg) + c) =
-          u32x2{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+          u32x2{pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w)};
   }
 }
 
@@ -403,26 +452,37 @@ void fwd(const NormFwd& a, hipStream_t st) {
   hipLaunchKernelGGL((k_rms_fwd<TPR, P>), grid_of(cdiv(a.M, n / TPR)), dim3(n), 0, st, a);
 }
 
-// Of the backward: threads a row, rows a workgroup takes at a time, and the
-// workgroups whose sums a second launch adds up (0: columns in the same launch).
+// Of the backward: workgroups for rows; how many sums of rows a second launch adds
+// up (0: none); the rows of a run down the columns (0: none).
 struct BwdPlan {
-  int tpr;
-  int64_t row_blocks, parts;
+  int64_t row_blocks, parts, run_rows;
 };
+constexpr int64_t kLongRowBwd = 16384;   // more than this: read twice
+int bwd_threads(int64_t K) { return K <= 2048 ? 256 : (K <= 4096 ? 512 : 1024); }
+
 BwdPlan plan_bwd(int64_t M, int64_t K, bool dg) {
-  BwdPlan p;
-  p.tpr = K <= 1024 ? 64 : (K <= 16384 ? 256 : 1024);
-  const int rows = p.tpr == 64 ? 4 : 1;
-  const int64_t blocks = cdiv(M, rows);
-  p.row_blocks = blocks;
-  p.parts = 0;
-  // By columns, dy and h are read twice; with sums of the workgroups, those are
-  // written and read, and there is a second launch.
-  if (dg && K <= kLongRow && M * K > (int64_t(1) << 21)) {
-    p.row_blocks = std::min<int64_t>(blocks, 512);
-    p.parts = p.row_blocks * rows;
+  BwdPlan p{cdiv(M, K <= 1024 ? 4 : 1), 0, 0};
+  if (!dg) return p;
+  if (K > kLongRowBwd) {
+    // columns in a launch of their own, in runs of rows that fill the GPU
+    const int64_t runs = std::max<int64_t>(1, std::min(M / 64, 1024 / cdiv(K, 128)));
+    p.run_rows = std::max<int64_t>(1, cdiv(M, runs));
+    p.parts = runs > 1 ? cdiv(M, p.run_rows) : 0;
+  } else if (M > 1024 || (M > 512 && M * K > (int64_t(1) << 22))) {
+    // Adding up columns reads dy and h twice, where sums of the workgroups are written
+    // and read and take a second launch (512 x 8192: columns 12.9 us, sums 16.0; 1024 x
+    // 4096: 15.0 and 16.3; 1024 x 8192: 23.1 and 19.9).  16 waves a CU: enough loads in
+    // flight, and the fewest sums (4096 x 8192: 57 us with 256 workgroups of 1024
+    // threads, 63 with 512, 61 with 512 of 512).
+    p.row_blocks = std::min<int64_t>(p.row_blocks, 256 * (1024 / bwd_threads(K)));
+    p.parts = p.row_blocks;
+  } else {
+    p.run_rows = std::max<int64_t>(1, M);
   }
   return p;
+}
+size_t bwd_need(const BwdPlan& p, int64_t K) {
+  return static_cast<size_t>(p.parts) * K * sizeof(float);
 }
 
 template <int TPR, int P>
@@ -469,7 +529,7 @@ int qlora_rms_norm_fwd(const uint16_t* x, const uint16_t* residual, const void* 
 
 size_t qlora_rms_norm_bwd_workspace_bytes(int64_t M, int64_t K) {
   if (check_norm(M, K) || M == 0) return 0;
-  return static_cast<size_t>(plan_bwd(M, K, true).parts) * K * sizeof(float);
+  return bwd_need(plan_bwd(M, K, true), K);
 }
 
 int qlora_rms_norm_bwd(const uint16_t* dy, const uint16_t* dres, const uint16_t* h,
@@ -483,34 +543,32 @@ int qlora_rms_norm_bwd(const uint16_t* dy, const uint16_t* dres, const uint16_t*
       !aligned16(dx) || !aligned16(dg))
     return QLORA_ERR_ALIGN;
   const BwdPlan p = plan_bwd(M, K, dg != nullptr);
-  const size_t need = static_cast<size_t>(p.parts) * K * sizeof(float);
+  const size_t need = bwd_need(p, K);
   if (need > 0 && (!workspace || workspace_bytes < need)) return QLORA_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return QLORA_ERR_ALIGN;
-  if (M == 0 && !dg) return QLORA_OK;
   const hipStream_t hs = static_cast<hipStream_t>(stream);
-  const NormBwd a{dy, dres, h, rstd, g, M, K, dx, dg, p.parts > 0 ? static_cast<float*>(workspace)
-                  : nullptr, p.row_blocks, g_fp32 != 0};
-  // columns in the same launch, where its workgroups are of 256 threads
-  const int64_t cols = dg && p.parts == 0 ? cdiv(K, 128) : 0;
-  const int64_t n = p.row_blocks + (p.tpr <= 256 ? cols : 0);
+  const NormBwd a{dy, dres, h, rstd, g, M, K, dx, dg,
+                  p.parts > 0 ? static_cast<float*>(workspace) : nullptr, p.row_blocks, p.run_rows,
+                  g_fp32 != 0};
+  const bool wide = K > kLongRowBwd;
+  const int64_t cols = p.run_rows > 0 ? cdiv(K, 128) * std::max<int64_t>(1, p.parts) : 0;
+  const int64_t n = p.row_blocks + (wide ? 0 : cols);
   hipError_t e = hipSuccess;
   if (n > 0) {
     if (K <= 512) e = bwd<64, 1>(a, n, hs);
     else if (K <= 1024) e = bwd<64, 2>(a, n, hs);
     else if (K <= 2048) e = bwd<256, 1>(a, n, hs);
-    else if (K <= 4096) e = bwd<256, 2>(a, n, hs);
-    else if (K <= 8192) e = bwd<256, 4>(a, n, hs);
-    else if (K <= 16384) e = bwd<256, 8>(a, n, hs);
-    else if (K <= 32768) e = bwd<1024, 4>(a, n, hs);
-    else if (K <= kLongRow) e = bwd<1024, 8>(a, n, hs);
+    else if (K <= 4096) e = bwd<512, 1>(a, n, hs);
+    else if (K <= 8192) e = bwd<1024, 1>(a, n, hs);
+    else if (!wide) e = bwd<1024, 2>(a, n, hs);
     else e = bwd<1024, 0>(a, n, hs);
   }
-  if (e == hipSuccess && p.tpr > 256 && cols > 0) {
+  if (e == hipSuccess && wide && cols > 0) {
     hipLaunchKernelGGL(k_rms_dg_columns, grid_of(cols), dim3(256), 0, hs, a);
     e = hipGetLastError();
   }
   if (e == hipSuccess && p.parts > 0) {
-    hipLaunchKernelGGL(k_rms_dg, dim3(static_cast<unsigned>(cdiv(K, 64))), dim3(256), 0, hs,
+    hipLaunchKernelGGL(k_rms_dg, dim3(static_cast<unsigned>(cdiv(K, 64))), dim3(1024), 0, hs,
                        a.part, p.parts, K, dg, g_fp32 != 0);
     e = hipGetLastError();
   }

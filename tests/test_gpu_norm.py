@@ -65,7 +65,8 @@ def test_forward(M, K, res, g32):
 
 @pytest.mark.parametrize("M,K", SIZES + [(0, 64), (300, 64), (1000, 1024), (700, 3000),
                                          (4099, 520), (300, 8192), (140, 16384), (60, 40000),
-                                         (40, 66000)])
+                                         (40, 66000), (300, 17000), (1100, 512), (1500, 1024),
+                                         (1030, 2400), (1100, 4104), (1025, 16384), (130, 65544)])
 @pytest.mark.parametrize("res,g32", [(True, False), (False, True)])
 def test_backward(M, K, res, g32):
     need_gpu()
@@ -185,7 +186,7 @@ def test_streams_graph_and_workspaces():
     calls between their replays."""
     need_gpu()
     say("norm in graphs")
-    M, K = 600, 4096     # sums of workgroups in a workspace
+    M, K = 1200, 4096    # sums of workgroups in a workspace
     x, r = torch.randn(M, K, device=dev()).bfloat16(), torch.randn(M, K, device=dev()).bfloat16()
     dy, g = torch.randn(M, K, device=dev()).bfloat16(), torch.rand(K, device=dev()) + 0.5
     ws = torch.full((q.lib().qlora_rms_norm_bwd_workspace_bytes(M, K),), 0xFF, dtype=torch.uint8,
