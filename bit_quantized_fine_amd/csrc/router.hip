@@ -44,8 +44,8 @@ struct Router {
   int groups, top_groups, group_top;
   int gs;                 // experts of a group
   uint32_t gs_mul;        // e / gs = e gs_mul >> 20
-  int gshift;             // log2 of the lanes that share a group in LDS
-  int glanes;             // lanes that hold one whole group each, or 0
+  int gshift;             // log2 of the lanes that look at one group
+  int in_lanes;           // those lanes hold the whole group (at most 16)
   int* ids;
   float* weights;
   const float* dweights;
@@ -162,37 +162,52 @@ __device__ __forceinline__ double sigmoid64(const Exp& exp_neg, double x) {
   return (x > 0.0 ? 1.0 : t) / (1.0 + t);
 }
 
+// EPL values from element e0 on, `none` past E.  Where E is whole pieces of a lane,
+// a piece is one load (rows then start at a multiple of four bytes).
+template <int EPL, class L>
+__device__ __forceinline__ void load_piece(const L* row, int e0, int E, float none, float* x) {
+  if (E % EPL == 0) {
+    L v[EPL];
+    const int at = e0 < E ? e0 : 0;
+    if constexpr (EPL * sizeof(L) >= 4) {
+      __builtin_memcpy(v, __builtin_assume_aligned(row + at, 4), sizeof(v));
+    } else {
+      v[0] = row[at];
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) x[i] = e0 < E ? to_f32(v[i]) : none;
+  } else {
+    L v[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) v[i] = row[e0 + i < E ? e0 + i : 0];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) x[i] = e0 + i < E ? to_f32(v[i]) : none;
+  }
+}
+
 // A token's logits: lane l holds experts l EPL ...; -inf past E.
 template <int EPL, class L>
 struct Logits {
   float x[EPL];
-  float top;    // the largest, -inf without any
   bool bad;     // a NaN or +inf among them
   __device__ void load(const L* row, int E, int lane) {
+    load_piece<EPL, L>(row, lane * EPL, E, -__builtin_inff(), x);
+    uint64_t b = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)   // signalling and quiet NaN, +inf
+      b |= __builtin_amdgcn_ballot_w64(__builtin_amdgcn_classf(x[i], 0x203));
+    bad = b != 0;
+  }
+  // the largest, -inf without any
+  __device__ float top() const {
     uint32_t k = 0;
-    bool b = false;
-    const int e0 = lane * EPL;
-    if (E % EPL == 0) {   // a lane's experts are one aligned piece, whole or absent
-      constexpr int kAlign = EPL * sizeof(L) < 16 ? EPL * sizeof(L) : 16;
-      L v[EPL];
-      if (e0 < E) __builtin_memcpy(v, __builtin_assume_aligned(row + e0, kAlign), sizeof(v));
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) x[i] = e0 < E ? to_f32(v[i]) : -__builtin_inff();
-    } else {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) x[i] = e0 + i < E ? to_f32(row[e0 + i]) : -__builtin_inff();
-    }
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      b |= !(x[i] < __builtin_inff());
-      k = max(k, order_key(x[i]));
-    }
-    bad = __builtin_amdgcn_ballot_w64(b) != 0;
+    for (int i = 0; i < EPL; ++i) k = max(k, order_key(x[i]));
     k = wave_max(k);
-    top = k ? key_value(k) : -__builtin_inff();
+    return k ? key_value(k) : -__builtin_inff();
   }
   // sum over the experts of exp(x - top), which this lane's d[i] receive
-  __device__ double exps(const Exp& exp_neg, double* d) const {
+  __device__ double exps(const Exp& exp_neg, float top, double* d) const {
     double s = 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -224,11 +239,11 @@ __device__ __forceinline__ int best_lane(uint64_t k) {
 }
 
 // The topk largest keys in order: lane j gets the expert of slot j, -1 if none is
-// left.  Up to eight keys a lane are sorted first, so that a round only moves the
+// left; *left: the largest key after them (0: none).  Up to eight keys a lane are sorted first, so that a round only moves the
 // winner's up: neighbours change places where the second is larger, which
 // leaves equal ones in their order.
 template <int EPL, class Key>
-__device__ __forceinline__ int choose(Key* k, int topk, int lane) {
+__device__ __forceinline__ int choose(Key* k, int topk, int lane, Key* left = nullptr) {
   int id = -1;
   if constexpr (EPL <= 8) {
     int at[EPL];
@@ -260,6 +275,7 @@ __device__ __forceinline__ int choose(Key* k, int topk, int lane) {
         k[EPL - 1] = 0;
       }
     }
+    if (left) *left = wave_max(k[0]);
   } else {
     Key cur = k[0];
 #pragma unroll
@@ -285,6 +301,7 @@ __device__ __forceinline__ int choose(Key* k, int topk, int lane) {
       e = read_lane(e, who);
       if (lane == j) id = e;
     }
+    if (left) *left = wave_max(cur);
   }
   return id;
 }
@@ -297,7 +314,18 @@ __device__ __forceinline__ void merge_two(double& t1, double& t2) {
   t2 = max(min(t1, o1), max(t2, o2));
   t1 = max(t1, o1);
 }
-__device__ __forceinline__ void two_best_of_lanes(double& t1, double& t2, int lanes) {
+template <int CTRL>
+__device__ __forceinline__ void merge_two(uint32_t& t1, uint32_t& t2) {
+  auto moved = [](uint32_t v) {
+    return static_cast<uint32_t>(
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, false));
+  };
+  const uint32_t o1 = moved(t1), o2 = moved(t2);
+  t2 = max(min(t1, o1), max(t2, o2));
+  t1 = max(t1, o1);
+}
+template <class T>
+__device__ __forceinline__ void two_best_of_lanes(T& t1, T& t2, int lanes) {
   if (lanes > 1) merge_two<0xB1>(t1, t2);    // quad_perm 1,0,3,2
   if (lanes > 2) merge_two<0x4E>(t1, t2);    // quad_perm 2,3,0,1
   if (lanes > 4) merge_two<0x141>(t1, t2);   // row_half_mirror
@@ -314,6 +342,93 @@ __device__ __forceinline__ double relative_weight(const Router& a, const Exp& ex
   if (!live) return 0.0;
   const double u = exp_neg(static_cast<double>(v) - static_cast<double>(m));
   return a.sigmoid ? u / (1.0 + exp_neg(-fabs(static_cast<double>(lx)))) : u;
+}
+
+// sigma(x) in 32 bits, off by less than 2^-21: t = exp(-|x|) is off by 2.6 2^-24
+// (the product's rounding times |x| t <= 0.37, the exponential's last place), and 1 +
+// t, its reciprocal and the product by 4 2^-24 of the result.
+__device__ __forceinline__ float sigmoid32(float x) {
+  const float t = __builtin_amdgcn_exp2f(fabsf(x) * -1.442695041f);
+  const float s = __builtin_amdgcn_rcpf(1.f + t);
+  return x > 0.f ? s : t * s;
+}
+
+// The choice by sigmoid and bias through 32 bits, with what it proves.  A rank r in
+// 32 bits is off by less than 2^-20 (1 + |r|); as that keeps the order of the
+// bounds, the nth largest rank is off by as much.  Groups and experts are chosen by
+// 32 bits; the chosen ones' ranks are then formed in 64, one a lane.  The choice
+// stands if no group at the border could change sides, every chosen rank is above
+// the best one left by more than that one's error, and they descend (equal ones by
+// index): then it is the one that 64 bits make.  Else (about one token in 10^3 of 256
+// experts) false: the choice is made anew.  For tokens without NaN and +inf, and
+// groups within lanes.  id and p: of this lane's slot, p in 64 bits.
+template <int EPL, class L>
+__device__ __forceinline__ bool choose_by_32(const Router& a, const Exp& exp_neg, const float* x,
+                                             const L* row, int lane, int& id, double& p) {
+  constexpr float kErr = 0x1p-20f;
+  float b[EPL];
+  load_piece<EPL, float>(a.bias, lane * EPL, a.E, 0.f, b);
+  uint32_t k[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const float v = sigmoid32(x[i]) + b[i];
+    k[i] = x[i] > -__builtin_inff() ? order_key(v) : 0u;   // (0 for NaN too)
+  }
+  if (a.choose_groups) {
+    uint32_t t1 = k[0], t2 = 0;
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) {
+      t2 = max(t2, min(t1, k[i]));
+      t1 = max(t1, k[i]);
+    }
+    const int lanes = 1 << a.gshift, g = lane >> a.gshift, sub = lane & (lanes - 1);
+    two_best_of_lanes(t1, t2, lanes);
+    const bool any = t1 != 0 && g < a.groups, both = a.group_top == 2 && t2 != 0;
+    const float v1 = key_value(t1), v2 = both ? key_value(t2) : 0.f;
+    // twice the errors of the two ranks, for the additions here
+    const float off = 2.f * kErr * (2.f + fabsf(v1) + fabsf(v2));
+    const float hi = any ? v1 + v2 + off : -__builtin_inff();
+    const float lo = any ? v1 + v2 - off : -__builtin_inff();
+    int sure, perhaps;   // groups ahead of this lane's
+    if (lanes >= a.groups) {   // each of a group's lanes looks at one other group
+      const float oh = __shfl(hi, sub << a.gshift), ol = __shfl(lo, sub << a.gshift);
+      const bool other = sub < a.groups && sub != g;
+      const uint32_t s = static_cast<uint32_t>(
+          __builtin_amdgcn_ballot_w64(other && ol > hi) >> (g << a.gshift));
+      const uint32_t m = static_cast<uint32_t>(
+          __builtin_amdgcn_ballot_w64(other && !(oh < lo)) >> (g << a.gshift));
+      const uint32_t mine = (1u << lanes) - 1;   // (lanes <= 16)
+      sure = __builtin_popcount(s & mine);
+      perhaps = __builtin_popcount(m & mine);
+    } else {
+      sure = perhaps = 0;
+      for (int q = 0; q < a.groups; ++q) {
+        sure += read_lane(lo, q << a.gshift) > hi;
+        perhaps += q != g && !(read_lane(hi, q << a.gshift) < lo);
+      }
+    }
+    const bool stays = any && perhaps < a.top_groups;
+    if (__builtin_amdgcn_ballot_w64(any && !stays && sure < a.top_groups) != 0) return false;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) k[i] = stays ? k[i] : 0u;
+  }
+  uint32_t left;
+  id = choose<EPL, uint32_t>(k, a.topk, lane, &left);
+  const bool live = id >= 0;
+  p = 0.0;
+  double rank = -__builtin_inf();
+  if (live) {
+    p = sigmoid64(exp_neg, static_cast<double>(to_f32(row[id])));
+    rank = p + static_cast<double>(a.bias[id]);
+  }
+  const float best_left = key_value(left);
+  bool wrong = live && left != 0 &&
+               !(rank > static_cast<double>(best_left) +
+                            static_cast<double>(kErr) * (1.0 + fabs(static_cast<double>(best_left))));
+  const double next = __shfl_down(rank, 1);
+  const int next_id = __shfl_down(id, 1);
+  wrong |= lane < 63 && next_id >= 0 && !(rank > next || (rank == next && id < next_id));
+  return __builtin_amdgcn_ballot_w64(wrong) == 0;
 }
 
 __device__ __forceinline__ int64_t wave_token() {
@@ -334,6 +449,27 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_fwd(Router a) {
   l.load(static_cast<const L*>(a.logits) + t * a.E, a.E, lane);
 
   const Exp exp_neg;
+  auto store = [&](int id, double w) {
+    if (in && lane < a.topk) {
+      a.ids[t * a.topk + lane] = id;
+      a.weights[t * a.topk + lane] =
+          l.bad && id >= 0 ? __builtin_nanf("")
+                           : static_cast<float>(static_cast<double>(a.scale) * w);
+    }
+  };
+  if (a.bias && a.sigmoid && !l.bad && (!a.choose_groups || a.in_lanes)) {   // uniform
+    int id;
+    double p;
+    if (choose_by_32<EPL, L>(a, exp_neg, l.x, static_cast<const L*>(a.logits) + t * a.E, lane, id,
+                             p)) {
+      const double total = a.renorm ? wave_sum(p) : 1.0;
+      if (total > 1e-250) {   // (else every chosen logit is below about -575)
+        store(id, p / total);
+        return;
+      }
+    }
+  }
+  float top = 0.f;
   double p[EPL], sum = 0.0;   // p: scores where they rank, exps otherwise unused
   const bool sums = a.choose_groups && a.group_top == 2;
   if (a.bias || sums) {
@@ -341,7 +477,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_fwd(Router a) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) p[i] = sigmoid64(exp_neg, l.x[i]);
     } else {
-      sum = l.exps(exp_neg, p);
+      top = l.top();
+      sum = l.exps(exp_neg, top, p);
       const double r = sum > 0.0 ? 1.0 / sum : 0.0;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) p[i] *= r;
@@ -370,18 +507,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_fwd(Router a) {
       t2 = max(t2, min(t1, u));
       t1 = max(t1, u);
     };
-    int g, sub, lanes;   // this lane's group, its place among the group's lanes, their number
-    if (a.glanes) {
-      lanes = a.glanes;
-      g = lane / lanes;
-      sub = lane & (lanes - 1);
+    // this lane's group, its place among the group's lanes, their number
+    const int lanes = 1 << a.gshift, g = lane >> a.gshift, sub = lane & (lanes - 1);
+    if (a.in_lanes) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) add(v[i]);
       two_best_of_lanes(t1, t2, lanes);
     } else {
-      lanes = 1 << a.gshift;
-      g = lane >> a.gshift;
-      sub = lane & (lanes - 1);
       double* mine = lds + (int64_t)wave_id() * a.E;
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
@@ -398,21 +530,21 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_fwd(Router a) {
     const double score = a.group_top == 2 && t2 > -__builtin_inf() ? t1 + t2 : t1;
     int better = 0;   // groups ahead of this lane's
     if (lanes >= a.groups) {   // each of a group's lanes looks at one other group
-      const double o = __shfl(score, sub * lanes);
+      const double o = __shfl(score, sub << a.gshift);
       const uint64_t ahead = __builtin_amdgcn_ballot_w64(
           sub < a.groups && (o > score || (o == score && sub < g)));
       better = __builtin_popcountll((ahead >> (lane - sub)) & ((2ull << (lanes - 1)) - 1));
     } else {
       for (int q = 0; q < a.groups; ++q) {
-        const double o = read_lane(score, q * lanes);
+        const double o = read_lane(score, q << a.gshift);
         better += o > score || (o == score && q < g);
       }
     }
     mine_stay = g < a.groups && t1 > -__builtin_inf() && better < a.top_groups;
-    if (!a.glanes) keep = __builtin_amdgcn_ballot_w64(mine_stay && sub == 0);
+    if (!a.in_lanes) keep = __builtin_amdgcn_ballot_w64(mine_stay && sub == 0);
   }
   auto stays = [&](int i) {
-    if (!a.choose_groups || a.glanes) return mine_stay;
+    if (!a.choose_groups || a.in_lanes) return mine_stay;
     const int e = lane * EPL + i;
     return e < a.E && ((keep >> (((e * a.gs_mul) >> 20) << a.gshift)) & 1) != 0;
   };
@@ -439,14 +571,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_fwd(Router a) {
   } else if (a.sigmoid) {
     w = live ? sigmoid64(exp_neg, lx) : 0.0;
   } else {
-    if (sum == 0.0) sum = l.exps(exp_neg, p);
-    w = live ? exp_neg(static_cast<double>(lx) - static_cast<double>(l.top)) / sum : 0.0;
+    if (sum == 0.0) {
+      top = l.top();
+      sum = l.exps(exp_neg, top, p);
+    }
+    w = live ? exp_neg(static_cast<double>(lx) - static_cast<double>(top)) / sum : 0.0;
   }
-  if (in && lane < a.topk) {
-    a.ids[t * a.topk + lane] = id;
-    a.weights[t * a.topk + lane] =
-        l.bad && live ? __builtin_nanf("") : static_cast<float>(static_cast<double>(a.scale) * w);
-  }
+  store(id, w);
 }
 
 // dlogits of one token.  Lane j holds slot j; sums over the slots run in their
@@ -487,8 +618,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_bwd(Router a) {
   } else if (a.sigmoid) {
     d = live ? dw * sigmoid64(exp_neg, lx) * sigmoid64(exp_neg, -static_cast<double>(lx)) : 0.0;
   } else {
-    r = 1.0 / l.exps(exp_neg, p);
-    d = live ? dw * exp_neg(static_cast<double>(lx) - static_cast<double>(l.top)) * r : 0.0;
+    const float top = l.top();
+    r = 1.0 / l.exps(exp_neg, top, p);
+    d = live ? dw * exp_neg(static_cast<double>(lx) - static_cast<double>(top)) * r : 0.0;
     for (int j = 0; j < a.topk; ++j) s += read_lane(d, j);
   }
   double out[EPL];
@@ -558,11 +690,15 @@ Router router(const void* logits, int64_t tokens, int E, const qlora_router_conf
   a.gs = E / c->groups;
   // (e < 1024 and gs < 1024: e gs < 2^20, so the quotient is exact)
   a.gs_mul = ((1u << 20) + a.gs - 1) / a.gs;
-  while ((c->groups << (a.gshift + 1)) <= 64) ++a.gshift;
   // whole groups in 1, 2, 4, 8 or 16 lanes: no way through LDS
   const int per = lane_experts(E);
-  for (int n = 1; n <= 16; n *= 2)
-    if (a.gs == n * per) a.glanes = n;
+  for (int n = 0; n <= 4; ++n)
+    if (a.gs == per << n) {
+      a.in_lanes = 1;
+      a.gshift = n;
+    }
+  if (!a.in_lanes)
+    while ((c->groups << (a.gshift + 1)) <= 64) ++a.gshift;
   return a;
 }
 
@@ -576,7 +712,7 @@ hipError_t launch(const Router& a, hipStream_t st) {
     hipLaunchKernelGGL((k_router_bwd<EPL, L>), grid, dim3(64 * kWaves), 0, st, a);
   else
     hipLaunchKernelGGL((k_router_fwd<EPL, L>), grid, dim3(64 * kWaves),
-                       a.choose_groups && !a.glanes ? kWaves * a.E * sizeof(double) : 0, st, a);
+                       a.choose_groups && !a.in_lanes ? kWaves * a.E * sizeof(double) : 0, st, a);
   return hipGetLastError();
 }
 

@@ -109,6 +109,49 @@ def test_many_tokens():
     np.testing.assert_allclose(w.sum(dim=1).cpu().numpy(), 1, rtol=8 * 2.0 ** -24)
 
 
+@pytest.mark.parametrize("E,groups,tg,gt", [(8, 1, 1, 1), (64, 8, 3, 2), (128, 16, 5, 1),
+                                            (256, 8, 4, 2), (256, 16, 4, 2), (252, 4, 2, 2),
+                                            (512, 8, 2, 1), (1024, 4, 1, 2)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_choices_next_to_each_other(E, groups, tg, gt, score):
+    """Ranks that 32 bits cannot tell apart, or tell apart wrongly: logits next to each
+    other with biases that make up for them, equal ones, ones that mask and force."""
+    need_gpu()
+    say(f"router, close ranks E={E} groups={groups}/{tg}/{gt} {score}")
+    rng = np.random.default_rng(E)
+    T, k = 40, min(8, E // groups * tg)
+    x = rng.standard_normal((T, E)).astype(np.float32)
+    p = np.stack([orr.scores(r.astype(np.float64), score) for r in x])
+    b = (0.5 - p.mean(axis=0)).astype(np.float32)
+    x[10:20] = x[0]                      # a token whose biases level all its ranks
+    b2 = (0.5 - p[0]).astype(np.float32)
+    x[20:24, 3] = -np.inf
+    x[24:28] = np.round(x[24:28])        # few different values
+    special = b.copy()
+    special[[0, E // 2, E - 1]] = [np.inf, -np.inf, np.nan]
+    special[1] = np.inf
+    t = torch.from_numpy(x).to(dev())
+    for bias in (b, b2, np.zeros(E, np.float32), special):
+        ids, _ = q.qlora_router_fwd(t, k, score, torch.from_numpy(bias).to(dev()), groups, tg, gt)
+        torch.cuda.synchronize()
+        got = ids.cpu().numpy()
+        for i in range(T):
+            r = orr.scores(x[i].astype(np.float64), score) + bias.astype(np.float64)
+            want = orr.choose(x[i].astype(np.float64), k, score, bias.astype(np.float64), groups, tg,
+                              gt)
+            if got[i].tolist() != want:
+                # 64-bit ranks may be rounded apart: the same ranks to 2^-50, expert for expert,
+                # and where groups are chosen, a border that close
+                a_, w_ = r[got[i]], r[np.array(want)]
+                close = np.abs(a_ - w_) <= 2.0 ** -50
+                assert (close | (groups > tg)).all() and (np.sort(got[i]) >= 0).all(), (i, got[i], want)
+                if groups > tg:
+                    two = -np.sort(-np.where(np.isnan(r) | (x[i] == -np.inf), -np.inf, r).reshape(
+                        groups, -1), axis=1)[:, :gt]
+                    s = np.sort(np.where(np.isfinite(two), two, 0).sum(axis=1))[::-1]
+                    assert close.all() or abs(s[tg - 1] - s[tg]) <= 2.0 ** -49, (i, got[i], want)
+
+
 def test_gradient_of_a_sure_choice():
     """Where one expert takes all but 1e-6, the gradient keeps its digits."""
     need_gpu()
