@@ -294,6 +294,15 @@ int bwd_impl(const uint16_t* dY, const uint16_t* X, int64_t M, const Nf4View& v,
       T = Tr;
     }
     if (e == hipSuccess) e = launch_grad_in_and_b(dY, M, v.N, B, T, r, s, G, dB, part, hs);
+    const GemmSplit sp = dx_gemm_split(M, v.N, v.K);
+    if (e == hipSuccess && x8 && dX && sp.splits > 1 && grad_a_act8_whole(M, v.K, r)) {
+      // dA waits for dX's partials and shares the launch that adds them up
+      e = launch_dx_gemm(dY, M, v, G, A, r, s, dX, part, tb, hs, d, false);
+      if (e == hipSuccess)
+        e = launch_grad_a_act8_and_sum(*x8, M, v.K, G, r, s, dA, part, sp.splits, M * v.K, dX, hs,
+                                       d);
+      return hip_status(e);
+    }
     if (e == hipSuccess)
       e = x8 ? launch_grad_a_act8(*x8, M, v.K, G, r, s, dA, part, hs, d)
              : launch_grad_a(X, M, v.K, G, r, s, dA, part, hs, d);

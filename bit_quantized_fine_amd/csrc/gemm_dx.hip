@@ -552,7 +552,7 @@ GemmSplit dx_gemm_split(int64_t M, int64_t N, int64_t K) {
 hipError_t launch_dx_gemm(const uint16_t* dY, int64_t M, const Nf4View& w,
                           const float* G, const uint16_t* A, int r, float s,
                           uint16_t* dX, float* part, const Nf4Tables& tb, hipStream_t stream,
-                          const Drop& d) {
+                          const Drop& d, bool add_up) {
   const int qtiles = static_cast<int>((M + kTileQ - 1) / kTileQ);
   const GemmSplit sp = dx_gemm_split(M, w.N, w.K);
   if (w.dense && d.on()) return hipErrorInvalidValue;
@@ -563,7 +563,7 @@ hipError_t launch_dx_gemm(const uint16_t* dY, int64_t M, const Nf4View& w,
                                  : launch_dx_tiles<kFormNoDq, kTileQ, false, false>);
   prof_begin(1, stream);
   hipError_t e = launch(dY, M, w, w.N, G, A, r, s, dX, part, tb, stream, qtiles, sp, nullptr, 0, d);
-  if (e == hipSuccess && sp.splits > 1)
+  if (e == hipSuccess && sp.splits > 1 && add_up)
     e = launch_split_reduce_bf16(part, sp.splits, M * w.K, dX, stream);
   prof_end(1, stream);
   return e;

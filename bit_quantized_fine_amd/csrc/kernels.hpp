@@ -122,7 +122,7 @@ GemmSplit dx_gemm_split(int64_t M, int64_t N, int64_t K);
 hipError_t launch_dx_gemm(const uint16_t* dY, int64_t M, const Nf4View& w,
                           const float* G, const uint16_t* A, int r, float s,
                           uint16_t* dX, float* part, const Nf4Tables& tb, hipStream_t stream,
-                          const Drop& d = {});
+                          const Drop& d = {}, bool add_up = true);   // false: partials stay
 
 // Rank-r products with a split reduction; partials go to `ws`.
 size_t rank_ws_floats(int64_t M, int64_t N, int64_t K, int r);
@@ -206,6 +206,13 @@ hipError_t launch_lora_down_act8(const Act8View& x8, int64_t M, int64_t K, const
 hipError_t launch_grad_a_act8(const Act8View& x8, int64_t M, int64_t K, const float* G, int r,
                               float s, uint16_t* dA, float* ws, hipStream_t stream,
                               const Drop& d);
+// With grad_a_act8_whole (dA in one split), dA and the sum of dX's partials
+// (part [splits][count]) in one launch.
+bool grad_a_act8_whole(int64_t M, int64_t K, int r);
+hipError_t launch_grad_a_act8_and_sum(const Act8View& x8, int64_t M, int64_t K, const float* G,
+                                      int r, float s, uint16_t* dA, const float* part, int splits,
+                                      int64_t count, uint16_t* dX, hipStream_t stream,
+                                      const Drop& d);
 hipError_t launch_grouped_down_act8(const Act8View& x8, int64_t M, const int* offsets, int E,
                                     int64_t K, const uint16_t* A, int r, float* T, float* ws,
                                     hipStream_t stream, const Drop& d);
