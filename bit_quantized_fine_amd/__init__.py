@@ -336,8 +336,8 @@ def _check_adapters(A, B, w):
     if A.dim() != 2:
         raise ValueError("A must be [K, r]")
     r = A.shape[1]
-    _need(A, "A", (w.K, r), torch.bfloat16)
-    _need(B, "B", (r, w.N), torch.bfloat16)
+    _is(A, "A", (w.K, r), torch.bfloat16)
+    _is(B, "B", (r, w.N), torch.bfloat16)
     return r
 
 
@@ -692,20 +692,23 @@ def _at(t):
 def _q4(w):
     """The C view of an NF4Weight or Q4Weight, and its checked tensors."""
     import torch
-    n = w.N * w.K
-    nb = n // 64
-    book, dq = (w.codebook, w.double_quant) if isinstance(w, Q4Weight) else ("nf4", True)
-    cb = CODEBOOKS[book] if book in CODEBOOKS else _codebook_id(book)
-    _is(w.codes, "w.codes", (n // 2,), torch.uint8)
-    if dq:
-        _is(w.absmax_q, "w.absmax_q", (nb,), torch.uint8)
-        _is(w.absmax_scale, "w.absmax_scale", ((nb + 255) // 256,), torch.float32)
-        q = w.absmax_q
+    if isinstance(w, Q4Weight):
+        codes, q, scale, N, K, book, dq = w
     else:
-        _is(w.absmax_scale, "w.absmax_scale", (nb,), torch.float32)
+        codes, q, scale, N, K = w
+        book, dq = "nf4", True
+    n = N * K
+    nb = n // 64
+    cb = CODEBOOKS[book] if book in CODEBOOKS else _codebook_id(book)
+    _is(codes, "w.codes", (n // 2,), torch.uint8)
+    if dq:
+        _is(q, "w.absmax_q", (nb,), torch.uint8)
+        _is(scale, "w.absmax_scale", ((nb + 255) // 256,), torch.float32)
+    else:
+        _is(scale, "w.absmax_scale", (nb,), torch.float32)
         q = None
-    return (_Q4Weight(w.codes.data_ptr(), _at(q), w.absmax_scale.data_ptr(), w.N, w.K, cb,
-                      1 if dq else 0), w.codes, q, w.absmax_scale)
+    return (_Q4Weight(codes.data_ptr(), _at(q), scale.data_ptr(), N, K, cb, 1 if dq else 0),
+            codes, q, scale)
 
 
 def _drop(p, state):
@@ -810,10 +813,14 @@ def _grads(fn, groups, dY, X, M, N, K, cw, wt, A, B, r, s, d, state, T, need_dx,
         T = dA = dB = None
     if not need_dx:
         dX = None
-    _maybe(T, "T", (M, r), torch.float32)
-    _maybe(dX, "dX", (M, K), torch.bfloat16)
-    _maybe(dA, "dA", shape_a, torch.bfloat16)
-    _maybe(dB, "dB", shape_b, torch.bfloat16)
+    if T is not None:
+        _is(T, "T", (M, r), torch.float32)
+    if dX is not None:
+        _is(dX, "dX", (M, K), torch.bfloat16)
+    if dA is not None:
+        _is(dA, "dA", shape_a, torch.bfloat16)
+    if dB is not None:
+        _is(dB, "dB", shape_b, torch.bfloat16)
     names = "X dY w.codes w.absmax_q w.absmax_scale offsets A B state T dX dA dB workspace"
     tensors = (X, dY, *wt, groups[0] if groups else None, A, B, state, T, dX, dA, dB, workspace)
     if kept is None:
@@ -824,11 +831,11 @@ def _grads(fn, groups, dY, X, M, N, K, cw, wt, A, B, r, s, d, state, T, need_dx,
         x = (ctypes.byref(x8), *more)
     workspace = _scratch(workspace, need, dev)
     if need_dx and dX is None:
-        dX = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        dX = torch.empty_like(X) if kept is None else dY.new_empty((M, K))
     if r > 0 and dA is None:
-        dA = torch.empty(shape_a, dtype=torch.bfloat16, device=dev)
+        dA = torch.empty_like(A)
     if r > 0 and dB is None:
-        dB = torch.empty(shape_b, dtype=torch.bfloat16, device=dev)
+        dB = torch.empty_like(B)
     where = (groups[0].data_ptr(), groups[1]) if groups else ()
     _call(fn, dev, dY.data_ptr(), *x, M, *where, ctypes.byref(cw), _at(A), _at(B), r, s,
           ctypes.byref(d), _at(T), _at(dX), _at(dA), _at(dB), _at(workspace), need)
@@ -1073,6 +1080,14 @@ def qlora_act8_unpack(x8: Act8, out=None):
     return out
 
 
+@functools.lru_cache(maxsize=1024)
+def _act8_bwd_need(M, E, N, K, r):
+    """Workspace bytes (E = 0: the plain layer)."""
+    if E == 0:
+        return lib().qlora_linear_act8_bwd_workspace_bytes(M, N, K, r)
+    return lib().qlora_grouped_act8_bwd_workspace_bytes(M, E, N, K, r)
+
+
 def qlora_linear_act8_bwd(dY, x8: Act8, w, A=None, B=None, s: float = 1.0, p: float = 0.0,
                           state=None, T=None, need_dx: bool = True, dX=None, dA=None, dB=None,
                           workspace=None):
@@ -1086,7 +1101,7 @@ def qlora_linear_act8_bwd(dY, x8: Act8, w, A=None, B=None, s: float = 1.0, p: fl
     d = _drop(p, state)
     return _grads("qlora_linear_act8_bwd", (), dY, x8.codes, M, w.N, K, cw, wt, A, B, r, s, d,
                   state, T, need_dx, dX, dA, dB, (K, r), (r, w.N), workspace,
-                  lib().qlora_linear_act8_bwd_workspace_bytes(M, w.N, K, r),
+                  _act8_bwd_need(M, 0, w.N, K, r),
                   (x8._c(), x8.scales, (), None))
 
 
@@ -1109,7 +1124,7 @@ def qlora_grouped_act8_bwd(dY, x8: Act8, offsets, w, E: int, A=None, B=None, s: 
     d = _drop(p, state)
     return _grads("qlora_grouped_act8_bwd", (offsets, E), dY, x8.codes, M, N, K, cw, wt, A, B, r,
                   s, d, state, T, need_dx, dX, dA, dB, (E, K, r), (E, r, N), workspace,
-                  lib().qlora_grouped_act8_bwd_workspace_bytes(M, E, N, K, r),
+                  _act8_bwd_need(M, E, N, K, r),
                   (x8._c(), x8.scales, (tokens, _at(order), topk), order))
 
 
