@@ -402,7 +402,8 @@ int check_act8(const qlora_act8* x8, int64_t M, int64_t K) {
     return QLORA_ERR_SHAPE;
   if (!x8) return QLORA_ERR_NULL;
   if (M > 0 && (!x8->codes || !x8->scales)) return QLORA_ERR_NULL;
-  if (!aligned16(x8->codes) || !aligned16(x8->scales)) return QLORA_ERR_ALIGN;
+  if (!aligned16(x8->codes) || (reinterpret_cast<uintptr_t>(x8->scales) & 3u))
+    return QLORA_ERR_ALIGN;
   return QLORA_OK;
 }
 
@@ -1075,6 +1076,10 @@ int qlora_grouped_act8_bwd(const uint16_t* dY, const qlora_act8* x8, int64_t tok
   if (tokens > INT32_MAX || (!order && tokens != M)) return QLORA_ERR_SHAPE;
   if ((st = check_act8(x8, tokens, w->K))) return st;
   if (reinterpret_cast<uintptr_t>(order) & 3u) return QLORA_ERR_ALIGN;
+  // (dA's tiles are narrower than the ones that the grouped calls' limit counts)
+  if (E >= 1 && E <= kMaxExperts && r >= 0 && r <= 256 && M >= 0 && M <= INT32_MAX &&
+      grouped_grad_a_act8_threads(M, E, w->K, r) >= int64_t(1) << 32)
+    return QLORA_ERR_SHAPE;
   const Act8View v{x8->codes, x8->scales, tokens, order, topk};
   return grouped_bwd_impl(dY, nullptr, &v, M, offsets, E, w, A, B, r, s, d, T_saved, dX, dA, dB,
                           workspace, workspace_bytes, stream);

@@ -404,6 +404,11 @@ hipError_t launch_grouped_down_act8(const Act8View& x8, int64_t M, const int* of
   return e;
 }
 
+int64_t grouped_grad_a_act8_threads(int64_t M, int E, int64_t K, int r) {
+  if (r <= 0) return 0;
+  return NT * cdiv(K, RB_X8) * cdiv(r, RB_R) * E * grad_splits(M, E, K, r);
+}
+
 hipError_t launch_grouped_grad_a_act8(const Act8View& x8, int64_t M, const int* offsets, int E,
                                       int64_t K, const float* G, int r, float s, uint16_t* dA,
                                       float* ws, hipStream_t stream, const Drop& d) {

@@ -216,6 +216,7 @@ hipError_t launch_grad_a_act8_and_sum(const Act8View& x8, int64_t M, int64_t K, 
 hipError_t launch_grouped_down_act8(const Act8View& x8, int64_t M, const int* offsets, int E,
                                     int64_t K, const uint16_t* A, int r, float* T, float* ws,
                                     hipStream_t stream, const Drop& d);
+int64_t grouped_grad_a_act8_threads(int64_t M, int E, int64_t K, int r);
 hipError_t launch_grouped_grad_a_act8(const Act8View& x8, int64_t M, const int* offsets, int E,
                                       int64_t K, const float* G, int r, float s, uint16_t* dA,
                                       float* ws, hipStream_t stream, const Drop& d);

@@ -55,7 +55,8 @@ struct NormBwd {
   uint16_t* dx;
   void* dg;                   // may be null
   float* part;                // sums of dy n that a second launch adds up, or null
-  int64_t row_blocks;         // workgroups for rows; the rest add up columns
+  int64_t row_blocks;         // workgroups for rows, and for columns after them (a
+  int64_t col_blocks;         // grid of several rows holds more than both)
   int64_t run_rows;           // rows of a run of those
   int g_fp32;
 };
@@ -290,7 +291,7 @@ __global__ __launch_bounds__(row_threads<TPR>()) void k_rms_bwd(NormBwd a) {
   const int64_t block = block_index();
   if constexpr (P > 0) {
     if (block >= a.row_blocks) {   // uniform
-      dg_columns<NTHR>(a, block - a.row_blocks, cols);
+      if (block - a.row_blocks < a.col_blocks) dg_columns<NTHR>(a, block - a.row_blocks, cols);
       return;
     }
   }
@@ -390,7 +391,7 @@ __global__ __launch_bounds__(row_threads<TPR>()) void k_rms_bwd(NormBwd a) {
 // Whole columns alone, for rows too long for the kernel above to add them up.
 __global__ __launch_bounds__(256) void k_rms_dg_columns(NormBwd a) {
   __shared__ float cols[256 * 9];
-  dg_columns<256>(a, block_index(), cols);
+  if (block_index() < a.col_blocks) dg_columns<256>(a, block_index(), cols);
 }
 
 // dg[c] = sum_p part[p][c]: 64 columns a workgroup, 64 runs of the parts, four
@@ -433,6 +434,7 @@ constexpr int64_t kMaxActs = int64_t(1) << 40;
 constexpr int64_t kLongRow = 65536;     // more than this: read twice
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 int hip_status(hipError_t e) { return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -509,7 +511,7 @@ int qlora_rms_norm_fwd(const uint16_t* x, const uint16_t* residual, const void* 
                        (y8 && (!y8->codes || !y8->scales)))))
     return QLORA_ERR_NULL;
   if (!aligned16(x) || !aligned16(residual) || !aligned16(g) || !aligned16(h) || !aligned16(y) ||
-      !aligned16(rstd) || (y8 && (!aligned16(y8->codes) || !aligned16(y8->scales))))
+      !aligned4(rstd) || (y8 && (!aligned16(y8->codes) || !aligned4(y8->scales))))
     return QLORA_ERR_ALIGN;
   if (M == 0) return QLORA_OK;
   const NormFwd a{x, residual, g, M, K, eps, h, y, rstd, y8 ? y8->codes : nullptr,
@@ -539,7 +541,7 @@ int qlora_rms_norm_bwd(const uint16_t* dy, const uint16_t* dres, const uint16_t*
   const int st = check_norm(M, K);
   if (st) return st;
   if (!g || (M > 0 && (!dy || !h || !rstd || !dx))) return QLORA_ERR_NULL;
-  if (!aligned16(dy) || !aligned16(dres) || !aligned16(h) || !aligned16(rstd) || !aligned16(g) ||
+  if (!aligned16(dy) || !aligned16(dres) || !aligned16(h) || !aligned4(rstd) || !aligned16(g) ||
       !aligned16(dx) || !aligned16(dg))
     return QLORA_ERR_ALIGN;
   const BwdPlan p = plan_bwd(M, K, dg != nullptr);
@@ -547,11 +549,11 @@ int qlora_rms_norm_bwd(const uint16_t* dy, const uint16_t* dres, const uint16_t*
   if (need > 0 && (!workspace || workspace_bytes < need)) return QLORA_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return QLORA_ERR_ALIGN;
   const hipStream_t hs = static_cast<hipStream_t>(stream);
-  const NormBwd a{dy, dres, h, rstd, g, M, K, dx, dg,
-                  p.parts > 0 ? static_cast<float*>(workspace) : nullptr, p.row_blocks, p.run_rows,
-                  g_fp32 != 0};
-  const bool wide = K > kLongRowBwd;
   const int64_t cols = p.run_rows > 0 ? cdiv(K, 128) * std::max<int64_t>(1, p.parts) : 0;
+  const NormBwd a{dy, dres, h, rstd, g, M, K, dx, dg,
+                  p.parts > 0 ? static_cast<float*>(workspace) : nullptr, p.row_blocks, cols,
+                  p.run_rows, g_fp32 != 0};
+  const bool wide = K > kLongRowBwd;
   const int64_t n = p.row_blocks + (wide ? 0 : cols);
   hipError_t e = hipSuccess;
   if (n > 0) {

@@ -163,17 +163,13 @@ __device__ __forceinline__ double sigmoid64(const Exp& exp_neg, double x) {
 }
 
 // EPL values from element e0 on, `none` past E.  Where E is whole pieces of a lane,
-// a piece is one load (rows then start at a multiple of four bytes).
+// a piece is one load (of any alignment: a token's row starts anywhere).
 template <int EPL, class L>
 __device__ __forceinline__ void load_piece(const L* row, int e0, int E, float none, float* x) {
   if (E % EPL == 0) {
     L v[EPL];
     const int at = e0 < E ? e0 : 0;
-    if constexpr (EPL * sizeof(L) >= 4) {
-      __builtin_memcpy(v, __builtin_assume_aligned(row + at, 4), sizeof(v));
-    } else {
-      v[0] = row[at];
-    }
+    __builtin_memcpy(v, row + at, sizeof(v));
 #pragma unroll
     for (int i = 0; i < EPL; ++i) x[i] = e0 < E ? to_f32(v[i]) : none;
   } else {
@@ -743,7 +739,8 @@ int qlora_router_fwd(const void* logits, int logits_fp32, int64_t tokens, int E,
   const int st = check_router(tokens, E, cfg);
   if (st) return st;
   if (tokens > 0 && (!logits || !ids || !weights)) return QLORA_ERR_NULL;
-  if (!aligned(logits, 16) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+  if (!aligned(logits, logits_fp32 ? 4 : 2) || !aligned(bias, 4) || !aligned(ids, 4) ||
+      !aligned(weights, 4))
     return QLORA_ERR_ALIGN;
   if (tokens == 0) return QLORA_OK;
   Router a = router(logits, tokens, E, cfg);
@@ -760,7 +757,9 @@ int qlora_router_bwd(const float* dweights, const void* logits, int logits_fp32,
   const int st = check_router(tokens, E, cfg);
   if (st) return st;
   if (tokens > 0 && (!dweights || !logits || !ids || !dlogits)) return QLORA_ERR_NULL;
-  if (!aligned(logits, 16) || !aligned(dlogits, 16) || !aligned(ids, 4) || !aligned(dweights, 4))
+  const uintptr_t size = logits_fp32 ? 4 : 2;
+  if (!aligned(logits, size) || !aligned(dlogits, size) || !aligned(ids, 4) ||
+      !aligned(dweights, 4))
     return QLORA_ERR_ALIGN;
   if (tokens == 0) return QLORA_OK;
   Router a = router(logits, tokens, E, cfg);

@@ -540,7 +540,7 @@ int qlora_expert_combine_bwd(const uint16_t* dOut, const uint16_t* Y, int64_t to
  *                    (0 where c = 0)
  *   value = bf16_rne(fl32(code * c))
  * A block that holds a NaN or an infinity gets c = NaN and codes 0, so that all
- * of it comes back as NaN.  codes and scales 16-byte aligned; K >= 64,
+ * of it comes back as NaN.  codes 16-byte, scales 4-byte aligned; K >= 64,
  * K <= 2^22, M >= 0, M*K <= 2^40 (QLORA_ERR_SHAPE otherwise); M = 0 is allowed.
  *
  * qlora_act8_pack writes the checkpoint of X, qlora_act8_unpack its values.
@@ -569,7 +569,8 @@ int qlora_act8_unpack(const qlora_act8* x8, int64_t M, int64_t K, uint16_t* X,
  *     order[i] / topk of it (1 <= topk <= 64, QLORA_ERR_EXPERT otherwise; tokens
  *     < 2^31).  An order that leads outside [0, tokens) is a row of zeros.
  * Dropout, other arguments, limits, workspaces and errors as those calls, and
- * the checkpoint's own.
+ * the checkpoint's own; dA's launch holds twice the threads (QLORA_ERR_SHAPE from
+ * 2^32 on, as with 64 experts of 2^22 columns at r = 256).
  */
 size_t qlora_linear_act8_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int r);
 size_t qlora_grouped_act8_bwd_workspace_bytes(int64_t M, int E, int64_t N, int64_t K, int r);
@@ -595,9 +596,10 @@ int qlora_grouped_act8_bwd(const uint16_t* dY, const qlora_act8* x8, int64_t tok
  *   residual NULL: h is x, and the argument h is not used (may be NULL).
  *   h may be x or residual (in place); y overlaps nothing.
  *   y8  NULL, or where the checkpoint of y goes (then K % 64 == 0).
- * Squares are summed in fp32.  K % 8 == 0, 8 <= K <= 2^22, M >= 0, M*K <= 2^40,
- * eps > 0 and finite (QLORA_ERR_SHAPE otherwise); M = 0 is allowed.  All
- * buffers 16-byte aligned.
+ * Squares are summed in fp32: a row of values past 2^64 / sqrt(K) has rstd = 0.
+ * K % 8 == 0, 8 <= K <= 2^22, M >= 0, M*K <= 2^40, eps > 0 and finite
+ * (QLORA_ERR_SHAPE otherwise); M = 0 is allowed.  All buffers 16-byte aligned
+ * (rstd and scales 4-byte).
  *
  * Backward, with dy the gradient of y and dres that of h from elsewhere (the
  * residual stream; NULL for none):
@@ -622,7 +624,8 @@ int qlora_rms_norm_bwd(const uint16_t* dy, const uint16_t* dres, const uint16_t*
  * their weights, as qlora_expert_plan (ids) and qlora_expert_combine (weights)
  * take them, and from the gradient of the weights (dweights of
  * qlora_expert_combine_bwd) that of the logits.
- *   logits [tokens, E] bf16, or fp32 with logits_fp32 != 0; 16-byte aligned.
+ *   logits [tokens, E] bf16, or fp32 with logits_fp32 != 0; these, bias, ids and
+ *     weights aligned to their elements.
  *   score: p = softmax over the token's experts, or the sigmoid of each logit.
  *   bias [E] fp32 or NULL (kept for balance: it takes part in the choice, not in
  *     the weights, and gets no gradient).

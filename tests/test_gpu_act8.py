@@ -330,5 +330,13 @@ def test_streams_graph_and_views():
     q.qlora_act8_unpack(q.qlora_act8_pack(X), out=big[2:2 + M])
     torch.cuda.synchronize()
     assert (big[:2] == 7).all() and (big[2 + M:] == 7).all() and torch.equal(big[2:2 + M], b[2])
+    # rows of a checkpoint, whose constants then start at any four bytes
+    part = q.Act8(b[0][3:50], b[1][3:50])
+    v = q.qlora_act8_unpack(part)
+    gs = q.qlora_linear_act8_bwd(dY[3:50], part, w, A, B, 0.5)
+    ws = q.qlora_linear_act8_bwd(dY[3:50].clone(), q.Act8(part.codes.clone(), part.scales.clone()), w,
+                                 A, B, 0.5)
+    torch.cuda.synchronize()
+    assert torch.equal(v, b[2][3:50]) and all(torch.equal(s, t) for s, t in zip(gs, ws))
     empty = q.qlora_act8_pack(X[:0])
     assert q.qlora_act8_unpack(empty).shape == (0, K)

@@ -181,6 +181,31 @@ def test_past_4g_elements():
     torch.testing.assert_close(dg, wg, rtol=1e-5, atol=1e-5)
 
 
+@pytest.mark.parametrize("M,K", [((1 << 21) + 3, 1032), ((1 << 23) + 9, 8)])
+def test_more_rows_than_one_row_of_workgroups(M, K):
+    """More workgroups than a row of the grid takes: the ones past the last row of the
+    matrix write nothing."""
+    need_gpu()
+    say(f"norm {M} x {K}")
+    _, x, r, tg, g = _inputs(4, K, 7, True)
+    X = torch.zeros((M, K), dtype=torch.bfloat16, device=dev())
+    X[:4], X[-4:] = bf16(x), bf16(x)
+    h, y, rstd = q.qlora_rms_norm_fwd(X, tg, eps=EPS)
+    _, wy, wr = q.qlora_rms_norm_fwd(bf16(x), tg, eps=EPS)
+    torch.cuda.synchronize()
+    for rows in (slice(0, 4), slice(M - 4, M)):
+        assert torch.equal(y[rows], wy) and torch.equal(rstd[rows], wr)
+    y.zero_()
+    y[-4:] = bf16(r)
+    dx, none = q.qlora_rms_norm_bwd(y, h, rstd, tg, need_dg=False)
+    dx2, dg = q.qlora_rms_norm_bwd(y, h, rstd, tg)
+    wx, wg = q.qlora_rms_norm_bwd(bf16(r), bf16(x), wr, tg)
+    torch.cuda.synchronize()
+    assert none is None and torch.equal(dx, dx2)
+    assert torch.equal(dx[-4:], wx) and not dx[4:-4].any()
+    torch.testing.assert_close(dg, wg, rtol=1e-5, atol=1e-5)
+
+
 def test_streams_graph_and_workspaces():
     """On another stream, and in two graphs that share no workspace with eager
     calls between their replays."""

@@ -260,5 +260,18 @@ def test_guards_streams_and_graph():
         e = step()
         torch.cuda.synchronize()
         assert all(torch.equal(u, v) for u, v in zip(a, e))
+    # rows of larger logits, which start at any element
+    for E2, dt in ((65, torch.bfloat16), (130, torch.bfloat16), (7, torch.bfloat16), (66, torch.float32),
+                   (3, torch.float32)):
+        big = torch.randn(T * E2 + 1, device=dev()).to(dt)[1:].view(T, E2)
+        bias = torch.randn(E2 + 1, device=dev())[1:]
+        for lo in (1, 2, 3):
+            for s in ("softmax", "sigmoid"):
+                i1, w1 = q.qlora_router_fwd(big[lo:lo + 40], 3, s, bias)
+                i2, w2 = q.qlora_router_fwd(big[lo:lo + 40].clone(), 3, s, bias.clone())
+                d1 = q.qlora_router_bwd(w1, big[lo:lo + 40], i1, s)
+                d2 = q.qlora_router_bwd(w2, big[lo:lo + 40].clone(), i2, s)
+                torch.cuda.synchronize()
+                assert torch.equal(i1, i2) and torch.equal(w1, w2) and torch.equal(d1, d2)
     ids, w = q.qlora_router_fwd(x[:0], k)
     assert ids.shape == (0, k) and q.qlora_router_bwd(dw[:0], x[:0], ids).shape == (0, E)

@@ -29,6 +29,11 @@ for K in (64, 4096, 1 << 22):
         st = [L.qlora_act8_pack(P, M, K, c8, None), L.qlora_act8_unpack(c8, M, K, P, None)]
         yz = max(blocks_yz(), default=0)
         out.append((M, K, yz, st, [l[0] for l in launches()]))
+for E in (1, 31, 32, 63, 64):   # 2^32 threads from 64 experts on: refused
+    st = [L.qlora_grouped_act8_bwd(P, c8, 64, P, 1, 64, P, E, weight(8 * E, 1 << 22, 0), P, P, 256, 1.0,
+                                   None, P, P, P, P, P, BIG, None)]
+    out.append((E, 0, max(blocks_yz(), default=0), [0 if s == 2 and E == 64 else s for s in st],
+                [l[0] for l in launches()] + [0] * (E == 64)))
 for M in (1, 16, 17, 2048, 1 << 22):
     for r in (8, 64, 256):
         for T in (None, P):

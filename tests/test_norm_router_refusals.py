@@ -38,7 +38,7 @@ def test_act8():
         assert f(K=32) == SHAPE and f(K=96) == SHAPE and f(K=0) == SHAPE and f(M=-1) == SHAPE
         assert f(K=(1 << 22) + 64) == SHAPE and f(M=(1 << 34) + 1) == SHAPE
         assert f(X=None) == NULL and f(c=x8(None)) == NULL and f(c=x8(4096, None)) == NULL
-        assert f(X=ODD) == ALIGN and f(c=x8(4104)) == ALIGN and f(c=x8(4096, 4100)) == ALIGN
+        assert f(X=ODD) == ALIGN and f(c=x8(4104)) == ALIGN and f(c=x8(4096, 4098)) == ALIGN
         assert f(M=0, X=None, c=x8(None, None)) == 0
     assert L.qlora_act8_pack(P, 4, 64, None, None) == NULL
     assert L.qlora_act8_unpack(None, 4, 64, P, None) == NULL
@@ -59,7 +59,7 @@ def grp(dY=P, c=None, tokens=8, order=P, topk=2, M=16, off=P, E=2, w=None, A=P, 
 def test_backward_from_a_checkpoint():
     for f, n in ((lin, 256), (grp, 512)):
         assert f(c=x8(None)) == NULL and f(c=x8(4096, None)) == NULL and f(dY=None) == NULL
-        assert f(c=x8(4104)) == ALIGN and f(c=x8(4096, 4104)) == ALIGN and f(dA=ODD) == ALIGN
+        assert f(c=x8(4104)) == ALIGN and f(c=x8(4096, 4098)) == ALIGN and f(dA=ODD) == ALIGN
         assert f(dA=None) == NULL and f(A=None) == NULL and f(r=12) == RANK
         assert f(w=weight(n, K=100)) == SHAPE and f(w=weight(n, book=5)) == FORMAT
         assert f(M=-1) == SHAPE and f(d=drop(1.0)) == DROPOUT and f(d=drop(0.5, None)) == NULL
@@ -75,6 +75,9 @@ def test_backward_from_a_checkpoint():
     assert need > 0 and lin(wsb=need - 1) == WORKSPACE and lin(ws=None) == WORKSPACE
     need = L.qlora_grouped_act8_bwd_workspace_bytes(16, 2, 256, 64, 8)
     assert need > 0 and grp(wsb=need - 1) == WORKSPACE
+    # dA's launch would hold 2^32 threads: 2^16 tiles of 64 columns, 4 of ranks, 64 experts
+    big = weight(64 * 8, 1 << 22, dq=0)
+    assert grp(w=big, E=64, r=256) == SHAPE
 
 
 def nf(x=P, res=P, g=P, g32=1, M=4, K=64, eps=1e-5, h=P, y=P, rstd=P, c=None):
@@ -90,7 +93,7 @@ def test_norm():
         assert f(K=12) == SHAPE and f(K=0) == SHAPE and f(M=-1) == SHAPE
         assert f(K=(1 << 22) + 8) == SHAPE and f(M=(1 << 37) + 1, K=8) == SHAPE
         assert f(g=None) == NULL and f(h=None) == NULL and f(rstd=None) == NULL
-        assert f(g=ODD) == ALIGN and f(h=ODD) == ALIGN and f(rstd=ODD) == ALIGN
+        assert f(g=ODD) == ALIGN and f(h=ODD) == ALIGN and f(rstd=ctypes.c_void_p(4098)) == ALIGN
     assert nf(x=None) == NULL and nf(y=None) == NULL and nf(x=ODD) == ALIGN and nf(y=ODD) == ALIGN
     assert nf(res=ODD) == ALIGN
     for eps in (0.0, -1e-5, float("nan"), float("inf")):
@@ -130,10 +133,13 @@ def test_router():
             assert f(c=bad) == EXPERT
         assert f(tokens=-1) == SHAPE and f(tokens=(1 << 29) + 1) == SHAPE
         assert f(logits=None) == NULL and f(ids=None) == NULL and f(weights=None) == NULL
-        assert f(logits=ODD) == ALIGN and f(ids=ctypes.c_void_p(4098)) == ALIGN
+        assert f(logits=ctypes.c_void_p(4098)) == ALIGN and f(ids=ctypes.c_void_p(4098)) == ALIGN
         assert f(tokens=0, logits=None, ids=None, weights=None) == 0
     assert rf(bias=ctypes.c_void_p(4098)) == ALIGN
-    assert rb(dlogits=None) == NULL and rb(dlogits=ODD) == ALIGN
+    assert rb(dlogits=None) == NULL and rb(dlogits=ctypes.c_void_p(4098)) == ALIGN
+    for f, args in ((q.lib().qlora_router_fwd, lambda p: (p, 0, 4, 8, None, cfg(), P, P, None)),
+                    (q.lib().qlora_router_bwd, lambda p: (P, p, 0, P, 4, 8, cfg(), P, None))):
+        assert f(*args(ctypes.c_void_p(4097))) == ALIGN
     L = q.lib()
     assert L.qlora_router_fwd(P, 1, 4, 8, None, None, P, P, None) == NULL
     assert L.qlora_router_bwd(P, P, 1, P, 4, 8, None, P, None) == NULL
