@@ -246,7 +246,11 @@ struct F32RedMajor {    // element (row, k) = scale * src[k * ld + row], fp32 ->
 // The same operands held as an 8-bit checkpoint: 16 codes a load and one
 // constant, made bf16 values when they are stored to LDS, in the tile layouts
 // of the bf16 loaders, so that a product gives the bits it would give on the
-// unpacked values.
+// unpacked values.  dA of 8192 rows on 8 experts, 4096 columns, r = 64, takes 45 us
+// through the tokens' order (bf16 rows in expert order: 38): the fp32 factor is
+// split anew in each tile of columns and a tile's steps wait for each other, so that
+// tiles of 64 columns, two workgroups a CU, are faster than tiles of 128, one a CU
+// (73 us).  Fetching the order two tiles ahead gained nothing.
 // ---------------------------------------------------------------------------
 
 template <int ROWS, bool DROP>

@@ -7,8 +7,14 @@
 // is given (a softmax or sigmoid keeps their order), else the 64 bits of p +
 // bias, formed in 64 bits: the scores of 256 experts lie about 2^-8 apart, so in
 // 32 bits about one token in 10^4 would get an order that depends on how its
-// scores were rounded.  A round of the choice is the wave's largest value by six
-// lane moves, and a ballot for its owner.
+// scores were rounded.  (By sigmoid and bias 32 bits choose and the chosen ones'
+// 64 bits prove it: choose_by_32.)  A round of the choice is the wave's largest
+// value by six lane moves, and a ballot for its owner.
+//
+// Bound by the vector instructions of a wave, about 550 by sigmoid, bias and groups:
+// 8192 tokens of 256 experts, topk 8, 10.3 us a call (8.4 MB would take 1.9; wholly in
+// 64 bits 13.8).  Smaller batches are a launch and the call (8 us).  The backward of
+// 8192 tokens of 64 experts takes 5.6 us.
 //
 // Weights and gradients are formed in 64 bits too, where they cost one lane's
 // work a slot: what is left of 1 - p where one expert takes nearly all would

@@ -63,7 +63,7 @@ def test_forward(M, K, res, g32):
         assert all(torch.equal(a, b) for a, b in zip(plain, out))
 
 
-@pytest.mark.parametrize("M,K", SIZES + [(0, 64), (300, 64), (1000, 1024), (700, 3000),
+@pytest.mark.parametrize("M,K", SIZES + [(0, 64), (0, 17000), (300, 64), (1000, 1024), (700, 3000),
                                          (4099, 520), (300, 8192), (140, 16384), (60, 40000),
                                          (40, 66000), (300, 17000), (1100, 512), (1500, 1024),
                                          (1030, 2400), (1100, 4104), (1025, 16384), (130, 65544)])
