@@ -7,14 +7,17 @@
 // is given (a softmax or sigmoid keeps their order), else the 64 bits of p +
 // bias, formed in 64 bits: the scores of 256 experts lie about 2^-8 apart, so in
 // 32 bits about one token in 10^4 would get an order that depends on how its
-// scores were rounded.  (By sigmoid and bias 32 bits choose and the chosen ones'
-// 64 bits prove it: choose_by_32.)  A round of the choice is the wave's largest
-// value by six lane moves, and a ballot for its owner.
+// scores were rounded.  A round of the choice is the wave's largest value by six
+// lane moves, and a ballot for its owner.
+//   By sigmoid and bias 32 bits choose and the chosen ones' 64 bits prove it
+// (choose_by_32), with many tokens for two in a wave.  A token's choice and weights
+// are the same on either way.
 //
-// Bound by the vector instructions of a wave, about 550 by sigmoid, bias and groups:
-// 8192 tokens of 256 experts, topk 8, 10.3 us a call (8.4 MB would take 1.9; wholly in
-// 64 bits 13.8).  Smaller batches are a launch and the call (8 us).  The backward of
-// 8192 tokens of 64 experts takes 5.6 us.
+// Bound by the vector instructions of a wave, about 650 by sigmoid, bias and groups for
+// two tokens: 8192 tokens of 256 experts, topk 8, take 8.0 us back to back in a graph
+// (8.4 MB would take 1.9; one token a wave 10.7, wholly in 64 bits 15).  Smaller batches
+// are a launch and the call (8 us).  The backward of 8192 tokens of 64 experts takes
+// 5.6 us.
 //
 // Weights and gradients are formed in 64 bits too, where they cost one lane's
 // work a slot: what is left of 1 - p where one expert takes nearly all would
@@ -22,6 +25,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "act8.hpp"
 #include "device_common.hpp"
 #include "kernels.hpp"
 #include "qlora_nf4.h"
@@ -30,8 +34,11 @@ namespace qnf4 {
 
 namespace {
 
-constexpr int kWaves = 4;          // tokens a workgroup
+constexpr int kWaves = 4;          // waves a workgroup
 constexpr int kMaxE = 1024;
+constexpr double kLeastSum = 1e-250;     // of sigmoids that are divided by their sum as
+                                         // they are (below, every logit is under -575)
+constexpr int64_t kPairTokens = 2048;   // from here on two tokens share a wave (in_pairs)
 constexpr int kMaxTopk = 64;
 constexpr int kMaxGroups = 64;
 // Workgroups lie in rows of this many along y (a launch holds fewer than 2^32
@@ -88,6 +95,18 @@ __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
       wave_max(static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
   return static_cast<uint64_t>(hi) << 32 | lo;
 }
+// Largest value over the W lanes (32 or 64) that hold a token, in all of them.
+template <int W>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  v = dpp_max_u32<0x140>(max_over8(v));   // row_mirror
+  const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);   // rows 0 and 1, 2 and 3
+  v = max(r[0], r[1]);
+  if constexpr (W == 64) {
+    const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = max(h[0], h[1]);
+  }
+  return v;
+}
 // v moved across lanes (zero where there is no lane to take it from).
 template <int CTRL, int ROWS = 0xF>
 __device__ __forceinline__ double dpp_f64(double v) {
@@ -106,6 +125,19 @@ __device__ __forceinline__ double wave_sum(double v) {
   v += dpp_f64<0x142, 0xA>(v);   // row_bcast 15, 31
   v += dpp_f64<0x143, 0xC>(v);
   return read_lane(v, 63);
+}
+// The same over the W lanes of a token (of 32 lanes: bit for bit the sum over a wave
+// whose other half is zero).
+template <int W>
+__device__ __forceinline__ double lanes_sum(double v) {
+  if constexpr (W == 64) return wave_sum(v);
+  v += dpp_f64<0x111>(v);
+  v += dpp_f64<0x112>(v);
+  v += dpp_f64<0x114>(v);
+  v += dpp_f64<0x118>(v);
+  v += dpp_f64<0x142, 0xA>(v);
+  const double a = read_lane(v, 31), b = read_lane(v, 63);
+  return (threadIdx.x & 32) ? b : a;
 }
 
 // exp(x) for x <= 0, to about one unit in the last place of 64 bits: x = n ln 2 +
@@ -241,11 +273,11 @@ __device__ __forceinline__ int best_lane(uint64_t k) {
 }
 
 // The topk largest keys in order: lane j gets the expert of slot j, -1 if none is
-// left; *left: the largest key after them (0: none).  Up to eight keys a lane are sorted first, so that a round only moves the
+// left.  Up to eight keys a lane are sorted first, so that a round only moves the
 // winner's up: neighbours change places where the second is larger, which
 // leaves equal ones in their order.
 template <int EPL, class Key>
-__device__ __forceinline__ int choose(Key* k, int topk, int lane, Key* left = nullptr) {
+__device__ __forceinline__ int choose(Key* k, int topk, int lane) {
   int id = -1;
   if constexpr (EPL <= 8) {
     int at[EPL];
@@ -277,7 +309,6 @@ __device__ __forceinline__ int choose(Key* k, int topk, int lane, Key* left = nu
         k[EPL - 1] = 0;
       }
     }
-    if (left) *left = wave_max(k[0]);
   } else {
     Key cur = k[0];
 #pragma unroll
@@ -303,7 +334,6 @@ __device__ __forceinline__ int choose(Key* k, int topk, int lane, Key* left = nu
       e = read_lane(e, who);
       if (lane == j) id = e;
     }
-    if (left) *left = wave_max(cur);
   }
   return id;
 }
@@ -355,122 +385,204 @@ __device__ __forceinline__ float sigmoid32(float x) {
   return x > 0.f ? s : t * s;
 }
 
-// The choice by sigmoid and bias through 32 bits, with what it proves.  A rank r in
-// 32 bits is off by less than 2^-20 (1 + |r|); as that keeps the order of the
-// bounds, the nth largest rank is off by as much.  Groups and experts are chosen by
-// 32 bits; the chosen ones' ranks are then formed in 64, one a lane.  The choice
-// stands if no group at the border could change sides, every chosen rank is above
-// the best one left by more than that one's error, and they descend (equal ones by
-// index): then it is the one that 64 bits make.  Else (about one token in 10^3 of 256
-// experts) false: the choice is made anew.  For tokens without NaN and +inf, and
-// groups within lanes.  id and p: of this lane's slot, p in 64 bits.
-template <int EPL, class L>
+// Sorts N keys (a power of two), the largest first: K. Batcher's merges of odd and
+// even places (D. Knuth, "The Art of Computer Programming" 3, 5.3.4).
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t* k) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int d = p; d >= 1; d /= 2)
+#pragma unroll
+      for (int i = d % p; i + d < N; ++i) {
+        if ((i - d % p) / d % 2 != 0 || i / (2 * p) != (i + d) / (2 * p)) continue;
+        const uint32_t hi = max(k[i], k[i + d]), lo = min(k[i], k[i + d]);
+        k[i] = hi;
+        k[i + d] = lo;
+      }
+}
+
+// Orders a wave's LDS accesses: what its lanes wrote before is there for the others.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The choice by sigmoid and bias through 32 bits, with what it proves.  A key is the
+// rank's 32 bits with the expert's place in its lane in the lowest ones, so that a
+// lane's keys differ and sorting them moves nothing else; a rank r read from a key
+// is off by less than kErr (1 + |r|) (2^-20 of it by score and sum, the rest by the
+// bits given away, at most 7 or 15 of 2^-23 r).  As that keeps the order of the
+// bounds, the nth largest rank is off by as much.
+//   Groups are chosen by the keys.  If some at the border could change sides (one
+// token in 10^3), each lane forms its best one or two ranks in 64 bits, which give
+// the groups' scores, unless a lane's next key could be among a group's best.
+//   Experts are chosen by the keys, one more than topk, each round's winner leaving
+// its expert in `slots` (LDS, one a lane).  Their ranks are then formed in 64 bits,
+// one a lane, and order them.  The choice stands if every chosen rank is above the
+// best key left by more than its error: then it is the one that 64 bits make.
+//   Else (about one token in 10^5 of 256 experts, and where two lanes won a round)
+// false: the choice is made anew.  For tokens without NaN and +inf, and groups
+// within lanes.  W lanes a token, this one's being `lane` of them from lane `base` of
+// the wave on; id and p: of this lane's slot, p in 64 bits.
+template <int W, int EPL, class L>
 __device__ __forceinline__ bool choose_by_32(const Router& a, const Exp& exp_neg, const float* x,
-                                             const L* row, int lane, int& id, double& p) {
-  constexpr float kErr = 0x1p-20f;
+                                             const L* row, int lane, int base, int* slots,
+                                             int& id, double& p) {
+  constexpr float kErr = EPL <= 8 ? 0x1p-19f : 0x1p-18f;
+  constexpr uint32_t kPlace = EPL - 1, kNone = 0x00800000u;   // keys below it: -inf
+  constexpr uint64_t kLanes = W == 64 ? ~0ull : 0xFFFFFFFFull;
+  slots[lane] = -1;
   float b[EPL];
   load_piece<EPL, float>(a.bias, lane * EPL, a.E, 0.f, b);
   uint32_t k[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const float v = sigmoid32(x[i]) + b[i];
-    k[i] = x[i] > -__builtin_inff() ? order_key(v) : 0u;   // (0 for NaN too)
+    const float r = sigmoid32(x[i]) + b[i];
+    // (not for NaN; never -0)
+    const float v = x[i] > -__builtin_inff() && r > -__builtin_inff() ? r : -__builtin_inff();
+    const int32_t bits = __builtin_bit_cast(int32_t, v);
+    const uint32_t key = static_cast<uint32_t>(bits) ^ (static_cast<uint32_t>(bits >> 31) | 0x80000000u);
+    k[i] = (key & ~kPlace) | (kPlace - i);
   }
+  sort_down<EPL>(k);
+  auto expert = [&](uint32_t key) {   // of this lane
+    return lane * EPL + static_cast<int>(kPlace - (key & kPlace));
+  };
+  auto score = [&](int e) { return sigmoid64(exp_neg, static_cast<double>(to_f32(row[e]))); };
+  // above every rank whose key is this one or a lower one
+  auto bound = [&](uint32_t key) {
+    const double v = key_value(key);
+    return v + static_cast<double>(kErr) * (1.0 + fabs(v));
+  };
+  uint64_t doubt = 0;   // lanes that see a reason against the choice
   if (a.choose_groups) {
-    uint32_t t1 = k[0], t2 = 0;
-#pragma unroll
-    for (int i = 1; i < EPL; ++i) {
-      t2 = max(t2, min(t1, k[i]));
-      t1 = max(t1, k[i]);
-    }
-    const int lanes = 1 << a.gshift, g = lane >> a.gshift, sub = lane & (lanes - 1);
+    uint32_t t1 = k[0], t2 = EPL > 1 ? k[EPL > 1 ? 1 : 0] : 0u;
+    // this lane's group, its place among the group's lanes, their number
+    const int shift = W == 64 ? a.gshift : a.gshift - 1;
+    const int lanes = 1 << shift, g = lane >> shift, sub = lane & (lanes - 1);
     two_best_of_lanes(t1, t2, lanes);
-    const bool any = t1 != 0 && g < a.groups, both = a.group_top == 2 && t2 != 0;
+    const bool any = t1 >= kNone && g < a.groups, both = a.group_top == 2 && t2 >= kNone;
     const float v1 = key_value(t1), v2 = both ? key_value(t2) : 0.f;
     // twice the errors of the two ranks, for the additions here
     const float off = 2.f * kErr * (2.f + fabsf(v1) + fabsf(v2));
     const float hi = any ? v1 + v2 + off : -__builtin_inff();
     const float lo = any ? v1 + v2 - off : -__builtin_inff();
-    int sure, perhaps;   // groups ahead of this lane's
-    if (lanes >= a.groups) {   // each of a group's lanes looks at one other group
-      const float oh = __shfl(hi, sub << a.gshift), ol = __shfl(lo, sub << a.gshift);
-      const bool other = sub < a.groups && sub != g;
-      const uint32_t s = static_cast<uint32_t>(
-          __builtin_amdgcn_ballot_w64(other && ol > hi) >> (g << a.gshift));
-      const uint32_t m = static_cast<uint32_t>(
-          __builtin_amdgcn_ballot_w64(other && !(oh < lo)) >> (g << a.gshift));
-      const uint32_t mine = (1u << lanes) - 1;   // (lanes <= 16)
-      sure = __builtin_popcount(s & mine);
-      perhaps = __builtin_popcount(m & mine);
-    } else {
-      sure = perhaps = 0;
-      for (int q = 0; q < a.groups; ++q) {
-        sure += read_lane(lo, q << a.gshift) > hi;
-        perhaps += q != g && !(read_lane(hi, q << a.gshift) < lo);
-      }
+    // groups ahead of this lane's, its lanes looking at one each
+    const int first = base + (g << shift);
+    const uint32_t mine = (1u << lanes) - 1;   // (lanes <= 16)
+    auto of_mine = [&](bool v) {
+      return __builtin_popcount(
+          static_cast<uint32_t>(__builtin_amdgcn_ballot_w64(v) >> first) & mine);
+    };
+    int sure = 0, perhaps = 0;
+    for (int q0 = 0; q0 < a.groups; q0 += lanes) {
+      const int q = q0 + sub, at = base + (q << shift);
+      const float oh = __shfl(hi, at), ol = __shfl(lo, at);
+      const bool other = q < a.groups && q != g;
+      sure += of_mine(other && ol > hi);
+      perhaps += of_mine(other && !(oh < lo));
     }
-    const bool stays = any && perhaps < a.top_groups;
-    if (__builtin_amdgcn_ballot_w64(any && !stays && sure < a.top_groups) != 0) return false;
+    bool stays = any && perhaps < a.top_groups;
+    const uint64_t border = __builtin_amdgcn_ballot_w64(any && !stays && sure < a.top_groups);
+    if (border != 0) {   // uniform
+      const bool two = EPL > 1 && a.group_top == 2, here = ((border >> base) & kLanes) != 0;
+      const uint32_t k1 = two ? k[EPL > 1 ? 1 : 0] : 0u;
+      const uint32_t k2 = two ? (EPL > 2 ? k[EPL > 2 ? 2 : 0] : 0u) : (EPL > 1 ? k[EPL > 1 ? 1 : 0] : 0u);
+      double d1 = -__builtin_inf(), d2 = d1;
+      if (k[0] >= kNone) d1 = score(expert(k[0])) + static_cast<double>(a.bias[expert(k[0])]);
+      if (k1 >= kNone) d2 = score(expert(k1)) + static_cast<double>(a.bias[expert(k1)]);
+      const double low = min(d1, d2);
+      d1 = max(d1, d2);
+      d2 = low;
+      two_best_of_lanes(d1, d2, lanes);
+      const bool unclear = here && k2 >= kNone && !(bound(k2) < (a.group_top == 2 ? d2 : d1));
+      const double sum = a.group_top == 2 && d2 > -__builtin_inf() ? d1 + d2 : d1;
+      int better = 0;
+      for (int q0 = 0; q0 < a.groups; q0 += lanes) {
+        const int q = q0 + sub;
+        const double o = __shfl(sum, base + (q << shift));
+        better += of_mine(q < a.groups && (o > sum || (o == sum && q < g)));
+      }
+      if (here) stays = any && better < a.top_groups;
+      doubt = __builtin_amdgcn_ballot_w64(unclear);
+    }
 #pragma unroll
     for (int i = 0; i < EPL; ++i) k[i] = stays ? k[i] : 0u;
   }
-  uint32_t left;
-  id = choose<EPL, uint32_t>(k, a.topk, lane, &left);
+  const int rounds = a.topk < W ? a.topk + 1 : W;
+  for (int j = 0; j < rounds; ++j) {
+    const uint32_t best = lanes_max<W>(k[0]);
+    const bool won = k[0] == best && best >= kNone;
+    const uint64_t at = __builtin_amdgcn_ballot_w64(won);
+    if constexpr (W == 64) {
+      doubt |= at & (at - 1);
+    } else {
+      const uint32_t l = static_cast<uint32_t>(at), h = static_cast<uint32_t>(at >> 32);
+      doubt |= static_cast<uint64_t>(h & (h - 1)) << 32 | (l & (l - 1));
+    }
+    if (won) {
+      slots[j] = expert(best);
+#pragma unroll
+      for (int i = 0; i + 1 < EPL; ++i) k[i] = k[i + 1];
+      k[EPL - 1] = 0;
+    }
+  }
+  const uint32_t left = lanes_max<W>(k[0]);
+  wave_lds_fence();
+  id = slots[lane];
   const bool live = id >= 0;
   p = 0.0;
   double rank = -__builtin_inf();
   if (live) {
-    p = sigmoid64(exp_neg, static_cast<double>(to_f32(row[id])));
+    p = score(id);
     rank = p + static_cast<double>(a.bias[id]);
   }
-  const float best_left = key_value(left);
-  bool wrong = live && left != 0 &&
-               !(rank > static_cast<double>(best_left) +
-                            static_cast<double>(kErr) * (1.0 + fabs(static_cast<double>(best_left))));
   const double next = __shfl_down(rank, 1);
   const int next_id = __shfl_down(id, 1);
-  wrong |= lane < 63 && next_id >= 0 && !(rank > next || (rank == next && id < next_id));
-  return __builtin_amdgcn_ballot_w64(wrong) == 0;
+  const bool turned = lane < W - 1 && next_id >= 0 && !(rank > next || (rank == next && id < next_id));
+  if (__builtin_amdgcn_ballot_w64(turned) != 0) {   // uniform
+    int place = 0;
+    for (int j = 0; j < rounds; ++j) {
+      const double r = __shfl(rank, base + j);
+      const int e = __shfl(id, base + j);
+      place += e >= 0 && (r > rank || (r == rank && e < id));
+    }
+    wave_lds_fence();
+    if (live) slots[place] = lane;   // (places of the live, which are the first lanes)
+    wave_lds_fence();
+    const int from = base + (live ? slots[lane] : lane);
+    id = __shfl(id, from);
+    p = __shfl(p, from);
+    rank = __shfl(rank, from);
+  }
+  if (lane >= a.topk) {
+    id = -1;
+    p = 0.0;
+  }
+  doubt |= __builtin_amdgcn_ballot_w64(id >= 0 && left >= kNone && !(rank > bound(left)));
+  return ((doubt >> base) & kLanes) == 0;
 }
 
 __device__ __forceinline__ int64_t wave_token() {
   return ((int64_t)blockIdx.y * kRowBlocks + blockIdx.x) * kWaves + wave_id();
 }
 
-}  // namespace
+__device__ __forceinline__ void store_slot(const Router& a, int64_t t, int slot, int id, bool bad,
+                                           double w) {
+  if (slot >= a.topk) return;
+  a.ids[t * a.topk + slot] = id;
+  a.weights[t * a.topk + slot] =
+      bad && id >= 0 ? __builtin_nanf("") : static_cast<float>(static_cast<double>(a.scale) * w);
+}
 
+// Token t by a wave, every value that the choice needs in 64 bits; mine: LDS for E
+// values where groups are chosen that do not lie within lanes.
 template <int EPL, class L>
-__global__ __launch_bounds__(64 * kWaves) void k_router_fwd(Router a) {
-  extern __shared__ double lds[];   // [kWaves][E] where groups are chosen
+__device__ __forceinline__ void route(const Router& a, const Exp& exp_neg, const Logits<EPL, L>& l,
+                                      int64_t t, bool in, double* mine) {
   const int lane = threadIdx.x & 63;
-  const int64_t token = wave_token();
-  const bool in = token < a.tokens;
-  // (a wave without a token repeats the last one, for the barriers)
-  const int64_t t = in ? token : a.tokens - 1;
-  Logits<EPL, L> l;
-  l.load(static_cast<const L*>(a.logits) + t * a.E, a.E, lane);
-
-  const Exp exp_neg;
-  auto store = [&](int id, double w) {
-    if (in && lane < a.topk) {
-      a.ids[t * a.topk + lane] = id;
-      a.weights[t * a.topk + lane] =
-          l.bad && id >= 0 ? __builtin_nanf("")
-                           : static_cast<float>(static_cast<double>(a.scale) * w);
-    }
-  };
-  if (a.bias && a.sigmoid && !l.bad && (!a.choose_groups || a.in_lanes)) {   // uniform
-    int id;
-    double p;
-    if (choose_by_32<EPL, L>(a, exp_neg, l.x, static_cast<const L*>(a.logits) + t * a.E, lane, id,
-                             p)) {
-      const double total = a.renorm ? wave_sum(p) : 1.0;
-      if (total > 1e-250) {   // (else every chosen logit is below about -575)
-        store(id, p / total);
-        return;
-      }
-    }
-  }
   float top = 0.f;
   double p[EPL], sum = 0.0;   // p: scores where they rank, exps otherwise unused
   const bool sums = a.choose_groups && a.group_top == 2;
@@ -516,7 +628,6 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_fwd(Router a) {
       for (int i = 0; i < EPL; ++i) add(v[i]);
       two_best_of_lanes(t1, t2, lanes);
     } else {
-      double* mine = lds + (int64_t)wave_id() * a.E;
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
         if (lane * EPL + i < a.E) mine[lane * EPL + i] = v[i];
@@ -566,12 +677,18 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_fwd(Router a) {
       id >= 0 ? to_f32(static_cast<const L*>(a.logits)[t * a.E + id]) : 0.f;
   const bool live = id >= 0;
   double w;
-  if (a.renorm) {
+  if (a.sigmoid) {
+    w = live ? sigmoid64(exp_neg, lx) : 0.0;
+    double total = a.renorm ? wave_sum(w) : 1.0;
+    if (!(total > kLeastSum)) {   // uniform
+      w = relative_weight(a, exp_neg, live, lx);
+      total = wave_sum(w);
+    }
+    w = live ? w / total : 0.0;
+  } else if (a.renorm) {
     w = relative_weight(a, exp_neg, live, lx);
     const double total = wave_sum(w);
     w = live ? w / total : 0.0;
-  } else if (a.sigmoid) {
-    w = live ? sigmoid64(exp_neg, lx) : 0.0;
   } else {
     if (sum == 0.0) {
       top = l.top();
@@ -579,7 +696,72 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_fwd(Router a) {
     }
     w = live ? exp_neg(static_cast<double>(lx) - static_cast<double>(top)) / sum : 0.0;
   }
-  store(id, w);
+  if (in) store_slot(a, t, lane, id, l.bad, w);
+}
+
+}  // namespace
+
+template <int EPL, class L>
+__global__ __launch_bounds__(64 * kWaves) void k_router_fwd(Router a) {
+  extern __shared__ double lds[];   // [kWaves][E] where groups are chosen
+  __shared__ int slots[kWaves][64];
+  const int lane = threadIdx.x & 63;
+  const int64_t token = wave_token();
+  const bool in = token < a.tokens;
+  // (a wave without a token repeats the last one, for the barriers)
+  const int64_t t = in ? token : a.tokens - 1;
+  const L* row = static_cast<const L*>(a.logits) + t * a.E;
+  Logits<EPL, L> l;
+  l.load(row, a.E, lane);
+  const Exp exp_neg;
+  if (a.bias && a.sigmoid && !l.bad && (!a.choose_groups || a.in_lanes)) {   // uniform
+    int id;
+    double p;
+    if (choose_by_32<64, EPL, L>(a, exp_neg, l.x, row, lane, 0, slots[wave_id()], id, p)) {
+      const double total = a.renorm ? wave_sum(p) : 1.0;
+      if (total > kLeastSum) {
+        if (in) store_slot(a, t, lane, id, false, p / total);
+        return;
+      }
+    }
+  }
+  route<EPL, L>(a, exp_neg, l, t, in, lds + (int64_t)wave_id() * a.E);
+}
+
+// The same by sigmoid and bias with two tokens a wave: the rounds of the choice, its
+// proof and the weights take as many instructions for both.  A token whose choice is
+// not proven gets the whole wave.  (EPL experts a lane of 32.)
+template <int EPL, class L>
+__global__ __launch_bounds__(64 * kWaves) void k_router_fwd_pairs(Router a) {
+  __shared__ int slots[kWaves][64];
+  const int half = (threadIdx.x >> 5) & 1, lane = threadIdx.x & 31;
+  const int64_t first = 2 * wave_token();
+  const bool in = first + half < a.tokens;
+  const int64_t t = in ? first + half : a.tokens - 1;
+  const L* row = static_cast<const L*>(a.logits) + t * a.E;
+  float x[EPL];
+  load_piece<EPL, L>(row, lane * EPL, a.E, -__builtin_inff(), x);
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) bad |= __builtin_amdgcn_classf(x[i], 0x203);
+  const Exp exp_neg;
+  int id;
+  double p;
+  bool ok = choose_by_32<32, EPL, L>(a, exp_neg, x, row, lane, 32 * half,
+                                     slots[wave_id()] + 32 * half, id, p);
+  const double total = a.renorm ? lanes_sum<32>(p) : 1.0;
+  ok = ok && total > kLeastSum;
+  const uint64_t no = __builtin_amdgcn_ballot_w64(bad || !ok);
+  const bool stands = (static_cast<uint32_t>(no >> (32 * half))) == 0;
+  if (stands && in) store_slot(a, t, lane, id, false, p / total);
+  if (no == 0) return;   // (uniform)
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    if (static_cast<uint32_t>(no >> (32 * h)) == 0 || first + h >= a.tokens) continue;   // uniform
+    Logits<EPL / 2, L> l;
+    l.load(static_cast<const L*>(a.logits) + (first + h) * a.E, a.E, threadIdx.x & 63);
+    route<EPL / 2, L>(a, exp_neg, l, first + h, true, nullptr);
+  }
 }
 
 // dlogits of one token.  Lane j holds slot j; sums over the slots run in their
@@ -705,11 +887,31 @@ Router router(const void* logits, int64_t tokens, int E, const qlora_router_conf
 }
 
 
+// Two tokens a wave by sigmoid and bias, where their slots and groups lie within 32
+// lanes and there are enough of them: 256 experts, 8 groups, topk 8, one and two a
+// wave: 1024 tokens 5.4 and 5.8 us, 2048 5.4 and 5.3, 4096 7.3 and 6.5, 8192 10.7 and
+// 8.0, 32768 27.9 and 20.3 (64 experts, topk 6: 18.8 and 12.0).
+bool in_pairs(const Router& a) {
+  return a.bias && a.sigmoid && a.tokens >= kPairTokens && a.E <= 256 && a.topk <= 32 &&
+         (!a.choose_groups || (a.in_lanes && a.gshift > 0));
+}
+
+template <int EPL, class L>
+hipError_t launch_pairs(const Router& a, hipStream_t st) {
+  const int64_t blocks = (a.tokens + 2 * kWaves - 1) / (2 * kWaves);
+  const dim3 grid(static_cast<unsigned>(std::min(blocks, kRowBlocks)),
+                  static_cast<unsigned>((blocks + kRowBlocks - 1) / kRowBlocks));
+  hipLaunchKernelGGL((k_router_fwd_pairs<EPL, L>), grid, dim3(64 * kWaves), 0, st, a);
+  return hipGetLastError();
+}
+
 template <bool BACK, int EPL, class L>
 hipError_t launch(const Router& a, hipStream_t st) {
   const int64_t blocks = (a.tokens + kWaves - 1) / kWaves;
   const dim3 grid(static_cast<unsigned>(std::min(blocks, kRowBlocks)),
                   static_cast<unsigned>((blocks + kRowBlocks - 1) / kRowBlocks));
+  if constexpr (!BACK && EPL <= 4)
+    if (in_pairs(a)) return launch_pairs<2 * EPL, L>(a, st);
   if constexpr (BACK)
     hipLaunchKernelGGL((k_router_bwd<EPL, L>), grid, dim3(64 * kWaves), 0, st, a);
   else

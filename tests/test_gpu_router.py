@@ -152,6 +152,53 @@ def test_choices_next_to_each_other(E, groups, tg, gt, score):
                     assert close.all() or abs(s[tg - 1] - s[tg]) <= 2.0 ** -49, (i, got[i], want)
 
 
+@pytest.mark.parametrize("E,topk,groups,tg,gt,fp32", [
+    (256, 8, 8, 4, 2, False), (256, 8, 8, 4, 2, True), (256, 32, 4, 2, 1, True), (250, 7, 1, 1, 1, True),
+    (128, 6, 16, 5, 2, True), (128, 1, 4, 2, 1, False), (100, 6, 1, 1, 1, False), (64, 6, 8, 3, 2, True),
+    (64, 6, 32, 9, 2, True), (33, 5, 1, 1, 1, True), (4, 4, 1, 1, 1, False), (1, 1, 1, 1, 1, True)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_many_tokens_as_few(E, topk, groups, tg, gt, fp32, renorm):
+    """Two tokens share a wave in a large batch: every token gets the bits that it gets in
+    a small one, with ranks next to each other and equal, masked, NaN and tiny scores."""
+    need_gpu()
+    say(f"router, 2051 tokens as few E={E} topk={topk} groups={groups}/{tg}/{gt} fp32={fp32}")
+    rng = np.random.default_rng(E + topk)
+    T = 2051
+    x = rng.standard_normal((T, E)).astype(np.float32)
+    x[100:200] = x[100]
+    x[200:300] = np.round(x[200:300])
+    x[300:400] = x[300] + 1e-6 * rng.standard_normal((100, E))
+    x[400:500][rng.random((100, E)) < 0.7] = -np.inf
+    x[500:502] = -np.inf
+    x[502:504] = -700 + x[502:504]           # sigmoids that hardly are numbers
+    x[504:506, 0] = np.nan
+    x[507, E - 1] = np.inf
+    t = torch.from_numpy(x).to(dev())
+    t = t if fp32 else t.bfloat16()
+    xs = t.double().cpu().numpy()
+    levels = [np.zeros(E), 0.05 * rng.standard_normal(E), 0.5 - orr.scores(xs[100], "sigmoid"),
+              0.5 - orr.scores(xs[300], "sigmoid")]
+    special = levels[1].copy()
+    special[0], special[E // 2], special[E - 1] = np.inf, -np.inf, np.nan
+    for i, level in enumerate(levels + [special]):
+        b = torch.from_numpy(level.astype(np.float32)).to(dev())
+        args = (topk, "sigmoid", b, groups, tg, gt, renorm, 2.5)
+        I = torch.full((T + 2, topk), 77, dtype=torch.int32, device=dev())
+        W = torch.full((T + 2, topk), 77.0, device=dev())
+        q.qlora_router_fwd(t, *args, ids=I[1:-1], weights=W[1:-1])
+        few = [q.qlora_router_fwd(t[j:j + 293], *args) for j in range(0, T, 293)]
+        torch.cuda.synchronize()
+        ids, w = torch.cat([f[0] for f in few]), torch.cat([f[1] for f in few])
+        assert (I[0] == 77).all() and (I[-1] == 77).all() and (W[0] == 77).all() and (W[-1] == 77).all()
+        np.testing.assert_array_equal(I[1:-1].cpu().numpy(), ids.cpu().numpy())
+        np.testing.assert_array_equal(W[1:-1].cpu().numpy(), w.cpu().numpy())
+        if i == 1:   # ranks that lie apart
+            some = np.r_[0:20, 400:420, 500:504, 2040:2051]
+            wid, ww = orr.fwd(xs[some], topk, "sigmoid", b.double().cpu().numpy(), groups, tg, gt, renorm, 2.5)
+            np.testing.assert_array_equal(ids.cpu().numpy()[some], wid)
+            within("weights", w[torch.from_numpy(some).to(dev())], ww, F32 * np.abs(ww) + 2.0 ** -149)
+
+
 def test_gradient_of_a_sure_choice():
     """Where one expert takes all but 1e-6, the gradient keeps its digits."""
     need_gpu()
