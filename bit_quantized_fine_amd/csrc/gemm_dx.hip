@@ -516,9 +516,30 @@ __global__ __launch_bounds__(XT) void k_dx_gemm(DxArgs args, Nf4Tables tb) {
   }
 }
 
+// The same for kQ tokens at most, in tiles of as many.
+template <int kForm, int kQ, bool kDrop>
+__global__ __launch_bounds__(XT) void k_dx_few(DxArgs args, Nf4Tables tb) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+  if constexpr (kForm != kFormDense)
+    build_rep_pair_table<XT>(reinterpret_cast<char*>(dyn), load_levels(tb), threadIdx.x);
+  const int lin = xcd_remap_dx(blockIdx.x, static_cast<int>(gridDim.x));
+  const int z = lin / args.ptiles, pt = lin - z * args.ptiles;
+  dx_tile<kForm, kQ, false, kDrop>(args, dyn, 0, 0, args.M, pt, z);
+}
+
 namespace {
 
-constexpr int kTileQ = 256;   // tokens a tile
+constexpr int kTileQ = 256;   // tokens a tile of k_dx_gemm
+
+template <int kForm, int kQ, bool kExperts, bool kDrop>
+constexpr auto dx_kernel() {
+  if constexpr (kQ < kTileQ) {
+    static_assert(!kExperts);
+    return &k_dx_few<kForm, kQ, kDrop>;
+  } else {
+    return &k_dx_gemm<kForm, kQ, kExperts, kDrop>;
+  }
+}
 
 template <int kForm, int kQ, bool kExperts, bool kDrop>
 hipError_t launch_dx_tiles(const uint16_t* dY, int64_t M, const Nf4View& w, int64_t N,
@@ -526,9 +547,9 @@ hipError_t launch_dx_tiles(const uint16_t* dY, int64_t M, const Nf4View& w, int6
                            float* part, const Nf4Tables& tb, hipStream_t stream, int qtiles,
                            const GemmSplit& sp, const int* offsets, int E, const Drop& d) {
   constexpr int kLds = DxTile<kQ>::LDS;
+  const auto kernel = dx_kernel<kForm, kQ, kExperts, kDrop>();
   static LdsLimit lds;
-  const hipError_t attr = lds.raise(
-      reinterpret_cast<const void*>(&k_dx_gemm<kForm, kQ, kExperts, kDrop>), kLds);
+  const hipError_t attr = lds.raise(reinterpret_cast<const void*>(kernel), kLds);
   if (attr != hipSuccess) return attr;
   if (sp.splits > 1 && !part) return hipErrorInvalidValue;
   const int ptiles = static_cast<int>((w.K + XP - 1) / XP);
@@ -538,8 +559,7 @@ hipError_t launch_dx_tiles(const uint16_t* dY, int64_t M, const Nf4View& w, int6
   const dim3 grid(kExperts ? static_cast<unsigned>(
                                  xcd_deal_grid((int64_t)qtiles * sp.splits, ptiles))
                            : ptiles * qtiles * sp.splits);
-  hipLaunchKernelGGL((k_dx_gemm<kForm, kQ, kExperts, kDrop>), grid, dim3(XT), kLds, stream, args,
-                     tb);
+  hipLaunchKernelGGL(kernel, grid, dim3(XT), kLds, stream, args, tb);
   return hipGetLastError();
 }
 
@@ -556,11 +576,22 @@ hipError_t launch_dx_gemm(const uint16_t* dY, int64_t M, const Nf4View& w,
   const int qtiles = static_cast<int>((M + kTileQ - 1) / kTileQ);
   const GemmSplit sp = dx_gemm_split(M, w.N, w.K);
   if (w.dense && d.on()) return hipErrorInvalidValue;
-  auto launch = w.dense ? launch_dx_tiles<kFormDense, kTileQ, false, false>
-                : d.on() ? (w.dq ? launch_dx_tiles<kFormDq, kTileQ, false, true>
-                                 : launch_dx_tiles<kFormNoDq, kTileQ, false, true>)
-                         : (w.dq ? launch_dx_tiles<kFormDq, kTileQ, false, false>
-                                 : launch_dx_tiles<kFormNoDq, kTileQ, false, false>);
+  // Up to 64 and up to 128 tokens, a tile of as many: the sums run in the same order and
+  // give the same bits, without 256 tokens' staging and products (a layer's backward from
+  // an 8-bit checkpoint in a graph, r = 16 at 1024 x 1024, 64 else: 16 tokens of 1024 x
+  // 1024 26.5 us in tiles of 256 and 18.9, of 11008 x 4096 46.7 and 33.3; 128 tokens of
+  // 11008 x 4096 55.1 and 49.4).
+  auto tiles = [&](auto q) {
+    constexpr int kQ = decltype(q)::value;
+    return w.dense ? launch_dx_tiles<kFormDense, kQ, false, false>
+           : d.on() ? (w.dq ? launch_dx_tiles<kFormDq, kQ, false, true>
+                            : launch_dx_tiles<kFormNoDq, kQ, false, true>)
+                    : (w.dq ? launch_dx_tiles<kFormDq, kQ, false, false>
+                            : launch_dx_tiles<kFormNoDq, kQ, false, false>);
+  };
+  auto launch = M <= 64    ? tiles(std::integral_constant<int, 64>{})
+                : M <= 128 ? tiles(std::integral_constant<int, 128>{})
+                           : tiles(std::integral_constant<int, kTileQ>{});
   prof_begin(1, stream);
   hipError_t e = launch(dY, M, w, w.N, G, A, r, s, dX, part, tb, stream, qtiles, sp, nullptr, 0, d);
   if (e == hipSuccess && sp.splits > 1 && add_up)
