@@ -16,8 +16,8 @@
 // Bound by the vector instructions of a wave, about 650 by sigmoid, bias and groups for
 // two tokens: 8192 tokens of 256 experts, topk 8, take 8.0 us back to back in a graph
 // (8.4 MB would take 1.9; one token a wave 10.7, wholly in 64 bits 15).  Smaller batches
-// are a launch and the call (8 us).  The backward of 8192 tokens of 64 experts takes
-// 5.6 us.
+// are a launch and the call (8 us).  The backward of 8192 tokens of 64 experts takes 4.5
+// us so, of 256 5.7.
 //
 // Weights and gradients are formed in 64 bits too, where they cost one lane's
 // work a slot: what is left of 1 - p where one expert takes nearly all would
@@ -38,12 +38,15 @@ constexpr int kWaves = 4;          // waves a workgroup
 constexpr int kMaxE = 1024;
 constexpr double kLeastSum = 1e-250;     // of sigmoids that are divided by their sum as
                                          // they are (below, every logit is under -575)
-constexpr int64_t kPairTokens = 2048;   // from here on two tokens share a wave (in_pairs)
+constexpr int64_t kPairTokens = 2048;      // from here on two tokens share a wave (in_pairs,
+constexpr int64_t kPairTokensBack = 4096;  // back_in_pairs)
 constexpr int kMaxTopk = 64;
 constexpr int kMaxGroups = 64;
 // Workgroups lie in rows of this many along y (a launch holds fewer than 2^32
 // threads along x).
 constexpr int64_t kRowBlocks = int64_t(1) << 23;
+
+typedef double f64x2 __attribute__((ext_vector_type(2)));
 
 struct Router {
   const void* logits;
@@ -76,6 +79,13 @@ __device__ __forceinline__ double read_lane(double v, int lane) {
   const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), lane);
   const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), lane);
   return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// Orders a wave's LDS accesses: what its lanes wrote before is there for the others.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // Largest value over the wave (zero where no lane has a larger one).
@@ -224,13 +234,15 @@ template <int EPL, class L>
 struct Logits {
   float x[EPL];
   bool bad;     // a NaN or +inf among them
-  __device__ void load(const L* row, int E, int lane) {
+  // W lanes a token, `lane` of them from lane `base` of the wave on
+  template <int W>
+  __device__ void load(const L* row, int E, int lane, int base) {
     load_piece<EPL, L>(row, lane * EPL, E, -__builtin_inff(), x);
     uint64_t b = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)   // signalling and quiet NaN, +inf
       b |= __builtin_amdgcn_ballot_w64(__builtin_amdgcn_classf(x[i], 0x203));
-    bad = b != 0;
+    bad = W == 64 ? b != 0 : static_cast<uint32_t>(b >> base) != 0;
   }
   // the largest, -inf without any
   __device__ float top() const {
@@ -367,10 +379,11 @@ __device__ __forceinline__ void two_best_of_lanes(T& t1, T& t2, int lanes) {
 // Relative weights u of the chosen (0 for lanes without one), for the
 // renormalised forms: exp(x - m), times 1 / (1 + exp(-|x|)) for a sigmoid, whose
 // factor exp(min(x, 0)) is the one shifted by m.
+template <int W>
 __device__ __forceinline__ double relative_weight(const Router& a, const Exp& exp_neg, bool live,
                                                   float lx) {
   const float v = a.sigmoid ? min(lx, 0.f) : lx;
-  const float m = key_value(wave_max(live ? order_key(v) : 0u));
+  const float m = key_value(lanes_max<W>(live ? order_key(v) : 0u));
   if (!live) return 0.0;
   const double u = exp_neg(static_cast<double>(v) - static_cast<double>(m));
   return a.sigmoid ? u / (1.0 + exp_neg(-fabs(static_cast<double>(lx)))) : u;
@@ -400,13 +413,6 @@ __device__ __forceinline__ void sort_down(uint32_t* k) {
         k[i] = hi;
         k[i + d] = lo;
       }
-}
-
-// Orders a wave's LDS accesses: what its lanes wrote before is there for the others.
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // The choice by sigmoid and bias through 32 bits, with what it proves.  A key is the
@@ -681,12 +687,12 @@ __device__ __forceinline__ void route(const Router& a, const Exp& exp_neg, const
     w = live ? sigmoid64(exp_neg, lx) : 0.0;
     double total = a.renorm ? wave_sum(w) : 1.0;
     if (!(total > kLeastSum)) {   // uniform
-      w = relative_weight(a, exp_neg, live, lx);
+      w = relative_weight<64>(a, exp_neg, live, lx);
       total = wave_sum(w);
     }
     w = live ? w / total : 0.0;
   } else if (a.renorm) {
-    w = relative_weight(a, exp_neg, live, lx);
+    w = relative_weight<64>(a, exp_neg, live, lx);
     const double total = wave_sum(w);
     w = live ? w / total : 0.0;
   } else {
@@ -712,7 +718,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_fwd(Router a) {
   const int64_t t = in ? token : a.tokens - 1;
   const L* row = static_cast<const L*>(a.logits) + t * a.E;
   Logits<EPL, L> l;
-  l.load(row, a.E, lane);
+  l.template load<64>(row, a.E, lane, 0);
   const Exp exp_neg;
   if (a.bias && a.sigmoid && !l.bad && (!a.choose_groups || a.in_lanes)) {   // uniform
     int id;
@@ -739,19 +745,16 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_fwd_pairs(Router a) {
   const bool in = first + half < a.tokens;
   const int64_t t = in ? first + half : a.tokens - 1;
   const L* row = static_cast<const L*>(a.logits) + t * a.E;
-  float x[EPL];
-  load_piece<EPL, L>(row, lane * EPL, a.E, -__builtin_inff(), x);
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) bad |= __builtin_amdgcn_classf(x[i], 0x203);
+  Logits<EPL, L> l;
+  l.template load<32>(row, a.E, lane, 32 * half);
   const Exp exp_neg;
   int id;
   double p;
-  bool ok = choose_by_32<32, EPL, L>(a, exp_neg, x, row, lane, 32 * half,
+  bool ok = choose_by_32<32, EPL, L>(a, exp_neg, l.x, row, lane, 32 * half,
                                      slots[wave_id()] + 32 * half, id, p);
   const double total = a.renorm ? lanes_sum<32>(p) : 1.0;
-  ok = ok && total > kLeastSum;
-  const uint64_t no = __builtin_amdgcn_ballot_w64(bad || !ok);
+  ok = ok && !l.bad && total > kLeastSum;
+  const uint64_t no = __builtin_amdgcn_ballot_w64(!ok);
   const bool stands = (static_cast<uint32_t>(no >> (32 * half))) == 0;
   if (stands && in) store_slot(a, t, lane, id, false, p / total);
   if (no == 0) return;   // (uniform)
@@ -759,21 +762,32 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_fwd_pairs(Router a) {
   for (int h = 0; h < 2; ++h) {
     if (static_cast<uint32_t>(no >> (32 * h)) == 0 || first + h >= a.tokens) continue;   // uniform
     Logits<EPL / 2, L> l;
-    l.load(static_cast<const L*>(a.logits) + (first + h) * a.E, a.E, threadIdx.x & 63);
+    l.template load<64>(static_cast<const L*>(a.logits) + (first + h) * a.E, a.E,
+                        threadIdx.x & 63, 0);
     route<EPL / 2, L>(a, exp_neg, l, first + h, true, nullptr);
   }
 }
 
-// dlogits of one token.  Lane j holds slot j; sums over the slots run in their
-// order in every lane.
-template <int EPL, class L>
+// dlogits, W lanes a token (32: two tokens a wave).  Lane j holds slot j; sums over the
+// slots run in their order in every lane.  A slot's gradient finds its expert through
+// LDS.
+template <int W, int EPL, class L>
 __global__ __launch_bounds__(64 * kWaves) void k_router_bwd(Router a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = wave_token();
-  if (t >= a.tokens) return;
+  __shared__ __attribute__((aligned(16))) double grads[kWaves * 64 * EPL];   // [token][expert]
+  __shared__ __attribute__((aligned(16))) f64x2 slots[kWaves * 64];
+  constexpr int T = 64 / W;
+  const int lane = threadIdx.x & (W - 1), base = threadIdx.x & 63 & ~(W - 1);
+  const int place = threadIdx.x / W;   // of the token in the workgroup
+  const int64_t token = T * wave_token() + base / W;
+  const bool in = token < a.tokens;
+  const int64_t t = in ? token : a.tokens - 1;
   const L* row = static_cast<const L*>(a.logits) + t * a.E;
+  double* const grad = grads + place * W * EPL;
+  f64x2* const slot = slots + place * W;
   Logits<EPL, L> l;
-  l.load(row, a.E, lane);
+  l.template load<W>(row, a.E, lane, base);
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) grad[lane * EPL + i] = 0.0;
   int id = -1;
   double dw = 0.0;
   float lx = 0.f;
@@ -789,46 +803,66 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_bwd(Router a) {
   const bool live = id >= 0;
   const Exp exp_neg;
   double d = 0.0;       // of this slot's expert
-  double s = 0.0;       // softmax without renorm: sum p dw
-  double p[EPL], r = 0.0;
+  double rest[EPL];     // softmax without renorm: of every expert, -p sum_j p_j dw_j
   if (a.renorm) {
-    const double u = relative_weight(a, exp_neg, live, lx), total = wave_sum(u);
+    const double u = relative_weight<W>(a, exp_neg, live, lx), total = lanes_sum<W>(u);
     const double q = live ? u / total : 0.0;
+    slot[lane] = f64x2{q, dw};
+    wave_lds_fence();
     // q_i sum_j q_j (dw_i - dw_j): no difference of nearly equal sums
     double v = 0.0;
-    for (int j = 0; j < a.topk; ++j) v += read_lane(q, j) * (dw - read_lane(dw, j));
+    for (int j = 0; j < a.topk; ++j) v += slot[j].x * (dw - slot[j].y);
     d = q * v;
     if (a.sigmoid) d *= sigmoid64(exp_neg, -static_cast<double>(lx));
   } else if (a.sigmoid) {
     d = live ? dw * sigmoid64(exp_neg, lx) * sigmoid64(exp_neg, -static_cast<double>(lx)) : 0.0;
-  } else {
+  } else if constexpr (W == 64) {   // (its sum over the experts would run in another order)
     const float top = l.top();
-    r = 1.0 / l.exps(exp_neg, top, p);
+    const double r = 1.0 / l.exps(exp_neg, top, rest);
     d = live ? dw * exp_neg(static_cast<double>(lx) - static_cast<double>(top)) * r : 0.0;
-    for (int j = 0; j < a.topk; ++j) s += read_lane(d, j);
-  }
-  double out[EPL];
+    slot[lane].x = d;
+    wave_lds_fence();
+    double sum = 0.0;
+    for (int j = 0; j < a.topk; ++j) sum += slot[j].x;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i)
-    out[i] = !a.renorm && !a.sigmoid && l.x[i] > -__builtin_inff() ? -p[i] * r * s : 0.0;
-  for (int j = 0; j < a.topk; ++j) {
-    const int e = read_lane(live ? id : -1, j) - lane * EPL;
-    const double v = read_lane(d, j);
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) out[i] += e == i ? v : 0.0;
+    for (int i = 0; i < EPL; ++i)
+      rest[i] = l.x[i] > -__builtin_inff() ? -rest[i] * r * sum : 0.0;
   }
-  L* dst = static_cast<L*>(a.dlogits) + t * a.E;
+  // an expert named by several slots gets their sum
+  wave_lds_fence();
+  if (live) grad[id] = lane;
+  wave_lds_fence();
+  const uint64_t twice = __builtin_amdgcn_ballot_w64(live && grad[live ? id : 0] != lane);
+  wave_lds_fence();
+  if (live) grad[id] = twice == 0 ? d : 0.0;
+  wave_lds_fence();
+  if (twice != 0) {   // uniform
+    for (int j = 0; j < a.topk; ++j) {
+      if (live && lane == j) grad[id] += d;
+      wave_lds_fence();
+    }
+  }
+  L out[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = lane * EPL + i;
+    double g = grad[lane * EPL + i];
+    if constexpr (W == 64)
+      if (!a.renorm && !a.sigmoid) g += rest[i];
     const float v = l.bad ? __builtin_nanf("")
-                          : static_cast<float>(static_cast<double>(a.scale) * out[i]);
-    if (e < a.E) {
-      if constexpr (sizeof(L) == 2)
-        dst[e] = static_cast<L>(pack_bf16x2(v, 0.f));
-      else
-        dst[e] = v;
-    }
+                          : static_cast<float>(static_cast<double>(a.scale) * g);
+    if constexpr (sizeof(L) == 2)
+      out[i] = static_cast<L>(pack_bf16x2(v, 0.f));
+    else
+      out[i] = v;
+  }
+  if (!in) return;
+  L* const dst = static_cast<L*>(a.dlogits) + t * a.E + lane * EPL;
+  if (a.E % EPL == 0) {
+    if (lane * EPL < a.E) __builtin_memcpy(dst, out, sizeof(out));
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (lane * EPL + i < a.E) dst[i] = out[i];
   }
 }
 
@@ -896,26 +930,38 @@ bool in_pairs(const Router& a) {
          (!a.choose_groups || (a.in_lanes && a.gshift > 0));
 }
 
-template <int EPL, class L>
-hipError_t launch_pairs(const Router& a, hipStream_t st) {
-  const int64_t blocks = (a.tokens + 2 * kWaves - 1) / (2 * kWaves);
-  const dim3 grid(static_cast<unsigned>(std::min(blocks, kRowBlocks)),
-                  static_cast<unsigned>((blocks + kRowBlocks - 1) / kRowBlocks));
-  hipLaunchKernelGGL((k_router_fwd_pairs<EPL, L>), grid, dim3(64 * kWaves), 0, st, a);
-  return hipGetLastError();
+// In the backward wherever no sum over a token's experts is formed (its order would
+// change): 256 experts, topk 8, softmax renormalised, one and two a wave: 2048 tokens
+// 3.9 and 4.3 us, 4096 4.8 and 4.8, 8192 6.3 and 5.7, 32768 16.0 and 13.9 (64 experts,
+// topk 6: 3.6 and 3.7, 4.2 and 3.9, 5.2 and 4.5, 12.5 and 8.7).
+bool back_in_pairs(const Router& a) {
+  return (a.sigmoid || a.renorm) && a.tokens >= kPairTokensBack && a.E <= 256 && a.topk <= 32;
+}
+
+dim3 grid_of(int64_t blocks) {
+  return dim3(static_cast<unsigned>(std::min(blocks, kRowBlocks)),
+              static_cast<unsigned>((blocks + kRowBlocks - 1) / kRowBlocks));
 }
 
 template <bool BACK, int EPL, class L>
 hipError_t launch(const Router& a, hipStream_t st) {
-  const int64_t blocks = (a.tokens + kWaves - 1) / kWaves;
-  const dim3 grid(static_cast<unsigned>(std::min(blocks, kRowBlocks)),
-                  static_cast<unsigned>((blocks + kRowBlocks - 1) / kRowBlocks));
-  if constexpr (!BACK && EPL <= 4)
-    if (in_pairs(a)) return launch_pairs<2 * EPL, L>(a, st);
+  const dim3 one = grid_of((a.tokens + kWaves - 1) / kWaves);
+  const dim3 two = grid_of((a.tokens + 2 * kWaves - 1) / (2 * kWaves));
+  const dim3 block(64 * kWaves);
+  if constexpr (EPL <= 4) {
+    if (BACK && back_in_pairs(a)) {
+      hipLaunchKernelGGL((k_router_bwd<32, 2 * EPL, L>), two, block, 0, st, a);
+      return hipGetLastError();
+    }
+    if (!BACK && in_pairs(a)) {
+      hipLaunchKernelGGL((k_router_fwd_pairs<2 * EPL, L>), two, block, 0, st, a);
+      return hipGetLastError();
+    }
+  }
   if constexpr (BACK)
-    hipLaunchKernelGGL((k_router_bwd<EPL, L>), grid, dim3(64 * kWaves), 0, st, a);
+    hipLaunchKernelGGL((k_router_bwd<64, EPL, L>), one, block, 0, st, a);
   else
-    hipLaunchKernelGGL((k_router_fwd<EPL, L>), grid, dim3(64 * kWaves),
+    hipLaunchKernelGGL((k_router_fwd<EPL, L>), one, block,
                        a.choose_groups && !a.in_lanes ? kWaves * a.E * sizeof(double) : 0, st, a);
   return hipGetLastError();
 }

@@ -199,6 +199,45 @@ def test_many_tokens_as_few(E, topk, groups, tg, gt, fp32, renorm):
             within("weights", w[torch.from_numpy(some).to(dev())], ww, F32 * np.abs(ww) + 2.0 ** -149)
 
 
+@pytest.mark.parametrize("E,topk,fp32", [(256, 8, False), (256, 32, True), (250, 7, False), (100, 6, True),
+                                         (64, 6, False), (33, 9, True), (8, 2, False), (1, 1, True)])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("sigmoid", True), ("sigmoid", False),
+                                          ("softmax", False)])
+def test_many_gradients_as_few(E, topk, fp32, score, renorm):
+    """The same of the backward, with ids that are missing, outside and named twice."""
+    need_gpu()
+    say(f"router backward, 4099 tokens as few E={E} topk={topk} {score} renorm={renorm}")
+    rng = np.random.default_rng(E + topk)
+    T = 4099
+    x = 2 * rng.standard_normal((T, E)).astype(np.float32)
+    x[100:300][rng.random((200, E)) < 0.5] = -np.inf
+    x[300:302] = -np.inf
+    x[302:304] = -700 + x[302:304]
+    x[305, 0], x[306, E - 1] = np.nan, np.inf
+    t = torch.from_numpy(x).to(dev())
+    t = t if fp32 else t.bfloat16()
+    ids = rng.integers(-2, E + 2, (T, topk)).astype(np.int32)       # any, some twice
+    ids[::2] = np.argsort(rng.random((len(ids[::2]), E)), axis=1)[:, :topk]   # all apart
+    ids = torch.from_numpy(ids).to(dev())
+    dw = torch.from_numpy(rng.standard_normal((T, topk)).astype(np.float32)).to(dev())
+    D = torch.full((T + 2, E), 77.0, device=dev(), dtype=t.dtype)
+    q.qlora_router_bwd(dw, t, ids, score, renorm, 2.5, dlogits=D[1:-1])
+    few = torch.cat([q.qlora_router_bwd(dw[j:j + 293], t[j:j + 293], ids[j:j + 293], score, renorm, 2.5)
+                     for j in range(0, T, 293)])
+    torch.cuda.synchronize()
+    assert (D[0] == 77).all() and (D[-1] == 77).all()
+    assert torch.equal(D[1:-1].nan_to_num(5e4), few.nan_to_num(5e4))
+    bad = torch.isnan(few).any(dim=1)
+    assert bad[305] and bad[306] and bad.sum() == 2 and torch.isnan(few[bad]).all()
+    some = np.r_[0:30, 100:130, 300:304, T - 20:T]
+    xs, n = t.double().cpu().numpy()[some], ids.cpu().numpy()[some]
+    n = np.where((n < 0) | (n >= E), -1, n)
+    n = np.where((n >= 0) & (np.take_along_axis(xs, np.maximum(n, 0), 1) == -np.inf), -1, n)
+    want, mag = orr.bwd(dw.double().cpu().numpy()[some], xs, n, score, renorm, 2.5)
+    got = few[torch.from_numpy(some).to(dev())]
+    within("dlogits", got, want, (F32 if fp32 else BF16) * np.abs(want) + 1e-13 * mag + 2.0 ** -149)
+
+
 def test_gradient_of_a_sure_choice():
     """Where one expert takes all but 1e-6, the gradient keeps its digits."""
     need_gpu()
