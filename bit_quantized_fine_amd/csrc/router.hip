@@ -10,14 +10,14 @@
 // scores were rounded.  A round of the choice is the wave's largest value by six
 // lane moves, and a ballot for its owner.
 //   By sigmoid and bias 32 bits choose and the chosen ones' 64 bits prove it
-// (choose_by_32), with many tokens for two in a wave.  A token's choice and weights
-// are the same on either way.
+// (choose_by_32).  Two tokens share a wave where the rules at the launches say so.  A
+// token's choice and weights are the same on either way.
 //
 // Bound by the vector instructions of a wave, about 650 by sigmoid, bias and groups for
 // two tokens: 8192 tokens of 256 experts, topk 8, take 8.0 us back to back in a graph
-// (8.4 MB would take 1.9; one token a wave 10.7, wholly in 64 bits 15).  Smaller batches
-// are a launch and the call (8 us).  The backward of 8192 tokens of 64 experts takes 4.5
-// us so, of 256 5.7.
+// (8.4 MB would take 1.9; one token a wave 10.7, wholly in 64 bits 15), of 64 experts by
+// a softmax 4.5.  Smaller batches are a launch and the call (8 us).  The backward of 8192
+// tokens of 64 experts takes 4.5 us, of 256 5.7.
 //
 // Weights and gradients are formed in 64 bits too, where they cost one lane's
 // work a slot: what is left of 1 - p where one expert takes nearly all would
@@ -734,7 +734,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_fwd(Router a) {
   route<EPL, L>(a, exp_neg, l, t, in, lds + (int64_t)wave_id() * a.E);
 }
 
-// The same by sigmoid and bias with two tokens a wave: the rounds of the choice, its
+// By sigmoid and bias with two tokens a wave: the rounds of the choice, its
 // proof and the weights take as many instructions for both.  A token whose choice is
 // not proven gets the whole wave.  (EPL experts a lane of 32.)
 template <int EPL, class L>
@@ -766,6 +766,88 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_fwd_pairs(Router a) {
                         threadIdx.x & 63, 0);
     route<EPL / 2, L>(a, exp_neg, l, first + h, true, nullptr);
   }
+}
+
+// By the logits themselves, without a bias and groups, two tokens a wave.  A bf16
+// logit's key has room for its expert (the lower index above); with fp32 ones the sort
+// moves the experts along, neighbours changing where the second is larger, which leaves
+// equal ones in their order.
+template <int EPL, class L>
+__global__ __launch_bounds__(64 * kWaves) void k_router_top_pairs(Router a) {
+  __shared__ int slots[kWaves][64];
+  const int half = (threadIdx.x >> 5) & 1, lane = threadIdx.x & 31;
+  const int64_t token = 2 * wave_token() + half;
+  const bool in = token < a.tokens;
+  const int64_t t = in ? token : a.tokens - 1;
+  const L* row = static_cast<const L*>(a.logits) + t * a.E;
+  int* const slot = slots[wave_id()] + 32 * half;
+  Logits<EPL, L> l;
+  l.template load<32>(row, a.E, lane, 32 * half);
+  slot[lane] = -1;
+  constexpr bool kInKey = sizeof(L) == 2;
+  constexpr uint32_t kIds = 0xFF;
+  uint32_t k[EPL];
+  int at[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    k[i] = order_key(l.x[i]);
+    at[i] = lane * EPL + i;
+    if (kInKey && k[i] != 0) k[i] = (k[i] & ~kIds) | (kIds - at[i]);
+  }
+  if constexpr (kInKey) {
+    sort_down<EPL>(k);
+  } else {
+#pragma unroll
+    for (int n = 0; n < EPL; ++n)
+#pragma unroll
+      for (int i = n & 1; i + 1 < EPL; i += 2) {
+        const bool swap = k[i] < k[i + 1];
+        const uint32_t hi = swap ? k[i + 1] : k[i], lo = swap ? k[i] : k[i + 1];
+        const int ih = swap ? at[i + 1] : at[i], il = swap ? at[i] : at[i + 1];
+        k[i] = hi;
+        k[i + 1] = lo;
+        at[i] = ih;
+        at[i + 1] = il;
+      }
+  }
+  for (int j = 0; j < a.topk; ++j) {
+    const uint32_t best = lanes_max<32>(k[0]);
+    const bool among = k[0] == best && best != 0;
+    uint32_t below = 0;
+    if constexpr (!kInKey) {   // the lowest lane of equal ones
+      const uint64_t all = __builtin_amdgcn_ballot_w64(among);
+      below = half ? __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(all >> 32), 0u)
+                   : __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(all), 0u);
+    }
+    if (among && below == 0) {
+      slot[j] = kInKey ? static_cast<int>(kIds - (best & kIds)) : at[0];
+#pragma unroll
+      for (int i = 0; i + 1 < EPL; ++i) {
+        k[i] = k[i + 1];
+        at[i] = at[i + 1];
+      }
+      k[EPL - 1] = 0;
+    }
+  }
+  wave_lds_fence();
+  const int id = slot[lane];
+  const bool live = id >= 0;
+  const float lx = live ? to_f32(row[id]) : 0.f;
+  const Exp exp_neg;
+  double w, total = 0.0;
+  if (a.sigmoid) {
+    w = live ? sigmoid64(exp_neg, lx) : 0.0;
+    total = a.renorm ? lanes_sum<32>(w) : 1.0;
+  }
+  const bool tiny = !(total > kLeastSum);
+  if (__builtin_amdgcn_ballot_w64(tiny) != 0) {   // uniform; with a softmax always
+    const double u = relative_weight<32>(a, exp_neg, live, lx), sum = lanes_sum<32>(u);
+    if (tiny) {
+      w = u;
+      total = sum;
+    }
+  }
+  if (in) store_slot(a, t, lane, id, l.bad, live ? w / total : 0.0);
 }
 
 // dlogits, W lanes a token (32: two tokens a wave).  Lane j holds slot j; sums over the
@@ -921,13 +1003,22 @@ Router router(const void* logits, int64_t tokens, int E, const qlora_router_conf
 }
 
 
-// Two tokens a wave by sigmoid and bias, where their slots and groups lie within 32
-// lanes and there are enough of them: 256 experts, 8 groups, topk 8, one and two a
-// wave: 1024 tokens 5.4 and 5.8 us, 2048 5.4 and 5.3, 4096 7.3 and 6.5, 8192 10.7 and
-// 8.0, 32768 27.9 and 20.3 (64 experts, topk 6: 18.8 and 12.0).
+// Two tokens a wave, where their slots and groups lie within 32 lanes and there are
+// enough of them: 256 experts, 8 groups, topk 8, sigmoid and bias, one and two a wave:
+// 1024 tokens 5.4 and 5.8 us, 2048 5.4 and 5.3, 4096 7.3 and 6.5, 8192 10.7 and 8.0,
+// 32768 27.9 and 20.3 (64 experts, topk 6: 18.8 and 12.0).
 bool in_pairs(const Router& a) {
   return a.bias && a.sigmoid && a.tokens >= kPairTokens && a.E <= 256 && a.topk <= 32 &&
          (!a.choose_groups || (a.in_lanes && a.gshift > 0));
+}
+// By the logits alone (but for a softmax without renorm, whose sum over the experts would
+// run in another order) at any number of tokens: the rounds are shorter than those of a
+// wave a token (64 experts, topk 6: 8 tokens 3.2 us and one a wave 3.6, 8192 4.5 and
+// 6.4, 32768 9.3 and 16.2; 256 experts, topk 8: 3.7 and 4.4, 5.8 and 8.7, 13.2 and
+// 23.8).  With fp32 logits eight experts a lane are too many to sort with their indices
+// (256 experts: 5.8 and 4.3).
+bool top_in_pairs(const Router& a) {
+  return !a.bias && !a.choose_groups && (a.sigmoid || a.renorm) && a.topk <= 32;
 }
 
 // In the backward wherever no sum over a token's experts is formed (its order would
@@ -949,12 +1040,16 @@ hipError_t launch(const Router& a, hipStream_t st) {
   const dim3 two = grid_of((a.tokens + 2 * kWaves - 1) / (2 * kWaves));
   const dim3 block(64 * kWaves);
   if constexpr (EPL <= 4) {
-    if (BACK && back_in_pairs(a)) {
-      hipLaunchKernelGGL((k_router_bwd<32, 2 * EPL, L>), two, block, 0, st, a);
-      return hipGetLastError();
+    void (*pairs)(Router) = nullptr;
+    if constexpr (BACK) {
+      if (back_in_pairs(a)) pairs = k_router_bwd<32, 2 * EPL, L>;
+    } else {
+      if (in_pairs(a)) pairs = k_router_fwd_pairs<2 * EPL, L>;
+      if constexpr (2 * EPL <= 4 || sizeof(L) == 2)
+        if (top_in_pairs(a)) pairs = k_router_top_pairs<2 * EPL, L>;
     }
-    if (!BACK && in_pairs(a)) {
-      hipLaunchKernelGGL((k_router_fwd_pairs<2 * EPL, L>), two, block, 0, st, a);
+    if (pairs) {
+      hipLaunchKernelGGL(pairs, two, block, 0, st, a);
       return hipGetLastError();
     }
   }

@@ -199,6 +199,46 @@ def test_many_tokens_as_few(E, topk, groups, tg, gt, fp32, renorm):
             within("weights", w[torch.from_numpy(some).to(dev())], ww, F32 * np.abs(ww) + 2.0 ** -149)
 
 
+@pytest.mark.parametrize("E,topk", [(256, 8), (256, 32), (250, 7), (128, 8), (100, 6), (64, 6), (64, 32),
+                                    (33, 5), (8, 2), (2, 2), (1, 1)])
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("sigmoid", True), ("sigmoid", False),
+                                          ("softmax", False)])
+def test_many_tokens_by_logit_as_few(E, topk, fp32, score, renorm):
+    """The same without a bias: logits equal within a lane and across, zeros of both
+    signs, masked, extreme, NaN, and sigmoids that hardly are numbers."""
+    need_gpu()
+    say(f"router by logit, 2051 tokens as few E={E} topk={topk} fp32={fp32} {score} renorm={renorm}")
+    rng = np.random.default_rng(E + topk)
+    T = 2051
+    x = rng.standard_normal((T, E)).astype(np.float32)
+    x[100:200] = np.round(2 * x[100:200]) / 2
+    x[200:300] = np.where(rng.random((100, E)) < 0.5, 0.0, -0.0)
+    x[300:400][rng.random((100, E)) < 0.7] = -np.inf
+    x[400:402] = -np.inf
+    x[402:405] = -700 + x[402:405]
+    x[405] = np.where(rng.random(E) < 0.5, 3.3e38, -3.3e38)
+    x[406, 0] = np.nan
+    x[407, E - 1] = np.inf
+    x[409], x[411] = np.nan, 1e-40 * x[411]
+    t = torch.from_numpy(x).to(dev())
+    t = t if fp32 else t.bfloat16()
+    args = (topk, score, None, 1, 1, 1, renorm, 2.5)
+    I = torch.full((T + 2, topk), 77, dtype=torch.int32, device=dev())
+    W = torch.full((T + 2, topk), 77.0, device=dev())
+    q.qlora_router_fwd(t, *args, ids=I[1:-1], weights=W[1:-1])
+    few = [q.qlora_router_fwd(t[j:j + 293], *args) for j in range(0, T, 293)]
+    torch.cuda.synchronize()
+    ids, w = torch.cat([f[0] for f in few]), torch.cat([f[1] for f in few])
+    assert (I[0] == 77).all() and (I[-1] == 77).all() and (W[0] == 77).all() and (W[-1] == 77).all()
+    np.testing.assert_array_equal(I[1:-1].cpu().numpy(), ids.cpu().numpy())
+    np.testing.assert_array_equal(W[1:-1].cpu().numpy(), w.cpu().numpy())
+    some = np.r_[0:20, 100:120, 200:210, 300:330, 400:406, 411, T - 11:T]
+    wid, ww = orr.fwd(t.double().cpu().numpy()[some], topk, score, None, 1, 1, 1, renorm, 2.5)
+    np.testing.assert_array_equal(I[1:-1].cpu().numpy()[some], wid)
+    within("weights", w[torch.from_numpy(some).to(dev())], ww, F32 * np.abs(ww) + 2.0 ** -149)
+
+
 @pytest.mark.parametrize("E,topk,fp32", [(256, 8, False), (256, 32, True), (250, 7, False), (100, 6, True),
                                          (64, 6, False), (33, 9, True), (8, 2, False), (1, 1, True)])
 @pytest.mark.parametrize("score,renorm", [("softmax", True), ("sigmoid", True), ("sigmoid", False),
