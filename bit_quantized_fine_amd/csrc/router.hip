@@ -71,9 +71,6 @@ struct Router {
 __device__ __forceinline__ int read_lane(int v, int lane) {
   return __builtin_amdgcn_readlane(v, lane);
 }
-__device__ __forceinline__ float read_lane(float v, int lane) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
-}
 __device__ __forceinline__ double read_lane(double v, int lane) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
   const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), lane);
@@ -98,12 +95,6 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   step(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x142, 0xA, 0xF, false));   // row_bcast 15
   step(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x143, 0xC, 0xF, false));   // row_bcast 31
   return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
-}
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-  const uint32_t hi = wave_max(static_cast<uint32_t>(v >> 32));
-  const uint32_t lo =
-      wave_max(static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
-  return static_cast<uint64_t>(hi) << 32 | lo;
 }
 // Largest value over the W lanes (32 or 64) that hold a token, in all of them.
 template <int W>
