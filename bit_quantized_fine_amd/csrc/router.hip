@@ -108,6 +108,21 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
   }
   return v;
 }
+// Whether a mask holds several lanes of one token (W lanes a token), and how many of this
+// lane's token come before it there.
+template <int W>
+__device__ __forceinline__ bool several(uint64_t at) {
+  if constexpr (W == 64) return (at & (at - 1)) != 0;
+  const uint32_t l = static_cast<uint32_t>(at), h = static_cast<uint32_t>(at >> 32);
+  return ((l & (l - 1)) | (h & (h - 1))) != 0;
+}
+template <int W>
+__device__ __forceinline__ uint32_t lanes_before(uint64_t at) {
+  const uint32_t l = static_cast<uint32_t>(at), h = static_cast<uint32_t>(at >> 32);
+  const uint32_t low = __builtin_amdgcn_mbcnt_lo(l, 0u);
+  if constexpr (W == 64) return __builtin_amdgcn_mbcnt_hi(h, low);
+  return (threadIdx.x & 32) ? __builtin_amdgcn_mbcnt_hi(h, 0u) : low;
+}
 // v moved across lanes (zero where there is no lane to take it from).
 template <int CTRL, int ROWS = 0xF>
 __device__ __forceinline__ double dpp_f64(double v) {
@@ -415,12 +430,12 @@ __device__ __forceinline__ void sort_down(uint32_t* k) {
 //   Groups are chosen by the keys.  If some at the border could change sides (one
 // token in 10^3), each lane forms its best one or two ranks in 64 bits, which give
 // the groups' scores, unless a lane's next key could be among a group's best.
-//   Experts are chosen by the keys, one more than topk, each round's winner leaving
-// its expert in `slots` (LDS, one a lane).  Their ranks are then formed in 64 bits,
-// one a lane, and order them.  The choice stands if every chosen rank is above the
-// best key left by more than its error: then it is the one that 64 bits make.
-//   Else (about one token in 10^5 of 256 experts, and where two lanes won a round)
-// false: the choice is made anew.  For tokens without NaN and +inf, and groups
+//   Experts are chosen by the keys, one more than topk, each round's winner (the first
+// of several lanes) leaving its expert in `slots` (LDS, one a lane).  Their ranks are
+// then formed in 64 bits, one a lane, and order them.  The choice stands if every chosen
+// rank is above the best key left by more than its error: then it is the one that 64
+// bits make.
+//   Else (about one token in 10^5 of 256 experts) false: the choice is made anew.  For tokens without NaN and +inf, and groups
 // within lanes.  W lanes a token, this one's being `lane` of them from lane `base` of
 // the wave on; id and p: of this lane's slot, p in 64 bits.
 template <int W, int EPL, class L>
@@ -511,14 +526,9 @@ __device__ __forceinline__ bool choose_by_32(const Router& a, const Exp& exp_neg
   const int rounds = a.topk < W ? a.topk + 1 : W;
   for (int j = 0; j < rounds; ++j) {
     const uint32_t best = lanes_max<W>(k[0]);
-    const bool won = k[0] == best && best >= kNone;
+    bool won = k[0] == best && best >= kNone;
     const uint64_t at = __builtin_amdgcn_ballot_w64(won);
-    if constexpr (W == 64) {
-      doubt |= at & (at - 1);
-    } else {
-      const uint32_t l = static_cast<uint32_t>(at), h = static_cast<uint32_t>(at >> 32);
-      doubt |= static_cast<uint64_t>(h & (h - 1)) << 32 | (l & (l - 1));
-    }
+    if (several<W>(at)) won = won && lanes_before<W>(at) == 0;   // uniform; one token in 10^5
     if (won) {
       slots[j] = expert(best);
 #pragma unroll
@@ -806,9 +816,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_top_pairs(Router a) {
     const bool among = k[0] == best && best != 0;
     uint32_t below = 0;
     if constexpr (!kInKey) {   // the lowest lane of equal ones
-      const uint64_t all = __builtin_amdgcn_ballot_w64(among);
-      below = half ? __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(all >> 32), 0u)
-                   : __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(all), 0u);
+      below = lanes_before<32>(__builtin_amdgcn_ballot_w64(among));
     }
     if (among && below == 0) {
       slot[j] = kInKey ? static_cast<int>(kIds - (best & kIds)) : at[0];
