@@ -401,3 +401,34 @@ def test_guards_streams_and_graph():
                 assert torch.equal(i1, i2) and torch.equal(w1, w2) and torch.equal(d1, d2)
     ids, w = q.qlora_router_fwd(x[:0], k)
     assert ids.shape == (0, k) and q.qlora_router_bwd(dw[:0], x[:0], ids).shape == (0, E)
+
+
+def test_many_tokens_in_a_graph():
+    """The batches whose tokens share waves, captured once and replayed on new inputs
+    with eager calls on another stream between the replays."""
+    need_gpu()
+    say("router, many tokens in a graph")
+    T, E, k = 4099, 96, 6
+    x, b = torch.randn(T, E, device=dev()), 0.1 * torch.randn(E, device=dev())
+    dw = torch.randn(T, k, device=dev())
+
+    def step():
+        a = q.qlora_router_fwd(x, k, "sigmoid", b, groups=3, top_groups=2, group_top=2)
+        c = q.qlora_router_fwd(x, k)
+        return (*a, *c, q.qlora_router_bwd(dw, x, a[0], "sigmoid"), q.qlora_router_bwd(dw, x, c[0]))
+    step()
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(4):
+        x.copy_(torch.randn(T, E, device=dev()))
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(side):
+            other = step()
+        torch.cuda.synchronize()
+        eager = step()
+        torch.cuda.synchronize()
+        for a, c, e in zip(got, other, eager):
+            assert torch.equal(a, c) and torch.equal(a, e)
