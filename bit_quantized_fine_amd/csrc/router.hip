@@ -882,9 +882,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_bwd(Router a) {
     if (id >= 0) dw = static_cast<double>(a.dweights[t * a.topk + lane]);
   }
   const bool live = id >= 0;
+  // an expert's slot leaves its mark; of several the last one
+  wave_lds_fence();
+  if (live) grad[id] = lane + 1;
+  wave_lds_fence();
+  const uint64_t twice = __builtin_amdgcn_ballot_w64(live && grad[live ? id : 0] != lane + 1);
   const Exp exp_neg;
   double d = 0.0;       // of this slot's expert
-  double rest[EPL];     // softmax without renorm: of every expert, -p sum_j p_j dw_j
+  double rest[EPL];     // softmax without renorm: of the experts without a slot, -p sum_j p_j dw_j
   if (a.renorm) {
     const double u = relative_weight<W>(a, exp_neg, live, lx), total = lanes_sum<W>(u);
     const double q = live ? u / total : 0.0;
@@ -900,20 +905,43 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_bwd(Router a) {
   } else if constexpr (W == 64) {   // (its sum over the experts would run in another order)
     const float top = l.top();
     const double r = 1.0 / l.exps(exp_neg, top, rest);
-    d = live ? dw * exp_neg(static_cast<double>(lx) - static_cast<double>(top)) * r : 0.0;
-    slot[lane].x = d;
-    wave_lds_fence();
-    double sum = 0.0;
-    for (int j = 0; j < a.topk; ++j) sum += slot[j].x;
+    // p_e (dw_e - sum_j p_j dw_j) as p_e (sum_j p_j (dw_e - dw_j) + dw_e u), u what the
+    // experts without a slot have: next to one expert that takes nearly all, the difference
+    // itself would lose the digits of 1 - p
+    bool first = live;
+    if (twice != 0) {   // uniform: an expert's first slot takes the sum of its slots' dw
+      slot[lane] = f64x2{static_cast<double>(id), dw};
+      wave_lds_fence();
+      double all = 0.0;
+      for (int j = 0; j < a.topk; ++j) {
+        if (!live || slot[j].x != id) continue;
+        first = first && j >= lane;
+        all += slot[j].y;
+      }
+      dw = all;
+      wave_lds_fence();
+    }
+    double u = 0.0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      rest[i] = l.x[i] > -__builtin_inff() ? -rest[i] * r * sum : 0.0;
+    for (int i = 0; i < EPL; ++i) {
+      if (grad[lane * EPL + i] != 0.0) rest[i] = 0.0;
+      u += rest[i];
+    }
+    u = wave_sum(u) * r;
+    const double p =
+        first ? exp_neg(static_cast<double>(lx) - static_cast<double>(top)) * r : 0.0;
+    slot[lane] = f64x2{p, dw};
+    wave_lds_fence();
+    double v = dw * u, sum = 0.0;
+    for (int j = 0; j < a.topk; ++j) {
+      v += slot[j].x * (dw - slot[j].y);
+      sum += slot[j].x * slot[j].y;
+    }
+    d = first ? p * v : 0.0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) rest[i] = l.x[i] > -__builtin_inff() ? -rest[i] * r * sum : 0.0;
   }
   // an expert named by several slots gets their sum
-  wave_lds_fence();
-  if (live) grad[id] = lane;
-  wave_lds_fence();
-  const uint64_t twice = __builtin_amdgcn_ballot_w64(live && grad[live ? id : 0] != lane);
   wave_lds_fence();
   if (live) grad[id] = twice == 0 ? d : 0.0;
   wave_lds_fence();
