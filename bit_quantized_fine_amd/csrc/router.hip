@@ -897,7 +897,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_bwd(Router a) {
     wave_lds_fence();
     // q_i sum_j q_j (dw_i - dw_j): no difference of nearly equal sums
     double v = 0.0;
-    for (int j = 0; j < a.topk; ++j) v += slot[j].x * (dw - slot[j].y);
+    if (twice == 0) {   // uniform
+      for (int j = 0; j < a.topk; ++j) v += slot[j].x * (dw - slot[j].y);
+    } else {
+      // the terms of one expert's slots cancel in their sum: left out (but for a slot's own,
+      // so that a token beside this one gets the same, infinities too)
+      for (int j = 0; j < a.topk; ++j)
+        if (__shfl(id, base + j) != id || j == lane) v += slot[j].x * (dw - slot[j].y);
+    }
     d = q * v;
     if (a.sigmoid) d *= sigmoid64(exp_neg, -static_cast<double>(lx));
   } else if (a.sigmoid) {

@@ -89,6 +89,40 @@ def test_ids_of_the_callers_own(E, topk):
     within("dlogits", dl, want, F32 * np.abs(want) + F64 * mag + 2.0 ** -149)
 
 
+@pytest.mark.parametrize("E,topk,copies", [(8, 3, 1), (96, 6, 1), (300, 20, 1), (64, 6, 80)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_renormalised_ids_of_the_callers_own(E, topk, copies, score):
+    """Renormalised weights: with q_i the slots' shares, expert e gets the sum over its
+    slots i and the others' slots j of q_i q_j (dw_i - dw_j); two slots of one expert
+    have nothing to give each other.  (With copies, enough tokens to share waves.)"""
+    need_gpu()
+    say(f"router, sure choices, any ids E={E} topk={topk} {score} renormalised")
+    x, ids, live, dw = _any_ids(np.random.default_rng(E), E, topk)
+    t = torch.from_numpy(x.astype(np.float32)).to(dev())
+    dwt = torch.from_numpy(dw.astype(np.float32)).to(dev())
+    idt = torch.from_numpy(ids.astype(np.int32)).to(dev())
+    dl = q.qlora_router_bwd(dwt.repeat(copies, 1), t.repeat(copies, 1), idt.repeat(copies, 1), score, True,
+                            2.5).view(copies, *t.shape)
+    torch.cuda.synchronize()
+    assert (dl == dl[:1]).all()
+    xs, d = t.double().cpu().numpy(), dwt.double().cpu().numpy()
+    want, mag = np.zeros(xs.shape), np.zeros(xs.shape)
+    for i, row in enumerate(xs):
+        n = np.flatnonzero(live[i])
+        e, v = ids[i, n], row[ids[i, n]]
+        low = np.minimum(v, 0) if score == "sigmoid" else v
+        u = np.exp(low - low.max(initial=-np.inf)) / (1 + np.exp(-np.abs(v)) if score == "sigmoid" else 1)
+        u = u / u.sum()
+        slope = 1 / (1 + np.exp(v)) if score == "sigmoid" else np.ones(len(v))
+        for a in range(len(n)):
+            for b in range(len(n)):
+                if e[a] != e[b]:
+                    term = 2.5 * slope[a] * u[a] * u[b] * (d[i, n[a]] - d[i, n[b]])
+                    want[i, e[a]] += term
+                    mag[i, e[a]] += abs(term)
+    within("dlogits", dl[0], want, F32 * np.abs(want) + F64 * mag + 2.0 ** -149)
+
+
 def test_against_differences():
     """The softmax that is not renormalised: the gradient of sum_i dw_i w_i by differences
     of 64-bit weights."""
