@@ -690,13 +690,17 @@ def _at(t):
 
 
 def _q4(w):
-    """The C view of an NF4Weight or Q4Weight, and its checked tensors."""
+    """The C view of an NF4Weight (or any object with its fields) or a Q4Weight,
+    and its checked tensors."""
     import torch
-    if isinstance(w, Q4Weight):
+    if isinstance(w, Q4Weight):   # (unpacked: half the time of reading the fields)
         codes, q, scale, N, K, book, dq = w
     else:
-        codes, q, scale, N, K = w
         book, dq = "nf4", True
+        if isinstance(w, NF4Weight):
+            codes, q, scale, N, K = w
+        else:
+            codes, q, scale, N, K = w.codes, w.absmax_q, w.absmax_scale, w.N, w.K
     n = N * K
     nb = n // 64
     cb = CODEBOOKS[book] if book in CODEBOOKS else _codebook_id(book)

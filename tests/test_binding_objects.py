@@ -1,0 +1,52 @@
+"""Weights that the binding takes by their fields (CPU: the calls end at the check that
+their tensors are on a GPU)."""
+import types
+
+import pytest
+import torch
+
+import bit_quantized_fine_amd as q
+
+
+def _weight(N=64, K=128):
+    return q.NF4Weight(torch.zeros(N * K // 2, dtype=torch.uint8),
+                       torch.zeros(N * K // 64, dtype=torch.uint8),
+                       torch.zeros((N * K // 64 + 255) // 256, dtype=torch.float32), N, K)
+
+
+class Kept(torch.nn.Module):
+    """A module that holds a weight's fields as buffers."""
+
+    def __init__(self, w):
+        super().__init__()
+        for name in ("codes", "absmax_q", "absmax_scale"):
+            self.register_buffer(name, getattr(w, name))
+        self.N, self.K = w.N, w.K
+
+
+def _calls(w):
+    X, dY = torch.zeros(4, 128, dtype=torch.bfloat16), torch.zeros(4, 64, dtype=torch.bfloat16)
+    off = torch.zeros(2, dtype=torch.int32)
+    return [lambda: q.qlora_linear_dropout_fwd(X, w), lambda: q.qlora_linear_dropout_bwd(dY, X, w),
+            lambda: q.qlora_grouped_fwd(X, off, w, 1), lambda: q.qlora_grouped_bwd(dY, X, off, w, 1)]
+
+
+@pytest.mark.parametrize("make", [lambda w: w, lambda w: types.SimpleNamespace(**w._asdict()), Kept],
+                         ids=["tuple", "namespace", "module"])
+def test_weights_are_taken_by_their_fields(make):
+    """Any object with an NF4Weight's fields, as the plain layer's calls take it."""
+    for call in _calls(make(_weight())):
+        with pytest.raises(ValueError, match="GPU tensor"):
+            call()
+
+
+def test_fields_of_other_weights_are_checked():
+    w = _weight()
+    bad = types.SimpleNamespace(**dict(w._asdict(), absmax_q=w.absmax_q.int()))
+    for call in _calls(bad):
+        with pytest.raises(TypeError, match="w.absmax_q must be"):
+            call()
+    w4 = q.Q4Weight(w.codes, None, torch.zeros(128), 64, 128, "int4", False)
+    for call in _calls(w4):
+        with pytest.raises(ValueError, match="GPU tensor"):
+            call()
