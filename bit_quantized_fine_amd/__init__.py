@@ -728,6 +728,15 @@ def _drop(p, state):
     return _Dropout(state.data_ptr(), p)
 
 
+def _int32(names, *values):
+    """Refuses numbers that ctypes would take modulo 2^32; names holds theirs,
+    separated by spaces."""
+    if max(values) >= 1 << 31 or min(values) < -1 << 31:
+        for name, v in zip(names.split(), values):
+            if not -1 << 31 <= v < 1 << 31:
+                raise ValueError(f"{name} = {v} does not fit 32 bits")
+
+
 def _scratch(workspace, need, dev):
     """The caller's workspace if it is large enough, else one of need bytes."""
     import torch
@@ -1118,6 +1127,7 @@ def qlora_grouped_act8_bwd(dY, x8: Act8, offsets, w, E: int, A=None, B=None, s: 
     row order[i] // topk of it.  Returns (dX bf16 [M,K] or None, dA bf16
     [E,K,r], dB bf16 [E,r,N])."""
     import torch
+    _int32("topk", topk)
     if dY.dim() != 2:
         raise ValueError("dY must be [M, N]")
     M = dY.shape[0]
@@ -1252,6 +1262,7 @@ def qlora_router_fwd(logits, topk: int, score: str = "softmax", bias=None, group
     left over has id -1 and weight 0."""
     import torch
     tokens, E, fp32 = _logits(logits)
+    _int32("topk groups top_groups group_top", topk, groups, top_groups, group_top)
     cfg = _RouterConfig(_score(score), topk, groups, top_groups, group_top, 1 if renorm else 0,
                         scale)
     if bias is not None:
@@ -1262,7 +1273,8 @@ def qlora_router_fwd(logits, topk: int, score: str = "softmax", bias=None, group
         _is(weights, "weights", (tokens, topk), torch.float32)
     dev = _one_gpu("logits bias ids weights", logits, bias, ids, weights)
     if ids is None:
-        ids = logits.new_empty((tokens, max(topk, 0)), dtype=torch.int32)
+        # (outputs of a topk that the call refuses have no room)
+        ids = logits.new_empty((tokens, topk if 0 < topk <= 64 else 0), dtype=torch.int32)
     if weights is None:
         weights = torch.empty_like(ids, dtype=torch.float32)
     _call("qlora_router_fwd", dev, logits.data_ptr(), fp32, tokens, E, _at(bias),

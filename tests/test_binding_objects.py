@@ -1,5 +1,5 @@
-"""Weights that the binding takes by their fields (CPU: the calls end at the check that
-their tensors are on a GPU)."""
+"""Weights that the binding takes by their fields, and numbers that a C argument cannot
+hold (CPU: the calls end at the check that their tensors are on a GPU)."""
 import types
 
 import pytest
@@ -50,3 +50,22 @@ def test_fields_of_other_weights_are_checked():
     for call in _calls(w4):
         with pytest.raises(ValueError, match="GPU tensor"):
             call()
+
+
+@pytest.mark.parametrize("name", ["topk", "groups", "top_groups", "group_top"])
+@pytest.mark.parametrize("wrong", [2 ** 32 + 2, -2 ** 32 + 2, 2 ** 31, -2 ** 31 - 1, 2 ** 70])
+def test_router_numbers_past_32_bits(name, wrong):
+    """A number that a C int cannot hold is refused, not taken modulo 2^32."""
+    kw = {"topk": 2, "groups": 2, "top_groups": 2, "group_top": 2, name: wrong}
+    with pytest.raises(ValueError, match=f"{name} .* 32 bits"):
+        q.qlora_router_fwd(torch.zeros(4, 8), **kw)
+
+
+@pytest.mark.parametrize("wrong", [2 ** 32 + 2, 2 ** 31, -2 ** 33])
+def test_grouped_numbers_past_32_bits(wrong):
+    w = _weight()
+    x8 = q.Act8(torch.zeros(4, 128, dtype=torch.int8), torch.zeros(4, 2))
+    with pytest.raises(ValueError, match="topk .* 32 bits"):
+        q.qlora_grouped_act8_bwd(torch.zeros(8, 64, dtype=torch.bfloat16), x8,
+                                 torch.zeros(2, dtype=torch.int32), w, 1,
+                                 order=torch.zeros(8, dtype=torch.int32), topk=wrong)
