@@ -7,10 +7,12 @@
 // A block that holds a NaN or an infinity gets c = NaN and codes 0: all of it
 // comes back as NaN, so an overflow does not pass for a number.
 //
-// A value is off by half a step of its block, amax / 254, and by the rounding
-// of the product to bf16 (2^-9 of the value, at most a quarter of that half
-// step).  The constant is not itself rounded to fewer bits: a power of two
-// would cost up to one bit of every code, against 6% of the bytes.
+// A value is off by half a step of its block, amax / 254, and by the rounding of the
+// product to bf16, half a step of bf16: up to 2^-8 of the value, so that the largest
+// values of a block lose up to as much again (1.87 half steps of the block at most, where
+// amax is 1.0625; exactly one where it is a power of two).  The constant is not itself
+// rounded to fewer bits: a power of two would cost up to one bit of every code, against
+// 6% of the bytes.
 #pragma once
 
 #include "device_common.hpp"
