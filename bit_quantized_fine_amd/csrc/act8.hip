@@ -4,9 +4,10 @@
 // codes the other, so the four lanes of an aligned quad hold a block and find
 // its largest magnitude with two lane moves.  Both kernels are bound by the
 // bytes they move (3.06 a value); a value costs about eight operations on its
-// way out and three on its way back.  4096 x 17920 values take 40 us out (5.6
-// TB/s) and 36 us back (6.2 TB/s); non-temporal accesses gained nothing out (38
-// against 35 to 41) and cost the way back (69 to 74).
+// way out and three on its way back.  With three sets of buffers in turn, 4096 x 17920
+// values take 42 us out (5.4 TB/s) and 45 us back (5.0; on one set, which the cache holds
+// in part, 40 and 36).  Non-temporal accesses gained nothing out (38 against 35 to 41, its
+// output in one buffer) and cost the way back (69 to 74 against 38).
 #include "act8.hpp"
 #include "kernels.hpp"
 #include "qlora_nf4.h"

@@ -9,11 +9,16 @@
 // A row stays in the registers of the threads that share it (64 to 1024 of them,
 // each with up to eight 16-byte pieces, in the backward with two), so that every byte
 // is read once; rows too long for that (65536 values, in the backward 16384) are read
-// twice.  Squares, sums and everything up to the one rounding of an output are fp32.
-// Both passes are bound by the bytes they move: 4096 x 6656 with residual and
-// checkpoint takes 45 us (247 MB, 5.5 TB/s), without the checkpoint 38 (5.8); the
-// backward of 4096 x 8192 46 us (268 MB and 8 of dg's sums, 6.0 TB/s), where a large
-// copy reaches 5.0.  Loads and stores marked non-temporal gained nothing (45.9 and
+// twice, and in the backward with dg a third time, by a launch of its own for the
+// columns.  Squares, sums and everything up to the one rounding of an output are fp32.
+// Bound by the bytes they move: with three sets of buffers in turn, 4096 x 6656 with
+// residual and checkpoint takes 52 us (247 MB, 4.8 TB/s), without the checkpoint 45
+// (4.8); the backward of 4096 x 8192 60 us (268 MB, 57 without dg), where a large copy
+// reaches 5.0 (on one set, which the 256 MB cache holds in part, 45, 38 and 57).
+// 4096 x 17920 take 114 us forward, 133 backward (read twice) and 189 with dg (three
+// times; 587 MB would take 118).  A row of up to 512 values is a wave's, which leaves lanes of
+// short ones idle: 131072 x 128 take 52 us forward and 68 backward (27 by their bytes),
+// x 256 60 and 76 (54).  Loads and stores marked non-temporal gained nothing (45.9 and
 // 43.1 us the forward, 58.1 and 57.2 the backward with dg, with and without).
 //
 // dg's sum runs over rows: each workgroup adds up the rows it takes (always the
