@@ -13,11 +13,17 @@
 // (choose_by_32).  Two tokens share a wave where the rules at the launches say so.  A
 // token's choice and weights are the same on either way.
 //
-// Bound by the vector instructions of a wave, about 650 by sigmoid, bias and groups for
-// two tokens: 8192 tokens of 256 experts, topk 8, take 8.0 us back to back in a graph
-// (8.4 MB would take 1.9; one token a wave 10.7, wholly in 64 bits 15), of 64 experts by
-// a softmax 4.5.  Smaller batches are a launch and the call (8 us).  The backward of 8192
-// tokens of 64 experts takes 4.5 us, of 256 5.7.
+// 8192 tokens of 256 experts by sigmoid, bias and groups, topk 8, take 8.0 us back to
+// back in a graph (8.4 MB would take 1.9; one token a wave 10.7, wholly in 64 bits 15).
+// All four waves a SIMD are resident at once, so that time is a wave's chain of
+// dependent steps: waves wait for half of their cycles, and the 650 vector instructions
+// for two tokens would take 4.3 us.  32768 tokens (20.3 us, 7 by their bytes) are bound
+// by those instructions, at least 17.3 us of them.  By the logit alone 8192 tokens of 64
+// experts take 4.5 us; 32768 of 256 in bf16 13.2 (4 by their bytes), 12.4 of them the
+// vector instructions of the sort and of eight rounds.
+//   Smaller batches are a launch and the call (8 us).  The backward of 8192 tokens of 64
+// experts takes 4.5 us, of 256 5.7 (a softmax that is not renormalised, one token a wave
+// with an exponential for every expert, 5.6 and 8.6).
 //
 // Weights and gradients are formed in 64 bits too, where they cost one lane's
 // work a slot: what is left of 1 - p where one expert takes nearly all would
@@ -435,9 +441,10 @@ __device__ __forceinline__ void sort_down(uint32_t* k) {
 // then formed in 64 bits, one a lane, and order them.  The choice stands if every chosen
 // rank is above the best key left by more than its error: then it is the one that 64
 // bits make.
-//   Else (about one token in 10^5 of 256 experts) false: the choice is made anew.  For tokens without NaN and +inf, and groups
-// within lanes.  W lanes a token, this one's being `lane` of them from lane `base` of
-// the wave on; id and p: of this lane's slot, p in 64 bits.
+//   Else (about one token in 10^5 of 256 experts) false: the choice is made anew.
+//   For tokens without NaN and +inf, and groups within lanes.  W lanes a token, this
+// one's being `lane` of them from lane `base` of the wave on; id and p: of this lane's
+// slot, p in 64 bits.
 template <int W, int EPL, class L>
 __device__ __forceinline__ bool choose_by_32(const Router& a, const Exp& exp_neg, const float* x,
                                              const L* row, int lane, int base, int* slots,
@@ -851,7 +858,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_top_pairs(Router a) {
 
 // dlogits, W lanes a token (32: two tokens a wave).  Lane j holds slot j; sums over the
 // slots run in their order in every lane.  A slot's gradient finds its expert through
-// LDS.
+// LDS.  Nothing is formed as a difference of nearly equal sums: what an expert that takes
+// nearly all leaves to the others keeps its digits.
 template <int W, int EPL, class L>
 __global__ __launch_bounds__(64 * kWaves) void k_router_bwd(Router a) {
   __shared__ __attribute__((aligned(16))) double grads[kWaves * 64 * EPL];   // [token][expert]
@@ -1035,7 +1043,6 @@ Router router(const void* logits, int64_t tokens, int E, const qlora_router_conf
     while ((c->groups << (a.gshift + 1)) <= 64) ++a.gshift;
   return a;
 }
-
 
 // Two tokens a wave, where their slots and groups lie within 32 lanes and there are
 // enough of them: 256 experts, 8 groups, topk 8, sigmoid and bias, one and two a wave:
