@@ -596,7 +596,8 @@ int qlora_grouped_act8_bwd(const uint16_t* dY, const qlora_act8* x8, int64_t tok
  *   residual NULL: h is x, and the argument h is not used (may be NULL).
  *   h may be x or residual (in place); y overlaps nothing.
  *   y8  NULL, or where the checkpoint of y goes (then K % 64 == 0).
- * Squares are summed in fp32: a row of values past 2^64 / sqrt(K) has rstd = 0.
+ * Squares are summed in fp32: a row of values past 2^64 / sqrt(K) has rstd = 0, and
+ * values under 2^-63 lose digits (which shows where eps is as small as 2^-126).
  * K % 8 == 0, 8 <= K <= 2^22, M >= 0, M*K <= 2^40, eps > 0 and finite
  * (QLORA_ERR_SHAPE otherwise); M = 0 is allowed.  All buffers 16-byte aligned
  * (rstd and scales 4-byte).
@@ -632,9 +633,9 @@ int qlora_rms_norm_bwd(const uint16_t* dy, const uint16_t* dres, const uint16_t*
  *   Choice: experts rank by p + bias, formed in 64 bits; without a bias by the
  *     logit (the same order, and apart where two scores round to one).  With
  *     top_groups < groups, the experts form `groups` equal groups in order, a
- *     group's score is the sum of its group_top (1 or 2) best ranks (of its best
- *     p where no bias is given), and the experts of the top_groups best
- *     groups stay.  The topk best experts, best first.  Ties, of experts and of
+ *     group's score is the sum of its group_top (1 or 2) best ranks in 64 bits
+ *     (without a bias the sum of its two best p, or its best logit), and the
+ *     experts of the top_groups best groups stay.  The topk best experts, best first.  Ties, of experts and of
  *     groups, go to the lower index.
  *   ids [tokens, topk] int32, weights [tokens, topk] fp32: p, or p over the sum
  *     of the chosen p with renorm = 1, times scale.
@@ -645,7 +646,8 @@ int qlora_rms_norm_bwd(const uint16_t* dy, const uint16_t* dres, const uint16_t*
  *   Backward, ids as the forward gave them: with u = p, or p over the sum of the
  *     chosen p, weights = scale u(logits) is differentiated with the choice held
  *     fixed; dlogits [tokens, E] has the logits' type.  A slot whose id is
- *     outside [0, E) counts as not taken.
+ *     outside [0, E), or names a masked expert, counts as not taken; an expert
+ *     named by several slots gets the sum of their gradients.
  *   1 <= E <= 1024, 1 <= topk <= 64, groups in [1, 64] divides E,
  *   1 <= top_groups <= groups, topk <= top_groups E / groups, scale finite
  *   (QLORA_ERR_EXPERT otherwise); 0 <= tokens, tokens*topk <= 2^30
