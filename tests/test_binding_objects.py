@@ -1,11 +1,15 @@
 """Weights that the binding takes by their fields, and numbers that a C argument cannot
 hold (CPU: the calls end at the check that their tensors are on a GPU)."""
+import os
 import types
 
 import pytest
 import torch
 
 import bit_quantized_fine_amd as q
+
+pytestmark = pytest.mark.skipif(not os.path.exists(q.LIB_PATH),
+                                reason="libqlora_nf4.so not built (run __graft_entry__.build())")
 
 
 def _weight(N=64, K=128):
